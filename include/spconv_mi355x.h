@@ -270,6 +270,39 @@ int spconv_wgrad(const void* feats, const void* dout, const spconv_nmap* nmap,
                  void* workspace, size_t workspace_bytes, void* dw,
                  int Ci, int Co, int dtype, void* stream);
 
+/* ---- Row-wise operators of a voxel block ---------------------------------
+ * They take (N, C) feature rows in the caller's order, contiguous, and stand
+ * next to the convolution: the norm before it, the recurrence along the map's
+ * schedule order, the gated linear unit after it.  All sums and statistics
+ * are fp32, each output is rounded once, two calls with the same inputs give
+ * bit-identical outputs.  C up to 4096.  Asynchronous on `stream`, no
+ * allocation, no synchronisation; N = 0 enqueues nothing but the zeros of
+ * outputs that sum over rows.  The row operators' conventions on errors are
+ * the library's. */
+
+/* Layer norm over each row's channels.
+ *   y[n, c] = (x[n, c] - mean[n]) * rstd[n] * weight[c] + bias[c]
+ *   rstd[n] = 1 / sqrt(mean over c of (x - mean)^2 + eps)
+ *   x, y   (dev) (N, C) of dtype, aligned to their elements; y may be x
+ *   weight, bias (dev) float32 (C,), or NULL for 1 and 0
+ *   mean, rstd   (dev) float32 (N,) written, or both NULL
+ *   eps >= 0. */
+int spconv_layernorm(const void* x, const float* weight, const float* bias, void* y, float* mean, float* rstd,
+                     int64_t N, int C, float eps, int dtype, void* stream);
+
+/* Gradient of spconv_layernorm, from the statistics that it wrote.  With
+ * xhat = (x - mean) rstd and g = dout weight:
+ *   dx      = rstd (g - mean_c(g) - xhat mean_c(g xhat))       (N, C), dtype
+ *   dweight = sum_n dout xhat,  dbias = sum_n dout             float32 (C,)
+ *   weight    (dev) as given to the forward (NULL for 1)
+ *   dweight, dbias (dev) written, or both NULL (then no workspace is needed)
+ *   workspace (dev) spconv_layernorm_grad_workspace_size bytes, 256-byte
+ *             aligned: per-workgroup partial sums, added in a fixed order. */
+int spconv_layernorm_grad_workspace_size(int64_t N, int C, int dtype, size_t* bytes);
+int spconv_layernorm_grad(const void* dout, const void* x, const float* mean, const float* rstd,
+                          const float* weight, void* workspace, size_t workspace_bytes, void* dx, float* dweight,
+                          float* dbias, int64_t N, int C, int dtype, void* stream);
+
 /* Release a handle (host memory only; the arena stays the caller's). */
 void spconv_nmap_destroy(spconv_nmap* h);
 

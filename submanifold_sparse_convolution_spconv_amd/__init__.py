@@ -25,6 +25,9 @@ Functions carry the C entry points' names:
     spconv_dgrad(dout, nmap, w) -> dfeats
     spconv_dgrad_noalloc(dout, nmap, w, out) -> out  (no workspace: a fixed scratch in the library)
     spconv_wgrad(feats, dout, nmap) -> dw
+Row-wise operators of a voxel block, on (N, C) feature rows:
+    spconv_layernorm(x, weight=None, bias=None, eps=1e-5, stats=False) -> y, or (y, mean, rstd)
+    spconv_layernorm_grad(dout, x, mean, rstd, weight=None) -> (dx, dweight, dbias)
 """
 from __future__ import annotations
 
@@ -40,6 +43,7 @@ __all__ = [
     "spconv_build_nmap_batched", "spconv_dgrad_workspace_size", "spconv_dgrad", "spconv_dgrad_noalloc",
     "SPCONV_NOALLOC_SCRATCH_BYTES",
     "spconv_wgrad_workspace_size", "spconv_wgrad",
+    "spconv_layernorm", "spconv_layernorm_grad_workspace_size", "spconv_layernorm_grad",
     "SPCONV_F32", "SPCONV_BF16", "STATUS",
 ]
 
@@ -108,6 +112,12 @@ def load_library():
     lib.spconv_wgrad_workspace_size.restype = i32
     lib.spconv_wgrad.argtypes = [vp, vp, vp, vp, sz, vp, i32, i32, i32, vp]
     lib.spconv_wgrad.restype = i32
+    f32, szp = ctypes.c_float, ctypes.POINTER(sz)
+    lib.spconv_layernorm.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, f32, i32, vp]
+    lib.spconv_layernorm_grad_workspace_size.argtypes = [i64, i32, i32, szp]
+    lib.spconv_layernorm_grad.argtypes = [vp, vp, vp, vp, vp, vp, sz, vp, vp, vp, i64, i32, i32, vp]
+    for f in (lib.spconv_layernorm, lib.spconv_layernorm_grad_workspace_size, lib.spconv_layernorm_grad):
+        f.restype = i32
     lib.spconv_nmap_destroy.argtypes = [vp]
     lib.spconv_nmap_destroy.restype = None
     lib.spconv_status_string.argtypes = [i32]
@@ -490,3 +500,102 @@ def spconv_wgrad(feats, dout, nmap: NMap, out=None, workspace=None):
                                          _ptr(out), Ci, Co, dt, _stream(nmap.device))
     _check(rc, "spconv_wgrad")
     return out
+
+
+def _row_dtype(x, name="x"):
+    """The dtype code of a feature tensor (N, C)."""
+    import torch
+    dt = {torch.float32: SPCONV_F32, torch.bfloat16: SPCONV_BF16}.get(x.dtype)
+    if dt is None or x.dim() != 2 or not x.is_cuda:
+        raise ValueError(f"{name} must be a float32 or bfloat16 (N, C) CUDA tensor")
+    return dt
+
+
+def _like(t, shape, dtype, device, name):
+    """t, contiguous, checked against what an input has to be; None stays."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != device:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on the features' device")
+    return t.contiguous()
+
+
+def _out(out, shape, dtype, device, name):
+    import torch
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if out.shape != shape or out.dtype != dtype or out.device != device or not out.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {tuple(shape)} tensor on the features' device")
+    return out
+
+
+def _workspace(workspace, n, device, size_name):
+    import torch
+    if workspace is None:
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    if workspace.dtype != torch.uint8 or workspace.numel() < n or workspace.device != device \
+            or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {size_name} bytes")
+    return workspace
+
+
+def spconv_layernorm(x, weight=None, bias=None, eps: float = 1e-5, stats: bool = False, out=None):
+    """Layer norm over each row's channels: x (N, C) float32 or bfloat16, CUDA,
+    C <= 4096; weight, bias float32 (C,) or None.  Returns y in x's dtype, with
+    ``stats`` (y, mean, rstd), float32 (N,) each, for the gradient."""
+    import torch
+    dt = _row_dtype(x)
+    N, C = x.shape
+    dev = x.device
+    x = x.contiguous()
+    weight = _like(weight, (C,), torch.float32, dev, "weight")
+    bias = _like(bias, (C,), torch.float32, dev, "bias")
+    y = _out(out, (N, C), x.dtype, dev, "out")
+    mean = torch.empty(N, dtype=torch.float32, device=dev) if stats else None
+    rstd = torch.empty(N, dtype=torch.float32, device=dev) if stats else None
+    with torch.cuda.device(dev):
+        rc = load_library().spconv_layernorm(_ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean), _ptr(rstd),
+                                             N, C, eps, dt, _stream(dev))
+    _check(rc, "spconv_layernorm")
+    return (y, mean, rstd) if stats else y
+
+
+def spconv_layernorm_grad_workspace_size(N: int, C: int, dtype: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().spconv_layernorm_grad_workspace_size(N, C, dtype, ctypes.byref(n)),
+           "spconv_layernorm_grad_workspace_size")
+    return n.value
+
+
+def spconv_layernorm_grad(dout, x, mean, rstd, weight=None, out=None, workspace=None):
+    """Gradient of spconv_layernorm: dout and x (N, C), the statistics that the
+    forward returned, its weight.  Returns (dx, dweight, dbias), dweight and
+    dbias float32 (C,), or None both where weight is None.  workspace: a uint8
+    tensor of at least spconv_layernorm_grad_workspace_size bytes (allocated
+    when None)."""
+    import torch
+    dt = _row_dtype(x)
+    N, C = x.shape
+    dev = x.device
+    x = x.contiguous()
+    dout = _like(dout, (N, C), x.dtype, dev, "dout")
+    mean = _like(mean, (N,), torch.float32, dev, "mean")
+    rstd = _like(rstd, (N,), torch.float32, dev, "rstd")
+    if dout is None or mean is None or rstd is None:
+        raise ValueError("dout, mean and rstd must be given")
+    weight = _like(weight, (C,), torch.float32, dev, "weight")
+    dx = _out(out, (N, C), x.dtype, dev, "out")
+    ws = dweight = dbias = None
+    n = 0
+    if weight is not None:
+        n = spconv_layernorm_grad_workspace_size(N, C, dt)
+        ws = _workspace(workspace, n, dev, "spconv_layernorm_grad_workspace_size")
+        n = ws.numel()
+        dweight = torch.empty(C, dtype=torch.float32, device=dev)
+        dbias = torch.empty(C, dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        rc = load_library().spconv_layernorm_grad(_ptr(dout), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight),
+                                                  _ptr(ws), n, _ptr(dx), _ptr(dweight), _ptr(dbias), N, C, dt,
+                                                  _stream(dev))
+    _check(rc, "spconv_layernorm_grad")
+    return dx, dweight, dbias

@@ -522,6 +522,73 @@ int spconv_wgrad(const void* feats, const void* dout, const spconv_nmap* nmap, v
     return e == hipSuccess ? SPCONV_OK : hip_fail(e, "spconv_wgrad");
 }
 
+// Checks shared by the row-wise operators: rows, channels, element type.
+static int check_rows(int64_t N, int C, int dtype, const char* what) {
+    if (dtype != SPCONV_F32 && dtype != SPCONV_BF16)
+        return fail(SPCONV_E_INVALID, "dtype must be SPCONV_F32 or SPCONV_BF16 (got %d)", dtype);
+    if (N < 0) return fail(SPCONV_E_INVALID, "N must be >= 0 (got %lld)", (long long)N);
+    if (N > kMaxN) return fail(SPCONV_E_UNSUPPORTED, "N must be < 2^31-1 (got %lld)", (long long)N);
+    if (C < 1) return fail(SPCONV_E_INVALID, "%s must be >= 1 (got %d)", what, C);
+    if (C > spc::kMaxRowChannels)
+        return fail(SPCONV_E_UNSUPPORTED, "%s must be <= %d (got %d)", what, spc::kMaxRowChannels, C);
+    return SPCONV_OK;
+}
+static size_t elem_size(int dtype) { return dtype == SPCONV_BF16 ? 2 : 4; }
+
+int spconv_layernorm(const void* x, const float* weight, const float* bias, void* y, float* mean, float* rstd,
+                     int64_t N, int C, float eps, int dtype, void* stream) {
+    int rc = check_rows(N, C, dtype, "C");
+    if (rc) return rc;
+    if (!(eps >= 0.f)) return fail(SPCONV_E_INVALID, "eps must be >= 0 (got %g)", (double)eps);
+    if (!mean != !rstd) return fail(SPCONV_E_INVALID, "mean and rstd must be given together");
+    if (N == 0) return SPCONV_OK;
+    if (!x || !y) return fail(SPCONV_E_INVALID, "x and y must be non-NULL");
+    const size_t es = elem_size(dtype);
+    if (!aligned(x, es) || !aligned(y, es)) return fail(SPCONV_E_INVALID, "x and y must be aligned to their elements");
+    if (!aligned(weight, 4) || !aligned(bias, 4) || !aligned(mean, 4) || !aligned(rstd, 4))
+        return fail(SPCONV_E_INVALID, "weight, bias, mean and rstd must be 4-byte aligned");
+    hipError_t e = spc::launch_norm({x, weight, bias, y, mean, rstd, N, C, eps, dtype}, (hipStream_t)stream);
+    return e == hipSuccess ? SPCONV_OK : hip_fail(e, "spconv_layernorm");
+}
+
+int spconv_layernorm_grad_workspace_size(int64_t N, int C, int dtype, size_t* bytes) {
+    if (!bytes) return fail(SPCONV_E_INVALID, "bytes pointer is NULL");
+    int rc = check_rows(N, C, dtype, "C");
+    if (rc) return rc;
+    *bytes = spc::norm_grad_workspace_bytes(N, C, dtype);
+    return SPCONV_OK;
+}
+
+int spconv_layernorm_grad(const void* dout, const void* x, const float* mean, const float* rstd,
+                          const float* weight, void* workspace, size_t workspace_bytes, void* dx, float* dweight,
+                          float* dbias, int64_t N, int C, int dtype, void* stream) {
+    size_t need = 0;
+    int rc = spconv_layernorm_grad_workspace_size(N, C, dtype, &need);
+    if (rc) return rc;
+    if (!dweight != !dbias) return fail(SPCONV_E_INVALID, "dweight and dbias must be given together");
+    const size_t es = elem_size(dtype);
+    if (N > 0) {
+        if (!dout || !x || !mean || !rstd || !dx)
+            return fail(SPCONV_E_INVALID, "dout, x, mean, rstd and dx must be non-NULL");
+        if (!aligned(dout, es) || !aligned(x, es) || !aligned(dx, es))
+            return fail(SPCONV_E_INVALID, "dout, x and dx must be aligned to their elements");
+        if (!aligned(mean, 4) || !aligned(rstd, 4) || !aligned(weight, 4))
+            return fail(SPCONV_E_INVALID, "mean, rstd and weight must be 4-byte aligned");
+        if (dweight) {
+            if (!workspace) return fail(SPCONV_E_INVALID, "workspace is NULL");
+            if (!aligned(workspace, 256)) return fail(SPCONV_E_INVALID, "workspace must be 256-byte aligned");
+            if (workspace_bytes < need)
+                return fail(SPCONV_E_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+        }
+    }
+    if (!aligned(dweight, 4) || !aligned(dbias, 4))
+        return fail(SPCONV_E_INVALID, "dweight and dbias must be 4-byte aligned");
+    // with no rows dweight and dbias are zero (written by the kernel; no workspace used)
+    hipError_t e = spc::launch_norm_grad({dout, x, mean, rstd, weight, workspace, dx, dweight, dbias, N, C, dtype},
+                                         (hipStream_t)stream);
+    return e == hipSuccess ? SPCONV_OK : hip_fail(e, "spconv_layernorm_grad");
+}
+
 void spconv_nmap_destroy(spconv_nmap* h) {
     if (valid_handle(h)) {
         h->magic = 0;

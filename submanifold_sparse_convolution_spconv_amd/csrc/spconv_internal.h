@@ -203,6 +203,39 @@ bool wgrad_supported(int dtype, int Ci, int Co);
 size_t wgrad_workspace_bytes(int64_t N, int K, int Ci, int Co, int dtype);
 hipError_t launch_wgrad(const WgradArgs& a, hipStream_t stream);
 
+// Row-wise operators: channels (and hidden widths) up to this.
+constexpr int kMaxRowChannels = 4096;
+
+struct NormArgs {
+    const void* x;
+    const float* weight;   // or NULL: 1
+    const float* bias;     // or NULL: 0
+    void* y;
+    float* mean;           // or NULL (then rstd too): statistics not kept
+    float* rstd;
+    int64_t N;
+    int C;
+    float eps;
+    int dtype;
+};
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
+
+struct NormGradArgs {
+    const void* dout;
+    const void* x;
+    const float* mean;
+    const float* rstd;
+    const float* weight;   // or NULL: 1
+    void* workspace;       // norm_grad_workspace_bytes, when dweight is wanted
+    void* dx;
+    float* dweight;        // or NULL (then dbias too)
+    float* dbias;
+    int64_t N;
+    int C, dtype;
+};
+size_t norm_grad_workspace_bytes(int64_t N, int C, int dtype);
+hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t stream);
+
 }  // namespace spc
 
 // Opaque handle of the public interface.

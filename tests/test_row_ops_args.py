@@ -1,0 +1,65 @@
+"""Refusals of the row-wise operators (no GPU needed): the C entry points'
+argument checks return the documented codes before anything is enqueued, and
+the Python functions refuse tensors that do not fit."""
+import ctypes
+
+import pytest
+import torch
+
+import submanifold_sparse_convolution_spconv_amd as sp
+
+FAKE = 0x7f0000000000           # aligned, never dereferenced: every call below fails a check or has no rows
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, -1, -2, -5
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return sp.load_library()
+
+
+def p(a):
+    return ctypes.c_void_p(a) if a else None
+
+
+def test_layernorm_refusals(lib):
+    def f(x=FAKE, w=FAKE, b=FAKE, y=FAKE, m=FAKE, r=FAKE, N=0, C=64, eps=1e-5, dt=1):
+        return lib.spconv_layernorm(p(x), p(w), p(b), p(y), p(m), p(r), N, C, eps, dt, None)
+    assert f() == OK                                     # no rows: nothing enqueued
+    assert f(x=0, y=0, w=0, b=0, m=0, r=0) == OK
+    assert f(dt=2) == INVALID and f(dt=-1) == INVALID
+    assert f(N=-1) == INVALID and f(N=1 << 31) == UNSUPPORTED
+    assert f(C=0) == INVALID and f(C=4097) == UNSUPPORTED and f(C=4096) == OK
+    assert f(eps=-1.0) == INVALID and f(eps=float("nan")) == INVALID
+    assert f(m=0) == INVALID and f(r=0) == INVALID       # one statistic without the other
+    assert f(N=4, x=0) == INVALID and f(N=4, y=0) == INVALID
+    assert f(N=4, x=FAKE + 1) == INVALID and f(N=4, x=FAKE + 2, dt=0) == INVALID
+    assert f(N=4, w=FAKE + 2) == INVALID and f(N=4, m=FAKE + 1) == INVALID
+    assert b"aligned" in lib.spconv_last_error()
+
+
+def test_layernorm_grad_refusals(lib):
+    n = ctypes.c_size_t(0)
+    S = lambda N, C, dt: lib.spconv_layernorm_grad_workspace_size(N, C, dt, ctypes.byref(n))
+    assert S(0, 64, 1) == OK and n.value == 0
+    assert S(1006716, 128, 1) == OK and 0 < n.value <= 2 << 20 and n.value % 256 == 0
+    assert S(10, 4097, 1) == UNSUPPORTED and S(10, 0, 1) == INVALID and S(-1, 8, 1) == INVALID and S(1, 8, 7) == INVALID
+    assert lib.spconv_layernorm_grad_workspace_size(10, 64, 1, None) == INVALID
+    assert S(4, 64, 1) == OK
+    need = n.value
+
+    def f(d=FAKE, x=FAKE, m=FAKE, r=FAKE, w=FAKE, ws=FAKE, wb=need, dx=FAKE, dw=FAKE, db=FAKE, N=4, C=64, dt=1):
+        return lib.spconv_layernorm_grad(p(d), p(x), p(m), p(r), p(w), p(ws), wb, p(dx), p(dw), p(db), N, C, dt, None)
+    for k in ("d", "x", "m", "r", "dx", "dw", "db", "ws"):
+        assert f(**{k: 0}) == INVALID, k
+    assert f(wb=need - 1) == WORKSPACE
+    assert f(ws=FAKE + 16) == INVALID and f(dx=FAKE + 1) == INVALID and f(dw=FAKE + 2) == INVALID
+    assert f(dt=3) == INVALID and f(C=5000) == UNSUPPORTED
+    assert f(N=0, dw=0, db=0) == OK                      # no rows and no sums over rows
+
+
+def test_python_refuses_host_tensors():
+    x = torch.zeros(4, 64)
+    with pytest.raises(ValueError):
+        sp.spconv_layernorm(x)
+    with pytest.raises(ValueError):
+        sp.spconv_layernorm_grad(x, x, x[:, 0], x[:, 0])
