@@ -303,6 +303,45 @@ int spconv_layernorm_grad(const void* dout, const void* x, const float* mean, co
                           const float* weight, void* workspace, size_t workspace_bytes, void* dx, float* dweight,
                           float* dbias, int64_t N, int C, int dtype, void* stream);
 
+/* Gated linear recurrence over the voxels of each scene, in a given order
+ * (the map's schedule order from spconv_nmap_export is a space-filling curve):
+ *   h[t] = f[t] h[t-1] + (1 - f[t]) x[t],   f[t] = sigmoid(z[t])
+ * per channel, along the positions t = offsets[b] .. offsets[b+1] - 1 of scene
+ * b, from h0[b] before the first.
+ *   x, z    (dev) (N, C) of dtype, in the caller's row order, aligned to their
+ *           elements
+ *   offsets (dev) int32 (scenes + 1,): 0 = offsets[0] <= ... <=
+ *           offsets[scenes] = N; scenes without positions may stand anywhere
+ *   order   (dev) int32 (N,): position t is row order[t], each row once; or
+ *           NULL: position t is row t
+ *   h0      (dev) float32 (scenes, C), or NULL for zero
+ *   h       (dev) (N, C) written, of dtype: row order[t] holds h[t]
+ *   last    (dev) float32 (scenes, C) written: each scene's last state (h0 of
+ *           a scene without positions)
+ *   workspace (dev) spconv_scan_workspace_size bytes, 256-byte aligned (may
+ *           be NULL when that is 0)
+ * The contents of offsets and order are not checked: bad values give wrong
+ * states, never an access outside the given arrays. */
+int spconv_scan_workspace_size(int64_t N, int C, int dtype, size_t* bytes);
+int spconv_scan(const void* x, const void* z, const int32_t* offsets, const int32_t* order, const float* h0,
+                void* workspace, size_t workspace_bytes, void* h, float* last, int64_t N, int C, int scenes,
+                int dtype, void* stream);
+
+/* Gradient of spconv_scan.  With g[t] = dout[t] + f[t+1] g[t+1] along a scene
+ * (dlast[b] added at its last position):
+ *   dx[t] = (1 - f[t]) g[t],  dz[t] = g[t] (h[t-1] - x[t]) f[t] (1 - f[t]),
+ *   dh0[b] = f[first] g[first]  (dlast[b] of a scene without positions)
+ *   dout    (dev) (N, C) of dtype, in the caller's row order
+ *   dlast   (dev) float32 (scenes, C): the gradient at `last`, or NULL for 0
+ *   dx, dz  (dev) (N, C) written, of dtype, in the caller's row order
+ *   dh0     (dev) float32 (scenes, C) written, or NULL
+ * The states are computed again; nothing of the forward is needed.  Other
+ * arguments, and what is said about them, are spconv_scan's. */
+int spconv_scan_grad_workspace_size(int64_t N, int C, int dtype, size_t* bytes);
+int spconv_scan_grad(const void* dout, const void* x, const void* z, const int32_t* offsets, const int32_t* order,
+                     const float* h0, const float* dlast, void* workspace, size_t workspace_bytes, void* dx,
+                     void* dz, float* dh0, int64_t N, int C, int scenes, int dtype, void* stream);
+
 /* Release a handle (host memory only; the arena stays the caller's). */
 void spconv_nmap_destroy(spconv_nmap* h);
 

@@ -28,6 +28,8 @@ Functions carry the C entry points' names:
 Row-wise operators of a voxel block, on (N, C) feature rows:
     spconv_layernorm(x, weight=None, bias=None, eps=1e-5, stats=False) -> y, or (y, mean, rstd)
     spconv_layernorm_grad(dout, x, mean, rstd, weight=None) -> (dx, dweight, dbias)
+    spconv_scan(x, z, offsets, order=None, h0=None) -> (h, last)
+    spconv_scan_grad(dout, x, z, offsets, order=None, h0=None, dlast=None) -> (dx, dz, dh0)
 """
 from __future__ import annotations
 
@@ -44,6 +46,7 @@ __all__ = [
     "SPCONV_NOALLOC_SCRATCH_BYTES",
     "spconv_wgrad_workspace_size", "spconv_wgrad",
     "spconv_layernorm", "spconv_layernorm_grad_workspace_size", "spconv_layernorm_grad",
+    "spconv_scan_workspace_size", "spconv_scan", "spconv_scan_grad_workspace_size", "spconv_scan_grad",
     "SPCONV_F32", "SPCONV_BF16", "STATUS",
 ]
 
@@ -116,7 +119,12 @@ def load_library():
     lib.spconv_layernorm.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, f32, i32, vp]
     lib.spconv_layernorm_grad_workspace_size.argtypes = [i64, i32, i32, szp]
     lib.spconv_layernorm_grad.argtypes = [vp, vp, vp, vp, vp, vp, sz, vp, vp, vp, i64, i32, i32, vp]
-    for f in (lib.spconv_layernorm, lib.spconv_layernorm_grad_workspace_size, lib.spconv_layernorm_grad):
+    lib.spconv_scan_workspace_size.argtypes = [i64, i32, i32, szp]
+    lib.spconv_scan.argtypes = [vp, vp, vp, vp, vp, vp, sz, vp, vp, i64, i32, i32, i32, vp]
+    lib.spconv_scan_grad_workspace_size.argtypes = [i64, i32, i32, szp]
+    lib.spconv_scan_grad.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp, vp, i64, i32, i32, i32, vp]
+    for f in (lib.spconv_scan_workspace_size, lib.spconv_scan, lib.spconv_scan_grad_workspace_size,
+              lib.spconv_scan_grad, lib.spconv_layernorm, lib.spconv_layernorm_grad_workspace_size, lib.spconv_layernorm_grad):
         f.restype = i32
     lib.spconv_nmap_destroy.argtypes = [vp]
     lib.spconv_nmap_destroy.restype = None
@@ -599,3 +607,77 @@ def spconv_layernorm_grad(dout, x, mean, rstd, weight=None, out=None, workspace=
                                                   _stream(dev))
     _check(rc, "spconv_layernorm_grad")
     return dx, dweight, dbias
+
+
+def _scan_args(x, z, offsets, order, h0):
+    import torch
+    dt = _row_dtype(x)
+    N, C = x.shape
+    dev = x.device
+    if z is None or offsets is None:
+        raise ValueError("z and offsets must be given")
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or offsets.device != dev:
+        raise ValueError("offsets must be an int32 (scenes + 1,) tensor on the features' device")
+    B = offsets.numel() - 1
+    x = x.contiguous()
+    z = _like(z, (N, C), x.dtype, dev, "z")
+    order = _like(order, (N,), torch.int32, dev, "order")
+    h0 = _like(h0, (B, C), torch.float32, dev, "h0")
+    return dt, N, C, B, dev, x, z, offsets.contiguous(), order, h0
+
+
+def spconv_scan_workspace_size(N: int, C: int, dtype: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().spconv_scan_workspace_size(N, C, dtype, ctypes.byref(n)), "spconv_scan_workspace_size")
+    return n.value
+
+
+def spconv_scan(x, z, offsets, order=None, h0=None, out=None, workspace=None):
+    """Gated linear recurrence h[t] = f h[t-1] + (1 - f) x[t], f = sigmoid(z[t]),
+    along each scene: x, z (N, C) float32 or bfloat16, CUDA, C <= 4096; offsets
+    int32 (scenes + 1,), the scenes' positions; order int32 (N,), the row of
+    each position (None: rows in order); h0 float32 (scenes, C), the states to
+    start from (None: zero).  Returns (h (N, C) in the caller's row order, last
+    (scenes, C) float32: each scene's last state).  workspace: a uint8 tensor of
+    at least spconv_scan_workspace_size bytes (allocated when None)."""
+    import torch
+    dt, N, C, B, dev, x, z, offsets, order, h0 = _scan_args(x, z, offsets, order, h0)
+    h = _out(out, (N, C), x.dtype, dev, "out")
+    last = torch.empty((B, C), dtype=torch.float32, device=dev)
+    ws = _workspace(workspace, spconv_scan_workspace_size(N, C, dt), dev, "spconv_scan_workspace_size")
+    with torch.cuda.device(dev):
+        rc = load_library().spconv_scan(_ptr(x), _ptr(z), _ptr(offsets), _ptr(order), _ptr(h0), _ptr(ws),
+                                        ws.numel(), _ptr(h), _ptr(last), N, C, B, dt, _stream(dev))
+    _check(rc, "spconv_scan")
+    return h, last
+
+
+def spconv_scan_grad_workspace_size(N: int, C: int, dtype: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().spconv_scan_grad_workspace_size(N, C, dtype, ctypes.byref(n)),
+           "spconv_scan_grad_workspace_size")
+    return n.value
+
+
+def spconv_scan_grad(dout, x, z, offsets, order=None, h0=None, dlast=None, workspace=None):
+    """Gradient of spconv_scan: dout (N, C) at h, dlast float32 (scenes, C) at
+    the last states (None: zero), the forward's inputs.  Returns (dx, dz, dh0),
+    dh0 float32 (scenes, C), or None where h0 is None.  workspace: a uint8
+    tensor of at least spconv_scan_grad_workspace_size bytes (allocated when
+    None)."""
+    import torch
+    dt, N, C, B, dev, x, z, offsets, order, h0 = _scan_args(x, z, offsets, order, h0)
+    dout = _like(dout, (N, C), x.dtype, dev, "dout")
+    if dout is None:
+        raise ValueError("dout must be given")
+    dlast = _like(dlast, (B, C), torch.float32, dev, "dlast")
+    dx = torch.empty_like(x)
+    dz = torch.empty_like(x)
+    dh0 = torch.empty_like(h0) if h0 is not None else None
+    ws = _workspace(workspace, spconv_scan_grad_workspace_size(N, C, dt), dev, "spconv_scan_grad_workspace_size")
+    with torch.cuda.device(dev):
+        rc = load_library().spconv_scan_grad(_ptr(dout), _ptr(x), _ptr(z), _ptr(offsets), _ptr(order), _ptr(h0),
+                                             _ptr(dlast), _ptr(ws), ws.numel(), _ptr(dx), _ptr(dz), _ptr(dh0),
+                                             N, C, B, dt, _stream(dev))
+    _check(rc, "spconv_scan_grad")
+    return dx, dz, dh0

@@ -589,6 +589,66 @@ int spconv_layernorm_grad(const void* dout, const void* x, const float* mean, co
     return e == hipSuccess ? SPCONV_OK : hip_fail(e, "spconv_layernorm_grad");
 }
 
+static int scan_size(int64_t N, int C, int dtype, bool grad, size_t* bytes) {
+    if (!bytes) return fail(SPCONV_E_INVALID, "bytes pointer is NULL");
+    int rc = check_rows(N, C, dtype, "C");
+    if (rc) return rc;
+    *bytes = spc::scan_workspace_bytes(N, C, dtype, grad);
+    return SPCONV_OK;
+}
+
+// Checks of both directions; a.out .. a.state are the outputs.
+static int scan_impl(const spc::ScanArgs& a, bool grad, size_t workspace_bytes, void* stream, const char* name) {
+    size_t need = 0;
+    int rc = scan_size(a.N, a.C, a.dtype, grad, &need);
+    if (rc) return rc;
+    if (a.scenes < 1) return fail(SPCONV_E_INVALID, "scenes must be >= 1 (got %d)", a.scenes);
+    if (!a.offsets) return fail(SPCONV_E_INVALID, "offsets is NULL");
+    if (!grad && !a.state) return fail(SPCONV_E_INVALID, "last is NULL");
+    if (!aligned(a.offsets, 4) || !aligned(a.order, 4) || !aligned(a.h0, 4) || !aligned(a.dlast, 4) ||
+        !aligned(a.state, 4))
+        return fail(SPCONV_E_INVALID, "offsets, order and the scenes' states must be 4-byte aligned");
+    if (a.N > 0) {
+        const size_t es = elem_size(a.dtype);
+        if (!a.x || !a.z || !a.out || (grad && (!a.dout || !a.dz)))
+            return fail(SPCONV_E_INVALID, grad ? "dout, x, z, dx and dz must be non-NULL"
+                                               : "x, z and h must be non-NULL");
+        if (!aligned(a.x, es) || !aligned(a.z, es) || !aligned(a.out, es) || !aligned(a.dout, es) ||
+            !aligned(a.dz, es))
+            return fail(SPCONV_E_INVALID, "feature rows must be aligned to their elements");
+        if (need) {
+            if (!a.workspace) return fail(SPCONV_E_INVALID, "workspace is NULL");
+            if (!aligned(a.workspace, 256)) return fail(SPCONV_E_INVALID, "workspace must be 256-byte aligned");
+            if (workspace_bytes < need)
+                return fail(SPCONV_E_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+        }
+    }
+    hipError_t e = spc::launch_scan(a, grad, (hipStream_t)stream);
+    return e == hipSuccess ? SPCONV_OK : hip_fail(e, name);
+}
+
+int spconv_scan_workspace_size(int64_t N, int C, int dtype, size_t* bytes) {
+    return scan_size(N, C, dtype, false, bytes);
+}
+
+int spconv_scan(const void* x, const void* z, const int32_t* offsets, const int32_t* order, const float* h0,
+                void* workspace, size_t workspace_bytes, void* h, float* last, int64_t N, int C, int scenes,
+                int dtype, void* stream) {
+    return scan_impl({x, z, nullptr, offsets, order, h0, nullptr, workspace, h, nullptr, last, N, C, scenes, dtype},
+                     false, workspace_bytes, stream, "spconv_scan");
+}
+
+int spconv_scan_grad_workspace_size(int64_t N, int C, int dtype, size_t* bytes) {
+    return scan_size(N, C, dtype, true, bytes);
+}
+
+int spconv_scan_grad(const void* dout, const void* x, const void* z, const int32_t* offsets, const int32_t* order,
+                     const float* h0, const float* dlast, void* workspace, size_t workspace_bytes, void* dx,
+                     void* dz, float* dh0, int64_t N, int C, int scenes, int dtype, void* stream) {
+    return scan_impl({x, z, dout, offsets, order, h0, dlast, workspace, dx, dz, dh0, N, C, scenes, dtype}, true,
+                     workspace_bytes, stream, "spconv_scan_grad");
+}
+
 void spconv_nmap_destroy(spconv_nmap* h) {
     if (valid_handle(h)) {
         h->magic = 0;

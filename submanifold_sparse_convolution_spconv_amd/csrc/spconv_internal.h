@@ -236,6 +236,24 @@ struct NormGradArgs {
 size_t norm_grad_workspace_bytes(int64_t N, int C, int dtype);
 hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t stream);
 
+struct ScanArgs {
+    const void* x;
+    const void* z;
+    const void* dout;      // gradient only
+    const int32_t* offsets;
+    const int32_t* order;  // or NULL: rows in sequence order
+    const float* h0;       // or NULL: 0
+    const float* dlast;    // gradient only; or NULL: 0
+    void* workspace;       // scan_workspace_bytes
+    void* out;             // forward: h; gradient: dx
+    void* dz;              // gradient only
+    float* state;          // forward: last; gradient: dh0 or NULL
+    int64_t N;
+    int C, scenes, dtype;
+};
+size_t scan_workspace_bytes(int64_t N, int C, int dtype, bool grad);
+hipError_t launch_scan(const ScanArgs& a, bool grad, hipStream_t stream);
+
 }  // namespace spc
 
 // Opaque handle of the public interface.

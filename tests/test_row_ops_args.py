@@ -57,9 +57,45 @@ def test_layernorm_grad_refusals(lib):
     assert f(N=0, dw=0, db=0) == OK                      # no rows and no sums over rows
 
 
+def test_scan_refusals(lib):
+    n = ctypes.c_size_t(0)
+    for S in (lib.spconv_scan_workspace_size, lib.spconv_scan_grad_workspace_size):
+        assert S(64, 128, 1, ctypes.byref(n)) == OK and n.value == 0      # one chunk of rows
+        assert S(1006716, 128, 1, ctypes.byref(n)) == OK and 0 < n.value < 256 << 20 and n.value % 256 == 0
+        assert S(4, 0, 1, ctypes.byref(n)) == INVALID and S(4, 4097, 0, ctypes.byref(n)) == UNSUPPORTED
+        assert S(-1, 8, 1, ctypes.byref(n)) == INVALID and S(1 << 31, 8, 1, ctypes.byref(n)) == UNSUPPORTED
+        assert S(4, 8, 2, ctypes.byref(n)) == INVALID and S(4, 8, 1, None) == INVALID
+    N = 100000
+    assert lib.spconv_scan_workspace_size(N, 64, 1, ctypes.byref(n)) == OK
+    need = n.value
+
+    def f(x=FAKE, z=FAKE, off=FAKE, order=FAKE, h0=FAKE, ws=FAKE, wb=need, h=FAKE, last=FAKE, N=N, C=64, B=3, dt=1):
+        return lib.spconv_scan(p(x), p(z), p(off), p(order), p(h0), p(ws), wb, p(h), p(last), N, C, B, dt, None)
+    for k in ("x", "z", "off", "ws", "h", "last"):
+        assert f(**{k: 0}) == INVALID, k
+    assert f(wb=need - 1) == WORKSPACE and f(ws=FAKE + 64) == INVALID
+    assert f(B=0) == INVALID and f(dt=9) == INVALID and f(C=4097) == UNSUPPORTED and f(N=-1) == INVALID
+    assert f(x=FAKE + 1) == INVALID and f(order=FAKE + 2) == INVALID and f(last=FAKE + 2) == INVALID
+    assert lib.spconv_scan_grad_workspace_size(N, 64, 1, ctypes.byref(n)) == OK
+    need = n.value
+
+    def g(d=FAKE, x=FAKE, z=FAKE, off=FAKE, dl=FAKE, ws=FAKE, wb=need, dx=FAKE, dz=FAKE, dh0=FAKE, C=64, B=3, dt=1):
+        return lib.spconv_scan_grad(p(d), p(x), p(z), p(off), None, None, p(dl), p(ws), wb, p(dx), p(dz), p(dh0), N, C,
+                                    B, dt, None)
+    for k in ("d", "x", "z", "off", "ws", "dx", "dz"):
+        assert g(**{k: 0}) == INVALID, k
+    assert g(wb=need - 1) == WORKSPACE and g(dh0=FAKE + 1) == INVALID and g(dl=FAKE + 2) == INVALID
+    assert g(B=-2) == INVALID and g(dt=2) == INVALID
+
+
 def test_python_refuses_host_tensors():
     x = torch.zeros(4, 64)
     with pytest.raises(ValueError):
         sp.spconv_layernorm(x)
     with pytest.raises(ValueError):
         sp.spconv_layernorm_grad(x, x, x[:, 0], x[:, 0])
+    o = torch.tensor([0, 4], dtype=torch.int32)
+    with pytest.raises(ValueError):
+        sp.spconv_scan(x, x, o)
+    with pytest.raises(ValueError):
+        sp.spconv_scan_grad(x, x, x, o)
