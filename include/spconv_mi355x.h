@@ -52,6 +52,11 @@ enum spconv_dtype {
     SPCONV_BF16 = 1             /* feats, w, out bfloat16; accumulation is fp32 either way */
 };
 
+enum spconv_act {
+    SPCONV_SILU = 0,            /* a sigmoid(a)                                            */
+    SPCONV_GELU = 1             /* a (1 + erf(a / sqrt 2)) / 2                             */
+};
+
 /* Opaque host-side handle of a built neighbour map.  The map's device data
  * lives in the caller's arena, which must outlive every use of the handle. */
 typedef struct spconv_nmap spconv_nmap;
@@ -302,6 +307,32 @@ int spconv_layernorm_grad_workspace_size(int64_t N, int C, int dtype, size_t* by
 int spconv_layernorm_grad(const void* dout, const void* x, const float* mean, const float* rstd,
                           const float* weight, void* workspace, size_t workspace_bytes, void* dx, float* dweight,
                           float* dbias, int64_t N, int C, int dtype, void* stream);
+
+/* Gated linear unit of a feed-forward block: both projections, the activation
+ * and the product in one pass.
+ *   a = x w[0] + bias[0],  b = x w[1] + bias[1],  h = act(a) b
+ *   x    (dev) (N, C),  w (dev) (2, C, F) row-major,  h (dev) (N, F) written;
+ *        all of dtype and 16-byte aligned
+ *   bias (dev) float32 (2, F), or NULL for zero
+ *   act  SPCONV_SILU or SPCONV_GELU
+ * C and F multiples of 8 up to 4096; others give SPCONV_E_UNSUPPORTED.  a and
+ * b stay in fp32; the output is rounded once. */
+int spconv_glu(const void* x, const void* w, const float* bias, void* h, int64_t N, int C, int F, int act,
+               int dtype, void* stream);
+
+/* Gradient of spconv_glu; a and b are computed again.
+ *   da = dout b act'(a),  db = dout act(a)
+ *   dx = da w[0]^T + db w[1]^T                     (N, C) of dtype
+ *   dw[0] = x^T da,  dw[1] = x^T db                (2, C, F) of dtype
+ *   dbias[s] = sum_n (da | db)                     float32 (2, F), or NULL
+ * With SPCONV_BF16, da and db are rounded to bfloat16 once as the operands of
+ * dx and dw (dbias adds them unrounded); all sums are fp32.
+ *   workspace (dev) spconv_glu_grad_workspace_size bytes, 256-byte aligned:
+ *             da and db, partial sums (added in a fixed order). */
+int spconv_glu_grad_workspace_size(int64_t N, int C, int F, int dtype, size_t* bytes);
+int spconv_glu_grad(const void* dout, const void* x, const void* w, const float* bias, void* workspace,
+                    size_t workspace_bytes, void* dx, void* dw, float* dbias, int64_t N, int C, int F, int act,
+                    int dtype, void* stream);
 
 /* Gated linear recurrence over the voxels of each scene, in a given order
  * (the map's schedule order from spconv_nmap_export is a space-filling curve):

@@ -28,6 +28,8 @@ Functions carry the C entry points' names:
 Row-wise operators of a voxel block, on (N, C) feature rows:
     spconv_layernorm(x, weight=None, bias=None, eps=1e-5, stats=False) -> y, or (y, mean, rstd)
     spconv_layernorm_grad(dout, x, mean, rstd, weight=None) -> (dx, dweight, dbias)
+    spconv_glu(x, w, bias=None, act="silu") -> h
+    spconv_glu_grad(dout, x, w, bias=None, act="silu") -> (dx, dw, dbias)
     spconv_scan(x, z, offsets, order=None, h0=None) -> (h, last)
     spconv_scan_grad(dout, x, z, offsets, order=None, h0=None, dlast=None) -> (dx, dz, dh0)
 """
@@ -46,6 +48,7 @@ __all__ = [
     "SPCONV_NOALLOC_SCRATCH_BYTES",
     "spconv_wgrad_workspace_size", "spconv_wgrad",
     "spconv_layernorm", "spconv_layernorm_grad_workspace_size", "spconv_layernorm_grad",
+    "spconv_glu", "spconv_glu_grad_workspace_size", "spconv_glu_grad", "SPCONV_SILU", "SPCONV_GELU",
     "spconv_scan_workspace_size", "spconv_scan", "spconv_scan_grad_workspace_size", "spconv_scan_grad",
     "SPCONV_F32", "SPCONV_BF16", "STATUS",
 ]
@@ -56,6 +59,8 @@ _LIB_PATH = os.environ.get("SPCONV_LIB") or os.path.join(_PKG, "libspconv_mi355x
 
 SPCONV_F32 = 0
 SPCONV_BF16 = 1
+SPCONV_SILU = 0
+SPCONV_GELU = 1
 STATUS = {0: "SPCONV_OK", -1: "SPCONV_E_INVALID", -2: "SPCONV_E_UNSUPPORTED",
           -3: "SPCONV_E_COORD_RANGE", -4: "SPCONV_E_DUPLICATE", -5: "SPCONV_E_WORKSPACE",
           -6: "SPCONV_E_HIP"}
@@ -119,11 +124,15 @@ def load_library():
     lib.spconv_layernorm.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, f32, i32, vp]
     lib.spconv_layernorm_grad_workspace_size.argtypes = [i64, i32, i32, szp]
     lib.spconv_layernorm_grad.argtypes = [vp, vp, vp, vp, vp, vp, sz, vp, vp, vp, i64, i32, i32, vp]
+    lib.spconv_glu.argtypes = [vp, vp, vp, vp, i64, i32, i32, i32, i32, vp]
+    lib.spconv_glu_grad_workspace_size.argtypes = [i64, i32, i32, i32, szp]
+    lib.spconv_glu_grad.argtypes = [vp, vp, vp, vp, vp, sz, vp, vp, vp, i64, i32, i32, i32, i32, vp]
     lib.spconv_scan_workspace_size.argtypes = [i64, i32, i32, szp]
     lib.spconv_scan.argtypes = [vp, vp, vp, vp, vp, vp, sz, vp, vp, i64, i32, i32, i32, vp]
     lib.spconv_scan_grad_workspace_size.argtypes = [i64, i32, i32, szp]
     lib.spconv_scan_grad.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp, vp, i64, i32, i32, i32, vp]
-    for f in (lib.spconv_scan_workspace_size, lib.spconv_scan, lib.spconv_scan_grad_workspace_size,
+    for f in (lib.spconv_glu, lib.spconv_glu_grad_workspace_size, lib.spconv_glu_grad,
+              lib.spconv_scan_workspace_size, lib.spconv_scan, lib.spconv_scan_grad_workspace_size,
               lib.spconv_scan_grad, lib.spconv_layernorm, lib.spconv_layernorm_grad_workspace_size, lib.spconv_layernorm_grad):
         f.restype = i32
     lib.spconv_nmap_destroy.argtypes = [vp]
@@ -607,6 +616,65 @@ def spconv_layernorm_grad(dout, x, mean, rstd, weight=None, out=None, workspace=
                                                   _stream(dev))
     _check(rc, "spconv_layernorm_grad")
     return dx, dweight, dbias
+
+
+_ACTS = {"silu": SPCONV_SILU, "gelu": SPCONV_GELU}
+
+
+def _glu_args(x, w, bias, act):
+    import torch
+    dt = _row_dtype(x)
+    N, C = x.shape
+    dev = x.device
+    if w is None or w.dtype != x.dtype or w.dim() != 3 or w.shape[0] != 2 or w.shape[1] != C or w.device != dev:
+        raise ValueError("w must be (2, C, F) of x's dtype on its device")
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}")
+    F = w.shape[2]
+    bias = _like(bias, (2, F), torch.float32, dev, "bias")
+    return dt, N, C, F, dev, x.contiguous(), w.contiguous(), bias, _ACTS[act]
+
+
+def spconv_glu(x, w, bias=None, act: str = "silu", out=None):
+    """Gated linear unit h = act(x w[0] + bias[0]) * (x w[1] + bias[1]): x (N, C)
+    and w (2, C, F), both float32 or both bfloat16, CUDA; bias float32 (2, F) or
+    None; act "silu" or "gelu" (erf); C and F multiples of 8 up to 4096.
+    Returns h (N, F) in their dtype."""
+    import torch
+    dt, N, C, F, dev, x, w, bias, a = _glu_args(x, w, bias, act)
+    h = _out(out, (N, F), x.dtype, dev, "out")
+    with torch.cuda.device(dev):
+        rc = load_library().spconv_glu(_ptr(x), _ptr(w), _ptr(bias), _ptr(h), N, C, F, a, dt, _stream(dev))
+    _check(rc, "spconv_glu")
+    return h
+
+
+def spconv_glu_grad_workspace_size(N: int, C: int, F: int, dtype: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().spconv_glu_grad_workspace_size(N, C, F, dtype, ctypes.byref(n)),
+           "spconv_glu_grad_workspace_size")
+    return n.value
+
+
+def spconv_glu_grad(dout, x, w, bias=None, act: str = "silu", workspace=None):
+    """Gradient of spconv_glu: dout (N, F), the forward's inputs.  Returns (dx
+    (N, C), dw (2, C, F), dbias float32 (2, F), or None where bias is None).
+    workspace: a uint8 tensor of at least spconv_glu_grad_workspace_size bytes
+    (allocated when None)."""
+    import torch
+    dt, N, C, F, dev, x, w, bias, a = _glu_args(x, w, bias, act)
+    dout = _like(dout, (N, F), x.dtype, dev, "dout")
+    if dout is None:
+        raise ValueError("dout must be given")
+    dx = torch.empty_like(x)
+    dw = torch.empty_like(w)
+    dbias = torch.empty_like(bias) if bias is not None else None
+    ws = _workspace(workspace, spconv_glu_grad_workspace_size(N, C, F, dt), dev, "spconv_glu_grad_workspace_size")
+    with torch.cuda.device(dev):
+        rc = load_library().spconv_glu_grad(_ptr(dout), _ptr(x), _ptr(w), _ptr(bias), _ptr(ws), ws.numel(),
+                                            _ptr(dx), _ptr(dw), _ptr(dbias), N, C, F, a, dt, _stream(dev))
+    _check(rc, "spconv_glu_grad")
+    return dx, dw, dbias
 
 
 def _scan_args(x, z, offsets, order, h0):

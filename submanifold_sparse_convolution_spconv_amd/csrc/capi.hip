@@ -589,6 +589,63 @@ int spconv_layernorm_grad(const void* dout, const void* x, const float* mean, co
     return e == hipSuccess ? SPCONV_OK : hip_fail(e, "spconv_layernorm_grad");
 }
 
+static int check_glu(int64_t N, int C, int F, int act, int dtype) {
+    int rc = check_rows(N, C, dtype, "C");
+    if (rc) return rc;
+    rc = check_rows(N, F, dtype, "F");
+    if (rc) return rc;
+    if (act != SPCONV_SILU && act != SPCONV_GELU)
+        return fail(SPCONV_E_INVALID, "act must be SPCONV_SILU or SPCONV_GELU (got %d)", act);
+    if (C % 8 || F % 8) return fail(SPCONV_E_UNSUPPORTED, "no kernel for C=%d F=%d (multiples of 8 up to %d)", C, F,
+                                    spc::kMaxRowChannels);
+    return SPCONV_OK;
+}
+
+int spconv_glu(const void* x, const void* w, const float* bias, void* h, int64_t N, int C, int F, int act,
+               int dtype, void* stream) {
+    int rc = check_glu(N, C, F, act, dtype);
+    if (rc) return rc;
+    if (N == 0) return SPCONV_OK;
+    if (!x || !w || !h) return fail(SPCONV_E_INVALID, "x, w and h must be non-NULL");
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(h, 16))
+        return fail(SPCONV_E_INVALID, "x, w and h must be 16-byte aligned");
+    if (!aligned(bias, 4)) return fail(SPCONV_E_INVALID, "bias must be 4-byte aligned");
+    hipError_t e = spc::launch_glu({x, w, bias, nullptr, nullptr, h, nullptr, nullptr, N, C, F, act, dtype}, false,
+                                   (hipStream_t)stream);
+    return e == hipSuccess ? SPCONV_OK : hip_fail(e, "spconv_glu");
+}
+
+int spconv_glu_grad_workspace_size(int64_t N, int C, int F, int dtype, size_t* bytes) {
+    if (!bytes) return fail(SPCONV_E_INVALID, "bytes pointer is NULL");
+    int rc = check_glu(N, C, F, SPCONV_SILU, dtype);
+    if (rc) return rc;
+    *bytes = spc::glu_grad_workspace_bytes(N, C, F, dtype);
+    return SPCONV_OK;
+}
+
+int spconv_glu_grad(const void* dout, const void* x, const void* w, const float* bias, void* workspace,
+                    size_t workspace_bytes, void* dx, void* dw, float* dbias, int64_t N, int C, int F, int act,
+                    int dtype, void* stream) {
+    int rc = check_glu(N, C, F, act, dtype);
+    if (rc) return rc;
+    const size_t need = spc::glu_grad_workspace_bytes(N, C, F, dtype);
+    if (!dw) return fail(SPCONV_E_INVALID, "dw is NULL");
+    if (!aligned(dw, 16)) return fail(SPCONV_E_INVALID, "dw must be 16-byte aligned");
+    if (!aligned(bias, 4) || !aligned(dbias, 4)) return fail(SPCONV_E_INVALID, "bias and dbias must be 4-byte aligned");
+    if (N > 0) {
+        if (!dout || !x || !w || !dx || !workspace)
+            return fail(SPCONV_E_INVALID, "dout, x, w, dx and workspace must be non-NULL");
+        if (!aligned(dout, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(dx, 16) || !aligned(workspace, 256))
+            return fail(SPCONV_E_INVALID, "dout, x, w and dx must be 16-byte and workspace 256-byte aligned");
+        if (workspace_bytes < need)
+            return fail(SPCONV_E_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    }
+    // with no rows dw and dbias are zero (written by the kernels; no workspace used)
+    hipError_t e = spc::launch_glu({x, w, bias, dout, workspace, dx, dw, dbias, N, C, F, act, dtype}, true,
+                                   (hipStream_t)stream);
+    return e == hipSuccess ? SPCONV_OK : hip_fail(e, "spconv_glu_grad");
+}
+
 static int scan_size(int64_t N, int C, int dtype, bool grad, size_t* bytes) {
     if (!bytes) return fail(SPCONV_E_INVALID, "bytes pointer is NULL");
     int rc = check_rows(N, C, dtype, "C");

@@ -236,6 +236,21 @@ struct NormGradArgs {
 size_t norm_grad_workspace_bytes(int64_t N, int C, int dtype);
 hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t stream);
 
+struct GluArgs {
+    const void* x;
+    const void* w;         // (2, C, F)
+    const float* bias;     // (2, F) or NULL
+    const void* dout;      // gradient only
+    void* workspace;       // gradient only: glu_grad_workspace_bytes
+    void* out;             // forward: h; gradient: dx
+    void* dw;              // gradient only
+    float* dbias;          // gradient only; or NULL
+    int64_t N;
+    int C, F, act, dtype;
+};
+size_t glu_grad_workspace_bytes(int64_t N, int C, int F, int dtype);
+hipError_t launch_glu(const GluArgs& a, bool grad, hipStream_t stream);
+
 struct ScanArgs {
     const void* x;
     const void* z;

@@ -57,6 +57,33 @@ def test_layernorm_grad_refusals(lib):
     assert f(N=0, dw=0, db=0) == OK                      # no rows and no sums over rows
 
 
+def test_glu_refusals(lib):
+    def f(x=FAKE, w=FAKE, b=FAKE, h=FAKE, N=4, C=64, F=32, act=0, dt=1):
+        return lib.spconv_glu(p(x), p(w), p(b), p(h), N, C, F, act, dt, None)
+    assert f(N=0) == OK
+    for k in ("x", "w", "h"):
+        assert f(**{k: 0}) == INVALID and f(**{k: FAKE + 8}) == INVALID, k
+    assert f(b=FAKE + 2) == INVALID
+    assert f(act=2) == INVALID and f(act=-1) == INVALID and f(dt=2) == INVALID and f(N=-1) == INVALID
+    assert f(N=1 << 31) == UNSUPPORTED and f(C=0) == INVALID and f(F=0) == INVALID
+    for k in ("C", "F"):
+        assert f(**{k: 12}) == UNSUPPORTED and f(**{k: 4104}) == UNSUPPORTED
+    n = ctypes.c_size_t(0)
+    S = lambda N, C, F, dt: lib.spconv_glu_grad_workspace_size(N, C, F, dt, ctypes.byref(n))
+    assert S(1000, 64, 32, 1) == OK and n.value % 256 == 0
+    assert S(1000, 60, 32, 1) == UNSUPPORTED and S(-1, 64, 32, 1) == INVALID and S(4, 64, 32, 5) == INVALID
+    assert lib.spconv_glu_grad_workspace_size(4, 64, 32, 1, None) == INVALID
+    assert S(4, 64, 32, 1) == OK
+    need = n.value
+
+    def g(d=FAKE, x=FAKE, w=FAKE, b=FAKE, ws=FAKE, wb=need, dx=FAKE, dw=FAKE, db=FAKE, N=4, C=64, F=32, act=0, dt=1):
+        return lib.spconv_glu_grad(p(d), p(x), p(w), p(b), p(ws), wb, p(dx), p(dw), p(db), N, C, F, act, dt, None)
+    for k in ("d", "x", "w", "ws", "dx", "dw"):
+        assert g(**{k: 0}) == INVALID and g(**{k: FAKE + 8}) == INVALID, k
+    assert g(wb=need - 1) == WORKSPACE and g(db=FAKE + 2) == INVALID
+    assert g(act=7) == INVALID and g(C=68) == UNSUPPORTED and g(dt=-1) == INVALID
+
+
 def test_scan_refusals(lib):
     n = ctypes.c_size_t(0)
     for S in (lib.spconv_scan_workspace_size, lib.spconv_scan_grad_workspace_size):
@@ -99,3 +126,7 @@ def test_python_refuses_host_tensors():
         sp.spconv_scan(x, x, o)
     with pytest.raises(ValueError):
         sp.spconv_scan_grad(x, x, x, o)
+    with pytest.raises(ValueError):
+        sp.spconv_glu(x, torch.zeros(2, 64, 32))
+    with pytest.raises(ValueError):
+        sp.spconv_glu_grad(x[:, :32], x, torch.zeros(2, 64, 32))
