@@ -7,7 +7,10 @@
 // (F2, V2) after (F1, V1) is (F2 F1, F2 V1 + V2).  So the sequence is cut into
 // chunks, one per workgroup, the chunks into segments of consecutive rows that
 // one lane walks for four channels; segments are joined by a scan over the
-// lanes and waves, chunks through the chain of their maps (see Chain).  A scene's first row forgets what came before: its
+// lanes and waves.  Long sequences take several kernels, none of which waits
+// for another workgroup: the chunks' maps, the states that enter the chunks
+// (composed from the maps in a fixed order), and the rows again with those
+// states.  A scene's first row forgets what came before: its
 // map is marked F = kForget, and composing selects instead of multiplying, so
 // infinities and NaN of one scene stay in it.
 //
@@ -74,12 +77,14 @@ struct ScanParams {
     void* h;           // forward: h; gradient: dx
     void* dz;
     float* last;       // forward: the scenes' last states; gradient: dh0
-    float* carry;      // gradient: [its chunks][C] state that enters the chunk
-    uint64_t* words;   // chunk maps by level (see Chain); NULL: one chunk
-    uint32_t* ticket;  // [channel tiles] chunks handed out
     int64_t N;
     int C, scenes;
     int64_t chunks;
+    // [directions][chunks][C] maps of the chunks, first to last and (gradient) last to
+    // first; the same of groups of chunks; the states that enter the chunks
+    Map* maps;
+    Map* groups;
+    float* carry;
 };
 
 // Four elements of a row, aligned to their element.
@@ -97,24 +102,32 @@ struct Quad<float> {
     typedef f32x4r_t vec;
     typedef f32x4ru_t uvec;
 };
-template <typename T>
-__device__ __forceinline__ typename Quad<T>::vec load_quad(const T* p, int n, float other) {
+// WHOLE: rows have a multiple of four channels, so a lane has four or none.
+// The load is then the same instruction in every lane (a missing row's or
+// channel's reads row 0 or channel 0 instead), so that all of a segment's are
+// in flight together; a branch around each would end that.
+template <typename T, bool WHOLE>
+__device__ __forceinline__ typename Quad<T>::vec load_quad(const T* base, int row, int C, int c0) {
+    const int n = C - c0;
     typename Quad<T>::vec v;
-    if (n >= kScanV) {
-        v = *(const typename Quad<T>::uvec*)p;
+    if constexpr (WHOLE) {
+        v = *(const typename Quad<T>::uvec*)(base + (int64_t)max(row, 0) * C + (n > 0 ? c0 : 0));
     } else {
+        const T* p = base + (int64_t)max(row, 0) * C;
 #pragma unroll
-        for (int i = 0; i < kScanV; ++i) v[i] = i < n ? p[i] : (T)other;
+        for (int i = 0; i < kScanV; ++i) v[i] = p[min(c0 + i, C - 1)];
     }
     return v;
 }
-template <typename T>
-__device__ __forceinline__ void store_quad(T* p, const float (&f)[kScanV], int n) {
+template <typename T, bool WHOLE>
+__device__ __forceinline__ void store_quad(T* base, int row, int C, int c0, const float (&f)[kScanV]) {
+    const int n = row >= 0 ? C - c0 : 0;
+    T* p = base + (int64_t)row * C + c0;
     typename Quad<T>::vec v;
 #pragma unroll
     for (int i = 0; i < kScanV; ++i) v[i] = (T)f[i];
-    if (n >= kScanV) {
-        *(typename Quad<T>::uvec*)p = v;
+    if constexpr (WHOLE) {
+        if (n > 0) *(typename Quad<T>::uvec*)p = v;
     } else {
 #pragma unroll
         for (int i = 0; i < kScanV; ++i)
@@ -122,128 +135,109 @@ __device__ __forceinline__ void store_quad(T* p, const float (&f)[kScanV], int n
     }
 }
 
-// ---- the chain ------------------------------------------------------------
-// The chunks' maps, in one pass over the rows: each workgroup takes the next
-// chunk, publishes the chunk's map, and composes the maps of all chunks before
-// it.  So that this is few loads and always the same composition (whichever
-// chunks were ready first), every 16 maps of a level are also published
-// composed, as one map of the level above, by the workgroup of the last of
-// them: chunk i reads the maps before its own on each level, at most 15 per
-// level below the top.  A chunk waits only for chunks handed out before it,
-// each of which publishes level 0 without waiting, so every wait ends.
-// A map is one 64-bit word (F low, V high), written and read whole by relaxed
-// device-scope accesses: no fences.  kNoWord, which a kernel before this one
-// fills in, marks a word not written yet; its F is a NaN that publishing never
-// writes.
-constexpr int kChainLog2 = 4;                  // log2 of the maps joined per level
-constexpr int kChainMask = (1 << kChainLog2) - 1;
-constexpr int kChainLevels = 4;
-constexpr uint64_t kNoWord = ~0ull;
-
-__host__ __device__ __forceinline__ int chain_top(int64_t chunks) {
-    int k = 0;
-    while (k + 1 < kChainLevels && (chunks >> (kChainLog2 * (k + 1))) > 0) ++k;
-    return k;
-}
-// first entry of level k; chain_at(chunks, chain_top + 1): all entries
-__host__ __device__ __forceinline__ int64_t chain_at(int64_t chunks, int k) {
-    int64_t at = 0;
-    for (int j = 0; j < k; ++j) at += chunks >> (kChainLog2 * j);
-    return at;
+// The value, as new to the compiler: what was computed from it before is then
+// computed again instead of being kept in registers.
+template <typename Q>
+__device__ __forceinline__ void forget_uses(Q& q) {
+    uint32_t w[sizeof(Q) / 4];
+    __builtin_memcpy(w, &q, sizeof q);
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(Q) / 4; ++i) asm volatile("" : "+v"(w[i]));
+    __builtin_memcpy(&q, w, sizeof q);
 }
 
-__device__ __forceinline__ void publish(uint64_t* w, Map m) {
-    const uint32_t F = m.F == m.F ? __float_as_uint(m.F) : 0x7FC00000u;
-    __hip_atomic_store(w, ((uint64_t)__float_as_uint(m.V) << 32) | F, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ uint64_t peek(const uint64_t* w) {
-    return __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-// The maps w[0], w[stride], ... (n of them) composed after m; waits for those
-// not published yet.  Eight loads are in flight at a time.
-__device__ __forceinline__ Map compose_words(const uint64_t* w, int64_t stride, int n, Map m) {
+// ---- chunks ---------------------------------------------------------------
+constexpr int kChunkGroup = 64;       // chunks per group
+constexpr int kCarryChannels = 64;    // channels per workgroup of k_scan_carry
+constexpr int kCarryParts = kScanThreads / kCarryChannels;
+
+// The maps w[0], w[stride], ... (n of them) composed after m, eight loads at a
+// time (the last again where fewer are left: no branch between the loads).
+__device__ __forceinline__ Map compose_maps(const Map* w, int64_t stride, int n, Map m) {
     constexpr int B = 8;
     for (int a = 0; a < n; a += B) {
-        uint64_t v[B];
+        Map v[B];
 #pragma unroll
-        for (int k = 0; k < B; ++k) v[k] = a + k < n ? peek(w + (a + k) * stride) : 0;
+        for (int k = 0; k < B; ++k) v[k] = w[min(a + k, n - 1) * stride];
 #pragma unroll
         for (int k = 0; k < B; ++k) {
-            if (a + k >= n) break;
-            while (v[k] == kNoWord) {
-                __builtin_amdgcn_s_sleep(1);
-                v[k] = peek(w + (a + k) * stride);
-            }
-            m = after(Map{__uint_as_float((uint32_t)v[k]), __uint_as_float((uint32_t)(v[k] >> 32))}, m);
+            const Map r = after(v[k], m);
+            if (a + k < n) m = r;
         }
     }
     return m;
 }
 
-// Publishes chunk i's map of channel c, and with it the maps of the groups
-// that chunk i completes.
-__device__ __forceinline__ void chain_publish(const ScanParams& p, int64_t i, int c, Map m) {
-    const int top = chain_top(p.chunks);
-    int64_t at = 0, n = p.chunks;
-    publish(p.words + i * p.C + c, m);
-    for (int k = 0; k < top && (i & kChainMask) == kChainMask; ++k) {
-        m = after(m, compose_words(p.words + (at + i - kChainMask) * p.C + c, p.C, kChainMask, {1.f, 0.f}));
-        at += n;
-        n >>= kChainLog2;
-        i >>= kChainLog2;
-        publish(p.words + (at + i) * p.C + c, m);
-    }
-}
-
-// The state that enters chunk i, into state[0 .. CT): the maps before it,
-// oldest first (the top level's, then each lower level's within the group),
-// shared by the workgroup's lanes of a channel.  Ends with a barrier.
+// The state after the n maps w[0], w[stride], ... from zero, for channel c:
+// P lanes of the workgroup compose a share each, joined in order through
+// `join` (P * CT maps).  Ends with a barrier; every lane of a channel gets it.
 template <int CT>
-__device__ __forceinline__ void chain_state(const ScanParams& p, int64_t i, Map* join, float* state) {
+__device__ __forceinline__ float state_after(const Map* w, int64_t stride, int n, bool live, Map* join) {
     constexpr int P = kScanThreads / CT;
     const int cl = threadIdx.x % CT, part = threadIdx.x / CT;
+    const int per = (n + P - 1) / P, a = min(n, part * per), b = min(n, a + per);
+    join[part * CT + cl] = live ? compose_maps(w + a * stride, stride, b - a, {1.f, 0.f}) : Map{1.f, 0.f};
+    __syncthreads();
+    float s = 0.f;
+    for (int q = 0; q < P; ++q) s = apply(join[q * CT + cl], s);
+    return s;
+}
+
+// Maps of groups of chunks; blockIdx.z: the direction.
+__global__ void __launch_bounds__(256) k_scan_groups(ScanParams p) {
+    const int c = blockIdx.y * 256 + threadIdx.x;
+    if (c >= p.C) return;
+    const bool back = blockIdx.z;
+    const int64_t first = (int64_t)blockIdx.x * kChunkGroup;
+    const int n = (int)min((int64_t)kChunkGroup, p.chunks - first);
+    const int64_t dir = back ? p.chunks : 0;
+    const Map* w = p.maps + (dir + first) * p.C + c;
+    if (back) w += (int64_t)(n - 1) * p.C;
+    const Map m = compose_maps(w, back ? -p.C : p.C, n, {1.f, 0.f});
+    p.groups[((back ? gridDim.x : 0) + blockIdx.x) * (int64_t)p.C + c] = m;
+}
+
+// States that enter the chunks of one group: the groups before it, then the
+// chunks before each of its own.
+__global__ void __launch_bounds__(kScanThreads) k_scan_carry(ScanParams p) {
+    constexpr int CT = kCarryChannels, PER = kChunkGroup / kCarryParts;
+    __shared__ Map join[kScanThreads], own[kScanThreads];
+    const int cl = threadIdx.x % CT, part = threadIdx.x / CT;
     const int c = blockIdx.y * CT + cl;
-    const int top = chain_top(p.chunks);
-    int64_t total = i >> (kChainLog2 * top);
-    for (int k = 0; k < top; ++k) total += (i >> (kChainLog2 * k)) & kChainMask;
-    const int64_t per = (total + P - 1) / P;
-    const int64_t e0 = min(total, part * per), e1 = min(total, e0 + per);
-    Map m = {1.f, 0.f};
-    if (c < p.C) {
-        int64_t seen = 0;
-        for (int k = top; k >= 0; --k) {
-            const int64_t idx = i >> (kChainLog2 * k);
-            const int64_t first = k == top ? 0 : idx & ~(int64_t)kChainMask, count = idx - first;
-            const int64_t a = max(e0 - seen, (int64_t)0), b = min(e1 - seen, count);
-            if (a < b)
-                m = compose_words(p.words + (chain_at(p.chunks, k) + first + a) * p.C + c, p.C, (int)(b - a), m);
-            seen += count;
-        }
+    const bool back = blockIdx.z, live = c < p.C;
+    const int64_t step = back ? -p.C : p.C;
+    const Map* g = p.groups + (back ? 2 * (int64_t)gridDim.x - 1 : 0) * p.C + c;
+    const int before = back ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x;
+    // this part's chunks, in the direction's order
+    const int64_t first = (int64_t)blockIdx.x * kChunkGroup;
+    const int n = (int)min((int64_t)kChunkGroup, p.chunks - first);
+    const int a = min(n, part * PER), e = min(n, a + PER);
+    const int64_t at = ((back ? p.chunks + first + n - 1 - a : first + a)) * p.C + c;
+    own[part * CT + cl] = live ? compose_maps(p.maps + at, step, e - a, {1.f, 0.f}) : Map{1.f, 0.f};
+    float s = state_after<CT>(g, step, before, live, join);
+    for (int q = 0; q < part; ++q) s = apply(own[q * CT + cl], s);
+    if (!live) return;
+    for (int k = 0; k < e - a; ++k) {
+        p.carry[at + k * step] = s;
+        s = apply(p.maps[at + k * step], s);
     }
-    join[part * CT + cl] = m;
-    __syncthreads();
-    if (part == 0) {
-        float s = 0.f;
-        for (int q = 0; q < P; ++q) s = apply(join[q * CT + cl], s);
-        state[cl] = s;
-    }
-    __syncthreads();
 }
 
-// Before a chained kernel: no map published, no chunk handed out.
-__global__ void __launch_bounds__(256) k_scan_clear(uint64_t* words, int64_t n, uint32_t* ticket, int tiles) {
-    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    for (int64_t e = t; e < n; e += (int64_t)gridDim.x * 256) words[e] = kNoWord;
-    if (t < tiles) ticket[t] = 0;
-}
-
-// The chunk this workgroup takes, in its direction's order.
-__device__ __forceinline__ int64_t next_chunk(const ScanParams& p) {
-    if (!p.words) return 0;
-    __shared__ uint32_t got;
-    if (threadIdx.x == 0) got = atomicAdd(p.ticket + blockIdx.y, 1u);
+// The state that enters this workgroup's chunk, for its channels: from
+// k_scan_carry, or (few chunks: no groups) from the maps.  Ends with a barrier.
+template <int CT, bool BACK>
+__device__ __forceinline__ void entering_state(const ScanParams& p, int64_t chunk, Map* join, float* state) {
+    const int cl = threadIdx.x % CT, c = blockIdx.y * CT + cl;
+    const int64_t dir = BACK ? p.chunks : 0;
+    float s = 0.f;
+    if (p.chunks > kChunkGroup) {
+        if (threadIdx.x < CT && c < p.C) s = p.carry[(dir + chunk) * p.C + c];
+    } else if (p.chunks > 1) {
+        const Map* w = p.maps + (dir + (BACK ? p.chunks - 1 : 0)) * p.C + c;
+        s = state_after<CT>(w, BACK ? -p.C : p.C, (int)(BACK ? p.chunks - 1 - chunk : chunk), c < p.C, join);
+    }
+    if (threadIdx.x < CT) state[cl] = s;
     __syncthreads();
-    return got;
 }
 
 // ---- scenes ---------------------------------------------------------------
@@ -307,9 +301,27 @@ template <int L>
 __device__ __forceinline__ void segment_rows(const ScanParams& p, int64_t pos, int (&row)[L]) {
 #pragma unroll
     for (int l = 0; l < L; ++l) {
-        int64_t r = pos + l;
-        if (r < p.N && p.order) r = (uint32_t)p.order[r];
-        row[l] = r < p.N ? (int)r : -1;
+        const int64_t t = pos + l;
+        const uint32_t r = p.order ? (uint32_t)p.order[min(t, p.N - 1)] : (uint32_t)t;
+        row[l] = t < p.N && r < p.N ? (int)r : -1;
+    }
+}
+
+// A row that is not there: f = 1, 1 - f = 0, so the state passes.
+template <int L>
+__device__ __forceinline__ bool any_missing(const int (&row)[L]) {
+    int any = 0;
+#pragma unroll
+    for (int l = 0; l < L; ++l) any |= row[l];
+    return __any(any < 0);
+}
+template <typename T>
+__device__ __forceinline__ void missing_row(int row, typename Quad<T>::vec& z, typename Quad<T>::vec& x) {
+    if (row >= 0) return;
+#pragma unroll
+    for (int i = 0; i < kScanV; ++i) {
+        z[i] = (T)__builtin_inff();
+        x[i] = (T)0.f;
     }
 }
 
@@ -354,51 +366,146 @@ __device__ __forceinline__ Map scan_waves(Map* wave_maps, int c) {
     return all;
 }
 
-// The states.  STATES false: only the states that enter the gradient's chunks
-// (two of them to one of these), into carry.
-template <typename T, int G, bool STATES>
-__global__ void __launch_bounds__(kScanThreads, 4) k_scan(ScanParams p) {
-    constexpr int V = kScanV, L = kScanRows, S = kScanThreads / G, R = S * L, CT = G * V;
-    __shared__ SceneMarks<R> marks;
+// Rows of a workgroup's chunk, and what its scenes need of them.
+template <typename T, int G, int L, bool WHOLE>
+struct Chunk {
+    static constexpr int V = kScanV, S = kScanThreads / G, R = S * L, CT = G * V;
+    int lane, seg, c0, nv;
+    int64_t p0;
+    int row[L];
+    __device__ __forceinline__ Chunk(const ScanParams& p, int64_t chunk) {
+        lane = threadIdx.x % G;
+        seg = threadIdx.x / G;
+        c0 = (blockIdx.y * G + lane) * V;
+        nv = p.C - c0;
+        p0 = chunk * R;
+        segment_rows<L>(p, p0 + seg * L, row);
+    }
+    __device__ __forceinline__ typename Quad<T>::vec load(const void* t, int l, int C) const {
+        return load_quad<T, WHOLE>((const T*)t, row[l], C, c0);
+    }
+    // element i of a scene's state, 0 without states
+    __device__ __forceinline__ float of_scene(const float* t, int b, int i, int C) const {
+        return t ? t[(int64_t)b * C + min(c0 + i, C - 1)] : 0.f;
+    }
+};
+
+// Maps of the chunks: first to last, and with GRAD last to first.
+template <typename T, int G, int L, bool WHOLE, bool GRAD>
+__global__ void __launch_bounds__(kScanThreads) k_scan_maps(ScanParams p) {
+    using K = Chunk<T, G, L, WHOLE>;
+    constexpr int V = K::V;
+    __shared__ SceneMarks<K::R> marks;
+    __shared__ Map wave_maps[GRAD ? 2 : 1][kScanWaves * K::CT];
+    const int64_t chunk = blockIdx.x;
+    const K k(p, chunk);
+    typename Quad<T>::vec x[L], z[L], d[L];
+#pragma unroll
+    for (int l = 0; l < L; ++l) {
+        z[l] = k.load(p.z, l, p.C);
+        x[l] = k.load(p.x, l, p.C);
+        if constexpr (GRAD) d[l] = k.load(p.dout, l, p.C);
+    }
+    mark_scenes(marks, p, k.p0);
+    if (any_missing(k.row)) {
+#pragma unroll
+        for (int l = 0; l < L; ++l) {
+            missing_row<T>(k.row[l], z[l], x[l]);
+            if (GRAD && k.row[l] < 0) d[l] = typename Quad<T>::vec{};
+        }
+    }
+    Map m[V], mb[V];
+    auto compose = [&](auto mk) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) m[i] = mb[i] = {1.f, 0.f};
+#pragma unroll
+        for (int l = 0; l < L; ++l) {
+            const int b = decltype(mk)::value ? marks.first[k.seg * L + l] : -1;
+            const int e = decltype(mk)::value && GRAD ? marks.last[k.seg * L + l] : -1;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const Step g = gate((float)z[l][i]);
+                const float v = g.n * (float)x[l][i];
+                float t = GRAD ? (float)d[l][i] : 0.f;
+                if (decltype(mk)::value) {
+                    if (GRAD && e >= 0) t += k.of_scene(p.dlast, e, i, p.C);
+                    if (b >= 0) {
+                        m[i] = {kForget, fmaf(g.f, k.of_scene(p.h0, b, i, p.C), v)};
+                        if (GRAD) mb[i] = after(mb[i], {kForget, 0.f});
+                    } else {
+                        m[i] = after({g.f, v}, m[i]);
+                        if (GRAD) mb[i] = after(mb[i], {g.f, g.f * t});
+                    }
+                } else {
+                    // the product of the factors serves both directions
+                    if (GRAD) mb[i].V = fmaf(m[i].F, g.f * t, mb[i].V);
+                    m[i] = {g.f * m[i].F, fmaf(g.f, m[i].V, v)};
+                    mb[i].F = m[i].F;
+                }
+            }
+        }
+    };
+    if (wave_marks<L>(marks, k.seg))
+        compose(std::true_type{});
+    else
+        compose(std::false_type{});
+    scan_wave<G, false>(m, wave_maps[0]);
+    if constexpr (GRAD) scan_wave<G, true>(mb, wave_maps[1]);
+    __syncthreads();
+    constexpr int CT = K::CT;
+    const int dir = threadIdx.x / CT, c = blockIdx.y * CT + threadIdx.x % CT;
+    if (dir < (GRAD ? 2 : 1) && c < p.C) {
+        const Map all = dir ? scan_waves<CT, true>(wave_maps[GRAD ? 1 : 0], threadIdx.x % CT)
+                            : scan_waves<CT, false>(wave_maps[0], threadIdx.x);
+        p.maps[(dir * p.chunks + chunk) * p.C + c] = all;
+    }
+}
+
+// The states, with the chunks' entering states known.  From the last chunk to
+// the first: the rows that k_scan_maps read last are still in the memory-side
+// cache.
+template <typename T, int G, bool WHOLE>
+__global__ void __launch_bounds__(kScanThreads) k_scan(ScanParams p) {
+    constexpr int L = kScanRows;
+    using K = Chunk<T, G, L, WHOLE>;
+    constexpr int V = K::V, CT = K::CT;
+    __shared__ SceneMarks<K::R> marks;
     __shared__ Map wave_maps[kScanWaves * CT], join[kScanThreads];
     __shared__ float state[CT];
-    const int64_t chunk = next_chunk(p), p0 = chunk * R;
-    const int lane = threadIdx.x % G, seg = threadIdx.x / G;
-    const int c0 = (blockIdx.y * G + lane) * V, nv = p.C - c0;
-    int row[L];
-    segment_rows<L>(p, p0 + seg * L, row);
+    if (p.N == 0) {              // nothing to read: the scenes' states alone
+        empty_scenes(p, p.h0, p.last, CT);
+        return;
+    }
+    const int64_t chunk = p.chunks - 1 - blockIdx.x;
+    const K k(p, chunk);
     typename Quad<T>::vec x[L], z[L];
 #pragma unroll
     for (int l = 0; l < L; ++l) {
-        const int64_t at = (int64_t)row[l] * p.C + c0;
-        // a row that is not there: f = 1, 1 - f = 0
-        z[l] = load_quad((const T*)p.z + at, row[l] >= 0 ? nv : 0, __builtin_inff());
-        x[l] = load_quad((const T*)p.x + at, row[l] >= 0 ? nv : 0, 0.f);
+        z[l] = k.load(p.z, l, p.C);
+        x[l] = k.load(p.x, l, p.C);
     }
-    mark_scenes(marks, p, p0);
-    const bool marked = wave_marks<L>(marks, seg);
-    constexpr int LK = STATES ? L : 1;
-    Map m[LK][V], pre[V];       // m[l]: the segment's rows 0 .. l composed
+    entering_state<CT, false>(p, chunk, join, state);
+    mark_scenes(marks, p, k.p0);
+    if (any_missing(k.row)) {
+#pragma unroll
+        for (int l = 0; l < L; ++l) missing_row<T>(k.row[l], z[l], x[l]);
+    }
+    const bool marked = wave_marks<L>(marks, k.seg);
+    Map pre[V];
     auto compose = [&](auto mk) {
 #pragma unroll
+        for (int i = 0; i < V; ++i) pre[i] = {1.f, 0.f};
+#pragma unroll
         for (int l = 0; l < L; ++l) {
-            const int b = decltype(mk)::value ? marks.first[seg * L + l] : -1;
+            const int b = decltype(mk)::value ? marks.first[k.seg * L + l] : -1;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const Step s = gate((float)z[l][i]);
-                const float v = s.n * (float)x[l][i];
-                const Map was = l ? m[STATES ? l - 1 : 0][i] : Map{1.f, 0.f};
-                Map now;
-                if (decltype(mk)::value) {
-                    now = after({s.f, v}, was);
-                    if (b >= 0) {
-                        const float in = p.h0 && i < nv ? p.h0[(int64_t)b * p.C + c0 + i] : 0.f;
-                        now = {kForget, fmaf(s.f, in, v)};
-                    }
-                } else {
-                    now = l ? Map{s.f * was.F, fmaf(s.f, was.V, v)} : Map{s.f, v};
-                }
-                m[STATES ? l : 0][i] = now;
+                const Step g = gate((float)z[l][i]);
+                const float v = g.n * (float)x[l][i];
+                if (decltype(mk)::value)
+                    pre[i] = b >= 0 ? Map{kForget, fmaf(g.f, k.of_scene(p.h0, b, i, p.C), v)} : after({g.f, v}, pre[i]);
+                else
+                    pre[i] = {g.f * pre[i].F, fmaf(g.f, pre[i].V, v)};
             }
         }
     };
@@ -406,89 +513,86 @@ __global__ void __launch_bounds__(kScanThreads, 4) k_scan(ScanParams p) {
         compose(std::true_type{});
     else
         compose(std::false_type{});
-#pragma unroll
-    for (int i = 0; i < V; ++i) pre[i] = m[LK - 1][i];
     scan_wave<G, false>(pre, wave_maps);
     __syncthreads();
-    if (threadIdx.x < CT) {
-        const Map all = scan_waves<CT, false>(wave_maps, threadIdx.x);
-        const int c = blockIdx.y * CT + threadIdx.x;
-        if (p.words && c < p.C) chain_publish(p, chunk, c, all);
-    }
-    if (p.words)
-        chain_state<CT>(p, chunk, join, state);
-    else
-        __syncthreads();
+    if (threadIdx.x < CT) scan_waves<CT, false>(wave_maps, threadIdx.x);
+    __syncthreads();
     float s[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        s[i] = apply(wave_maps[(threadIdx.x >> 6) * CT + lane * V + i], p.words ? state[lane * V + i] : 0.f);
-        s[i] = apply(pre[i], s[i]);
+    for (int i = 0; i < V; ++i)
+        s[i] = apply(pre[i], apply(wave_maps[(threadIdx.x >> 6) * CT + k.lane * V + i], state[k.lane * V + i]));
+    // the rows again, from their entering state: the gates cost less than the
+    // registers that would keep them (64 for 32 elements)
+#pragma unroll
+    for (int l = 0; l < L; ++l) {
+        forget_uses(z[l]);
+        forget_uses(x[l]);
     }
-    if constexpr (!STATES) {
-        if (seg == 0 || seg == S / 2) {
+    auto walk = [&](auto mk) {
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (i < nv) p.carry[(2 * chunk + (seg ? 1 : 0)) * p.C + c0 + i] = s[i];
-        }
-        return;
-    }
+        for (int l = 0; l < L; ++l) {
+            const int b = decltype(mk)::value ? marks.first[k.seg * L + l] : -1;
+            const int e = decltype(mk)::value ? marks.last[k.seg * L + l] : -1;
 #pragma unroll
-    for (int l = 0; l < LK; ++l) {
-        float o[V];
-        if (marked) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) o[i] = apply(m[l][i], s[i]);
-            const int e = marks.last[seg * L + l];
-            if (e >= 0) {
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (i < nv) p.last[(int64_t)e * p.C + c0 + i] = o[i];
+            for (int i = 0; i < V; ++i) {
+                if (decltype(mk)::value && b >= 0) s[i] = k.of_scene(p.h0, b, i, p.C);
+                const Step g = gate((float)z[l][i]);
+                s[i] = fmaf(g.f, s[i], g.n * (float)x[l][i]);
+                if (decltype(mk)::value && e >= 0 && i < k.nv) p.last[(int64_t)e * p.C + k.c0 + i] = s[i];
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) o[i] = fmaf(m[l][i].F, s[i], m[l][i].V);
+            store_quad<T, WHOLE>((T*)p.h, k.row[l], p.C, k.c0, s);
         }
-        if (row[l] >= 0) store_quad((T*)p.h + (int64_t)row[l] * p.C + c0, o, nv);
-    }
+    };
+    if (marked)
+        walk(std::true_type{});
+    else
+        walk(std::false_type{});
     empty_scenes(p, p.h0, p.last, CT);
 }
 
-// The gradient, from the last chunk to the first, with the states that enter
-// the chunks known (carry; NULL: one chunk).
-template <typename T, int G>
+// The gradient, with the states that enter the chunks known in both
+// directions; from the last chunk to the first, like k_scan.
+template <typename T, int G, bool WHOLE>
 __global__ void __launch_bounds__(kScanThreads, 4) k_scan_grad(ScanParams p) {
-    constexpr int V = kScanV, L = kScanGradRows, S = kScanThreads / G, R = S * L, CT = G * V;
-    __shared__ SceneMarks<R> marks;
-    __shared__ Map wave_maps[2][kScanWaves * CT], join[kScanThreads];
-    __shared__ float state[CT];
-    const int64_t back = next_chunk(p), chunk = p.chunks - 1 - back, p0 = chunk * R;
-    const int lane = threadIdx.x % G, seg = threadIdx.x / G;
-    const int c0 = (blockIdx.y * G + lane) * V, nv = p.C - c0;
-    int row[L];
-    segment_rows<L>(p, p0 + seg * L, row);
+    constexpr int L = kScanGradRows;
+    using K = Chunk<T, G, L, WHOLE>;
+    constexpr int V = K::V, CT = K::CT;
+    __shared__ SceneMarks<K::R> marks;
+    __shared__ Map wave_maps[2][kScanWaves * CT], join[2][kScanThreads];
+    __shared__ float state[2][CT];
+    if (p.N == 0) {
+        if (p.last) empty_scenes(p, p.dlast, p.last, CT);
+        return;
+    }
+    const int64_t chunk = p.chunks - 1 - blockIdx.x;
+    const K k(p, chunk);
     typename Quad<T>::vec x[L], z[L], d[L];
 #pragma unroll
     for (int l = 0; l < L; ++l) {
-        const int64_t at = (int64_t)row[l] * p.C + c0;
-        z[l] = load_quad((const T*)p.z + at, row[l] >= 0 ? nv : 0, __builtin_inff());
-        x[l] = load_quad((const T*)p.x + at, row[l] >= 0 ? nv : 0, 0.f);
-        d[l] = load_quad((const T*)p.dout + at, row[l] >= 0 ? nv : 0, 0.f);
+        z[l] = k.load(p.z, l, p.C);
+        x[l] = k.load(p.x, l, p.C);
+        d[l] = k.load(p.dout, l, p.C);
     }
-    float s[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) s[i] = p.carry && i < nv ? p.carry[chunk * p.C + c0 + i] : 0.f;
-    mark_scenes(marks, p, p0);
-    const bool marked = wave_marks<L>(marks, seg);
-    Map m[V], mb[V];
-    float f[L][V], n[L][V], dh[L][V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) m[i] = mb[i] = {1.f, 0.f};
-    auto compose = [&](auto mk) {
+    entering_state<CT, false>(p, chunk, join[0], state[0]);
+    entering_state<CT, true>(p, chunk, join[1], state[1]);
+    mark_scenes(marks, p, k.p0);
+    if (any_missing(k.row)) {
 #pragma unroll
         for (int l = 0; l < L; ++l) {
-            const int b = decltype(mk)::value ? marks.first[seg * L + l] : -1;
-            const int e = decltype(mk)::value ? marks.last[seg * L + l] : -1;
+            missing_row<T>(k.row[l], z[l], x[l]);
+            if (k.row[l] < 0) d[l] = typename Quad<T>::vec{};
+        }
+    }
+    const bool marked = wave_marks<L>(marks, k.seg);
+    Map m[V], mb[V];
+    float f[L][V], n[L][V], dh[L][V];
+    auto compose = [&](auto mk) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) m[i] = mb[i] = {1.f, 0.f};
+#pragma unroll
+        for (int l = 0; l < L; ++l) {
+            const int b = decltype(mk)::value ? marks.first[k.seg * L + l] : -1;
+            const int e = decltype(mk)::value ? marks.last[k.seg * L + l] : -1;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const Step g = gate((float)z[l][i]);
@@ -497,10 +601,9 @@ __global__ void __launch_bounds__(kScanThreads, 4) k_scan_grad(ScanParams p) {
                 n[l][i] = g.n;
                 float t = (float)d[l][i];
                 if (decltype(mk)::value) {
-                    if (e >= 0 && p.dlast && i < nv) t += p.dlast[(int64_t)e * p.C + c0 + i];
+                    if (e >= 0) t += k.of_scene(p.dlast, e, i, p.C);
                     if (b >= 0) {
-                        const float in = p.h0 && i < nv ? p.h0[(int64_t)b * p.C + c0 + i] : 0.f;
-                        m[i] = {kForget, fmaf(g.f, in, v)};
+                        m[i] = {kForget, fmaf(g.f, k.of_scene(p.h0, b, i, p.C), v)};
                         mb[i] = after(mb[i], {kForget, 0.f});
                     } else {
                         m[i] = after({g.f, v}, m[i]);
@@ -509,55 +612,46 @@ __global__ void __launch_bounds__(kScanThreads, 4) k_scan_grad(ScanParams p) {
                 } else {
                     mb[i].V = fmaf(m[i].F, g.f * t, mb[i].V);
                     m[i] = {g.f * m[i].F, fmaf(g.f, m[i].V, v)};
+                    mb[i].F = m[i].F;
                 }
                 dh[l][i] = t;
             }
-        }
-        if (!decltype(mk)::value) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) mb[i].F = m[i].F;
         }
     };
     if (marked)
         compose(std::true_type{});
     else
         compose(std::false_type{});
-    scan_wave<G, true>(mb, wave_maps[1]);
     scan_wave<G, false>(m, wave_maps[0]);
+    scan_wave<G, true>(mb, wave_maps[1]);
     __syncthreads();
-    if (threadIdx.x < CT) {
-        const Map all = scan_waves<CT, true>(wave_maps[1], threadIdx.x);
-        const int c = blockIdx.y * CT + threadIdx.x;
-        if (p.words && c < p.C) chain_publish(p, back, c, all);
-    } else if (threadIdx.x < 2 * CT) {
-        scan_waves<CT, false>(wave_maps[0], threadIdx.x - CT);
-    }
-    if (p.words)
-        chain_state<CT>(p, back, join, state);
-    else
-        __syncthreads();
+    if (threadIdx.x < CT)
+        scan_waves<CT, false>(wave_maps[0], threadIdx.x);
+    else if (threadIdx.x < 2 * CT)
+        scan_waves<CT, true>(wave_maps[1], threadIdx.x - CT);
+    __syncthreads();
     // forward: the states again, and (h[t-1] - x) f (1 - f)
-    float y[V], q[L][V];
+    float s[V], y[V], q[L][V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int at = (threadIdx.x >> 6) * CT + lane * V + i;
-        s[i] = apply(m[i], apply(wave_maps[0][at], s[i]));
-        y[i] = apply(mb[i], apply(wave_maps[1][at], p.words ? state[lane * V + i] : 0.f));
+        const int at = (threadIdx.x >> 6) * CT + k.lane * V + i;
+        s[i] = apply(m[i], apply(wave_maps[0][at], state[0][k.lane * V + i]));
+        y[i] = apply(mb[i], apply(wave_maps[1][at], state[1][k.lane * V + i]));
     }
 #pragma unroll
     for (int l = 0; l < L; ++l) {
-        const int b = marked ? marks.first[seg * L + l] : -1;
+        const int b = marked ? marks.first[k.seg * L + l] : -1;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const float xv = (float)x[l][i];
-            if (b >= 0) s[i] = p.h0 && i < nv ? p.h0[(int64_t)b * p.C + c0 + i] : 0.f;
+            if (b >= 0) s[i] = k.of_scene(p.h0, b, i, p.C);
             q[l][i] = (s[i] - xv) * (f[l][i] * n[l][i]);
             s[i] = fmaf(f[l][i], s[i], n[l][i] * xv);
         }
     }
 #pragma unroll
     for (int l = L - 1; l >= 0; --l) {
-        const int b = marked ? marks.first[seg * L + l] : -1;
+        const int b = marked ? marks.first[k.seg * L + l] : -1;
         float ox[V], oz[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -569,15 +663,12 @@ __global__ void __launch_bounds__(kScanThreads, 4) k_scan_grad(ScanParams p) {
         if (b >= 0) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                if (p.last && i < nv) p.last[(int64_t)b * p.C + c0 + i] = y[i];
+                if (p.last && i < k.nv) p.last[(int64_t)b * p.C + k.c0 + i] = y[i];
                 y[i] = 0.f;
             }
         }
-        if (row[l] >= 0) {
-            const int64_t at = (int64_t)row[l] * p.C + c0;
-            store_quad((T*)p.h + at, ox, nv);
-            store_quad((T*)p.dz + at, oz, nv);
-        }
+        store_quad<T, WHOLE>((T*)p.h, k.row[l], p.C, k.c0, ox);
+        store_quad<T, WHOLE>((T*)p.dz, k.row[l], p.C, k.c0, oz);
     }
     if (p.last) empty_scenes(p, p.dlast, p.last, CT);
 }
@@ -593,64 +684,67 @@ int64_t scan_chunks(int64_t N, int C, bool grad) {
     const int64_t R = (int64_t)(kScanThreads / scan_group(C)) * (grad ? kScanGradRows : kScanRows);
     return std::max<int64_t>(1, (N + R - 1) / R);
 }
-// Workspace: the words of the longer chain (the gradient runs two, one after
-// the other), the tickets, the gradient's entering states.
+// Workspace: the chunks' maps, the groups' maps and the entering states, each
+// for both directions in the gradient.
 struct ScanLayout {
-    int64_t chunks, gchunks;     // of the forward and of the gradient
-    int tiles;
-    size_t ticket, carry, total;
+    int64_t chunks, groups;
+    int tiles, dirs;
+    size_t group_at, carry_at, total;
 };
-int64_t chain_entries(int64_t chunks) { return chain_at(chunks, chain_top(chunks) + 1); }
 ScanLayout scan_layout(int64_t N, int C, bool grad) {
-    static_assert(kScanRows == 2 * kScanGradRows, "two chunks of the gradient to one of the forward");
     ScanLayout l{};
-    l.chunks = scan_chunks(N, C, false);
-    l.gchunks = scan_chunks(N, C, true);
+    l.chunks = scan_chunks(N, C, grad);
+    l.groups = (l.chunks + kChunkGroup - 1) / kChunkGroup;
     l.tiles = (C + scan_group(C) * kScanV - 1) / (scan_group(C) * kScanV);
-    const int64_t n = grad ? l.gchunks : l.chunks;
-    if (n == 1) return l;
-    l.ticket = align_up((size_t)chain_entries(n) * C * 8, 256);
-    l.carry = l.ticket + align_up((size_t)l.tiles * 4, 256);
-    l.total = l.carry + (grad ? align_up((size_t)2 * l.chunks * C * 4, 256) : 0);
+    l.dirs = grad ? 2 : 1;
+    if (l.chunks == 1) return l;
+    l.group_at = l.total = align_up((size_t)l.dirs * l.chunks * C * sizeof(Map), 256);
+    if (l.groups == 1) return l;
+    l.carry_at = l.group_at + align_up((size_t)l.dirs * l.groups * C * sizeof(Map), 256);
+    l.total = l.carry_at + align_up((size_t)l.dirs * l.chunks * C * 4, 256);
     return l;
 }
 
-template <typename T, int G>
+template <typename T, int G, bool WHOLE>
 hipError_t scan_go(ScanParams p, bool grad, const ScanLayout& l, char* ws, hipStream_t st) {
-    auto chain = [&](int64_t chunks) {
-        p.chunks = chunks;
-        p.words = chunks > 1 ? (uint64_t*)ws : nullptr;
-        p.ticket = chunks > 1 ? (uint32_t*)(ws + l.ticket) : nullptr;
-        if (chunks == 1) return;
-        const int64_t n = chain_entries(chunks) * p.C;
-        k_scan_clear<<<(unsigned)std::min<int64_t>((n + 1023) / 1024, 2048), 256, 0, st>>>(p.words, n, p.ticket,
-                                                                                           l.tiles);
-    };
-    if (grad) {
-        if (l.gchunks > 1) {
-            p.carry = (float*)(ws + l.carry);
-            chain(l.chunks);
-            k_scan<T, G, false><<<dim3((unsigned)l.chunks, l.tiles), kScanThreads, 0, st>>>(p);
-        }
-        chain(l.gchunks);
-        k_scan_grad<T, G><<<dim3((unsigned)l.gchunks, l.tiles), kScanThreads, 0, st>>>(p);
-    } else {
-        chain(l.chunks);
-        k_scan<T, G, true><<<dim3((unsigned)l.chunks, l.tiles), kScanThreads, 0, st>>>(p);
+    const dim3 grid((unsigned)l.chunks, l.tiles);
+    p.chunks = l.chunks;
+    p.maps = (Map*)ws;
+    p.groups = (Map*)(ws + l.group_at);
+    p.carry = (float*)(ws + l.carry_at);
+    if (l.chunks > 1) {
+        if (grad)
+            k_scan_maps<T, G, kScanGradRows, WHOLE, true><<<grid, kScanThreads, 0, st>>>(p);
+        else
+            k_scan_maps<T, G, kScanRows, WHOLE, false><<<grid, kScanThreads, 0, st>>>(p);
     }
+    if (l.groups > 1) {
+        k_scan_groups<<<dim3((unsigned)l.groups, (p.C + 255) / 256, l.dirs), 256, 0, st>>>(p);
+        k_scan_carry<<<dim3((unsigned)l.groups, (p.C + kCarryChannels - 1) / kCarryChannels, l.dirs), kScanThreads, 0,
+                       st>>>(p);
+    }
+    if (grad)
+        k_scan_grad<T, G, WHOLE><<<grid, kScanThreads, 0, st>>>(p);
+    else
+        k_scan<T, G, WHOLE><<<grid, kScanThreads, 0, st>>>(p);
     return hipGetLastError();
+}
+
+template <typename T, int G>
+hipError_t scan_whole(const ScanParams& p, bool grad, const ScanLayout& l, char* ws, hipStream_t st) {
+    return p.C % kScanV ? scan_go<T, G, false>(p, grad, l, ws, st) : scan_go<T, G, true>(p, grad, l, ws, st);
 }
 
 template <typename T>
 hipError_t scan_dispatch(const ScanParams& p, bool grad, char* ws, hipStream_t st) {
     const ScanLayout l = scan_layout(p.N, p.C, grad);
     switch (scan_group(p.C)) {
-        case 1: return scan_go<T, 1>(p, grad, l, ws, st);
-        case 2: return scan_go<T, 2>(p, grad, l, ws, st);
-        case 4: return scan_go<T, 4>(p, grad, l, ws, st);
-        case 8: return scan_go<T, 8>(p, grad, l, ws, st);
-        case 16: return scan_go<T, 16>(p, grad, l, ws, st);
-        default: return scan_go<T, 32>(p, grad, l, ws, st);
+        case 1: return scan_whole<T, 1>(p, grad, l, ws, st);
+        case 2: return scan_whole<T, 2>(p, grad, l, ws, st);
+        case 4: return scan_whole<T, 4>(p, grad, l, ws, st);
+        case 8: return scan_whole<T, 8>(p, grad, l, ws, st);
+        case 16: return scan_whole<T, 16>(p, grad, l, ws, st);
+        default: return scan_whole<T, 32>(p, grad, l, ws, st);
     }
 }
 
