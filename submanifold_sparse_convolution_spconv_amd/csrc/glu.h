@@ -1,0 +1,75 @@
+// Shared by the gated linear unit's kernels: arguments, activations, stores.
+#pragma once
+
+#include "rowops.h"
+
+namespace spc {
+
+typedef __bf16 bf16x4r_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) bf16x4r_t lds_bf16x4r_t;
+
+struct GluParams {
+    const void* x;
+    const void* w;
+    const float* bias;
+    const void* dout;
+    void* h;           // forward
+    void* dab;         // (N, 2, F): da, db
+    void* dx;
+    float* bpart;      // [row tiles][2][F] partial sums of dbias
+    float* wpart;      // [splits][C][2 F] partial sums of dw
+    int64_t N;
+    int C, F;
+    int64_t rows_per_split;
+};
+
+__device__ __forceinline__ float fast_sigmoid(float a) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896f * a));
+}
+
+// act(a) and act'(a)
+struct Act {
+    float v, d;
+};
+template <int ACT>
+__device__ __forceinline__ Act activation(float a) {
+    if constexpr (ACT == SPCONV_SILU) {
+        const float s = fast_sigmoid(a);
+        const float v = a * s;
+        return {v, s * (1.f + a - v)};
+    } else {
+        const float cdf = 0.5f * (1.f + erff(a * 0.70710678f));
+        const float pdf = 0.39894228f * __builtin_amdgcn_exp2f(-0.72134752f * a * a);
+        return {a * cdf, cdf + a * pdf};
+    }
+}
+
+template <typename T>
+struct Four;
+template <>
+struct Four<__bf16> {
+    typedef bf16x4r_t vec;
+};
+template <>
+struct Four<float> {
+    typedef f32x4r_t vec;
+};
+template <typename T>
+__device__ __forceinline__ void store_four(T* p, const float (&f)[4]) {
+    typename Four<T>::vec v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (T)f[i];
+    *(typename Four<T>::vec*)p = v;
+}
+
+// bfloat16 rows of at most kGluRowC channels: both projections of a row come
+// from weights that stay in LDS (glu_rows.hip).
+constexpr int kGluRowC = 128;
+hipError_t launch_glu_rows(const GluParams& p, int act, hipStream_t st);
+hipError_t launch_glu_rows_dx(const GluParams& p, int act, hipStream_t st);
+// dw's and dbias' partial sums: `splits` splits of rows_per_split rows; the
+// number of splits that fills the card.
+int glu_rows_splits(int64_t N, int F);
+hipError_t launch_glu_rows_dw(const GluParams& p, int act, int splits, hipStream_t st);
+
+}  // namespace spc

@@ -13,7 +13,7 @@
 // pieces without a shuffle.  Operands go through LDS; the one whose reduction
 // axis is not contiguous in memory is read back with the transposing LDS read
 // (bf16) or one word per lane (fp32).
-#include "rowops.h"
+#include "glu.h"
 
 #include <algorithm>
 
@@ -21,31 +21,7 @@ namespace spc {
 
 namespace {
 
-typedef __bf16 bf16x4r_t __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) bf16x4r_t lds_bf16x4r_t;
-
 constexpr int kGluThreads = 256;
-
-__device__ __forceinline__ float fast_sigmoid(float a) {
-    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896f * a));
-}
-
-// act(a) and act'(a)
-struct Act {
-    float v, d;
-};
-template <int ACT>
-__device__ __forceinline__ Act activation(float a) {
-    if constexpr (ACT == SPCONV_SILU) {
-        const float s = fast_sigmoid(a);
-        const float v = a * s;
-        return {v, s * (1.f + a - v)};
-    } else {
-        const float cdf = 0.5f * (1.f + erff(a * 0.70710678f));
-        const float pdf = 0.39894228f * __builtin_amdgcn_exp2f(-0.72134752f * a * a);
-        return {a * cdf, cdf + a * pdf};
-    }
-}
 
 // One operand tile in LDS: M outputs x BK of the reduction.  KC: the reduction
 // is contiguous in memory and in LDS ([m][k]); else the outputs are ([k][m]).
@@ -120,21 +96,6 @@ template <typename T>
 constexpr int kTileK = sizeof(T) == 2 ? 32 : 16;
 constexpr int kTile = 128;     // outputs of each kind per workgroup
 
-struct GluParams {
-    const void* x;
-    const void* w;
-    const float* bias;
-    const void* dout;
-    void* h;           // forward
-    void* dab;         // (N, 2, F): da, db
-    void* dx;
-    float* bpart;      // [row tiles][2][F] partial sums of dbias
-    float* wpart;      // [splits][C][2 F] partial sums of dw
-    int64_t N;
-    int C, F;
-    int64_t rows_per_split;
-};
-
 // acc += A B over the reduction [k0, k1), both operands staged a BK at a time
 // with the next tiles' loads in flight.  load_a / load_b (m, k) give the piece
 // at output m and reduction index k (0 outside); m_at / n_at the first output
@@ -199,24 +160,6 @@ __device__ __forceinline__ typename Piece<T>::vec piece_or_zero(const T* p, bool
         for (int i = 0; i < Piece<T>::V; ++i) v[i] = (T)0.f;
     }
     return v;
-}
-
-template <typename T>
-struct Four;
-template <>
-struct Four<__bf16> {
-    typedef bf16x4r_t vec;
-};
-template <>
-struct Four<float> {
-    typedef f32x4r_t vec;
-};
-template <typename T>
-__device__ __forceinline__ void store_four(T* p, const float (&f)[4]) {
-    typename Four<T>::vec v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = (T)f[i];
-    *(typename Four<T>::vec*)p = v;
 }
 
 // 128 rows x 64 hidden features, both projections: h, or (GRAD) da and db with
@@ -395,6 +338,9 @@ __global__ void __launch_bounds__(256) k_glu_dbias_join(const float* part, int64
     }
 }
 
+// Few channels and enough rows to give every CU a block of them: glu_rows.hip.
+bool use_rows(int64_t N, int C, int dtype) { return dtype == SPCONV_BF16 && C <= kGluRowC && N >= 32768; }
+
 struct GluLayout {
     size_t dab, bpart, wpart, total;
     int64_t tiles, rows_per_split;
@@ -402,6 +348,15 @@ struct GluLayout {
 };
 GluLayout glu_layout(int64_t N, int C, int F, int dtype) {
     GluLayout l{};
+    if (use_rows(N, C, dtype)) {
+        const int want = glu_rows_splits(N, F);
+        l.rows_per_split = round_up((N + want - 1) / want, 64);
+        l.splits = (int)((N + l.rows_per_split - 1) / l.rows_per_split);
+        l.tiles = l.splits;
+        l.wpart = align_up((size_t)l.splits * 2 * F * 4, 256);
+        l.total = l.wpart + align_up((size_t)l.splits * C * 2 * F * 4, 256);
+        return l;
+    }
     l.tiles = (N + kTile - 1) / kTile;
     // enough workgroups for four per CU, at least 512 rows each
     const int64_t t = (int64_t)((2 * F + kTile - 1) / kTile) * ((C + kTile - 1) / kTile);
@@ -419,6 +374,15 @@ GluLayout glu_layout(int64_t N, int C, int F, int dtype) {
     return l;
 }
 
+template <typename T>
+hipError_t glu_join(const GluParams& p, const GluLayout& l, void* dw, float* dbias, hipStream_t st) {
+    const int64_t n = (int64_t)p.C * p.F / 2;
+    k_glu_dw_join<T><<<(unsigned)std::min<int64_t>((n + 255) / 256, 2048), 256, 0, st>>>(p.wpart, l.splits, p.C, p.F,
+                                                                                         (T*)dw);
+    if (dbias) k_glu_dbias_join<<<(2 * p.F + 15) / 16, 256, 0, st>>>(p.bpart, l.tiles, 2 * p.F, dbias);
+    return hipGetLastError();
+}
+
 template <typename T, int ACT>
 hipError_t glu_go(const GluParams& p, bool grad, const GluLayout& l, void* dw, float* dbias, hipStream_t st) {
     // row tiles in the first grid dimension, next to the tiles of their columns
@@ -433,11 +397,7 @@ hipError_t glu_go(const GluParams& p, bool grad, const GluLayout& l, void* dw, f
         k_glu_dx<T><<<(unsigned)(l.tiles * ct), kGluThreads, 0, st>>>(p);
         k_glu_dw<T><<<dim3((2 * p.F + kTile - 1) / kTile, ct, l.splits), kGluThreads, 0, st>>>(p);
     }
-    const int64_t n = (int64_t)p.C * p.F / 2;
-    k_glu_dw_join<T><<<(unsigned)std::min<int64_t>((n + 255) / 256, 2048), 256, 0, st>>>(p.wpart, l.splits, p.C, p.F,
-                                                                                         (T*)dw);
-    if (dbias) k_glu_dbias_join<<<(2 * p.F + 15) / 16, 256, 0, st>>>(p.bpart, l.tiles, 2 * p.F, dbias);
-    return hipGetLastError();
+    return glu_join<T>(p, l, dw, dbias, st);
 }
 
 }  // namespace
@@ -464,6 +424,12 @@ hipError_t launch_glu(const GluArgs& a, bool grad, hipStream_t stream) {
     p.C = a.C;
     p.F = a.F;
     p.rows_per_split = l.rows_per_split;
+    if (use_rows(a.N, a.C, a.dtype)) {
+        if (!grad) return launch_glu_rows(p, a.act, stream);
+        hipError_t e = launch_glu_rows_dx(p, a.act, stream);
+        if (e == hipSuccess) e = launch_glu_rows_dw(p, a.act, l.splits, stream);
+        return e == hipSuccess ? glu_join<__bf16>(p, l, a.dw, a.dbias, stream) : e;
+    }
     if (a.dtype == SPCONV_BF16)
         return a.act == SPCONV_SILU ? glu_go<__bf16, SPCONV_SILU>(p, grad, l, a.dw, a.dbias, stream)
                                     : glu_go<__bf16, SPCONV_GELU>(p, grad, l, a.dw, a.dbias, stream);

@@ -1,0 +1,407 @@
+// Gated linear unit of bfloat16 rows with at most 128 channels, and its
+// gradient, for gfx950.  (Wider rows: glu.hip.)
+//
+// With few channels the products are short and the rows' traffic is what
+// counts: x and dout are read from memory once, and a, b, da and db never
+// leave the chip.  The forward and dx keep a slab of the weights in LDS (C x
+// 2 x 256 features at 128 channels: 128 KB) and hand each wave rows of its own;
+// dw keeps the weights and its sums in registers and hands each wave features
+// of its own.  Each of the two gradient kernels computes a and b again: 4 N C F
+// operations, where writing da and db and reading them twice would be 12 N F
+// bytes, which takes longer below about 300 channels.
+//
+// Matrix instructions (16 x 16 x 32) number their outputs so that lanes end up
+// with eight consecutive features (channels) of a row: output m of tile t is
+// feature 8 (m >> 2) + 4 t + (m & 3) of 32.  That makes 16-byte accesses of h,
+// dout and dx, and makes da and db, once rounded, the operand of the next
+// product as they are.
+#include "glu.h"
+
+#include <algorithm>
+
+namespace spc {
+
+namespace {
+
+constexpr int kRowThreads = 512;      // two waves per SIMD
+constexpr int kRowWaves = kRowThreads / 64;
+constexpr int NT = 2;                 // 16-row tiles per wave
+constexpr int kWaveRows = 16 * NT;
+constexpr int kBlockRows = kRowWaves * kWaveRows;
+constexpr int kSlabElems = 65536;     // of w in LDS: 128 KB
+constexpr int kCUs = 256;
+
+__device__ __forceinline__ f32x4r_t mma(bf16x8r_t a, bf16x8r_t b, f32x4r_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ bf16x8r_t join8(bf16x4r_t lo, bf16x4r_t hi) {
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+// lane a of each 16 addresses four elements of its own and receives element
+// a & 3 of the four lanes 4 (a >> 2) .. of the addressing order: the 16 x 4
+// transpose of what was addressed as 4 rows of 4 pieces
+__device__ __forceinline__ bf16x4r_t read_tr(const __bf16* p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4r_t*)p);
+}
+__device__ __forceinline__ bf16x8r_t load8(const __bf16* p, bool in) {
+    bf16x8r_t v = {};
+    if (in) v = *(const bf16x8r_t*)p;
+    return v;
+}
+
+// Weights in LDS: row c, 16-byte units of 8 features (the slab's gates, then
+// its values), unit u of row c at u ^ swizzle(c).  Both ways of reading are
+// free of bank conflicts: 16 rows' unit u (dx), and the four units of four
+// consecutive rows (the projections, transposed).
+__device__ __forceinline__ int swizzle(int c) { return ((c & 3) << 2) | ((c >> 3) & 3); }
+
+// slab features [f0, f0 + fs) of w (fs a multiple of 64, zeros past F and C)
+template <int KC>
+__device__ __forceinline__ void load_slab(__bf16* lw, float* lb, const GluParams& p, int f0, int fs) {
+    const __bf16* w = (const __bf16*)p.w;
+    const int units = fs / 8;
+    for (int e = threadIdx.x; e < KC * 32 * 2 * units; e += kRowThreads) {
+        const int c = e / (2 * units), u = e % (2 * units), s = u >= units, f = f0 + (u - s * units) * 8;
+        const bf16x8r_t v = load8(w + ((int64_t)s * p.C + c) * p.F + f, c < p.C && f < p.F);
+        *(bf16x8r_t*)(lw + (c * 2 * units + (u ^ swizzle(c))) * 8) = v;
+    }
+    for (int e = threadIdx.x; e < 2 * fs; e += kRowThreads) {
+        const int s = e >= fs, f = f0 + e - s * fs;
+        lb[e] = p.bias && f < p.F ? p.bias[s * p.F + f] : 0.f;
+    }
+}
+
+// The rows of a wave as operands: x[n][s] holds channels 32 s + 8 g .. of row
+// 16 n + a.
+template <int KC>
+__device__ __forceinline__ void load_rows(bf16x8r_t (&x)[NT][KC], const GluParams& p, int64_t r0) {
+    const int a = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int64_t r = r0 + 16 * n + a;
+#pragma unroll
+        for (int s = 0; s < KC; ++s)
+            x[n][s] = load8((const __bf16*)p.x + r * p.C + 32 * s + 8 * g, r < p.N && 32 * s + 8 * g < p.C);
+    }
+}
+
+// The forward, and with DX the input gradient: blocks of 256 rows per
+// workgroup, 32 per wave, over the slabs of the hidden features.
+template <int KC, int ACT, bool DX>
+__global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p, int fs) {
+    extern __shared__ __align__(16) char smem[];
+    __bf16* lw = (__bf16*)smem;
+    float* lb = (float*)(smem + (size_t)KC * 32 * 2 * fs * 2);
+    const int wave = threadIdx.x >> 6, a = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
+    const int C = p.C, F = p.F, units = fs / 8;
+    const int64_t blocks = (p.N + kBlockRows - 1) / kBlockRows;
+    const bool whole = fs >= F;
+    if (whole) {
+        load_slab<KC>(lw, lb, p, 0, fs);
+        __syncthreads();
+    }
+    bf16x8r_t x[NT][KC], xn[NT][KC];
+    load_rows<KC>(xn, p, (int64_t)blockIdx.x * kBlockRows + wave * kWaveRows);
+    for (int64_t blk = blockIdx.x; blk < blocks; blk += gridDim.x) {
+        const int64_t r0 = blk * kBlockRows + wave * kWaveRows;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int s = 0; s < KC; ++s) x[n][s] = xn[n][s];
+        load_rows<KC>(xn, p, r0 + (int64_t)gridDim.x * kBlockRows);
+        f32x4r_t dx[DX ? 2 * KC : 1][NT];
+        if constexpr (DX) {
+#pragma unroll
+            for (int i = 0; i < 2 * KC; ++i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) dx[i][n] = f32x4r_t{0.f, 0.f, 0.f, 0.f};
+        }
+        for (int f0 = 0; f0 < F; f0 += fs) {
+            if (!whole) {
+                __syncthreads();
+                load_slab<KC>(lw, lb, p, f0, fs);
+                __syncthreads();
+            }
+            const int fe = min(fs, F - f0);
+            bf16x8r_t dn[NT];
+            auto load_dout = [&](int fl) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int64_t r = r0 + 16 * n + a;
+                    dn[n] = load8((const __bf16*)p.dout + r * F + f0 + fl + 8 * g, r < p.N && fl + 8 * g < fe);
+                }
+            };
+            if constexpr (DX) load_dout(0);
+            for (int fl = 0; fl < fe; fl += 32) {
+                bf16x8r_t dh[NT];
+                if constexpr (DX) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) dh[n] = dn[n];
+                    load_dout(fl + 32);
+                }
+                f32x4r_t pa[2][NT], pb[2][NT];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const f32x4r_t ba = *(const f32x4r_t*)(lb + fl + 8 * g + 4 * t);
+                    const f32x4r_t bb = *(const f32x4r_t*)(lb + fs + fl + 8 * g + 4 * t);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        pa[t][n] = ba;
+                        pb[t][n] = bb;
+                    }
+                }
+                const int u0 = fl / 8 + (a & 3);
+#pragma unroll
+                for (int s = 0; s < KC; ++s) {
+                    const int c = 32 * s + 8 * g + (a >> 2);     // and c + 4: same swizzle, other row
+                    const __bf16* row = lw + (size_t)c * 2 * units * 8;
+                    const int sw = swizzle(c);
+                    const __bf16* ga = row + (u0 ^ sw) * 8;
+                    const __bf16* gb = row + ((units + u0) ^ sw) * 8;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const bf16x8r_t wa = join8(read_tr(ga + 4 * t), read_tr(ga + 4 * t + 4 * 2 * units * 8));
+                        const bf16x8r_t wb = join8(read_tr(gb + 4 * t), read_tr(gb + 4 * t + 4 * 2 * units * 8));
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            pa[t][n] = mma(wa, x[n][s], pa[t][n]);
+                            pb[t][n] = mma(wb, x[n][s], pb[t][n]);
+                        }
+                    }
+                }
+                if constexpr (!DX) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        bf16x8r_t o;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            o[e] = (__bf16)(activation<ACT>(pa[e >> 2][n][e & 3]).v * pb[e >> 2][n][e & 3]);
+                        const int64_t r = r0 + 16 * n + a;
+                        if (r < p.N && fl + 8 * g < fe)
+                            *(bf16x8r_t*)((__bf16*)p.h + r * F + f0 + fl + 8 * g) = o;
+                    }
+                } else {
+                    bf16x8r_t da[NT], db[NT];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const Act t = activation<ACT>(pa[e >> 2][n][e & 3]);
+                            const float d = (float)dh[n][e];
+                            da[n][e] = (__bf16)(d * pb[e >> 2][n][e & 3] * t.d);
+                            db[n][e] = (__bf16)(d * t.v);
+                        }
+#pragma unroll
+                    for (int i = 0; i < 2 * KC; ++i) {
+                        // output m: channel 32 (i / 2) + 8 (m >> 2) + 4 (i & 1) + (m & 3)
+                        const int c = 32 * (i >> 1) + 8 * (a >> 2) + 4 * (i & 1) + (a & 3);
+                        const __bf16* row = lw + (size_t)c * 2 * units * 8;
+                        const int u = fl / 8 + g, sw = swizzle(c);
+                        const bf16x8r_t wa = *(const bf16x8r_t*)(row + (u ^ sw) * 8);
+                        const bf16x8r_t wb = *(const bf16x8r_t*)(row + ((units + u) ^ sw) * 8);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) dx[i][n] = mma(wa, da[n], dx[i][n]);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) dx[i][n] = mma(wb, db[n], dx[i][n]);
+                    }
+                }
+            }
+        }
+        if constexpr (DX) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int s = 0; s < KC; ++s) {
+                    bf16x8r_t o;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = (__bf16)dx[2 * s + (e >> 2)][n][e & 3];
+                    const int64_t r = r0 + 16 * n + a;
+                    const int c = 32 * s + 8 * g;
+                    if (r < p.N && c < C) *(bf16x8r_t*)((__bf16*)p.dx + r * C + c) = o;
+                }
+        }
+    }
+}
+
+// dw and dbias of one split of the rows and 128 features, 16 per wave: 64 rows
+// at a time, x shared through LDS, dout (of its own features) per wave.
+//
+// Here the projections are D = x w: a lane gets four consecutive rows of one
+// feature, so da and db, rounded, are the transposed operand of x^T da with
+// its reduction (32 rows) numbered 4 g + e (rows of the first 16) and 16 + 4 g
+// + e; x is read back transposed in the same order, dout too.
+constexpr int kDwFeatures = 128;
+constexpr int kDwRows = 64;
+
+// x tile: row r, 16-byte unit u of 16 at u ^ swz(r): conflict-free for 16
+// rows' unit u and for two units of four consecutive rows
+__device__ __forceinline__ int swizzle_row(int r) { return ((r & 7) << 1) | ((r >> 3) & 1); }
+
+template <int KC, int ACT>
+__global__ void __launch_bounds__(kRowThreads) k_glu_rows_dw(GluParams p, int slabs) {
+    __shared__ __align__(16) __bf16 lx[2][kDwRows * 128];
+    __shared__ __align__(16) __bf16 ld[kRowWaves][2][kDwRows * 16];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, a = lane & 15, g = lane >> 4;
+    const int C = p.C, F = p.F;
+    // the slabs of one split on one XCD (workgroups go round the 8 in turn)
+    const int slab = (blockIdx.x >> 3) % slabs;
+    const int64_t split = (int64_t)(blockIdx.x >> 3) / slabs * 8 + (blockIdx.x & 7);
+    const int64_t k0 = split * p.rows_per_split, k1 = min(p.N, k0 + p.rows_per_split);
+    if (k0 >= p.N) return;
+    const int f = slab * kDwFeatures + wave * 16;      // this wave's first feature
+    const __bf16* w = (const __bf16*)p.w;
+
+    // weights as operands: feature f + a, channels 32 s + 8 g ..
+    bf16x8r_t wt[2][KC];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int k = 0; k < KC; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int c = 32 * k + 8 * g + e;
+                wt[s][k][e] = c < C && f + a < F ? w[((int64_t)s * C + c) * F + f + a] : (__bf16)0.f;
+            }
+    const float ba = p.bias && f + a < F ? p.bias[f + a] : 0.f, bb = p.bias && f + a < F ? p.bias[F + f + a] : 0.f;
+
+    // 64 rows of x: 1024 16-byte units, two per thread; of dout: 128 units per wave
+    bf16x8r_t rx[2], rd[2];
+    auto fetch = [&](int64_t k) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int e = threadIdx.x + kRowThreads * j, r = e >> 4, u = e & 15;
+            rx[j] = load8((const __bf16*)p.x + (k + r) * C + 8 * u, k + r < k1 && 8 * u < C);
+            const int q = lane + 64 * j, rr = q >> 1, h = q & 1;
+            rd[j] = load8((const __bf16*)p.dout + (k + rr) * F + f + 8 * h, k + rr < k1 && f + 8 * h < F);
+        }
+    };
+    auto put = [&](int b) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int e = threadIdx.x + kRowThreads * j, r = e >> 4, u = e & 15;
+            *(bf16x8r_t*)(lx[b] + (r * 16 + (u ^ swizzle_row(r))) * 8) = rx[j];
+            const int q = lane + 64 * j;
+            *(bf16x8r_t*)(ld[wave][b] + q * 8) = rd[j];
+        }
+    };
+    f32x4r_t dw[2][2 * KC];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < 2 * KC; ++i) dw[s][i] = f32x4r_t{0.f, 0.f, 0.f, 0.f};
+    float sa = 0.f, sb = 0.f;
+    fetch(k0);
+    put(0);
+    int b = 0;
+    for (int64_t k = k0; k < k1; k += kDwRows, b ^= 1) {
+        if (k + kDwRows < k1) fetch(k + kDwRows);
+        __syncthreads();
+        float ua = 0.f, ub = 0.f;         // this block's sums first: short chains
+#pragma unroll
+        for (int hf = 0; hf < kDwRows / 32; ++hf) {
+            bf16x4r_t da[2], db[2];
+#pragma unroll
+            for (int rt = 0; rt < 2; ++rt) {
+                const int r = 32 * hf + 16 * rt + a;
+                f32x4r_t va = {ba, ba, ba, ba}, vb = {bb, bb, bb, bb};
+#pragma unroll
+                for (int s = 0; s < KC; ++s) {
+                    const bf16x8r_t xf = *(const bf16x8r_t*)(lx[b] + (r * 16 + ((4 * s + g) ^ swizzle_row(r))) * 8);
+                    va = mma(xf, wt[0][s], va);
+                    vb = mma(xf, wt[1][s], vb);
+                }
+                const int rd0 = 32 * hf + 16 * rt + 4 * g + (a >> 2);
+                const bf16x4r_t dh = read_tr(ld[wave][b] + rd0 * 16 + 4 * (a & 3));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const Act t = activation<ACT>(va[e]);
+                    const float d = (float)dh[e];
+                    const float u = d * vb[e] * t.d, v = d * t.v;
+                    ua += u;
+                    ub += v;
+                    da[rt][e] = (__bf16)u;
+                    db[rt][e] = (__bf16)v;
+                }
+            }
+            const bf16x8r_t fa = join8(da[0], da[1]), fb = join8(db[0], db[1]);
+            const int r = 32 * hf + 4 * g + (a >> 2);
+#pragma unroll
+            for (int i = 0; i < 2 * KC; ++i) {
+                const int u = 2 * i + ((a & 3) >> 1), h = 4 * (a & 1);
+                const bf16x8r_t xt = join8(read_tr(lx[b] + (r * 16 + (u ^ swizzle_row(r))) * 8 + h),
+                                           read_tr(lx[b] + ((r + 16) * 16 + (u ^ swizzle_row(r + 16))) * 8 + h));
+                dw[0][i] = mma(fa, xt, dw[0][i]);
+                dw[1][i] = mma(fb, xt, dw[1][i]);
+            }
+        }
+        sa += ua;
+        sb += ub;
+        if (k + kDwRows < k1) put(b ^ 1);
+    }
+    // output m = 4 g + e: feature f + m; channel 16 i + a
+    float* part = p.wpart + split * C * 2 * F;
+#pragma unroll
+    for (int i = 0; i < 2 * KC; ++i) {
+        const int c = 16 * i + a;
+        if (c >= C || f + 4 * g >= F) continue;
+        *(f32x4r_t*)(part + (int64_t)c * 2 * F + f + 4 * g) = dw[0][i];
+        *(f32x4r_t*)(part + (int64_t)c * 2 * F + F + f + 4 * g) = dw[1][i];
+    }
+    if (p.bpart) {
+        // the four row groups of a feature
+        sa += __shfl_xor(sa, 16);
+        sb += __shfl_xor(sb, 16);
+        sa += __shfl_xor(sa, 32);
+        sb += __shfl_xor(sb, 32);
+        if (g == 0 && f + a < F) {
+            p.bpart[split * 2 * F + f + a] = sa;
+            p.bpart[(split * 2 + 1) * F + f + a] = sb;
+        }
+    }
+}
+
+template <int KC, int ACT>
+hipError_t rows_go(const GluParams& p, int what, int splits, hipStream_t st) {
+    if (what == 2) {
+        const int slabs = (p.F + kDwFeatures - 1) / kDwFeatures;
+        k_glu_rows_dw<KC, ACT><<<(unsigned)((splits + 7) / 8 * 8 * slabs), kRowThreads, 0, st>>>(p, slabs);
+        return hipGetLastError();
+    }
+    const int fs = std::min((p.F + 63) / 64 * 64, kSlabElems / (KC * 32 * 2));
+    const size_t lds = (size_t)KC * 32 * 2 * fs * 2 + (size_t)2 * fs * 4;
+    const unsigned grid = (unsigned)std::min<int64_t>((p.N + kBlockRows - 1) / kBlockRows, kCUs);
+    const void* fn = what ? (const void*)k_glu_rows<KC, ACT, true> : (const void*)k_glu_rows<KC, ACT, false>;
+    const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+    if (what)
+        k_glu_rows<KC, ACT, true><<<grid, kRowThreads, lds, st>>>(p, fs);
+    else
+        k_glu_rows<KC, ACT, false><<<grid, kRowThreads, lds, st>>>(p, fs);
+    return hipGetLastError();
+}
+
+template <int ACT>
+hipError_t rows_dispatch(const GluParams& p, int what, int splits, hipStream_t st) {
+    if (p.C <= 32) return rows_go<1, ACT>(p, what, splits, st);
+    if (p.C <= 64) return rows_go<2, ACT>(p, what, splits, st);
+    return rows_go<4, ACT>(p, what, splits, st);
+}
+hipError_t rows_act(const GluParams& p, int act, int what, int splits, hipStream_t st) {
+    return act == SPCONV_SILU ? rows_dispatch<SPCONV_SILU>(p, what, splits, st)
+                              : rows_dispatch<SPCONV_GELU>(p, what, splits, st);
+}
+
+}  // namespace
+
+hipError_t launch_glu_rows(const GluParams& p, int act, hipStream_t st) { return rows_act(p, act, 0, 0, st); }
+hipError_t launch_glu_rows_dx(const GluParams& p, int act, hipStream_t st) { return rows_act(p, act, 1, 0, st); }
+int glu_rows_splits(int64_t N, int F) {
+    // a workgroup holds a CU's registers: one each
+    const int64_t slabs = (F + kDwFeatures - 1) / kDwFeatures;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(kCUs / slabs, (N + kDwRows - 1) / kDwRows));
+}
+hipError_t launch_glu_rows_dw(const GluParams& p, int act, int splits, hipStream_t st) {
+    return rows_act(p, act, 2, splits, st);
+}
+
+}  // namespace spc

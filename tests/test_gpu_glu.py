@@ -121,6 +121,20 @@ def test_many_rows(N, C, F, dt):
     check_grad(d, x, w, b, "silu")
 
 
+@pytest.mark.parametrize("N, C, F", [(32768, 128, 256), (40007, 128, 264), (33000, 8, 8), (50001, 40, 1000),
+                                     (66000, 64, 72), (65537, 104, 512), (100003, 24, 136), (33333, 96, 2048)])
+def test_rows_with_few_channels(N, C, F):
+    """bfloat16 with many rows: weights kept on the chip, in one slab or several."""
+    for kind, bias in (("silu", True), ("gelu", False)):
+        x, w, b, d = inputs(N, C, F, torch.bfloat16, bias)
+        check_forward(x, w, b, kind)
+        check_grad(d, x, w, b, kind)
+    for r in (0, 17, 63, 64, 255, 256, 8191, 32767, N - 1):
+        one = torch.zeros_like(d)
+        one[r] = d[r]
+        check_grad(one, x, w, b, "silu")
+
+
 @DTS
 @pytest.mark.parametrize("N, C, F", [(3000, 128, 256), (3001, 64, 168), (2500, 256, 680), (2049, 40, 24)])
 def test_single_rows(N, C, F, dt):
