@@ -36,7 +36,7 @@ __device__ __forceinline__ Act activation(float a) {
     if constexpr (ACT == SPCONV_SILU) {
         const float s = fast_sigmoid(a);
         const float v = a * s;
-        return {v, s * (1.f + a - v)};
+        return {v, fmaf(-s, v, s) + v};       // s (1 + a (1 - s))
     } else {
         const float cdf = 0.5f * (1.f + erff(a * 0.70710678f));
         const float pdf = 0.39894228f * __builtin_amdgcn_exp2f(-0.72134752f * a * a);

@@ -14,6 +14,7 @@
 // axis is not contiguous in memory is read back with the transposing LDS read
 // (bf16) or one word per lane (fp32).
 #include "glu.h"
+#include "join.h"
 
 #include <algorithm>
 
@@ -303,39 +304,23 @@ __global__ void __launch_bounds__(kGluThreads) k_glu_dw(GluParams p) {
     }
 }
 
-// dw[s][c][f]: the splits' partials added in their order, rounded once.
+// dw[s][c][f]: the splits' partials (C, 2 F) added in their order, rounded once.
 template <typename T>
-__global__ void __launch_bounds__(256) k_glu_dw_join(const float* part, int splits, int C, int F, T* dw) {
-    const int64_t n = (int64_t)C * 2 * F / 4;
-    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
-        f32x4r_t s = {0.f, 0.f, 0.f, 0.f};
-        for (int k = 0; k < splits; ++k) s += ((const f32x4r_t*)part)[k * n + e];
-        const int64_t c = e * 4 / (2 * F);
-        const int m = (int)(e * 4 % (2 * F));
-        const float o[4] = {s[0], s[1], s[2], s[3]};
-        store_four(dw + (m < F ? c * F + m : (C + c) * F + (m - F)), o);
-    }
+__global__ void __launch_bounds__(kJoinCols * 16) k_glu_dw_join(const float* part, int splits, int C, int F, T* dw) {
+    const int64_t n = (int64_t)C * 2 * F;
+    const float t = join_column<16>(part, splits, n);
+    const int64_t e = (int64_t)blockIdx.x * kJoinCols + threadIdx.x;
+    if (threadIdx.x >= kJoinCols || e >= n) return;
+    const int64_t c = e / (2 * F);
+    const int m = (int)(e % (2 * F));
+    dw[m < F ? c * F + m : (C + c) * F + (m - F)] = (T)t;
 }
 
-// dbias: 16 columns x 16 slices of the row tiles per workgroup, added in order.
-__global__ void __launch_bounds__(256) k_glu_dbias_join(const float* part, int64_t tiles, int n, float* dbias) {
-    __shared__ float s[16][17];
-    const int col = threadIdx.x & 15, sl = threadIdx.x >> 4;
-    const int e = blockIdx.x * 16 + col;
-    const int64_t per = (tiles + 15) / 16;
-    float v = 0.f;
-    if (e < n) {
-        const int64_t t1 = min(tiles, (sl + 1) * per);
-        for (int64_t t = sl * per; t < t1; ++t) v += part[t * n + e];
-    }
-    s[sl][col] = v;
-    __syncthreads();
-    if (sl == 0 && e < n) {
-        float t = 0.f;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) t += s[k][col];
-        dbias[e] = t;
-    }
+__global__ void __launch_bounds__(kJoinCols * 64) k_glu_dbias_join(const float* part, int64_t tiles, int n,
+                                                                   float* dbias) {
+    const float t = join_column<64>(part, tiles, n);
+    const int e = blockIdx.x * kJoinCols + threadIdx.x;
+    if (threadIdx.x < kJoinCols && e < n) dbias[e] = t;
 }
 
 // Few channels and enough rows to give every CU a block of them: glu_rows.hip.
@@ -376,10 +361,12 @@ GluLayout glu_layout(int64_t N, int C, int F, int dtype) {
 
 template <typename T>
 hipError_t glu_join(const GluParams& p, const GluLayout& l, void* dw, float* dbias, hipStream_t st) {
-    const int64_t n = (int64_t)p.C * p.F / 2;
-    k_glu_dw_join<T><<<(unsigned)std::min<int64_t>((n + 255) / 256, 2048), 256, 0, st>>>(p.wpart, l.splits, p.C, p.F,
-                                                                                         (T*)dw);
-    if (dbias) k_glu_dbias_join<<<(2 * p.F + 15) / 16, 256, 0, st>>>(p.bpart, l.tiles, 2 * p.F, dbias);
+    const int64_t n = (int64_t)p.C * 2 * p.F;
+    k_glu_dw_join<T><<<(unsigned)((n + kJoinCols - 1) / kJoinCols), kJoinCols * 16, 0, st>>>(p.wpart, l.splits, p.C,
+                                                                                             p.F, (T*)dw);
+    if (dbias)
+        k_glu_dbias_join<<<(2 * p.F + kJoinCols - 1) / kJoinCols, kJoinCols * 64, 0, st>>>(p.bpart, l.tiles, 2 * p.F,
+                                                                                           dbias);
     return hipGetLastError();
 }
 

@@ -49,24 +49,34 @@ __device__ __forceinline__ bf16x8r_t load8(const __bf16* p, bool in) {
     return v;
 }
 
-// Weights in LDS: row c, 16-byte units of 8 features (the slab's gates, then
-// its values), unit u of row c at u ^ swizzle(c).  Both ways of reading are
-// free of bank conflicts: 16 rows' unit u (dx), and the four units of four
-// consecutive rows (the projections, transposed).
+// Weights in LDS: row c holds the slab's gates and then its values, in 16-byte
+// units of 8 features; unit u of row c stands at u ^ swizzle(c), its two halves
+// exchanged where c & 8.  Read as 8-byte pieces, both ways are then free of
+// bank conflicts over 32 lanes: 16 rows' unit u (dx), and the four units of
+// four consecutive rows (the projections, transposed).  The slab's size is
+// fixed, so that rows and tiles are constant offsets from one address per
+// group of 32 features.
 __device__ __forceinline__ int swizzle(int c) { return ((c & 3) << 2) | ((c >> 3) & 3); }
-
-// slab features [f0, f0 + fs) of w (fs a multiple of 64, zeros past F and C)
 template <int KC>
-__device__ __forceinline__ void load_slab(__bf16* lw, float* lb, const GluParams& p, int f0, int fs) {
+constexpr int kSlab = kSlabElems / (KC * 32 * 2);       // features
+
+// Features [f0, f0 + kSlab) of w, as far as F goes up to a multiple of 32
+// (zeros past F and C).
+template <int KC>
+__device__ __forceinline__ void load_slab(__bf16* lw, float* lb, const GluParams& p, int f0) {
+    constexpr int FS = kSlab<KC>, UNITS = FS / 8;
     const __bf16* w = (const __bf16*)p.w;
-    const int units = fs / 8;
-    for (int e = threadIdx.x; e < KC * 32 * 2 * units; e += kRowThreads) {
-        const int c = e / (2 * units), u = e % (2 * units), s = u >= units, f = f0 + (u - s * units) * 8;
+    const int n = min((p.F - f0 + 31) / 32 * 4, UNITS);    // units with features
+    for (int e = threadIdx.x; e < KC * 32 * 2 * n; e += kRowThreads) {
+        const int c = e / (2 * n), u = e % (2 * n), s = u >= n, ul = u - s * n, f = f0 + ul * 8;
         const bf16x8r_t v = load8(w + ((int64_t)s * p.C + c) * p.F + f, c < p.C && f < p.F);
-        *(bf16x8r_t*)(lw + (c * 2 * units + (u ^ swizzle(c))) * 8) = v;
+        __bf16* q = lw + (c * 2 * UNITS + s * UNITS + (ul ^ swizzle(c))) * 8;
+        const int h = (c >> 1) & 4;
+        *(bf16x4r_t*)(q + h) = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+        *(bf16x4r_t*)(q + (h ^ 4)) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
     }
-    for (int e = threadIdx.x; e < 2 * fs; e += kRowThreads) {
-        const int s = e >= fs, f = f0 + e - s * fs;
+    for (int e = threadIdx.x; e < 2 * FS; e += kRowThreads) {
+        const int s = e >= FS, f = f0 + e - s * FS;
         lb[e] = p.bias && f < p.F ? p.bias[s * p.F + f] : 0.f;
     }
 }
@@ -88,16 +98,24 @@ __device__ __forceinline__ void load_rows(bf16x8r_t (&x)[NT][KC], const GluParam
 // The forward, and with DX the input gradient: blocks of 256 rows per
 // workgroup, 32 per wave, over the slabs of the hidden features.
 template <int KC, int ACT, bool DX>
-__global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p, int fs) {
+__global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p) {
     extern __shared__ __align__(16) char smem[];
     __bf16* lw = (__bf16*)smem;
-    float* lb = (float*)(smem + (size_t)KC * 32 * 2 * fs * 2);
+    float* lb = (float*)(smem + (size_t)kSlabElems * 2);
+    constexpr int FS = kSlab<KC>, PITCH = 2 * FS;        // elements per row
     const int wave = threadIdx.x >> 6, a = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
-    const int C = p.C, F = p.F, units = fs / 8;
+    const int C = p.C, F = p.F;
+    // projections: row 8 g + (a >> 2) of each 32, piece (a & 3) of the group's
+    // units; dx: row 8 (a >> 2) + (a & 3) of each 32, unit g of the group
+    const __bf16* w1 = lw + (8 * g + (a >> 2)) * PITCH + 4 * (g & 1);
+    const int x1 = swizzle(8 * g + (a >> 2)) ^ (a & 3);
+    const __bf16* w2 = lw + (8 * (a >> 2) + (a & 3)) * PITCH + 4 * ((a >> 2) & 1);
+    const int x2 = swizzle(8 * (a >> 2) + (a & 3)) ^ g;
+    const int t1 = 4 - 8 * (g & 1), t2 = 4 - 8 * ((a >> 2) & 1);       // to the other half
     const int64_t blocks = (p.N + kBlockRows - 1) / kBlockRows;
-    const bool whole = fs >= F;
+    const bool whole = FS >= F;
     if (whole) {
-        load_slab<KC>(lw, lb, p, 0, fs);
+        load_slab<KC>(lw, lb, p, 0);
         __syncthreads();
     }
     bf16x8r_t x[NT][KC], xn[NT][KC];
@@ -116,13 +134,13 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p, int fs) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) dx[i][n] = f32x4r_t{0.f, 0.f, 0.f, 0.f};
         }
-        for (int f0 = 0; f0 < F; f0 += fs) {
+        for (int f0 = 0; f0 < F; f0 += FS) {
             if (!whole) {
                 __syncthreads();
-                load_slab<KC>(lw, lb, p, f0, fs);
+                load_slab<KC>(lw, lb, p, f0);
                 __syncthreads();
             }
-            const int fe = min(fs, F - f0);
+            const int fe = min(FS, F - f0);
             bf16x8r_t dn[NT];
             auto load_dout = [&](int fl) {
 #pragma unroll
@@ -143,25 +161,21 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p, int fs) {
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const f32x4r_t ba = *(const f32x4r_t*)(lb + fl + 8 * g + 4 * t);
-                    const f32x4r_t bb = *(const f32x4r_t*)(lb + fs + fl + 8 * g + 4 * t);
+                    const f32x4r_t bb = *(const f32x4r_t*)(lb + FS + fl + 8 * g + 4 * t);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         pa[t][n] = ba;
                         pb[t][n] = bb;
                     }
                 }
-                const int u0 = fl / 8 + (a & 3);
+                const __bf16* q1 = w1 + ((fl / 8) ^ x1) * 8;
 #pragma unroll
                 for (int s = 0; s < KC; ++s) {
-                    const int c = 32 * s + 8 * g + (a >> 2);     // and c + 4: same swizzle, other row
-                    const __bf16* row = lw + (size_t)c * 2 * units * 8;
-                    const int sw = swizzle(c);
-                    const __bf16* ga = row + (u0 ^ sw) * 8;
-                    const __bf16* gb = row + ((units + u0) ^ sw) * 8;
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        const bf16x8r_t wa = join8(read_tr(ga + 4 * t), read_tr(ga + 4 * t + 4 * 2 * units * 8));
-                        const bf16x8r_t wb = join8(read_tr(gb + 4 * t), read_tr(gb + 4 * t + 4 * 2 * units * 8));
+                        const __bf16* q = q1 + (t ? t1 : 0) + 32 * s * PITCH;
+                        const bf16x8r_t wa = join8(read_tr(q), read_tr(q + 4 * PITCH));
+                        const bf16x8r_t wb = join8(read_tr(q + FS), read_tr(q + FS + 4 * PITCH));
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             pa[t][n] = mma(wa, x[n][s], pa[t][n]);
@@ -191,14 +205,13 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p, int fs) {
                             da[n][e] = (__bf16)(d * pb[e >> 2][n][e & 3] * t.d);
                             db[n][e] = (__bf16)(d * t.v);
                         }
+                    // output m of tile i: channel 32 (i / 2) + 8 (m >> 2) + 4 (i & 1) + (m & 3)
+                    const __bf16* q2 = w2 + ((fl / 8) ^ x2) * 8;
 #pragma unroll
                     for (int i = 0; i < 2 * KC; ++i) {
-                        // output m: channel 32 (i / 2) + 8 (m >> 2) + 4 (i & 1) + (m & 3)
-                        const int c = 32 * (i >> 1) + 8 * (a >> 2) + 4 * (i & 1) + (a & 3);
-                        const __bf16* row = lw + (size_t)c * 2 * units * 8;
-                        const int u = fl / 8 + g, sw = swizzle(c);
-                        const bf16x8r_t wa = *(const bf16x8r_t*)(row + (u ^ sw) * 8);
-                        const bf16x8r_t wb = *(const bf16x8r_t*)(row + ((units + u) ^ sw) * 8);
+                        const __bf16* q = q2 + (32 * (i >> 1) + 4 * (i & 1)) * PITCH;
+                        const bf16x8r_t wa = join8(*(const bf16x4r_t*)q, *(const bf16x4r_t*)(q + t2));
+                        const bf16x8r_t wb = join8(*(const bf16x4r_t*)(q + FS), *(const bf16x4r_t*)(q + FS + t2));
 #pragma unroll
                         for (int n = 0; n < NT; ++n) dx[i][n] = mma(wa, da[n], dx[i][n]);
 #pragma unroll
@@ -367,16 +380,12 @@ hipError_t rows_go(const GluParams& p, int what, int splits, hipStream_t st) {
         k_glu_rows_dw<KC, ACT><<<(unsigned)((splits + 7) / 8 * 8 * slabs), kRowThreads, 0, st>>>(p, slabs);
         return hipGetLastError();
     }
-    const int fs = std::min((p.F + 63) / 64 * 64, kSlabElems / (KC * 32 * 2));
-    const size_t lds = (size_t)KC * 32 * 2 * fs * 2 + (size_t)2 * fs * 4;
+    const size_t lds = (size_t)kSlabElems * 2 + (size_t)2 * kSlab<KC> * 4;
     const unsigned grid = (unsigned)std::min<int64_t>((p.N + kBlockRows - 1) / kBlockRows, kCUs);
-    const void* fn = what ? (const void*)k_glu_rows<KC, ACT, true> : (const void*)k_glu_rows<KC, ACT, false>;
-    const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    const auto fn = what ? k_glu_rows<KC, ACT, true> : k_glu_rows<KC, ACT, false>;
+    const hipError_t e = hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
-    if (what)
-        k_glu_rows<KC, ACT, true><<<grid, kRowThreads, lds, st>>>(p, fs);
-    else
-        k_glu_rows<KC, ACT, false><<<grid, kRowThreads, lds, st>>>(p, fs);
+    fn<<<grid, kRowThreads, lds, st>>>(p);
     return hipGetLastError();
 }
 

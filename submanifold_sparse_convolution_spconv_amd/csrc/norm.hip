@@ -15,7 +15,7 @@
 // workgroup (L = 256), whose four waves join their sums through LDS, so that
 // a lane never holds more than 16 elements of a row next to its weights.
 // Workgroups stay and walk the rows, with the weights in registers.
-#include "rowops.h"
+#include "join.h"
 
 #include <algorithm>
 
@@ -260,30 +260,11 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_grad(NormParams p) {
     }
 }
 
-// out[c] = sum over `blocks` partial rows, in their order: 16 columns x 16
-// slices of the rows per workgroup, slices joined in order.
-__global__ void __launch_bounds__(256) k_norm_join(const float* part, int blocks, int C, float* dweight,
-                                                   float* dbias) {
-    __shared__ float s[16][17];
-    const int col = threadIdx.x & 15, sl = threadIdx.x >> 4;
-    const int e = blockIdx.x * 16 + col;
-    const int per = (blocks + 15) / 16;
-    float a = 0.f;
-    if (e < 2 * C) {
-        const int b1 = min(blocks, (sl + 1) * per);
-        for (int b = sl * per; b < b1; ++b) a += part[(int64_t)b * 2 * C + e];
-    }
-    s[sl][col] = a;
-    __syncthreads();
-    if (sl == 0 && e < 2 * C) {
-        float t = 0.f;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) t += s[k][col];
-        if (e < C)
-            dweight[e] = t;
-        else
-            dbias[e - C] = t;
-    }
+__global__ void __launch_bounds__(kJoinCols * 64) k_norm_join(const float* part, int blocks, int C, float* dweight,
+                                                              float* dbias) {
+    const float t = join_column<64>(part, blocks, 2 * C);
+    const int e = blockIdx.x * kJoinCols + threadIdx.x;
+    if (threadIdx.x < kJoinCols && e < 2 * C) (e < C ? dweight : dbias - C)[e] = t;
 }
 
 // Lanes per row and pieces per lane for rows of C elements: the smallest
@@ -359,7 +340,7 @@ hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t stream) {
         if (e != hipSuccess) return e;
     }
     if (!a.dweight) return hipSuccess;
-    k_norm_join<<<(2 * a.C + 15) / 16, 256, 0, stream>>>(
+    k_norm_join<<<(2 * a.C + kJoinCols - 1) / kJoinCols, kJoinCols * 64, 0, stream>>>(
         (const float*)a.workspace, norm_grad_blocks(a.N, a.C, a.dtype), a.C, a.dweight, a.dbias);
     return hipGetLastError();
 }
