@@ -43,9 +43,17 @@ __device__ __forceinline__ bf16x8r_t join8(bf16x4r_t lo, bf16x4r_t hi) {
 __device__ __forceinline__ bf16x4r_t read_tr(const __bf16* p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4r_t*)p);
 }
-__device__ __forceinline__ bf16x8r_t load8(const __bf16* p, bool in) {
-    bf16x8r_t v = {};
-    if (in) v = *(const bf16x8r_t*)p;
+// Rows' loads stand under no branch: a branch between loads makes the compiler
+// wait for all of them at the first use of any.  Lanes past the end read a
+// valid place instead, and what they got is replaced where it is used.
+__device__ __forceinline__ bf16x8r_t load8(const __bf16* p) { return *(const bf16x8r_t*)p; }
+__device__ __forceinline__ bf16x8r_t keep(bf16x8r_t v, bool in) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    u32x4 w;
+    __builtin_memcpy(&w, &v, 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = in ? w[i] : 0u;
+    __builtin_memcpy(&v, &w, 16);
     return v;
 }
 
@@ -69,7 +77,8 @@ __device__ __forceinline__ void load_slab(__bf16* lw, float* lb, const GluParams
     const int n = min((p.F - f0 + 31) / 32 * 4, UNITS);    // units with features
     for (int e = threadIdx.x; e < KC * 32 * 2 * n; e += kRowThreads) {
         const int c = e / (2 * n), u = e % (2 * n), s = u >= n, ul = u - s * n, f = f0 + ul * 8;
-        const bf16x8r_t v = load8(w + ((int64_t)s * p.C + c) * p.F + f, c < p.C && f < p.F);
+        const bool in = c < p.C && f < p.F;
+        const bf16x8r_t v = keep(load8(w + (in ? ((int64_t)s * p.C + c) * p.F + f : 0)), in);
         __bf16* q = lw + (c * 2 * UNITS + s * UNITS + (ul ^ swizzle(c))) * 8;
         const int h = (c >> 1) & 4;
         *(bf16x4r_t*)(q + h) = __builtin_shufflevector(v, v, 0, 1, 2, 3);
@@ -82,16 +91,15 @@ __device__ __forceinline__ void load_slab(__bf16* lw, float* lb, const GluParams
 }
 
 // The rows of a wave as operands: x[n][s] holds channels 32 s + 8 g .. of row
-// 16 n + a.
+// 16 n + a (channel 0 on where those are past C, the last row past the rows).
 template <int KC>
 __device__ __forceinline__ void load_rows(bf16x8r_t (&x)[NT][KC], const GluParams& p, int64_t r0) {
     const int a = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int64_t r = r0 + 16 * n + a;
+        const __bf16* row = (const __bf16*)p.x + min(r0 + 16 * n + a, p.N - 1) * p.C;
 #pragma unroll
-        for (int s = 0; s < KC; ++s)
-            x[n][s] = load8((const __bf16*)p.x + r * p.C + 32 * s + 8 * g, r < p.N && 32 * s + 8 * g < p.C);
+        for (int s = 0; s < KC; ++s) x[n][s] = load8(row + (32 * s + 8 * g < p.C ? 32 * s + 8 * g : 0));
     }
 }
 
@@ -125,7 +133,7 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int s = 0; s < KC; ++s) x[n][s] = xn[n][s];
+            for (int s = 0; s < KC; ++s) x[n][s] = keep(xn[n][s], 32 * s + 8 * g < C);
         load_rows<KC>(xn, p, r0 + (int64_t)gridDim.x * kBlockRows);
         f32x4r_t dx[DX ? 2 * KC : 1][NT];
         if constexpr (DX) {
@@ -143,18 +151,17 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p) {
             const int fe = min(FS, F - f0);
             bf16x8r_t dn[NT];
             auto load_dout = [&](int fl) {
+                const int f = f0 + (fl + 8 * g < fe ? fl + 8 * g : 0);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const int64_t r = r0 + 16 * n + a;
-                    dn[n] = load8((const __bf16*)p.dout + r * F + f0 + fl + 8 * g, r < p.N && fl + 8 * g < fe);
-                }
+                for (int n = 0; n < NT; ++n)
+                    dn[n] = load8((const __bf16*)p.dout + min(r0 + 16 * n + a, p.N - 1) * F + f);
             };
             if constexpr (DX) load_dout(0);
             for (int fl = 0; fl < fe; fl += 32) {
                 bf16x8r_t dh[NT];
                 if constexpr (DX) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) dh[n] = dn[n];
+                    for (int n = 0; n < NT; ++n) dh[n] = keep(dn[n], fl + 8 * g < fe);
                     load_dout(fl + 32);
                 }
                 f32x4r_t pa[2][NT], pb[2][NT];
@@ -273,7 +280,9 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows_dw(GluParams p, int sl
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int c = 32 * k + 8 * g + e;
-                wt[s][k][e] = c < C && f + a < F ? w[((int64_t)s * C + c) * F + f + a] : (__bf16)0.f;
+                const bool in = c < C && f + a < F;
+                const __bf16 v = w[in ? ((int64_t)s * C + c) * F + f + a : 0];
+                wt[s][k][e] = in ? v : (__bf16)0.f;
             }
     const float ba = p.bias && f + a < F ? p.bias[f + a] : 0.f, bb = p.bias && f + a < F ? p.bias[F + f + a] : 0.f;
 
@@ -283,18 +292,18 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows_dw(GluParams p, int sl
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int e = threadIdx.x + kRowThreads * j, r = e >> 4, u = e & 15;
-            rx[j] = load8((const __bf16*)p.x + (k + r) * C + 8 * u, k + r < k1 && 8 * u < C);
+            rx[j] = load8((const __bf16*)p.x + min(k + r, k1 - 1) * C + (8 * u < C ? 8 * u : 0));
             const int q = lane + 64 * j, rr = q >> 1, h = q & 1;
-            rd[j] = load8((const __bf16*)p.dout + (k + rr) * F + f + 8 * h, k + rr < k1 && f + 8 * h < F);
+            rd[j] = load8((const __bf16*)p.dout + min(k + rr, k1 - 1) * F + (f + 8 * h < F ? f + 8 * h : 0));
         }
     };
-    auto put = [&](int b) {
+    auto put = [&](int b, int64_t k) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int e = threadIdx.x + kRowThreads * j, r = e >> 4, u = e & 15;
-            *(bf16x8r_t*)(lx[b] + (r * 16 + (u ^ swizzle_row(r))) * 8) = rx[j];
-            const int q = lane + 64 * j;
-            *(bf16x8r_t*)(ld[wave][b] + q * 8) = rd[j];
+            *(bf16x8r_t*)(lx[b] + (r * 16 + (u ^ swizzle_row(r))) * 8) = keep(rx[j], k + r < k1 && 8 * u < C);
+            const int q = lane + 64 * j, rr = q >> 1, h = q & 1;
+            *(bf16x8r_t*)(ld[wave][b] + q * 8) = keep(rd[j], k + rr < k1 && f + 8 * h < F);
         }
     };
     f32x4r_t dw[2][2 * KC];
@@ -304,10 +313,10 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows_dw(GluParams p, int sl
         for (int i = 0; i < 2 * KC; ++i) dw[s][i] = f32x4r_t{0.f, 0.f, 0.f, 0.f};
     float sa = 0.f, sb = 0.f;
     fetch(k0);
-    put(0);
+    put(0, k0);
     int b = 0;
     for (int64_t k = k0; k < k1; k += kDwRows, b ^= 1) {
-        if (k + kDwRows < k1) fetch(k + kDwRows);
+        fetch(min(k + kDwRows, k1 - 1));
         __syncthreads();
         float ua = 0.f, ub = 0.f;         // this block's sums first: short chains
 #pragma unroll
@@ -349,7 +358,7 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows_dw(GluParams p, int sl
         }
         sa += ua;
         sb += ub;
-        if (k + kDwRows < k1) put(b ^ 1);
+        put(b ^ 1, k + kDwRows);
     }
     // output m = 4 g + e: feature f + m; channel 16 i + a
     float* part = p.wpart + split * C * 2 * F;
