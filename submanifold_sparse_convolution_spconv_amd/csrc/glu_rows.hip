@@ -43,6 +43,16 @@ __device__ __forceinline__ bf16x8r_t join8(bf16x4r_t lo, bf16x4r_t hi) {
 __device__ __forceinline__ bf16x4r_t read_tr(const __bf16* p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4r_t*)p);
 }
+// the same at byte offset q of LDS, and 16 bytes there
+__device__ __forceinline__ bf16x4r_t read_tr(uint32_t q) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4r_t*)(uintptr_t)q);
+}
+typedef __attribute__((address_space(3))) bf16x8r_t lds_bf16x8r_t;
+__device__ __forceinline__ bf16x8r_t read_unit(uint32_t q) { return *(lds_bf16x8r_t*)(uintptr_t)q; }
+__device__ __forceinline__ void opaque(uint32_t& v) { asm volatile("" : "+v"(v)); }
+// Matrix instructions and LDS reads stay on their sides of this, so that the
+// next step's operands are read before this step's products, not after.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0x416); }
 // Rows' loads stand under no branch: a branch between loads makes the compiler
 // wait for all of them at the first use of any.  Lanes past the end read a
 // valid place instead, and what they got is replaced where it is used.
@@ -58,12 +68,10 @@ __device__ __forceinline__ bf16x8r_t keep(bf16x8r_t v, bool in) {
 }
 
 // Weights in LDS: row c holds the slab's gates and then its values, in 16-byte
-// units of 8 features; unit u of row c stands at u ^ swizzle(c), its two halves
-// exchanged where c & 8.  Read as 8-byte pieces, both ways are then free of
-// bank conflicts over 32 lanes: 16 rows' unit u (dx), and the four units of
-// four consecutive rows (the projections, transposed).  The slab's size is
-// fixed, so that rows and tiles are constant offsets from one address per
-// group of 32 features.
+// units of 8 features; unit u of row c stands at u ^ swizzle(c): 16 rows' unit u
+// (dx) and the four units of four consecutive rows (the projections,
+// transposed) lie on different banks.  The slab's size is fixed, so that rows
+// and tiles are constant offsets from one address per group of 32 features.
 __device__ __forceinline__ int swizzle(int c) { return ((c & 3) << 2) | ((c >> 3) & 3); }
 template <int KC>
 constexpr int kSlab = kSlabElems / (KC * 32 * 2);       // features
@@ -79,10 +87,7 @@ __device__ __forceinline__ void load_slab(__bf16* lw, float* lb, const GluParams
         const int c = e / (2 * n), u = e % (2 * n), s = u >= n, ul = u - s * n, f = f0 + ul * 8;
         const bool in = c < p.C && f < p.F;
         const bf16x8r_t v = keep(load8(w + (in ? ((int64_t)s * p.C + c) * p.F + f : 0)), in);
-        __bf16* q = lw + (c * 2 * UNITS + s * UNITS + (ul ^ swizzle(c))) * 8;
-        const int h = (c >> 1) & 4;
-        *(bf16x4r_t*)(q + h) = __builtin_shufflevector(v, v, 0, 1, 2, 3);
-        *(bf16x4r_t*)(q + (h ^ 4)) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
+        *(bf16x8r_t*)(lw + (c * 2 * UNITS + s * UNITS + (ul ^ swizzle(c))) * 8) = v;
     }
     for (int e = threadIdx.x; e < 2 * FS; e += kRowThreads) {
         const int s = e >= FS, f = f0 + e - s * FS;
@@ -113,13 +118,14 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p) {
     constexpr int FS = kSlab<KC>, PITCH = 2 * FS;        // elements per row
     const int wave = threadIdx.x >> 6, a = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
     const int C = p.C, F = p.F;
-    // projections: row 8 g + (a >> 2) of each 32, piece (a & 3) of the group's
-    // units; dx: row 8 (a >> 2) + (a & 3) of each 32, unit g of the group
-    const __bf16* w1 = lw + (8 * g + (a >> 2)) * PITCH + 4 * (g & 1);
-    const int x1 = swizzle(8 * g + (a >> 2)) ^ (a & 3);
-    const __bf16* w2 = lw + (8 * (a >> 2) + (a & 3)) * PITCH + 4 * ((a >> 2) & 1);
-    const int x2 = swizzle(8 * (a >> 2) + (a & 3)) ^ g;
-    const int t1 = 4 - 8 * (g & 1), t2 = 4 - 8 * ((a >> 2) & 1);       // to the other half
+    // Byte offsets in LDS.  Projections: row 8 g + (a >> 2) of each 32, piece
+    // (a & 3) of the group's units; dx: row 8 (a >> 2) + (a & 3) of each 32,
+    // unit g of the group.
+    const uint32_t w0 = (uint32_t)(uintptr_t)(lds_bf16x4r_t*)lw;
+    const uint32_t w1 = w0 + (8 * g + (a >> 2)) * PITCH * 2;
+    const uint32_t x1 = (swizzle(8 * g + (a >> 2)) ^ (a & 3)) * 16;
+    const uint32_t w2 = w0 + (8 * (a >> 2) + (a & 3)) * PITCH * 2;
+    const uint32_t x2 = (swizzle(8 * (a >> 2) + (a & 3)) ^ g) * 16;
     const int64_t blocks = (p.N + kBlockRows - 1) / kBlockRows;
     const bool whole = FS >= F;
     if (whole) {
@@ -175,20 +181,27 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p) {
                         pb[t][n] = bb;
                     }
                 }
-                const __bf16* q1 = w1 + ((fl / 8) ^ x1) * 8;
+                // step i: tile i & 1 of both projections over channels 32 (i / 2) ..
+                const uint32_t q1 = w1 + ((fl * 2) ^ x1);
+                uint32_t q1h = q1 + 0x10000;         // an offset reaches 64 KB
+                opaque(q1h);
+                auto read1 = [&](int i, bf16x8r_t (&w)[2]) {
+                    const uint32_t at = 8 * (i & 1) + 64 * (i >> 1) * PITCH;
+                    const uint32_t q = (at < 0x10000 ? q1 : q1h) + (at & 0xFFFF);
+                    w[0] = join8(read_tr(q), read_tr(q + 8 * PITCH));
+                    w[1] = join8(read_tr(q + 2 * FS), read_tr(q + 2 * FS + 8 * PITCH));
+                };
+                bf16x8r_t wf[2][2];
+                read1(0, wf[0]);
 #pragma unroll
-                for (int s = 0; s < KC; ++s) {
+                for (int i = 0; i < 2 * KC; ++i) {
+                    if (i + 1 < 2 * KC) read1(i + 1, wf[(i + 1) & 1]);
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const __bf16* q = q1 + (t ? t1 : 0) + 32 * s * PITCH;
-                        const bf16x8r_t wa = join8(read_tr(q), read_tr(q + 4 * PITCH));
-                        const bf16x8r_t wb = join8(read_tr(q + FS), read_tr(q + FS + 4 * PITCH));
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            pa[t][n] = mma(wa, x[n][s], pa[t][n]);
-                            pb[t][n] = mma(wb, x[n][s], pb[t][n]);
-                        }
+                    for (int n = 0; n < NT; ++n) {
+                        pa[i & 1][n] = mma(wf[i & 1][0], x[n][i >> 1], pa[i & 1][n]);
+                        pb[i & 1][n] = mma(wf[i & 1][1], x[n][i >> 1], pb[i & 1][n]);
                     }
+                    keep_order();
                 }
                 if constexpr (!DX) {
 #pragma unroll
@@ -213,16 +226,24 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p) {
                             db[n][e] = (__bf16)(d * t.v);
                         }
                     // output m of tile i: channel 32 (i / 2) + 8 (m >> 2) + 4 (i & 1) + (m & 3)
-                    const __bf16* q2 = w2 + ((fl / 8) ^ x2) * 8;
+                    const uint32_t q2 = w2 + ((fl * 2) ^ x2);
+                    uint32_t q2h = q2 + 0x10000;
+                    opaque(q2h);
+                    auto read2 = [&](int i, bf16x8r_t (&w)[2]) {
+                        const uint32_t at = (32 * (i >> 1) + 4 * (i & 1)) * PITCH * 2;
+                        const uint32_t q = (at < 0x10000 ? q2 : q2h) + (at & 0xFFFF);
+                        w[0] = read_unit(q);
+                        w[1] = read_unit(q + 2 * FS);
+                    };
+                    read2(0, wf[0]);
 #pragma unroll
                     for (int i = 0; i < 2 * KC; ++i) {
-                        const __bf16* q = q2 + (32 * (i >> 1) + 4 * (i & 1)) * PITCH;
-                        const bf16x8r_t wa = join8(*(const bf16x4r_t*)q, *(const bf16x4r_t*)(q + t2));
-                        const bf16x8r_t wb = join8(*(const bf16x4r_t*)(q + FS), *(const bf16x4r_t*)(q + FS + t2));
+                        if (i + 1 < 2 * KC) read2(i + 1, wf[(i + 1) & 1]);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) dx[i][n] = mma(wa, da[n], dx[i][n]);
+                        for (int n = 0; n < NT; ++n) dx[i][n] = mma(wf[i & 1][0], da[n], dx[i][n]);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) dx[i][n] = mma(wb, db[n], dx[i][n]);
+                        for (int n = 0; n < NT; ++n) dx[i][n] = mma(wf[i & 1][1], db[n], dx[i][n]);
+                        keep_order();
                     }
                 }
             }
