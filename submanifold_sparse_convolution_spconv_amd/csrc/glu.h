@@ -21,6 +21,7 @@ struct GluParams {
     int64_t N;
     int C, F;
     int64_t rows_per_split;
+    bool stream;       // outputs past the caches
 };
 
 __device__ __forceinline__ float fast_sigmoid(float a) {

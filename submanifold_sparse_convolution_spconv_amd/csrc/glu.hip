@@ -411,6 +411,7 @@ hipError_t launch_glu(const GluArgs& a, bool grad, hipStream_t stream) {
     p.C = a.C;
     p.F = a.F;
     p.rows_per_split = l.rows_per_split;
+    p.stream = a.N * (grad ? a.C : a.F) * (a.dtype == SPCONV_BF16 ? 2 : 4) > kStreamBytes;
     if (use_rows(a.N, a.C, a.dtype)) {
         if (!grad) return launch_glu_rows(p, a.act, stream);
         hipError_t e = launch_glu_rows_dx(p, a.act, stream);

@@ -66,6 +66,7 @@ struct NormParams {
     int64_t N;
     int C;
     float eps;
+    bool stream;      // outputs past the caches
 };
 
 template <typename T, int L, int NV, int U>
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(kNormThreads) k_norm(NormParams p) {
                 float o[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i) o[i] = ((float)raw[u][j][i] - m[u]) * rs * wt[j][i] + bs[j][i];
-                store_piece(y + r * C + (j * L + lane) * V, o, nv[j]);
+                store_piece(y + r * C + (j * L + lane) * V, o, nv[j], p.stream);
             }
             if (p.mean && lane == 0) {
                 p.mean[r] = m[u];
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_grad(NormParams p) {
                     const float xh = ((float)rx[u][j][i] - mean[u]) * rs[u];
                     o[i] = ((float)rd[u][j][i] * wt[j][i] - m1 - xh * m2) * rs[u];
                 }
-                store_piece(dx + r * C + (j * L + lane) * V, o, nv[j]);
+                store_piece(dx + r * C + (j * L + lane) * V, o, nv[j], p.stream);
             }
         }
     }
@@ -318,6 +319,8 @@ int norm_grad_blocks(int64_t N, int C, int dtype) {
     return (int)std::min<int64_t>((N + rows - 1) / rows, kNormGradBlocks);
 }
 
+bool norm_streams(int64_t N, int C, int dtype) { return N * C * (dtype == SPCONV_BF16 ? 2 : 4) > kStreamBytes; }
+
 }  // namespace
 
 size_t norm_grad_workspace_bytes(int64_t N, int C, int dtype) {
@@ -326,7 +329,8 @@ size_t norm_grad_workspace_bytes(int64_t N, int C, int dtype) {
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
     if (a.N == 0) return hipSuccess;
-    const NormParams p{a.x, a.weight, a.bias, a.y, a.mean, a.rstd, nullptr, nullptr, a.N, a.C, a.eps};
+    const NormParams p{a.x, a.weight, a.bias, a.y, a.mean, a.rstd, nullptr, nullptr, a.N, a.C, a.eps,
+                       norm_streams(a.N, a.C, a.dtype)};
     return a.dtype == SPCONV_BF16 ? norm_dispatch<__bf16>(p, false, kNormBlocks, stream)
                                   : norm_dispatch<float>(p, false, kNormBlocks, stream);
 }
@@ -334,7 +338,8 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
 hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t stream) {
     if (a.N > 0) {
         const NormParams p{a.x, a.weight, nullptr, a.dx, const_cast<float*>(a.mean), const_cast<float*>(a.rstd),
-                           a.dout, a.dweight ? (float*)a.workspace : nullptr, a.N, a.C, 0.f};
+                           a.dout, a.dweight ? (float*)a.workspace : nullptr, a.N, a.C, 0.f,
+                           norm_streams(a.N, a.C, a.dtype)};
         const hipError_t e = a.dtype == SPCONV_BF16 ? norm_dispatch<__bf16>(p, true, kNormGradBlocks, stream)
                                                     : norm_dispatch<float>(p, true, kNormGradBlocks, stream);
         if (e != hipSuccess) return e;

@@ -80,6 +80,7 @@ struct ScanParams {
     int64_t N;
     int C, scenes;
     int64_t chunks;
+    bool stream;       // outputs past the caches
     // [directions][chunks][C] maps of the chunks, first to last and (gradient) last to
     // first; the same of groups of chunks; the states that enter the chunks
     Map* maps;
@@ -120,14 +121,14 @@ __device__ __forceinline__ typename Quad<T>::vec load_quad(const T* base, int ro
     return v;
 }
 template <typename T, bool WHOLE>
-__device__ __forceinline__ void store_quad(T* base, int row, int C, int c0, const float (&f)[kScanV]) {
+__device__ __forceinline__ void store_quad(T* base, int row, int C, int c0, const float (&f)[kScanV], bool stream) {
     const int n = row >= 0 ? C - c0 : 0;
     T* p = base + (int64_t)row * C + c0;
     typename Quad<T>::vec v;
 #pragma unroll
     for (int i = 0; i < kScanV; ++i) v[i] = (T)f[i];
     if constexpr (WHOLE) {
-        if (n > 0) *(typename Quad<T>::uvec*)p = v;
+        if (n > 0) store_vec((typename Quad<T>::uvec*)p, (typename Quad<T>::uvec)v, stream);
     } else {
 #pragma unroll
         for (int i = 0; i < kScanV; ++i)
@@ -540,7 +541,7 @@ __global__ void __launch_bounds__(kScanThreads) k_scan(ScanParams p) {
                 s[i] = fmaf(g.f, s[i], g.n * (float)x[l][i]);
                 if (decltype(mk)::value && e >= 0 && i < k.nv) p.last[(int64_t)e * p.C + k.c0 + i] = s[i];
             }
-            store_quad<T, WHOLE>((T*)p.h, k.row[l], p.C, k.c0, s);
+            store_quad<T, WHOLE>((T*)p.h, k.row[l], p.C, k.c0, s, p.stream);
         }
     };
     if (marked)
@@ -667,8 +668,8 @@ __global__ void __launch_bounds__(kScanThreads, 4) k_scan_grad(ScanParams p) {
                 y[i] = 0.f;
             }
         }
-        store_quad<T, WHOLE>((T*)p.h, k.row[l], p.C, k.c0, ox);
-        store_quad<T, WHOLE>((T*)p.dz, k.row[l], p.C, k.c0, oz);
+        store_quad<T, WHOLE>((T*)p.h, k.row[l], p.C, k.c0, ox, p.stream);
+        store_quad<T, WHOLE>((T*)p.dz, k.row[l], p.C, k.c0, oz, p.stream);
     }
     if (p.last) empty_scenes(p, p.dlast, p.last, CT);
 }
@@ -767,6 +768,7 @@ hipError_t launch_scan(const ScanArgs& a, bool grad, hipStream_t stream) {
     p.N = a.N;
     p.C = a.C;
     p.scenes = a.scenes;
+    p.stream = a.N * a.C * (a.dtype == SPCONV_BF16 ? 2 : 4) > kStreamBytes;
     char* ws = (char*)a.workspace;
     return a.dtype == SPCONV_BF16 ? scan_dispatch<__bf16>(p, grad, ws, stream) : scan_dispatch<float>(p, grad, ws, stream);
 }
