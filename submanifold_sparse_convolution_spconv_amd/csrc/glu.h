@@ -16,8 +16,9 @@ struct GluParams {
     void* h;           // forward
     void* dab;         // (N, 2, F): da, db
     void* dx;
-    float* bpart;      // [row tiles][2][F] partial sums of dbias
-    float* wpart;      // [splits][C][2 F] partial sums of dw
+    void* dw;
+    float* bpart;      // [row tiles][2][F] partial sums of dbias; or NULL
+    float* wpart;      // [splits][C][2 F] partial sums of dw; NULL: one split, into dw
     int64_t N;
     int C, F;
     int64_t rows_per_split;

@@ -22,17 +22,33 @@ namespace spc {
 
 namespace {
 
-constexpr int kGluThreads = 256;
+constexpr int kGluThreads = 256;      // four waves, two by two over a tile
+
+template <typename V>
+__device__ __forceinline__ V keep(V v, bool in) {
+    uint32_t w[sizeof(V) / 4];
+    __builtin_memcpy(w, &v, sizeof v);
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(V) / 4; ++i) w[i] = in ? w[i] : 0u;
+    __builtin_memcpy(&v, w, sizeof v);
+    return v;
+}
+
+template <typename T>
+constexpr int kTileK = sizeof(T) == 2 ? 64 : 32;      // of the reduction per step
 
 // One operand tile in LDS: M outputs x BK of the reduction.  KC: the reduction
 // is contiguous in memory and in LDS ([m][k]); else the outputs are ([k][m]).
-// The pitches keep the fragment reads free of bank conflicts.
-template <typename T, bool KC, int M, int BK>
+// The pitches keep the fragment reads free of bank conflicts: 16 rows' 16-byte
+// units (KC, bf16: an odd number of units), four rows' pairs of units (bf16),
+// one word per lane (fp32).
+template <typename T, bool KC, int M>
 struct Stage {
     static constexpr bool K_CONTIGUOUS = KC;
+    static constexpr int BK = kTileK<T>;
     static constexpr int V = Piece<T>::V;
     static constexpr int PER = M * BK / V / kGluThreads;        // pieces per thread
-    static constexpr int PITCH = KC ? BK + V : M + (sizeof(T) == 2 ? 8 : 16);
+    static constexpr int PITCH = KC ? BK + V : M + 16;
     static constexpr int ELEMS = (KC ? M : BK) * PITCH;
     static_assert(PER >= 1 && M * BK / V % kGluThreads == 0, "whole pieces per thread");
     // piece j of this thread: output m and reduction index k of its first element
@@ -46,10 +62,52 @@ struct Stage {
             m = p % (M / V) * V;
         }
     }
-    static __device__ __forceinline__ void put(T* lds, int j, typename Piece<T>::vec v) {
-        int m, k;
-        where(j, m, k);
-        *(typename Piece<T>::vec*)(lds + (KC ? m * PITCH + k : k * PITCH + m)) = v;
+};
+
+// One operand of a product on its way to LDS: pointers of this thread's pieces
+// (KC: one per piece, its k the same for all; else one, a multiple of k apart),
+// and the pieces of the next step in registers.  Loads stand under no branch
+// (a branch between loads makes the compiler wait for all of them at the first
+// use): pieces outside read a valid place and become 0 on the way to LDS.
+template <typename T, bool KC, int M>
+struct Operand {
+    using S = Stage<T, KC, M>;
+    static constexpr int NP = KC ? S::PER : 1;
+    const T* at[NP];
+    bool in[NP];
+    int64_t pitch;       // of k, where the outputs are contiguous
+    typename Piece<T>::vec raw[S::PER];
+    // place(m): the element at reduction index 0 of output m, valid where
+    // inside(m); `safe`: some valid element
+    template <class P, class I>
+    __device__ __forceinline__ Operand(P place, I inside, const T* safe, int64_t k_pitch) : pitch(k_pitch) {
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+            int m, k;
+            S::where(j, m, k);
+            in[j] = inside(m);
+            at[j] = in[j] ? place(m) : safe;
+        }
+    }
+    // pieces of the step at k; klim: the reduction's end
+    __device__ __forceinline__ void fetch(int64_t k, int64_t klim) {
+#pragma unroll
+        for (int j = 0; j < S::PER; ++j) {
+            int m, kk;
+            S::where(j, m, kk);
+            const int o = KC ? j : 0;
+            const int64_t ki = min(k + kk, klim - (KC ? S::V : 1));
+            raw[j] = *(const typename Piece<T>::vec*)(at[o] + (in[o] ? (KC ? ki : ki * pitch) : 0));
+        }
+    }
+    __device__ __forceinline__ void put(T* lds, int64_t k, int64_t klim) const {
+#pragma unroll
+        for (int j = 0; j < S::PER; ++j) {
+            int m, kk;
+            S::where(j, m, kk);
+            *(typename Piece<T>::vec*)(lds + (KC ? m * S::PITCH + kk : kk * S::PITCH + m)) =
+                keep(raw[j], in[KC ? j : 0] && k + kk < klim);
+        }
     }
 };
 
@@ -93,100 +151,113 @@ struct Frag<float> {
     }
 };
 
-template <typename T>
-constexpr int kTileK = sizeof(T) == 2 ? 32 : 16;
-constexpr int kTile = 128;     // outputs of each kind per workgroup
+// Tiles of TILE x TILE outputs; a wave holds NB x NB blocks of 16 x 16.
+template <int TILE>
+constexpr int kBlocks = TILE / 32;
 
-// acc += A B over the reduction [k0, k1), both operands staged a BK at a time
-// with the next tiles' loads in flight.  load_a / load_b (m, k) give the piece
-// at output m and reduction index k (0 outside); m_at / n_at the first output
-// of this wave's i-th / j-th 16-wide tile.
-template <typename T, bool AKC, bool BKC, class LA, class LB, class MA, class NA>
-__device__ __forceinline__ void tile_product(f32x4r_t (&acc)[4][4], int64_t k0, int64_t k1, LA load_a, LB load_b,
-                                             MA m_at, NA n_at) {
-    constexpr int BK = kTileK<T>;
-    using A = Stage<T, AKC, kTile, BK>;
-    using B = Stage<T, BKC, kTile, BK>;
-    __shared__ __align__(16) T la[A::ELEMS];
-    __shared__ __align__(16) T lb[B::ELEMS];
-    typename Piece<T>::vec ra[A::PER], rb[B::PER];
-    auto fetch = [&](int64_t k) {
-        int m, kk;
+// LDS of a product: two buffers of both operands.
+template <typename T, bool AKC, bool BKC, int TILE>
+constexpr size_t kProductBytes = 2 * sizeof(T) * (Stage<T, AKC, TILE>::ELEMS + Stage<T, BKC, TILE>::ELEMS);
+template <typename T, int TILE>
+constexpr size_t kMostBytes = std::max(kProductBytes<T, false, true, TILE>,
+                                       std::max(kProductBytes<T, true, true, TILE>, kProductBytes<T, false, false, TILE>));
+
+// acc += A B over the reduction [k0, k1).  The next step's pieces are loaded
+// while this step's are multiplied; two buffers, one barrier per step.  m_at /
+// n_at: the first output of this wave's i-th / j-th block.  fp32 adds its
+// products in runs of 512 of the reduction, so that a long sum is not one
+// chain.
+template <typename T, bool AKC, bool BKC, int TILE, class MA, class NA>
+__device__ __forceinline__ void tile_product(f32x4r_t (&acc)[kBlocks<TILE>][kBlocks<TILE>], Operand<T, AKC, TILE>& A,
+                                             Operand<T, BKC, TILE>& B, int64_t k0, int64_t k1, char* smem, MA m_at,
+                                             NA n_at) {
+    using SA = Stage<T, AKC, TILE>;
+    using SB = Stage<T, BKC, TILE>;
+    constexpr int BK = kTileK<T>, NB = kBlocks<TILE>;
+    T* la = (T*)smem;
+    T* lb = la + 2 * SA::ELEMS;
+    f32x4r_t run[sizeof(T) == 4 ? NB : 1][NB];
+    if (sizeof(T) == 4) {
 #pragma unroll
-        for (int j = 0; j < A::PER; ++j) {
-            A::where(j, m, kk);
-            ra[j] = load_a(m, k + kk);
-        }
+        for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int j = 0; j < B::PER; ++j) {
-            B::where(j, m, kk);
-            rb[j] = load_b(m, k + kk);
-        }
-    };
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4r_t{0.f, 0.f, 0.f, 0.f};
-    fetch(k0);
-    for (int64_t k = k0; k < k1; k += BK) {
+            for (int j = 0; j < NB; ++j) run[sizeof(T) == 4 ? i : 0][j] = f32x4r_t{0.f, 0.f, 0.f, 0.f};
+    }
+    A.fetch(k0, k1);
+    B.fetch(k0, k1);
+    int b = 0;
+    for (int64_t k = k0; k < k1; k += BK, b ^= 1) {
+        A.put(la + b * SA::ELEMS, k, k1);
+        B.put(lb + b * SB::ELEMS, k, k1);
         __syncthreads();
-#pragma unroll
-        for (int j = 0; j < A::PER; ++j) A::put(la, j, ra[j]);
-#pragma unroll
-        for (int j = 0; j < B::PER; ++j) B::put(lb, j, rb[j]);
-        __syncthreads();
-        if (k + BK < k1) fetch(k + BK);
+        A.fetch(k + BK, k1);
+        B.fetch(k + BK, k1);
+        const T* pa = la + b * SA::ELEMS;
+        const T* pb = lb + b * SB::ELEMS;
 #pragma unroll
         for (int s = 0; s < BK; s += Frag<T>::K) {
-            typename Frag<T>::type fa[4], fb[4];
+            typename Frag<T>::type fa[NB], fb[NB];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) fa[i] = Frag<T>::template read<A>(la, m_at(i), s);
+            for (int i = 0; i < NB; ++i) fa[i] = Frag<T>::template read<SA>(pa, m_at(i), s);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) fb[j] = Frag<T>::template read<B>(lb, n_at(j), s);
+            for (int j = 0; j < NB; ++j) fb[j] = Frag<T>::template read<SB>(pb, n_at(j), s);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < NB; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = Frag<T>::mma(fa[i], fb[j], acc[i][j]);
+                for (int j = 0; j < NB; ++j) {
+                    if constexpr (sizeof(T) == 4)
+                        run[i][j] = Frag<T>::mma(fa[i], fb[j], run[i][j]);
+                    else
+                        acc[i][j] = Frag<T>::mma(fa[i], fb[j], acc[i][j]);
+                }
+        }
+        if constexpr (sizeof(T) == 4) {
+            if (((k - k0) & 511) == 512 - BK || k + BK >= k1) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int j = 0; j < NB; ++j) {
+                        acc[i][j] += run[i][j];
+                        run[i][j] = f32x4r_t{0.f, 0.f, 0.f, 0.f};
+                    }
+            }
         }
     }
+    __syncthreads();        // the buffers may be used again
 }
-
-template <typename T>
-__device__ __forceinline__ typename Piece<T>::vec piece_or_zero(const T* p, bool in) {
-    typename Piece<T>::vec v;
-    if (in) {
-        v = *(const typename Piece<T>::vec*)p;
-    } else {
+template <int NB>
+__device__ __forceinline__ void clear_blocks(f32x4r_t (&acc)[NB][NB]) {
 #pragma unroll
-        for (int i = 0; i < Piece<T>::V; ++i) v[i] = (T)0.f;
-    }
-    return v;
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) acc[i][j] = f32x4r_t{0.f, 0.f, 0.f, 0.f};
 }
 
-// 128 rows x 64 hidden features, both projections: h, or (GRAD) da and db with
-// their sums over the tile's rows.
-template <typename T, int ACT, bool GRAD>
-__global__ void __launch_bounds__(kGluThreads) k_glu_project(GluParams p) {
-    __shared__ float bsum[2][2][64];
+// TILE rows x TILE / 2 hidden features, both projections: h, or (GRAD) da and
+// db with their sums over the tile's rows.
+template <typename T, int ACT, bool GRAD, int TILE>
+__global__ void __launch_bounds__(kGluThreads, 2) k_glu_project(GluParams p) {
+    constexpr int NB = kBlocks<TILE>, FT = TILE / 2;
+    __shared__ __align__(16) char smem[kProductBytes<T, false, true, TILE>];
+    __shared__ float bsum[2][2][FT];
     const int wave = threadIdx.x >> 6, wm = wave & 1, wn = wave >> 1;
     const int a = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
     const int C = p.C, F = p.F;
-    const int ft = (F + 63) / 64, f0 = (int)(blockIdx.x % ft) * 64;
-    const int64_t tile = blockIdx.x / ft, r0 = tile * kTile;
+    const int ft = (F + FT - 1) / FT, f0 = (int)(blockIdx.x % ft) * FT;
+    const int64_t tile = blockIdx.x / ft, r0 = tile * TILE;
     const T* x = (const T*)p.x;
     const T* w = (const T*)p.w;
-    f32x4r_t acc[4][4];        // [0, 1]: a, [2, 3]: b, of 16 features each
-    tile_product<T, false, true>(
-        acc, 0, C,
-        [&](int m, int64_t k) {
-            const int s = m >> 6, f = f0 + (m & 63);
-            return piece_or_zero(w + ((int64_t)s * C + k) * F + f, k < C && f < F);
-        },
-        [&](int n, int64_t k) { return piece_or_zero(x + (r0 + n) * C + k, r0 + n < p.N && k < C); },
-        [&](int i) { return 64 * (i >> 1) + 32 * wm + 16 * (i & 1); }, [&](int j) { return 64 * wn + 16 * j; });
+    Operand<T, false, TILE> A([&](int m) { return w + (int64_t)(m / FT) * C * F + f0 + m % FT; },
+                              [&](int m) { return f0 + m % FT < F; }, w, F);
+    Operand<T, true, TILE> B([&](int n) { return x + (r0 + n) * C; }, [&](int n) { return r0 + n < p.N; }, x, 0);
+    f32x4r_t acc[NB][NB];      // gates in the first half of i, values in the second
+    clear_blocks(acc);
+    tile_product<T, false, true, TILE>(
+        acc, A, B, 0, C, smem, [&](int i) { return FT * (2 * i / NB) + FT / 2 * wm + 16 * (i % (NB / 2)); },
+        [&](int j) { return TILE / 2 * wn + 16 * j; });
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int fl = 32 * wm + 16 * i + 4 * g, f = f0 + fl;
+    for (int i = 0; i < NB / 2; ++i) {
+        const int fl = FT / 2 * wm + 16 * i + 4 * g, f = f0 + fl;
         f32x4r_t ba = {0.f, 0.f, 0.f, 0.f}, bb = ba;
         if (p.bias && f < F) {
 #pragma unroll
@@ -196,23 +267,30 @@ __global__ void __launch_bounds__(kGluThreads) k_glu_project(GluParams p) {
             }
         }
         f32x4r_t sa = {0.f, 0.f, 0.f, 0.f}, sb = sa;
+        typename Four<T>::vec dh[NB];
+        if constexpr (GRAD) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t r = r0 + 64 * wn + 16 * j + a;
+            for (int j = 0; j < NB; ++j) {
+                const int64_t r = min(r0 + TILE / 2 * wn + 16 * j + a, p.N - 1);
+                dh[j] = *(const typename Four<T>::vec*)((const T*)p.dout + r * F + (f < F ? f : 0));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            const int64_t r = r0 + TILE / 2 * wn + 16 * j + a;
             if (r >= p.N || f >= F) continue;
-            const f32x4r_t va = acc[i][j] + ba, vb = acc[i + 2][j] + bb;
+            const f32x4r_t va = acc[i][j] + ba, vb = acc[i + NB / 2][j] + bb;
             float o[4], q[4];
             if constexpr (!GRAD) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[e] = activation<ACT>(va[e]).v * vb[e];
                 store_four((T*)p.h + r * F + f, o);
             } else {
-                const typename Four<T>::vec dh = *(const typename Four<T>::vec*)((const T*)p.dout + r * F + f);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const Act t = activation<ACT>(va[e]);
-                    o[e] = (float)dh[e] * vb[e] * t.d;
-                    q[e] = (float)dh[e] * t.v;
+                    o[e] = (float)dh[j][e] * vb[e] * t.d;
+                    q[e] = (float)dh[j][e] * t.v;
                     sa[e] += o[e];
                     sb[e] += q[e];
                 }
@@ -237,38 +315,40 @@ __global__ void __launch_bounds__(kGluThreads) k_glu_project(GluParams p) {
     if constexpr (GRAD) {
         if (!p.bpart) return;
         __syncthreads();
-        const int s = threadIdx.x >> 6, f = threadIdx.x & 63;
-        if (threadIdx.x < 128 && f0 + f < F)
+        const int s = threadIdx.x / FT, f = threadIdx.x % FT;
+        if (threadIdx.x < 2 * FT && f0 + f < F)
             p.bpart[(tile * 2 + s) * F + f0 + f] = bsum[0][s][f] + bsum[1][s][f];
     }
 }
 
-// dx: 128 rows x 128 channels, reduced over both halves of dab.
-template <typename T>
-__global__ void __launch_bounds__(kGluThreads) k_glu_dx(GluParams p) {
+// dx: TILE rows x TILE channels, reduced over both halves of dab.
+template <typename T, int TILE>
+__device__ __forceinline__ void glu_dx_tile(const GluParams& p, int64_t block, char* smem) {
+    constexpr int NB = kBlocks<TILE>;
     const int wave = threadIdx.x >> 6, wm = wave & 1, wn = wave >> 1;
     const int a = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
     const int C = p.C, F = p.F;
-    const int ct = (C + kTile - 1) / kTile, c0 = (int)(blockIdx.x % ct) * kTile;
-    const int64_t r0 = (int64_t)(blockIdx.x / ct) * kTile;
-    const T* w = (const T*)p.w;
-    const T* dab = (const T*)p.dab;
-    f32x4r_t acc[4][4];
-    tile_product<T, true, true>(
-        acc, 0, 2 * F,
-        [&](int m, int64_t k) {
-            const int c = c0 + m;
-            const int64_t at = k < F ? (int64_t)c * F + k : (int64_t)(C + c) * F + (k - F);
-            return piece_or_zero(w + at, c < C && k < 2 * F);
-        },
-        [&](int n, int64_t k) { return piece_or_zero(dab + (r0 + n) * 2 * F + k, r0 + n < p.N && k < 2 * F); },
-        [&](int i) { return 64 * wm + 16 * i; }, [&](int j) { return 64 * wn + 16 * j; });
+    const int ct = (C + TILE - 1) / TILE, c0 = (int)(block % ct) * TILE;
+    const int64_t r0 = block / ct * TILE;
+    f32x4r_t acc[NB][NB];
+    clear_blocks(acc);
+#pragma unroll 1
+    for (int s = 0; s < 2; ++s) {
+        const T* w = (const T*)p.w + (int64_t)s * C * F;
+        const T* dab = (const T*)p.dab + s * F;
+        Operand<T, true, TILE> A([&](int m) { return w + (int64_t)(c0 + m) * F; }, [&](int m) { return c0 + m < C; }, w,
+                                 0);
+        Operand<T, true, TILE> B([&](int n) { return dab + (r0 + n) * 2 * F; }, [&](int n) { return r0 + n < p.N; },
+                                 dab, 0);
+        tile_product<T, true, true, TILE>(acc, A, B, 0, F, smem, [&](int i) { return TILE / 2 * wm + 16 * i; },
+                                          [&](int j) { return TILE / 2 * wn + 16 * j; });
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int c = c0 + 64 * wm + 16 * i + 4 * g;
+    for (int i = 0; i < NB; ++i) {
+        const int c = c0 + TILE / 2 * wm + 16 * i + 4 * g;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t r = r0 + 64 * wn + 16 * j + a;
+        for (int j = 0; j < NB; ++j) {
+            const int64_t r = r0 + TILE / 2 * wn + 16 * j + a;
             if (r >= p.N || c >= C) continue;
             const float o[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
             store_four((T*)p.dx + r * C + c, o);
@@ -276,64 +356,94 @@ __global__ void __launch_bounds__(kGluThreads) k_glu_dx(GluParams p) {
     }
 }
 
-// Partial dw of one split of the rows: 128 columns of dab x 128 channels.
-template <typename T>
-__global__ void __launch_bounds__(kGluThreads) k_glu_dw(GluParams p) {
+// dw of one split of the rows: TILE columns of dab x TILE channels, as a
+// partial sum, or (one split) as it is.
+template <typename T, int TILE>
+__device__ __forceinline__ void glu_dw_tile(const GluParams& p, int64_t block, char* smem) {
+    constexpr int NB = kBlocks<TILE>;
     const int wave = threadIdx.x >> 6, wm = wave & 1, wn = wave >> 1;
     const int a = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
-    const int C = p.C, F2 = 2 * p.F;
-    const int m0 = blockIdx.x * kTile, c0 = blockIdx.y * kTile;
-    const int64_t k0 = (int64_t)blockIdx.z * p.rows_per_split, k1 = min(p.N, k0 + p.rows_per_split);
+    const int C = p.C, F = p.F, F2 = 2 * F;
+    const int mt = (F2 + TILE - 1) / TILE, ct = (C + TILE - 1) / TILE;
+    const int m0 = (int)(block % mt) * TILE, c0 = (int)(block / mt % ct) * TILE;
+    const int64_t split = block / mt / ct;
+    const int64_t k0 = split * p.rows_per_split, k1 = min(p.N, k0 + p.rows_per_split);
     const T* x = (const T*)p.x;
     const T* dab = (const T*)p.dab;
-    f32x4r_t acc[4][4];
-    tile_product<T, false, false>(
-        acc, k0, k1,
-        [&](int m, int64_t k) { return piece_or_zero(dab + k * F2 + m0 + m, k < k1 && m0 + m < F2); },
-        [&](int n, int64_t k) { return piece_or_zero(x + k * C + c0 + n, k < k1 && c0 + n < C); },
-        [&](int i) { return 64 * wm + 16 * i; }, [&](int j) { return 64 * wn + 16 * j; });
-    float* part = p.wpart + (int64_t)blockIdx.z * C * F2;
+    Operand<T, false, TILE> A([&](int m) { return dab + m0 + m; }, [&](int m) { return m0 + m < F2; }, dab, F2);
+    Operand<T, false, TILE> B([&](int n) { return x + c0 + n; }, [&](int n) { return c0 + n < C; }, x, C);
+    f32x4r_t acc[NB][NB];
+    clear_blocks(acc);
+    tile_product<T, false, false, TILE>(acc, A, B, k0, k1, smem, [&](int i) { return TILE / 2 * wm + 16 * i; },
+                                        [&](int j) { return TILE / 2 * wn + 16 * j; });
+    float* part = p.wpart + split * C * F2;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int m = m0 + 64 * wm + 16 * i + 4 * g;
+    for (int i = 0; i < NB; ++i) {
+        const int m = m0 + TILE / 2 * wm + 16 * i + 4 * g;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int c = c0 + 64 * wn + 16 * j + a;
-            if (m < F2 && c < C) *(f32x4r_t*)(part + (int64_t)c * F2 + m) = acc[i][j];
+        for (int j = 0; j < NB; ++j) {
+            const int64_t c = c0 + TILE / 2 * wn + 16 * j + a;
+            if (m >= F2 || c >= C) continue;
+            if (p.wpart) {
+                *(f32x4r_t*)(part + c * F2 + m) = acc[i][j];
+            } else {
+                const float o[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                store_four((T*)p.dw + (m < F ? c * F + m : (C + c) * F + (m - F)), o);
+            }
         }
     }
 }
 
-// dw[s][c][f]: the splits' partials (C, 2 F) added in their order, rounded once.
-template <typename T>
-__global__ void __launch_bounds__(kJoinCols * 16) k_glu_dw_join(const float* part, int splits, int C, int F, T* dw) {
-    const int64_t n = (int64_t)C * 2 * F;
-    const float t = join_column<16>(part, splits, n);
-    const int64_t e = (int64_t)blockIdx.x * kJoinCols + threadIdx.x;
-    if (threadIdx.x >= kJoinCols || e >= n) return;
-    const int64_t c = e / (2 * F);
-    const int m = (int)(e % (2 * F));
-    dw[m < F ? c * F + m : (C + c) * F + (m - F)] = (T)t;
+// Both products of the gradient: they need the same da and db and nothing of
+// each other.
+template <typename T, int TILE>
+__global__ void __launch_bounds__(kGluThreads, 2) k_glu_products(GluParams p, unsigned dx_blocks) {
+    __shared__ __align__(16) char smem[kMostBytes<T, TILE>];
+    if (blockIdx.x < dx_blocks)
+        glu_dx_tile<T, TILE>(p, blockIdx.x, smem);
+    else
+        glu_dw_tile<T, TILE>(p, blockIdx.x - dx_blocks, smem);
 }
 
-__global__ void __launch_bounds__(kJoinCols * 64) k_glu_dbias_join(const float* part, int64_t tiles, int n,
-                                                                   float* dbias) {
-    const float t = join_column<64>(part, tiles, n);
-    const int e = blockIdx.x * kJoinCols + threadIdx.x;
-    if (threadIdx.x < kJoinCols && e < n) dbias[e] = t;
+// The partial sums of dw (splits, C, 2 F) and dbias (tiles, 2 F) added in
+// their order and rounded once; the first w_blocks workgroups serve dw.
+template <typename T>
+__global__ void __launch_bounds__(kJoinCols * 16) k_glu_join(GluParams p, int splits, int64_t tiles, float* dbias,
+                                                             unsigned w_blocks) {
+    const int F = p.F;
+    const bool w = blockIdx.x < w_blocks;
+    const int64_t n = w ? (int64_t)p.C * 2 * F : 2 * F;
+    const int64_t block = blockIdx.x - (w ? 0 : w_blocks);
+    const float t = join_column<16>(w ? p.wpart : p.bpart, w ? splits : tiles, n, block);
+    const int64_t e = block * kJoinCols + threadIdx.x;
+    if (threadIdx.x >= kJoinCols || e >= n) return;
+    if (!w) {
+        dbias[e] = t;
+        return;
+    }
+    const int64_t c = e / (2 * F);
+    const int m = (int)(e % (2 * F));
+    ((T*)p.dw)[m < F ? c * F + m : (p.C + c) * F + (m - F)] = (T)t;
 }
 
 // Few channels and enough rows to give every CU a block of them: glu_rows.hip.
 bool use_rows(int64_t N, int C, int dtype) { return dtype == SPCONV_BF16 && C <= kGluRowC && N >= 32768; }
 
+// Tiles of 128 where they fill the card (the operands are then read half as
+// often), of 64 where they would not.
+int64_t tiles_of(int64_t n, int tile) { return (n + tile - 1) / tile; }
+int project_tile(int64_t N, int F) { return tiles_of(N, 128) * tiles_of(F, 64) >= 256 ? 128 : 64; }
+
 struct GluLayout {
     size_t dab, bpart, wpart, total;
-    int64_t tiles, rows_per_split;
-    int splits;
+    int64_t tiles, rows_per_split;    // row tiles of the projections; rows per split of dw
+    int splits, tile, ptile;          // tile of the products and of the projections
+    bool rows;
 };
 GluLayout glu_layout(int64_t N, int C, int F, int dtype) {
     GluLayout l{};
-    if (use_rows(N, C, dtype)) {
+    l.rows = use_rows(N, C, dtype);
+    if (l.rows) {
         const int want = glu_rows_splits(N, F);
         l.rows_per_split = round_up((N + want - 1) / want, 64);
         l.splits = (int)((N + l.rows_per_split - 1) / l.rows_per_split);
@@ -342,49 +452,67 @@ GluLayout glu_layout(int64_t N, int C, int F, int dtype) {
         l.total = l.wpart + align_up((size_t)l.splits * C * 2 * F * 4, 256);
         return l;
     }
-    l.tiles = (N + kTile - 1) / kTile;
-    // enough workgroups for four per CU, at least 512 rows each
-    const int64_t t = (int64_t)((2 * F + kTile - 1) / kTile) * ((C + kTile - 1) / kTile);
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>((1024 + t - 1) / t, (N + 511) / 512));
-    l.rows_per_split = round_up((N + want - 1) / std::max<int64_t>(want, 1), 32);
+    l.ptile = project_tile(N, F);
+    l.tiles = tiles_of(N, l.ptile);
+    l.tile = tiles_of(N, 128) * tiles_of(C, 128) >= 192 ? 128 : 64;
+    // enough workgroups for two per CU, at least 128 rows each
+    const int64_t t = tiles_of(2 * F, l.tile) * tiles_of(C, l.tile);
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>((512 + t - 1) / t, N / 128));
+    l.rows_per_split = round_up((N + want - 1) / want, 64);
     l.splits = l.rows_per_split ? (int)((N + l.rows_per_split - 1) / l.rows_per_split) : 0;
     size_t at = 0;
     l.dab = at;
     at += align_up((size_t)N * 2 * F * (dtype == SPCONV_BF16 ? 2 : 4), 256);
     l.bpart = at;
-    at += align_up((size_t)l.tiles * 2 * F * 4, 256);
+    if (l.tiles > 1) at += align_up((size_t)l.tiles * 2 * F * 4, 256);
     l.wpart = at;
-    at += align_up((size_t)l.splits * C * 2 * F * 4, 256);
+    if (l.splits > 1) at += align_up((size_t)l.splits * C * 2 * F * 4, 256);
     l.total = at;
     return l;
 }
 
-template <typename T>
-hipError_t glu_join(const GluParams& p, const GluLayout& l, void* dw, float* dbias, hipStream_t st) {
-    const int64_t n = (int64_t)p.C * 2 * p.F;
-    k_glu_dw_join<T><<<(unsigned)((n + kJoinCols - 1) / kJoinCols), kJoinCols * 16, 0, st>>>(p.wpart, l.splits, p.C,
-                                                                                             p.F, (T*)dw);
-    if (dbias)
-        k_glu_dbias_join<<<(2 * p.F + kJoinCols - 1) / kJoinCols, kJoinCols * 64, 0, st>>>(p.bpart, l.tiles, 2 * p.F,
-                                                                                           dbias);
+template <typename T, int ACT, int TILE>
+hipError_t glu_project(const GluParams& p, bool grad, hipStream_t st) {
+    const unsigned blocks = (unsigned)(tiles_of(p.N, TILE) * tiles_of(p.F, TILE / 2));
+    if (grad)
+        k_glu_project<T, ACT, true, TILE><<<blocks, kGluThreads, 0, st>>>(p);
+    else
+        k_glu_project<T, ACT, false, TILE><<<blocks, kGluThreads, 0, st>>>(p);
     return hipGetLastError();
 }
 
-template <typename T, int ACT>
-hipError_t glu_go(const GluParams& p, bool grad, const GluLayout& l, void* dw, float* dbias, hipStream_t st) {
-    // row tiles in the first grid dimension, next to the tiles of their columns
-    const unsigned proj = (unsigned)(l.tiles * ((p.F + 63) / 64));
-    if (!grad) {
-        k_glu_project<T, ACT, false><<<proj, kGluThreads, 0, st>>>(p);
-        return hipGetLastError();
+template <typename T, int TILE>
+hipError_t glu_products(const GluParams& p, const GluLayout& l, hipStream_t st) {
+    const unsigned dx = (unsigned)(tiles_of(p.N, TILE) * tiles_of(p.C, TILE));
+    const unsigned dw = (unsigned)(tiles_of(2 * p.F, TILE) * tiles_of(p.C, TILE) * l.splits);
+    k_glu_products<T, TILE><<<dx + dw, kGluThreads, 0, st>>>(p, dx);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t glu_go(GluParams p, int act, bool grad, const GluLayout& l, float* dbias, hipStream_t st) {
+    hipError_t e = hipSuccess;
+    if (l.rows) {
+        if constexpr (sizeof(T) == 2) {
+            if (!grad) return launch_glu_rows(p, act, st);
+            e = launch_glu_rows_dx(p, act, st);
+            if (e == hipSuccess) e = launch_glu_rows_dw(p, act, l.splits, st);
+        }
+    } else if (p.N > 0) {
+        if (act == SPCONV_SILU)
+            e = l.ptile == 128 ? glu_project<T, SPCONV_SILU, 128>(p, grad, st) : glu_project<T, SPCONV_SILU, 64>(p, grad, st);
+        else
+            e = l.ptile == 128 ? glu_project<T, SPCONV_GELU, 128>(p, grad, st) : glu_project<T, SPCONV_GELU, 64>(p, grad, st);
+        if (!grad || e != hipSuccess) return e;
+        e = l.tile == 128 ? glu_products<T, 128>(p, l, st) : glu_products<T, 64>(p, l, st);
     }
-    const int ct = (p.C + kTile - 1) / kTile;
-    if (p.N > 0) {
-        k_glu_project<T, ACT, true><<<proj, kGluThreads, 0, st>>>(p);
-        k_glu_dx<T><<<(unsigned)(l.tiles * ct), kGluThreads, 0, st>>>(p);
-        k_glu_dw<T><<<dim3((2 * p.F + kTile - 1) / kTile, ct, l.splits), kGluThreads, 0, st>>>(p);
-    }
-    return glu_join<T>(p, l, dw, dbias, st);
+    if (e != hipSuccess) return e;
+    // what was not written as it is (no rows: the zeros of both)
+    const bool w = p.wpart || p.N == 0, b = dbias && (p.bpart != dbias || p.N == 0);
+    const unsigned wb = w ? (unsigned)(((int64_t)p.C * 2 * p.F + kJoinCols - 1) / kJoinCols) : 0;
+    const unsigned bb = b ? (unsigned)((2 * p.F + kJoinCols - 1) / kJoinCols) : 0;
+    if (wb + bb) k_glu_join<T><<<wb + bb, kJoinCols * 16, 0, st>>>(p, l.splits, l.tiles, dbias, wb);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -401,28 +529,21 @@ hipError_t launch_glu(const GluArgs& a, bool grad, hipStream_t stream) {
     p.dout = a.dout;
     p.h = a.out;
     p.dx = a.out;
+    p.dw = a.dw;
     if (grad) {
+        // sums of one tile or split are results already
         char* ws = (char*)a.workspace;
         p.dab = ws + l.dab;
-        p.bpart = a.dbias ? (float*)(ws + l.bpart) : nullptr;
-        p.wpart = (float*)(ws + l.wpart);
+        if (a.dbias) p.bpart = l.rows || l.tiles > 1 ? (float*)(ws + l.bpart) : a.dbias;
+        if (l.rows || l.splits > 1) p.wpart = (float*)(ws + l.wpart);
     }
     p.N = a.N;
     p.C = a.C;
     p.F = a.F;
     p.rows_per_split = l.rows_per_split;
     p.stream = a.N * (grad ? a.C : a.F) * (a.dtype == SPCONV_BF16 ? 2 : 4) > kStreamBytes;
-    if (use_rows(a.N, a.C, a.dtype)) {
-        if (!grad) return launch_glu_rows(p, a.act, stream);
-        hipError_t e = launch_glu_rows_dx(p, a.act, stream);
-        if (e == hipSuccess) e = launch_glu_rows_dw(p, a.act, l.splits, stream);
-        return e == hipSuccess ? glu_join<__bf16>(p, l, a.dw, a.dbias, stream) : e;
-    }
-    if (a.dtype == SPCONV_BF16)
-        return a.act == SPCONV_SILU ? glu_go<__bf16, SPCONV_SILU>(p, grad, l, a.dw, a.dbias, stream)
-                                    : glu_go<__bf16, SPCONV_GELU>(p, grad, l, a.dw, a.dbias, stream);
-    return a.act == SPCONV_SILU ? glu_go<float, SPCONV_SILU>(p, grad, l, a.dw, a.dbias, stream)
-                                : glu_go<float, SPCONV_GELU>(p, grad, l, a.dw, a.dbias, stream);
+    return a.dtype == SPCONV_BF16 ? glu_go<__bf16>(p, a.act, grad, l, a.dbias, stream)
+                                  : glu_go<float>(p, a.act, grad, l, a.dbias, stream);
 }
 
 }  // namespace spc

@@ -56,6 +56,12 @@ __device__ __forceinline__ void opaque(uint32_t& v) { asm volatile("" : "+v"(v))
 // Matrix instructions and LDS reads stay on their sides of this, so that the
 // next step's operands are read before this step's products, not after.
 __device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0x416); }
+__device__ __forceinline__ void store_unit(__bf16* p, bf16x8r_t v, bool stream) {
+    if (stream)
+        __builtin_nontemporal_store(v, (bf16x8r_t*)p);
+    else
+        *(bf16x8r_t*)p = v;
+}
 // Rows' loads stand under no branch: a branch between loads makes the compiler
 // wait for all of them at the first use of any.  Lanes past the end read a
 // valid place instead, and what they got is replaced where it is used.
@@ -215,7 +221,7 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p) {
                             o[e] = (__bf16)(activation<ACT>(pa[e >> 2][n][e & 3]).v * pb[e >> 2][n][e & 3]);
                         const int64_t r = r0 + 16 * n + a;
                         if (r < p.N && fl + 8 * g < fe)
-                            store_vec((bf16x8r_t*)((__bf16*)p.h + r * F + f0 + fl + 8 * g), o, p.stream);
+                            store_unit((__bf16*)p.h + r * F + f0 + fl + 8 * g, o, p.stream);
                     }
                 } else {
                     bf16x8r_t da[NT], db[NT];
@@ -261,7 +267,7 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p) {
                     for (int e = 0; e < 8; ++e) o[e] = (__bf16)dx[2 * s + (e >> 2)][n][e & 3];
                     const int64_t r = r0 + 16 * n + a;
                     const int c = 32 * s + 8 * g;
-                    if (r < p.N && c < C) store_vec((bf16x8r_t*)((__bf16*)p.dx + r * C + c), o, p.stream);
+                    if (r < p.N && c < C) store_unit((__bf16*)p.dx + r * C + c, o, p.stream);
                 }
         }
     }

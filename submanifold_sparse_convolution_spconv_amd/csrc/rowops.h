@@ -48,14 +48,6 @@ __device__ __forceinline__ typename Piece<T>::vec load_piece(const T* p, int n) 
 // be left there for the next kernel, and they would push out its inputs (half
 // of the 256 MB memory-side cache).
 constexpr int64_t kStreamBytes = 128 << 20;
-template <typename V>
-__device__ __forceinline__ void store_vec(V* p, V v, bool stream) {
-    if (stream)
-        __builtin_nontemporal_store(v, p);
-    else
-        *p = v;
-}
-
 template <typename T>
 __device__ __forceinline__ void store_piece(T* p, const float (&f)[Piece<T>::V], int n, bool stream) {
     constexpr int V = Piece<T>::V;
@@ -63,7 +55,11 @@ __device__ __forceinline__ void store_piece(T* p, const float (&f)[Piece<T>::V],
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = (T)f[i];
     if (n >= V) {
-        store_vec((typename Piece<T>::uvec*)p, (typename Piece<T>::uvec)v, stream);
+        typename Piece<T>::uvec* q = (typename Piece<T>::uvec*)p;
+        if (stream)
+            __builtin_nontemporal_store((typename Piece<T>::uvec)v, q);
+        else
+            *q = v;
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i)

@@ -128,7 +128,11 @@ __device__ __forceinline__ void store_quad(T* base, int row, int C, int c0, cons
 #pragma unroll
     for (int i = 0; i < kScanV; ++i) v[i] = (T)f[i];
     if constexpr (WHOLE) {
-        if (n > 0) store_vec((typename Quad<T>::uvec*)p, (typename Quad<T>::uvec)v, stream);
+        typename Quad<T>::uvec* q = (typename Quad<T>::uvec*)p;
+        if (n > 0 && stream)
+            __builtin_nontemporal_store((typename Quad<T>::uvec)v, q);
+        else if (n > 0)
+            *q = v;
     } else {
 #pragma unroll
         for (int i = 0; i < kScanV; ++i)
