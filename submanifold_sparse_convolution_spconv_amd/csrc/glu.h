@@ -40,9 +40,19 @@ __device__ __forceinline__ Act activation(float a) {
         const float v = a * s;
         return {v, fmaf(-s, v, s) + v};       // s (1 + a (1 - s))
     } else {
-        const float cdf = 0.5f * (1.f + erff(a * 0.70710678f));
-        const float pdf = 0.39894228f * __builtin_amdgcn_exp2f(-0.72134752f * a * a);
-        return {a * cdf, cdf + a * pdf};
+        // The normal distribution from erfc(x) = t P(t) e^(-x^2) + 1.5e-7 at
+        // most, t = 1 / (1 + 0.3275911 x) (Abramowitz and Stegun, 7.1.26); the
+        // density needs the same exponential.
+        const float x = fabsf(a) * 0.70710678f;
+        const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
+        const float e = __builtin_amdgcn_exp2f(-0.72134752f * a * a);
+        float q = fmaf(1.061405429f, t, -1.453152027f);
+        q = fmaf(q, t, 1.421413741f);
+        q = fmaf(q, t, -0.284496736f);
+        q = fmaf(q, t, 0.254829592f);
+        q *= 0.5f * t * e;
+        const float cdf = a >= 0.f ? 1.f - q : q;
+        return {a * cdf, fmaf(0.39894228f * a, e, cdf)};
     }
 }
 

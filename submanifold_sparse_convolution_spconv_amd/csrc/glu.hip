@@ -414,16 +414,16 @@ __global__ void __launch_bounds__(kJoinCols * 16) k_glu_join(GluParams p, int sp
     const bool w = blockIdx.x < w_blocks;
     const int64_t n = w ? (int64_t)p.C * 2 * F : 2 * F;
     const int64_t block = blockIdx.x - (w ? 0 : w_blocks);
-    const float t = join_column<16>(w ? p.wpart : p.bpart, w ? splits : tiles, n, block);
-    const int64_t e = block * kJoinCols + threadIdx.x;
+    const JoinVec<4> t = join_columns<16, 4>(w ? p.wpart : p.bpart, w ? splits : tiles, n, block);
+    const int64_t e = (block * kJoinCols + threadIdx.x) * 4;
     if (threadIdx.x >= kJoinCols || e >= n) return;
     if (!w) {
-        dbias[e] = t;
+        *(f32x4r_t*)(dbias + e) = f32x4r_t{t.f[0], t.f[1], t.f[2], t.f[3]};
         return;
     }
     const int64_t c = e / (2 * F);
     const int m = (int)(e % (2 * F));
-    ((T*)p.dw)[m < F ? c * F + m : (p.C + c) * F + (m - F)] = (T)t;
+    store_four((T*)p.dw + (m < F ? c * F + m : (p.C + c) * F + (m - F)), t.f);
 }
 
 // Few channels and enough rows to give every CU a block of them: glu_rows.hip.
@@ -432,7 +432,9 @@ bool use_rows(int64_t N, int C, int dtype) { return dtype == SPCONV_BF16 && C <=
 // Tiles of 128 where they fill the card (the operands are then read half as
 // often), of 64 where they would not.
 int64_t tiles_of(int64_t n, int tile) { return (n + tile - 1) / tile; }
-int project_tile(int64_t N, int F) { return tiles_of(N, 128) * tiles_of(F, 64) >= 256 ? 128 : 64; }
+// (fp32, whose matrix instructions take four times as long as their operands'
+// reads, only has the small ones.)
+int big_tile(bool fills, int dtype) { return fills && dtype == SPCONV_BF16 ? 128 : 64; }
 
 struct GluLayout {
     size_t dab, bpart, wpart, total;
@@ -452,9 +454,9 @@ GluLayout glu_layout(int64_t N, int C, int F, int dtype) {
         l.total = l.wpart + align_up((size_t)l.splits * C * 2 * F * 4, 256);
         return l;
     }
-    l.ptile = project_tile(N, F);
+    l.ptile = big_tile(tiles_of(N, 128) * tiles_of(F, 64) >= 256, dtype);
     l.tiles = tiles_of(N, l.ptile);
-    l.tile = tiles_of(N, 128) * tiles_of(C, 128) >= 192 ? 128 : 64;
+    l.tile = big_tile(tiles_of(N, 128) * tiles_of(C, 128) >= 192, dtype);
     // enough workgroups for two per CU, at least 128 rows each
     const int64_t t = tiles_of(2 * F, l.tile) * tiles_of(C, l.tile);
     const int64_t want = std::max<int64_t>(1, std::min<int64_t>((512 + t - 1) / t, N / 128));
@@ -471,21 +473,26 @@ GluLayout glu_layout(int64_t N, int C, int F, int dtype) {
     return l;
 }
 
-template <typename T, int ACT, int TILE>
-hipError_t glu_project(const GluParams& p, bool grad, hipStream_t st) {
-    const unsigned blocks = (unsigned)(tiles_of(p.N, TILE) * tiles_of(p.F, TILE / 2));
-    if (grad)
-        k_glu_project<T, ACT, true, TILE><<<blocks, kGluThreads, 0, st>>>(p);
-    else
-        k_glu_project<T, ACT, false, TILE><<<blocks, kGluThreads, 0, st>>>(p);
+template <typename T, int ACT>
+hipError_t glu_project(const GluParams& p, bool grad, const GluLayout& l, hipStream_t st) {
+    const unsigned blocks = (unsigned)(l.tiles * tiles_of(p.F, l.ptile / 2));
+    auto fn = grad ? k_glu_project<T, ACT, true, 64> : k_glu_project<T, ACT, false, 64>;
+    if constexpr (sizeof(T) == 2) {
+        if (l.ptile == 128) fn = grad ? k_glu_project<T, ACT, true, 128> : k_glu_project<T, ACT, false, 128>;
+    }
+    fn<<<blocks, kGluThreads, 0, st>>>(p);
     return hipGetLastError();
 }
 
-template <typename T, int TILE>
+template <typename T>
 hipError_t glu_products(const GluParams& p, const GluLayout& l, hipStream_t st) {
-    const unsigned dx = (unsigned)(tiles_of(p.N, TILE) * tiles_of(p.C, TILE));
-    const unsigned dw = (unsigned)(tiles_of(2 * p.F, TILE) * tiles_of(p.C, TILE) * l.splits);
-    k_glu_products<T, TILE><<<dx + dw, kGluThreads, 0, st>>>(p, dx);
+    const unsigned dx = (unsigned)(tiles_of(p.N, l.tile) * tiles_of(p.C, l.tile));
+    const unsigned dw = (unsigned)(tiles_of(2 * p.F, l.tile) * tiles_of(p.C, l.tile) * l.splits);
+    auto fn = k_glu_products<T, 64>;
+    if constexpr (sizeof(T) == 2) {
+        if (l.tile == 128) fn = k_glu_products<T, 128>;
+    }
+    fn<<<dx + dw, kGluThreads, 0, st>>>(p, dx);
     return hipGetLastError();
 }
 
@@ -499,18 +506,15 @@ hipError_t glu_go(GluParams p, int act, bool grad, const GluLayout& l, float* db
             if (e == hipSuccess) e = launch_glu_rows_dw(p, act, l.splits, st);
         }
     } else if (p.N > 0) {
-        if (act == SPCONV_SILU)
-            e = l.ptile == 128 ? glu_project<T, SPCONV_SILU, 128>(p, grad, st) : glu_project<T, SPCONV_SILU, 64>(p, grad, st);
-        else
-            e = l.ptile == 128 ? glu_project<T, SPCONV_GELU, 128>(p, grad, st) : glu_project<T, SPCONV_GELU, 64>(p, grad, st);
+        e = act == SPCONV_SILU ? glu_project<T, SPCONV_SILU>(p, grad, l, st) : glu_project<T, SPCONV_GELU>(p, grad, l, st);
         if (!grad || e != hipSuccess) return e;
-        e = l.tile == 128 ? glu_products<T, 128>(p, l, st) : glu_products<T, 64>(p, l, st);
+        e = glu_products<T>(p, l, st);
     }
     if (e != hipSuccess) return e;
     // what was not written as it is (no rows: the zeros of both)
     const bool w = p.wpart || p.N == 0, b = dbias && (p.bpart != dbias || p.N == 0);
-    const unsigned wb = w ? (unsigned)(((int64_t)p.C * 2 * p.F + kJoinCols - 1) / kJoinCols) : 0;
-    const unsigned bb = b ? (unsigned)((2 * p.F + kJoinCols - 1) / kJoinCols) : 0;
+    const unsigned wb = w ? (unsigned)tiles_of((int64_t)p.C * 2 * p.F, 4 * kJoinCols) : 0;
+    const unsigned bb = b ? (unsigned)tiles_of(2 * p.F, 4 * kJoinCols) : 0;
     if (wb + bb) k_glu_join<T><<<wb + bb, kJoinCols * 16, 0, st>>>(p, l.splits, l.tiles, dbias, wb);
     return hipGetLastError();
 }

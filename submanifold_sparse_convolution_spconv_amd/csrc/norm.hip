@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_grad(NormParams p) {
 
 __global__ void __launch_bounds__(kJoinCols * 64) k_norm_join(const float* part, int blocks, int C, float* dweight,
                                                               float* dbias) {
-    const float t = join_column<64>(part, blocks, 2 * C, blockIdx.x);
+    const float t = join_columns<64, 1>(part, blocks, 2 * C, blockIdx.x).f[0];
     const int e = blockIdx.x * kJoinCols + threadIdx.x;
     if (threadIdx.x < kJoinCols && e < 2 * C) (e < C ? dweight : dbias - C)[e] = t;
 }
