@@ -66,6 +66,11 @@ template <>
 struct Four<float> {
     typedef f32x4r_t vec;
 };
+// E (4 or 8) consecutive elements.
+template <typename T, int E>
+struct Group {
+    typedef T vec __attribute__((ext_vector_type(E)));
+};
 template <typename T>
 __device__ __forceinline__ void store_four(T* p, const float (&f)[4]) {
     typename Four<T>::vec v;

@@ -17,6 +17,7 @@
 #include "join.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace spc {
 
@@ -40,15 +41,15 @@ constexpr int kTileK = sizeof(T) == 2 ? 64 : 32;      // of the reduction per st
 // One operand tile in LDS: M outputs x BK of the reduction.  KC: the reduction
 // is contiguous in memory and in LDS ([m][k]); else the outputs are ([k][m]).
 // The pitches keep the fragment reads free of bank conflicts: 16 rows' 16-byte
-// units (KC, bf16: an odd number of units), four rows' pairs of units (bf16),
-// one word per lane (fp32).
+// units (KC, bf16: an odd number of units), four rows' four units (bf16), one
+// word per lane (fp32).
 template <typename T, bool KC, int M>
 struct Stage {
     static constexpr bool K_CONTIGUOUS = KC;
     static constexpr int BK = kTileK<T>;
     static constexpr int V = Piece<T>::V;
     static constexpr int PER = M * BK / V / kGluThreads;        // pieces per thread
-    static constexpr int PITCH = KC ? BK + V : M + 16;
+    static constexpr int PITCH = KC ? BK + V : M + (sizeof(T) == 2 ? 32 : 16);
     static constexpr int ELEMS = (KC ? M : BK) * PITCH;
     static_assert(PER >= 1 && M * BK / V % kGluThreads == 0, "whole pieces per thread");
     // piece j of this thread: output m and reduction index k of its first element
@@ -76,7 +77,7 @@ struct Operand {
     const T* at[NP];
     bool in[NP];
     int64_t pitch;       // of k, where the outputs are contiguous
-    typename Piece<T>::vec raw[S::PER];
+    typename Piece<T>::vec raw[2][S::PER];
     // place(m): the element at reduction index 0 of output m, valid where
     // inside(m); `safe`: some valid element
     template <class P, class I>
@@ -90,6 +91,7 @@ struct Operand {
         }
     }
     // pieces of the step at k; klim: the reduction's end
+    template <int SLOT>
     __device__ __forceinline__ void fetch(int64_t k, int64_t klim) {
 #pragma unroll
         for (int j = 0; j < S::PER; ++j) {
@@ -97,16 +99,17 @@ struct Operand {
             S::where(j, m, kk);
             const int o = KC ? j : 0;
             const int64_t ki = min(k + kk, klim - (KC ? S::V : 1));
-            raw[j] = *(const typename Piece<T>::vec*)(at[o] + (in[o] ? (KC ? ki : ki * pitch) : 0));
+            raw[SLOT][j] = *(const typename Piece<T>::vec*)(at[o] + (in[o] ? (KC ? ki : ki * pitch) : 0));
         }
     }
+    template <int SLOT>
     __device__ __forceinline__ void put(T* lds, int64_t k, int64_t klim) const {
 #pragma unroll
         for (int j = 0; j < S::PER; ++j) {
             int m, kk;
             S::where(j, m, kk);
             *(typename Piece<T>::vec*)(lds + (KC ? m * S::PITCH + kk : kk * S::PITCH + m)) =
-                keep(raw[j], in[KC ? j : 0] && k + kk < klim);
+                keep(raw[SLOT][j], in[KC ? j : 0] && k + kk < klim);
         }
     }
 };
@@ -119,15 +122,17 @@ template <>
 struct Frag<__bf16> {
     static constexpr int K = 32;
     typedef bf16x8r_t type;
-    template <class S>
+    // STEP: outputs between one piece of four and the next (4: 16 outputs in
+    // a row; 8: with m0 and m0 + 4, 32 in a row, eight of them per lane)
+    template <class S, int STEP>
     static __device__ __forceinline__ type read(const __bf16* lds, int m0, int k0) {
         const int a = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
         if constexpr (S::K_CONTIGUOUS) {
             return *(const type*)(lds + (m0 + a) * S::PITCH + k0 + 8 * g);
         } else {
-            // lane a of group g addresses row 8 g (+ 4) + a / 4, columns
-            // 4 (a % 4) ..; it receives column a of the four rows
-            const __bf16* p = lds + (k0 + 8 * g + (a >> 2)) * S::PITCH + m0 + 4 * (a & 3);
+            // lane a of group g addresses row 8 g (+ 4) + a / 4, piece a % 4;
+            // it receives output a of the four rows
+            const __bf16* p = lds + (k0 + 8 * g + (a >> 2)) * S::PITCH + m0 + STEP * (a & 3);
             const bf16x4r_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4r_t*)p);
             const bf16x4r_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4r_t*)(p + 4 * S::PITCH));
             return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -141,10 +146,11 @@ template <>
 struct Frag<float> {
     static constexpr int K = 4;
     typedef float type;
-    template <class S>
+    template <class S, int STEP>
     static __device__ __forceinline__ type read(const float* lds, int m0, int k0) {
         const int a = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
-        return S::K_CONTIGUOUS ? lds[(m0 + a) * S::PITCH + k0 + g] : lds[(k0 + g) * S::PITCH + m0 + a];
+        return S::K_CONTIGUOUS ? lds[(m0 + a) * S::PITCH + k0 + g]
+                               : lds[(k0 + g) * S::PITCH + m0 + STEP * (a >> 2) + (a & 3)];
     }
     static __device__ __forceinline__ f32x4r_t mma(type a, type b, f32x4r_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
@@ -162,12 +168,13 @@ template <typename T, int TILE>
 constexpr size_t kMostBytes = std::max(kProductBytes<T, false, true, TILE>,
                                        std::max(kProductBytes<T, true, true, TILE>, kProductBytes<T, false, false, TILE>));
 
-// acc += A B over the reduction [k0, k1).  The next step's pieces are loaded
-// while this step's are multiplied; two buffers, one barrier per step.  m_at /
+// acc += A B over the reduction [k0, k1).  The pieces of the next two steps
+// are on their way while this step's are multiplied; two buffers, one barrier
+// per step.  m_at /
 // n_at: the first output of this wave's i-th / j-th block.  fp32 adds its
 // products in runs of 512 of the reduction, so that a long sum is not one
 // chain.
-template <typename T, bool AKC, bool BKC, int TILE, class MA, class NA>
+template <typename T, bool AKC, bool BKC, int TILE, int ASTEP = 4, class MA, class NA>
 __device__ __forceinline__ void tile_product(f32x4r_t (&acc)[kBlocks<TILE>][kBlocks<TILE>], Operand<T, AKC, TILE>& A,
                                              Operand<T, BKC, TILE>& B, int64_t k0, int64_t k1, char* smem, MA m_at,
                                              NA n_at) {
@@ -183,24 +190,22 @@ __device__ __forceinline__ void tile_product(f32x4r_t (&acc)[kBlocks<TILE>][kBlo
 #pragma unroll
             for (int j = 0; j < NB; ++j) run[sizeof(T) == 4 ? i : 0][j] = f32x4r_t{0.f, 0.f, 0.f, 0.f};
     }
-    A.fetch(k0, k1);
-    B.fetch(k0, k1);
-    int b = 0;
-    for (int64_t k = k0; k < k1; k += BK, b ^= 1) {
-        A.put(la + b * SA::ELEMS, k, k1);
-        B.put(lb + b * SB::ELEMS, k, k1);
+    auto step = [&](auto slot, int64_t k) {
+        constexpr int SLOT = decltype(slot)::value;
+        A.template put<SLOT>(la + SLOT * SA::ELEMS, k, k1);
+        B.template put<SLOT>(lb + SLOT * SB::ELEMS, k, k1);
         __syncthreads();
-        A.fetch(k + BK, k1);
-        B.fetch(k + BK, k1);
-        const T* pa = la + b * SA::ELEMS;
-        const T* pb = lb + b * SB::ELEMS;
+        A.template fetch<SLOT>(k + 2 * BK, k1);
+        B.template fetch<SLOT>(k + 2 * BK, k1);
+        const T* pa = la + SLOT * SA::ELEMS;
+        const T* pb = lb + SLOT * SB::ELEMS;
 #pragma unroll
         for (int s = 0; s < BK; s += Frag<T>::K) {
             typename Frag<T>::type fa[NB], fb[NB];
 #pragma unroll
-            for (int i = 0; i < NB; ++i) fa[i] = Frag<T>::template read<SA>(pa, m_at(i), s);
+            for (int i = 0; i < NB; ++i) fa[i] = Frag<T>::template read<SA, ASTEP>(pa, m_at(i), s);
 #pragma unroll
-            for (int j = 0; j < NB; ++j) fb[j] = Frag<T>::template read<SB>(pb, n_at(j), s);
+            for (int j = 0; j < NB; ++j) fb[j] = Frag<T>::template read<SB, 4>(pb, n_at(j), s);
 #pragma unroll
             for (int i = 0; i < NB; ++i)
 #pragma unroll
@@ -222,6 +227,14 @@ __device__ __forceinline__ void tile_product(f32x4r_t (&acc)[kBlocks<TILE>][kBlo
                     }
             }
         }
+    };
+    A.template fetch<0>(k0, k1);
+    B.template fetch<0>(k0, k1);
+    A.template fetch<1>(k0 + BK, k1);
+    B.template fetch<1>(k0 + BK, k1);
+    for (int64_t k = k0; k < k1; k += 2 * BK) {
+        step(std::integral_constant<int, 0>{}, k);
+        if (k + BK < k1) step(std::integral_constant<int, 1>{}, k + BK);
     }
     __syncthreads();        // the buffers may be used again
 }
@@ -250,59 +263,85 @@ __global__ void __launch_bounds__(kGluThreads, 2) k_glu_project(GluParams p) {
     Operand<T, false, TILE> A([&](int m) { return w + (int64_t)(m / FT) * C * F + f0 + m % FT; },
                               [&](int m) { return f0 + m % FT < F; }, w, F);
     Operand<T, true, TILE> B([&](int n) { return x + (r0 + n) * C; }, [&](int n) { return r0 + n < p.N; }, x, 0);
+    // A lane's features: E in a row (of the wave's FT / 2: 4 from each block, 8
+    // from each pair of blocks).
+    constexpr int PAIR = NB / 2 >= 2 ? 2 : 1, E = 4 * PAIR, NP = NB / 2 / PAIR;
+    typedef typename Group<T, E>::vec group;
     f32x4r_t acc[NB][NB];      // gates in the first half of i, values in the second
-    clear_blocks(acc);
-    tile_product<T, false, true, TILE>(
-        acc, A, B, 0, C, smem, [&](int i) { return FT * (2 * i / NB) + FT / 2 * wm + 16 * (i % (NB / 2)); },
-        [&](int j) { return TILE / 2 * wn + 16 * j; });
+    int f[NP];
+    group dh[GRAD ? NP : 1][NB];
 #pragma unroll
-    for (int i = 0; i < NB / 2; ++i) {
-        const int fl = FT / 2 * wm + 16 * i + 4 * g, f = f0 + fl;
-        f32x4r_t ba = {0.f, 0.f, 0.f, 0.f}, bb = ba;
-        if (p.bias && f < F) {
+    for (int i = 0; i < NP; ++i) {
+        f[i] = f0 + FT / 2 * wm + 16 * PAIR * i + E * g;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                ba[e] = p.bias[f + e];
-                bb[e] = p.bias[F + f + e];
+        for (int q = 0; q < PAIR; ++q) {
+            const int at = f[i] < F ? f[i] + 4 * q : 0;
+            f32x4r_t ba = {0.f, 0.f, 0.f, 0.f}, bb = ba;
+            if (p.bias) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    ba[e] = p.bias[at + e];
+                    bb[e] = p.bias[F + at + e];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                acc[PAIR * i + q][j] = ba;
+                acc[NB / 2 + PAIR * i + q][j] = bb;
             }
         }
-        f32x4r_t sa = {0.f, 0.f, 0.f, 0.f}, sb = sa;
-        typename Four<T>::vec dh[NB];
         if constexpr (GRAD) {
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
                 const int64_t r = min(r0 + TILE / 2 * wn + 16 * j + a, p.N - 1);
-                dh[j] = *(const typename Four<T>::vec*)((const T*)p.dout + r * F + (f < F ? f : 0));
+                dh[i][j] = *(const group*)((const T*)p.dout + r * F + (f[i] < F ? f[i] : 0));
             }
         }
+    }
+    tile_product<T, false, true, TILE, 4 * PAIR>(
+        acc, A, B, 0, C, smem,
+        [&](int i) {
+            const int k = i % (NB / 2);
+            return FT * (2 * i / NB) + FT / 2 * wm + 16 * PAIR * (k / PAIR) + 4 * (k % PAIR);
+        },
+        [&](int j) { return TILE / 2 * wn + 16 * j; });
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        float sa[E], sb[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) sa[e] = sb[e] = 0.f;
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             const int64_t r = r0 + TILE / 2 * wn + 16 * j + a;
-            if (r >= p.N || f >= F) continue;
-            const f32x4r_t va = acc[i][j] + ba, vb = acc[i + NB / 2][j] + bb;
-            float o[4], q[4];
-            if constexpr (!GRAD) {
+            if (r >= p.N || f[i] >= F) continue;
+            group o, q;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[e] = activation<ACT>(va[e]).v * vb[e];
-                store_four((T*)p.h + r * F + f, o);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const Act t = activation<ACT>(va[e]);
-                    o[e] = (float)dh[j][e] * vb[e] * t.d;
-                    q[e] = (float)dh[j][e] * t.v;
-                    sa[e] += o[e];
-                    sb[e] += q[e];
+            for (int e = 0; e < E; ++e) {
+                const float va = acc[PAIR * i + e / 4][j][e % 4], vb = acc[NB / 2 + PAIR * i + e / 4][j][e % 4];
+                const Act t = activation<ACT>(va);
+                if constexpr (!GRAD) {
+                    o[e] = (T)(t.v * vb);
+                } else {
+                    const float d = (float)dh[i][j][e], u = d * vb * t.d, v = d * t.v;
+                    sa[e] += u;
+                    sb[e] += v;
+                    o[e] = (T)u;
+                    q[e] = (T)v;
                 }
-                T* d = (T*)p.dab + r * 2 * F + f;
-                store_four(d, o);
-                store_four(d + F, q);
+            }
+            if constexpr (!GRAD) {
+                *(group*)((T*)p.h + r * F + f[i]) = o;
+            } else {
+                T* d = (T*)p.dab + r * 2 * F + f[i];
+                *(group*)d = o;
+                *(group*)(d + F) = q;
             }
         }
         if constexpr (GRAD) {
             if (p.bpart) {
+                const int fl = f[i] - f0;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < E; ++e) {
                     const float u = group_sum<16>(sa[e]), v = group_sum<16>(sb[e]);
                     if (a == 0) {
                         bsum[wn][0][fl + e] = u;
@@ -315,9 +354,9 @@ __global__ void __launch_bounds__(kGluThreads, 2) k_glu_project(GluParams p) {
     if constexpr (GRAD) {
         if (!p.bpart) return;
         __syncthreads();
-        const int s = threadIdx.x / FT, f = threadIdx.x % FT;
-        if (threadIdx.x < 2 * FT && f0 + f < F)
-            p.bpart[(tile * 2 + s) * F + f0 + f] = bsum[0][s][f] + bsum[1][s][f];
+        const int s = threadIdx.x / FT, fl = threadIdx.x % FT;
+        if (threadIdx.x < 2 * FT && f0 + fl < F)
+            p.bpart[(tile * 2 + s) * F + f0 + fl] = bsum[0][s][fl] + bsum[1][s][fl];
     }
 }
 
