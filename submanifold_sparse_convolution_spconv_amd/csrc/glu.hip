@@ -65,51 +65,70 @@ struct Stage {
     }
 };
 
-// One operand of a product on its way to LDS: pointers of this thread's pieces
-// (KC: one per piece, its k the same for all; else one, a multiple of k apart),
-// and the pieces of the next step in registers.  Loads stand under no branch
-// (a branch between loads makes the compiler wait for all of them at the first
-// use): pieces outside read a valid place and become 0 on the way to LDS.
+// One operand of a product on its way to LDS: this thread's pieces of the next
+// two steps in registers.  An address is the tile's place at the step (the same
+// for the workgroup) and a 32-bit offset of the thread, so a step costs no
+// address arithmetic.  Loads stand under no branch that differs between lanes
+// (the compiler would wait for all of them at the first use): pieces outside
+// read a valid place and become 0 on the way to LDS, on tiles and steps that
+// have any.
 template <typename T, bool KC, int M>
 struct Operand {
     using S = Stage<T, KC, M>;
-    static constexpr int NP = KC ? S::PER : 1;
-    const T* at[NP];
+    static constexpr int NP = KC ? S::PER : 1;                  // outputs per thread
+    static constexpr int KSTEP = kGluThreads / (M / S::V);      // !KC: k from piece to piece
+    const T* base;        // output 0 at reduction index 0
+    int64_t pitch;        // of k, where the outputs are contiguous
+    bool full;            // every output of the tile is inside
+    int kk;               // k of the first piece
+    uint32_t off[NP];     // of the outputs; 0 where outside
     bool in[NP];
-    int64_t pitch;       // of k, where the outputs are contiguous
     typename Piece<T>::vec raw[2][S::PER];
-    // place(m): the element at reduction index 0 of output m, valid where
-    // inside(m); `safe`: some valid element
-    template <class P, class I>
-    __device__ __forceinline__ Operand(P place, I inside, const T* safe, int64_t k_pitch) : pitch(k_pitch) {
+    // offset(m): elements from output 0 to output m, valid where inside(m)
+    template <class O, class I>
+    __device__ __forceinline__ Operand(const T* base, O offset, I inside, bool full, int64_t k_pitch)
+        : base(base), pitch(k_pitch), full(full) {
+        int m;
 #pragma unroll
-        for (int j = 0; j < NP; ++j) {
-            int m, k;
-            S::where(j, m, k);
+        for (int j = NP - 1; j >= 0; --j) {
+            S::where(j, m, kk);
             in[j] = inside(m);
-            at[j] = in[j] ? place(m) : safe;
+            off[j] = in[j] ? offset(m) : 0;
         }
     }
     // pieces of the step at k; klim: the reduction's end
     template <int SLOT>
     __device__ __forceinline__ void fetch(int64_t k, int64_t klim) {
+        if (k >= klim) return;
+        const bool tail = k + S::BK > klim;
 #pragma unroll
         for (int j = 0; j < S::PER; ++j) {
-            int m, kk;
-            S::where(j, m, kk);
-            const int o = KC ? j : 0;
-            const int64_t ki = min(k + kk, klim - (KC ? S::V : 1));
-            raw[SLOT][j] = *(const typename Piece<T>::vec*)(at[o] + (in[o] ? (KC ? ki : ki * pitch) : 0));
+            const T* p;
+            if constexpr (KC) {
+                const int kc = tail ? min(kk, (int)(klim - k) - S::V) : kk;
+                p = (base + k) + (off[j] + (uint32_t)kc);
+            } else {
+                const int last = (int)(klim - k) - 1, kj = kk + KSTEP * j;
+                if (tail)
+                    p = (base + k * pitch) + (off[0] + (uint32_t)min(kj, last) * (uint32_t)pitch);
+                else
+                    p = (base + (k + KSTEP * j) * pitch) + (off[0] + (uint32_t)kk * (uint32_t)pitch);
+            }
+            raw[SLOT][j] = *(const typename Piece<T>::vec*)p;
         }
     }
     template <int SLOT>
     __device__ __forceinline__ void put(T* lds, int64_t k, int64_t klim) const {
+        const bool all = full && k + S::BK <= klim;
 #pragma unroll
         for (int j = 0; j < S::PER; ++j) {
-            int m, kk;
-            S::where(j, m, kk);
-            *(typename Piece<T>::vec*)(lds + (KC ? m * S::PITCH + kk : kk * S::PITCH + m)) =
-                keep(raw[SLOT][j], in[KC ? j : 0] && k + kk < klim);
+            int m, kj;
+            S::where(j, m, kj);
+            T* p = lds + (KC ? m * S::PITCH + kj : kj * S::PITCH + m);
+            if (all)
+                *(typename Piece<T>::vec*)p = raw[SLOT][j];
+            else
+                *(typename Piece<T>::vec*)p = keep(raw[SLOT][j], in[KC ? j : 0] && k + kj < klim);
         }
     }
 };
@@ -260,9 +279,10 @@ __global__ void __launch_bounds__(kGluThreads, 2) k_glu_project(GluParams p) {
     const int64_t tile = blockIdx.x / ft, r0 = tile * TILE;
     const T* x = (const T*)p.x;
     const T* w = (const T*)p.w;
-    Operand<T, false, TILE> A([&](int m) { return w + (int64_t)(m / FT) * C * F + f0 + m % FT; },
-                              [&](int m) { return f0 + m % FT < F; }, w, F);
-    Operand<T, true, TILE> B([&](int n) { return x + (r0 + n) * C; }, [&](int n) { return r0 + n < p.N; }, x, 0);
+    Operand<T, false, TILE> A(w + f0, [&](int m) { return (uint32_t)(m / FT) * C * F + m % FT; },
+                              [&](int m) { return f0 + m % FT < F; }, f0 + FT <= F, F);
+    Operand<T, true, TILE> B(x + r0 * C, [&](int n) { return (uint32_t)n * C; },
+                             [&](int n) { return r0 + n < p.N; }, r0 + TILE <= p.N, 0);
     // A lane's features: E in a row (of the wave's FT / 2: 4 from each block, 8
     // from each pair of blocks).
     constexpr int PAIR = NB / 2 >= 2 ? 2 : 1, E = 4 * PAIR, NP = NB / 2 / PAIR;
@@ -373,12 +393,10 @@ __device__ __forceinline__ void glu_dx_tile(const GluParams& p, int64_t block, c
     clear_blocks(acc);
 #pragma unroll 1
     for (int s = 0; s < 2; ++s) {
-        const T* w = (const T*)p.w + (int64_t)s * C * F;
-        const T* dab = (const T*)p.dab + s * F;
-        Operand<T, true, TILE> A([&](int m) { return w + (int64_t)(c0 + m) * F; }, [&](int m) { return c0 + m < C; }, w,
-                                 0);
-        Operand<T, true, TILE> B([&](int n) { return dab + (r0 + n) * 2 * F; }, [&](int n) { return r0 + n < p.N; },
-                                 dab, 0);
+        Operand<T, true, TILE> A((const T*)p.w + ((int64_t)s * C + c0) * F, [&](int m) { return (uint32_t)m * F; },
+                                 [&](int m) { return c0 + m < C; }, c0 + TILE <= C, 0);
+        Operand<T, true, TILE> B((const T*)p.dab + r0 * 2 * F + s * F, [&](int n) { return (uint32_t)n * 2 * F; },
+                                 [&](int n) { return r0 + n < p.N; }, r0 + TILE <= p.N, 0);
         tile_product<T, true, true, TILE>(acc, A, B, 0, F, smem, [&](int i) { return TILE / 2 * wm + 16 * i; },
                                           [&](int j) { return TILE / 2 * wn + 16 * j; });
     }
@@ -407,10 +425,10 @@ __device__ __forceinline__ void glu_dw_tile(const GluParams& p, int64_t block, c
     const int m0 = (int)(block % mt) * TILE, c0 = (int)(block / mt % ct) * TILE;
     const int64_t split = block / mt / ct;
     const int64_t k0 = split * p.rows_per_split, k1 = min(p.N, k0 + p.rows_per_split);
-    const T* x = (const T*)p.x;
-    const T* dab = (const T*)p.dab;
-    Operand<T, false, TILE> A([&](int m) { return dab + m0 + m; }, [&](int m) { return m0 + m < F2; }, dab, F2);
-    Operand<T, false, TILE> B([&](int n) { return x + c0 + n; }, [&](int n) { return c0 + n < C; }, x, C);
+    Operand<T, false, TILE> A((const T*)p.dab + m0, [&](int m) { return (uint32_t)m; },
+                              [&](int m) { return m0 + m < F2; }, m0 + TILE <= F2, F2);
+    Operand<T, false, TILE> B((const T*)p.x + c0, [&](int n) { return (uint32_t)n; },
+                              [&](int n) { return c0 + n < C; }, c0 + TILE <= C, C);
     f32x4r_t acc[NB][NB];
     clear_blocks(acc);
     tile_product<T, false, false, TILE>(acc, A, B, k0, k1, smem, [&](int i) { return TILE / 2 * wm + 16 * i; },
