@@ -23,7 +23,15 @@ namespace spc {
 
 namespace {
 
-constexpr int kGluThreads = 256;      // four waves, two by two over a tile
+// Tiles of TILE x TILE outputs: two waves along the first operand, WN along the
+// second; a wave holds NM x NN blocks of 16 x 16.  Eight waves share the large
+// tile rather than four: with half the accumulators each, four fit on a SIMD,
+// and short reductions spend less of their time waiting.
+template <int TILE>
+struct Shape {
+    static constexpr int WN = TILE / 32, THREADS = 128 * WN;
+    static constexpr int NM = TILE / 32, NN = TILE / 16 / WN;
+};
 
 template <typename V>
 __device__ __forceinline__ V keep(V v, bool in) {
@@ -48,13 +56,14 @@ struct Stage {
     static constexpr bool K_CONTIGUOUS = KC;
     static constexpr int BK = kTileK<T>;
     static constexpr int V = Piece<T>::V;
-    static constexpr int PER = M * BK / V / kGluThreads;        // pieces per thread
+    static constexpr int THREADS = Shape<M>::THREADS;
+    static constexpr int PER = M * BK / V / THREADS;             // pieces per thread
     static constexpr int PITCH = KC ? BK + V : M + (sizeof(T) == 2 ? 32 : 16);
     static constexpr int ELEMS = (KC ? M : BK) * PITCH;
-    static_assert(PER >= 1 && M * BK / V % kGluThreads == 0, "whole pieces per thread");
+    static_assert(PER >= 1 && M * BK / V % THREADS == 0, "whole pieces per thread");
     // piece j of this thread: output m and reduction index k of its first element
     static __device__ __forceinline__ void where(int j, int& m, int& k) {
-        const int p = threadIdx.x + kGluThreads * j;
+        const int p = threadIdx.x + THREADS * j;
         if constexpr (KC) {
             m = p / (BK / V);
             k = p % (BK / V) * V;
@@ -76,7 +85,7 @@ template <typename T, bool KC, int M>
 struct Operand {
     using S = Stage<T, KC, M>;
     static constexpr int NP = KC ? S::PER : 1;                  // outputs per thread
-    static constexpr int KSTEP = kGluThreads / (M / S::V);      // !KC: k from piece to piece
+    static constexpr int KSTEP = S::THREADS / (M / S::V);      // !KC: k from piece to piece
     const T* base;        // output 0 at reduction index 0
     int64_t pitch;        // of k, where the outputs are contiguous
     bool full;            // every output of the tile is inside
@@ -176,10 +185,6 @@ struct Frag<float> {
     }
 };
 
-// Tiles of TILE x TILE outputs; a wave holds NB x NB blocks of 16 x 16.
-template <int TILE>
-constexpr int kBlocks = TILE / 32;
-
 // LDS of a product: two buffers of both operands.
 template <typename T, bool AKC, bool BKC, int TILE>
 constexpr size_t kProductBytes = 2 * sizeof(T) * (Stage<T, AKC, TILE>::ELEMS + Stage<T, BKC, TILE>::ELEMS);
@@ -194,20 +199,20 @@ constexpr size_t kMostBytes = std::max(kProductBytes<T, false, true, TILE>,
 // products in runs of 512 of the reduction, so that a long sum is not one
 // chain.
 template <typename T, bool AKC, bool BKC, int TILE, int ASTEP = 4, class MA, class NA>
-__device__ __forceinline__ void tile_product(f32x4r_t (&acc)[kBlocks<TILE>][kBlocks<TILE>], Operand<T, AKC, TILE>& A,
+__device__ __forceinline__ void tile_product(f32x4r_t (&acc)[Shape<TILE>::NM][Shape<TILE>::NN], Operand<T, AKC, TILE>& A,
                                              Operand<T, BKC, TILE>& B, int64_t k0, int64_t k1, char* smem, MA m_at,
                                              NA n_at) {
     using SA = Stage<T, AKC, TILE>;
     using SB = Stage<T, BKC, TILE>;
-    constexpr int BK = kTileK<T>, NB = kBlocks<TILE>;
+    constexpr int BK = kTileK<T>, NM = Shape<TILE>::NM, NN = Shape<TILE>::NN;
     T* la = (T*)smem;
     T* lb = la + 2 * SA::ELEMS;
-    f32x4r_t run[sizeof(T) == 4 ? NB : 1][NB];
+    f32x4r_t run[sizeof(T) == 4 ? NM : 1][NN];
     if (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
+        for (int i = 0; i < NM; ++i)
 #pragma unroll
-            for (int j = 0; j < NB; ++j) run[sizeof(T) == 4 ? i : 0][j] = f32x4r_t{0.f, 0.f, 0.f, 0.f};
+            for (int j = 0; j < NN; ++j) run[sizeof(T) == 4 ? i : 0][j] = f32x4r_t{0.f, 0.f, 0.f, 0.f};
     }
     auto step = [&](auto slot, int64_t k) {
         constexpr int SLOT = decltype(slot)::value;
@@ -220,15 +225,15 @@ __device__ __forceinline__ void tile_product(f32x4r_t (&acc)[kBlocks<TILE>][kBlo
         const T* pb = lb + SLOT * SB::ELEMS;
 #pragma unroll
         for (int s = 0; s < BK; s += Frag<T>::K) {
-            typename Frag<T>::type fa[NB], fb[NB];
+            typename Frag<T>::type fa[NM], fb[NN];
 #pragma unroll
-            for (int i = 0; i < NB; ++i) fa[i] = Frag<T>::template read<SA, ASTEP>(pa, m_at(i), s);
+            for (int i = 0; i < NM; ++i) fa[i] = Frag<T>::template read<SA, ASTEP>(pa, m_at(i), s);
 #pragma unroll
-            for (int j = 0; j < NB; ++j) fb[j] = Frag<T>::template read<SB, 4>(pb, n_at(j), s);
+            for (int j = 0; j < NN; ++j) fb[j] = Frag<T>::template read<SB, 4>(pb, n_at(j), s);
 #pragma unroll
-            for (int i = 0; i < NB; ++i)
+            for (int i = 0; i < NM; ++i)
 #pragma unroll
-                for (int j = 0; j < NB; ++j) {
+                for (int j = 0; j < NN; ++j) {
                     if constexpr (sizeof(T) == 4)
                         run[i][j] = Frag<T>::mma(fa[i], fb[j], run[i][j]);
                     else
@@ -238,9 +243,9 @@ __device__ __forceinline__ void tile_product(f32x4r_t (&acc)[kBlocks<TILE>][kBlo
         if constexpr (sizeof(T) == 4) {
             if (((k - k0) & 511) == 512 - BK || k + BK >= k1) {
 #pragma unroll
-                for (int i = 0; i < NB; ++i)
+                for (int i = 0; i < NM; ++i)
 #pragma unroll
-                    for (int j = 0; j < NB; ++j) {
+                    for (int j = 0; j < NN; ++j) {
                         acc[i][j] += run[i][j];
                         run[i][j] = f32x4r_t{0.f, 0.f, 0.f, 0.f};
                     }
@@ -257,21 +262,21 @@ __device__ __forceinline__ void tile_product(f32x4r_t (&acc)[kBlocks<TILE>][kBlo
     }
     __syncthreads();        // the buffers may be used again
 }
-template <int NB>
-__device__ __forceinline__ void clear_blocks(f32x4r_t (&acc)[NB][NB]) {
+template <int NM, int NN>
+__device__ __forceinline__ void clear_blocks(f32x4r_t (&acc)[NM][NN]) {
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
+    for (int i = 0; i < NM; ++i)
 #pragma unroll
-        for (int j = 0; j < NB; ++j) acc[i][j] = f32x4r_t{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < NN; ++j) acc[i][j] = f32x4r_t{0.f, 0.f, 0.f, 0.f};
 }
 
 // TILE rows x TILE / 2 hidden features, both projections: h, or (GRAD) da and
 // db with their sums over the tile's rows.
 template <typename T, int ACT, bool GRAD, int TILE>
-__global__ void __launch_bounds__(kGluThreads, 2) k_glu_project(GluParams p) {
-    constexpr int NB = kBlocks<TILE>, FT = TILE / 2;
+__global__ void __launch_bounds__(Shape<TILE>::THREADS, 4) k_glu_project(GluParams p) {
+    constexpr int NM = Shape<TILE>::NM, NN = Shape<TILE>::NN, WN = Shape<TILE>::WN, FT = TILE / 2;
     __shared__ __align__(16) char smem[kProductBytes<T, false, true, TILE>];
-    __shared__ float bsum[2][2][FT];
+    __shared__ float bsum[WN][2][FT];
     const int wave = threadIdx.x >> 6, wm = wave & 1, wn = wave >> 1;
     const int a = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
     const int C = p.C, F = p.F;
@@ -285,11 +290,11 @@ __global__ void __launch_bounds__(kGluThreads, 2) k_glu_project(GluParams p) {
                              [&](int n) { return r0 + n < p.N; }, r0 + TILE <= p.N, 0);
     // A lane's features: E in a row (of the wave's FT / 2: 4 from each block, 8
     // from each pair of blocks).
-    constexpr int PAIR = NB / 2 >= 2 ? 2 : 1, E = 4 * PAIR, NP = NB / 2 / PAIR;
+    constexpr int PAIR = NM / 2 >= 2 ? 2 : 1, E = 4 * PAIR, NP = NM / 2 / PAIR;
     typedef typename Group<T, E>::vec group;
-    f32x4r_t acc[NB][NB];      // gates in the first half of i, values in the second
+    f32x4r_t acc[NM][NN];      // gates in the first half of i, values in the second
     int f[NP];
-    group dh[GRAD ? NP : 1][NB];
+    group dh[GRAD ? NP : 1][NN];
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         f[i] = f0 + FT / 2 * wm + 16 * PAIR * i + E * g;
@@ -305,15 +310,15 @@ __global__ void __launch_bounds__(kGluThreads, 2) k_glu_project(GluParams p) {
                 }
             }
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
+            for (int j = 0; j < NN; ++j) {
                 acc[PAIR * i + q][j] = ba;
-                acc[NB / 2 + PAIR * i + q][j] = bb;
+                acc[NM / 2 + PAIR * i + q][j] = bb;
             }
         }
         if constexpr (GRAD) {
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                const int64_t r = min(r0 + TILE / 2 * wn + 16 * j + a, p.N - 1);
+            for (int j = 0; j < NN; ++j) {
+                const int64_t r = min(r0 + 16 * NN * wn + 16 * j + a, p.N - 1);
                 dh[i][j] = *(const group*)((const T*)p.dout + r * F + (f[i] < F ? f[i] : 0));
             }
         }
@@ -321,23 +326,23 @@ __global__ void __launch_bounds__(kGluThreads, 2) k_glu_project(GluParams p) {
     tile_product<T, false, true, TILE, 4 * PAIR>(
         acc, A, B, 0, C, smem,
         [&](int i) {
-            const int k = i % (NB / 2);
-            return FT * (2 * i / NB) + FT / 2 * wm + 16 * PAIR * (k / PAIR) + 4 * (k % PAIR);
+            const int k = i % (NM / 2);
+            return FT * (2 * i / NM) + FT / 2 * wm + 16 * PAIR * (k / PAIR) + 4 * (k % PAIR);
         },
-        [&](int j) { return TILE / 2 * wn + 16 * j; });
+        [&](int j) { return 16 * NN * wn + 16 * j; });
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         float sa[E], sb[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) sa[e] = sb[e] = 0.f;
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-            const int64_t r = r0 + TILE / 2 * wn + 16 * j + a;
+        for (int j = 0; j < NN; ++j) {
+            const int64_t r = r0 + 16 * NN * wn + 16 * j + a;
             if (r >= p.N || f[i] >= F) continue;
             group o, q;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const float va = acc[PAIR * i + e / 4][j][e % 4], vb = acc[NB / 2 + PAIR * i + e / 4][j][e % 4];
+                const float va = acc[PAIR * i + e / 4][j][e % 4], vb = acc[NM / 2 + PAIR * i + e / 4][j][e % 4];
                 const Act t = activation<ACT>(va);
                 if constexpr (!GRAD) {
                     o[e] = (T)(t.v * vb);
@@ -375,21 +380,25 @@ __global__ void __launch_bounds__(kGluThreads, 2) k_glu_project(GluParams p) {
         if (!p.bpart) return;
         __syncthreads();
         const int s = threadIdx.x / FT, fl = threadIdx.x % FT;
-        if (threadIdx.x < 2 * FT && f0 + fl < F)
-            p.bpart[(tile * 2 + s) * F + f0 + fl] = bsum[0][s][fl] + bsum[1][s][fl];
+        if (threadIdx.x < 2 * FT && f0 + fl < F) {
+            float t = 0.f;
+#pragma unroll
+            for (int k = 0; k < WN; ++k) t += bsum[k][s][fl];
+            p.bpart[(tile * 2 + s) * F + f0 + fl] = t;
+        }
     }
 }
 
 // dx: TILE rows x TILE channels, reduced over both halves of dab.
 template <typename T, int TILE>
 __device__ __forceinline__ void glu_dx_tile(const GluParams& p, int64_t block, char* smem) {
-    constexpr int NB = kBlocks<TILE>;
+    constexpr int NM = Shape<TILE>::NM, NN = Shape<TILE>::NN;
     const int wave = threadIdx.x >> 6, wm = wave & 1, wn = wave >> 1;
     const int a = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
     const int C = p.C, F = p.F;
     const int ct = (C + TILE - 1) / TILE, c0 = (int)(block % ct) * TILE;
     const int64_t r0 = block / ct * TILE;
-    f32x4r_t acc[NB][NB];
+    f32x4r_t acc[NM][NN];
     clear_blocks(acc);
 #pragma unroll 1
     for (int s = 0; s < 2; ++s) {
@@ -397,15 +406,15 @@ __device__ __forceinline__ void glu_dx_tile(const GluParams& p, int64_t block, c
                                  [&](int m) { return c0 + m < C; }, c0 + TILE <= C, 0);
         Operand<T, true, TILE> B((const T*)p.dab + r0 * 2 * F + s * F, [&](int n) { return (uint32_t)n * 2 * F; },
                                  [&](int n) { return r0 + n < p.N; }, r0 + TILE <= p.N, 0);
-        tile_product<T, true, true, TILE>(acc, A, B, 0, F, smem, [&](int i) { return TILE / 2 * wm + 16 * i; },
-                                          [&](int j) { return TILE / 2 * wn + 16 * j; });
+        tile_product<T, true, true, TILE>(acc, A, B, 0, F, smem, [&](int i) { return 16 * NM * wm + 16 * i; },
+                                          [&](int j) { return 16 * NN * wn + 16 * j; });
     }
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-        const int c = c0 + TILE / 2 * wm + 16 * i + 4 * g;
+    for (int i = 0; i < NM; ++i) {
+        const int c = c0 + 16 * NM * wm + 16 * i + 4 * g;
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-            const int64_t r = r0 + TILE / 2 * wn + 16 * j + a;
+        for (int j = 0; j < NN; ++j) {
+            const int64_t r = r0 + 16 * NN * wn + 16 * j + a;
             if (r >= p.N || c >= C) continue;
             const float o[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
             store_four((T*)p.dx + r * C + c, o);
@@ -417,7 +426,7 @@ __device__ __forceinline__ void glu_dx_tile(const GluParams& p, int64_t block, c
 // partial sum, or (one split) as it is.
 template <typename T, int TILE>
 __device__ __forceinline__ void glu_dw_tile(const GluParams& p, int64_t block, char* smem) {
-    constexpr int NB = kBlocks<TILE>;
+    constexpr int NM = Shape<TILE>::NM, NN = Shape<TILE>::NN;
     const int wave = threadIdx.x >> 6, wm = wave & 1, wn = wave >> 1;
     const int a = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
     const int C = p.C, F = p.F, F2 = 2 * F;
@@ -429,17 +438,17 @@ __device__ __forceinline__ void glu_dw_tile(const GluParams& p, int64_t block, c
                               [&](int m) { return m0 + m < F2; }, m0 + TILE <= F2, F2);
     Operand<T, false, TILE> B((const T*)p.x + c0, [&](int n) { return (uint32_t)n; },
                               [&](int n) { return c0 + n < C; }, c0 + TILE <= C, C);
-    f32x4r_t acc[NB][NB];
+    f32x4r_t acc[NM][NN];
     clear_blocks(acc);
-    tile_product<T, false, false, TILE>(acc, A, B, k0, k1, smem, [&](int i) { return TILE / 2 * wm + 16 * i; },
-                                        [&](int j) { return TILE / 2 * wn + 16 * j; });
+    tile_product<T, false, false, TILE>(acc, A, B, k0, k1, smem, [&](int i) { return 16 * NM * wm + 16 * i; },
+                                        [&](int j) { return 16 * NN * wn + 16 * j; });
     float* part = p.wpart + split * C * F2;
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-        const int m = m0 + TILE / 2 * wm + 16 * i + 4 * g;
+    for (int i = 0; i < NM; ++i) {
+        const int m = m0 + 16 * NM * wm + 16 * i + 4 * g;
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-            const int64_t c = c0 + TILE / 2 * wn + 16 * j + a;
+        for (int j = 0; j < NN; ++j) {
+            const int64_t c = c0 + 16 * NN * wn + 16 * j + a;
             if (m >= F2 || c >= C) continue;
             if (p.wpart) {
                 *(f32x4r_t*)(part + c * F2 + m) = acc[i][j];
@@ -454,7 +463,7 @@ __device__ __forceinline__ void glu_dw_tile(const GluParams& p, int64_t block, c
 // Both products of the gradient: they need the same da and db and nothing of
 // each other.
 template <typename T, int TILE>
-__global__ void __launch_bounds__(kGluThreads, 2) k_glu_products(GluParams p, unsigned dx_blocks) {
+__global__ void __launch_bounds__(Shape<TILE>::THREADS, 4) k_glu_products(GluParams p, unsigned dx_blocks) {
     __shared__ __align__(16) char smem[kMostBytes<T, TILE>];
     if (blockIdx.x < dx_blocks)
         glu_dx_tile<T, TILE>(p, blockIdx.x, smem);
@@ -533,11 +542,12 @@ GluLayout glu_layout(int64_t N, int C, int F, int dtype) {
 template <typename T, int ACT>
 hipError_t glu_project(const GluParams& p, bool grad, const GluLayout& l, hipStream_t st) {
     const unsigned blocks = (unsigned)(l.tiles * tiles_of(p.F, l.ptile / 2));
+    const int threads = l.ptile == 128 ? Shape<128>::THREADS : Shape<64>::THREADS;
     auto fn = grad ? k_glu_project<T, ACT, true, 64> : k_glu_project<T, ACT, false, 64>;
     if constexpr (sizeof(T) == 2) {
         if (l.ptile == 128) fn = grad ? k_glu_project<T, ACT, true, 128> : k_glu_project<T, ACT, false, 128>;
     }
-    fn<<<blocks, kGluThreads, 0, st>>>(p);
+    fn<<<blocks, threads, 0, st>>>(p);
     return hipGetLastError();
 }
 
@@ -545,11 +555,12 @@ template <typename T>
 hipError_t glu_products(const GluParams& p, const GluLayout& l, hipStream_t st) {
     const unsigned dx = (unsigned)(tiles_of(p.N, l.tile) * tiles_of(p.C, l.tile));
     const unsigned dw = (unsigned)(tiles_of(2 * p.F, l.tile) * tiles_of(p.C, l.tile) * l.splits);
+    const int threads = l.tile == 128 ? Shape<128>::THREADS : Shape<64>::THREADS;
     auto fn = k_glu_products<T, 64>;
     if constexpr (sizeof(T) == 2) {
         if (l.tile == 128) fn = k_glu_products<T, 128>;
     }
-    fn<<<dx + dw, kGluThreads, 0, st>>>(p, dx);
+    fn<<<dx + dw, threads, 0, st>>>(p, dx);
     return hipGetLastError();
 }
 
