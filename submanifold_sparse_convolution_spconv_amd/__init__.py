@@ -519,13 +519,41 @@ def spconv_wgrad(feats, dout, nmap: NMap, out=None, workspace=None):
     return out
 
 
+# The row operators' calls are short (a single voxel's takes a few microseconds
+# on the GPU), so what stands around them here is kept short too: addresses as
+# plain integers, a device guard only where another device is current.
 def _row_dtype(x, name="x"):
     """The dtype code of a feature tensor (N, C)."""
     import torch
-    dt = {torch.float32: SPCONV_F32, torch.bfloat16: SPCONV_BF16}.get(x.dtype)
+    dt = SPCONV_F32 if x.dtype == torch.float32 else SPCONV_BF16 if x.dtype == torch.bfloat16 else None
     if dt is None or x.dim() != 2 or not x.is_cuda:
         raise ValueError(f"{name} must be a float32 or bfloat16 (N, C) CUDA tensor")
     return dt
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(name, dev, *args):
+    """The C function on the current stream of dev."""
+    import torch
+    fn = getattr(_lib or load_library(), name)
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        _check(rc, name)
+
+
+def _size(name, *args):
+    n = ctypes.c_size_t(0)
+    rc = getattr(_lib or load_library(), name)(*args, ctypes.byref(n))
+    if rc:
+        _check(rc, name)
+    return n.value
 
 
 def _like(t, shape, dtype, device, name):
@@ -547,13 +575,15 @@ def _out(out, shape, dtype, device, name):
 
 
 def _workspace(workspace, n, device, size_name):
+    """The workspace and its bytes: the caller's, checked, or one of n bytes
+    (none for 0)."""
     import torch
     if workspace is None:
-        return torch.empty(n, dtype=torch.uint8, device=device)
+        return (torch.empty(n, dtype=torch.uint8, device=device) if n else None), n
     if workspace.dtype != torch.uint8 or workspace.numel() < n or workspace.device != device \
             or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {size_name} bytes")
-    return workspace
+    return workspace, workspace.numel()
 
 
 def spconv_layernorm(x, weight=None, bias=None, eps: float = 1e-5, stats: bool = False, out=None):
@@ -570,18 +600,12 @@ def spconv_layernorm(x, weight=None, bias=None, eps: float = 1e-5, stats: bool =
     y = _out(out, (N, C), x.dtype, dev, "out")
     mean = torch.empty(N, dtype=torch.float32, device=dev) if stats else None
     rstd = torch.empty(N, dtype=torch.float32, device=dev) if stats else None
-    with torch.cuda.device(dev):
-        rc = load_library().spconv_layernorm(_ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean), _ptr(rstd),
-                                             N, C, eps, dt, _stream(dev))
-    _check(rc, "spconv_layernorm")
+    _call("spconv_layernorm", dev, _at(x), _at(weight), _at(bias), _at(y), _at(mean), _at(rstd), N, C, eps, dt)
     return (y, mean, rstd) if stats else y
 
 
 def spconv_layernorm_grad_workspace_size(N: int, C: int, dtype: int) -> int:
-    n = ctypes.c_size_t(0)
-    _check(load_library().spconv_layernorm_grad_workspace_size(N, C, dtype, ctypes.byref(n)),
-           "spconv_layernorm_grad_workspace_size")
-    return n.value
+    return _size("spconv_layernorm_grad_workspace_size", N, C, dtype)
 
 
 def spconv_layernorm_grad(dout, x, mean, rstd, weight=None, out=None, workspace=None):
@@ -605,16 +629,12 @@ def spconv_layernorm_grad(dout, x, mean, rstd, weight=None, out=None, workspace=
     ws = dweight = dbias = None
     n = 0
     if weight is not None:
-        n = spconv_layernorm_grad_workspace_size(N, C, dt)
-        ws = _workspace(workspace, n, dev, "spconv_layernorm_grad_workspace_size")
-        n = ws.numel()
+        ws, n = _workspace(workspace, spconv_layernorm_grad_workspace_size(N, C, dt), dev,
+                           "spconv_layernorm_grad_workspace_size")
         dweight = torch.empty(C, dtype=torch.float32, device=dev)
         dbias = torch.empty(C, dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        rc = load_library().spconv_layernorm_grad(_ptr(dout), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight),
-                                                  _ptr(ws), n, _ptr(dx), _ptr(dweight), _ptr(dbias), N, C, dt,
-                                                  _stream(dev))
-    _check(rc, "spconv_layernorm_grad")
+    _call("spconv_layernorm_grad", dev, _at(dout), _at(x), _at(mean), _at(rstd), _at(weight), _at(ws), n, _at(dx),
+          _at(dweight), _at(dbias), N, C, dt)
     return dx, dweight, dbias
 
 
@@ -643,17 +663,12 @@ def spconv_glu(x, w, bias=None, act: str = "silu", out=None):
     import torch
     dt, N, C, F, dev, x, w, bias, a = _glu_args(x, w, bias, act)
     h = _out(out, (N, F), x.dtype, dev, "out")
-    with torch.cuda.device(dev):
-        rc = load_library().spconv_glu(_ptr(x), _ptr(w), _ptr(bias), _ptr(h), N, C, F, a, dt, _stream(dev))
-    _check(rc, "spconv_glu")
+    _call("spconv_glu", dev, _at(x), _at(w), _at(bias), _at(h), N, C, F, a, dt)
     return h
 
 
 def spconv_glu_grad_workspace_size(N: int, C: int, F: int, dtype: int) -> int:
-    n = ctypes.c_size_t(0)
-    _check(load_library().spconv_glu_grad_workspace_size(N, C, F, dtype, ctypes.byref(n)),
-           "spconv_glu_grad_workspace_size")
-    return n.value
+    return _size("spconv_glu_grad_workspace_size", N, C, F, dtype)
 
 
 def spconv_glu_grad(dout, x, w, bias=None, act: str = "silu", workspace=None):
@@ -669,11 +684,9 @@ def spconv_glu_grad(dout, x, w, bias=None, act: str = "silu", workspace=None):
     dx = torch.empty_like(x)
     dw = torch.empty_like(w)
     dbias = torch.empty_like(bias) if bias is not None else None
-    ws = _workspace(workspace, spconv_glu_grad_workspace_size(N, C, F, dt), dev, "spconv_glu_grad_workspace_size")
-    with torch.cuda.device(dev):
-        rc = load_library().spconv_glu_grad(_ptr(dout), _ptr(x), _ptr(w), _ptr(bias), _ptr(ws), ws.numel(),
-                                            _ptr(dx), _ptr(dw), _ptr(dbias), N, C, F, a, dt, _stream(dev))
-    _check(rc, "spconv_glu_grad")
+    ws, n = _workspace(workspace, spconv_glu_grad_workspace_size(N, C, F, dt), dev, "spconv_glu_grad_workspace_size")
+    _call("spconv_glu_grad", dev, _at(dout), _at(x), _at(w), _at(bias), _at(ws), n, _at(dx), _at(dw), _at(dbias), N,
+          C, F, a, dt)
     return dx, dw, dbias
 
 
@@ -695,9 +708,7 @@ def _scan_args(x, z, offsets, order, h0):
 
 
 def spconv_scan_workspace_size(N: int, C: int, dtype: int) -> int:
-    n = ctypes.c_size_t(0)
-    _check(load_library().spconv_scan_workspace_size(N, C, dtype, ctypes.byref(n)), "spconv_scan_workspace_size")
-    return n.value
+    return _size("spconv_scan_workspace_size", N, C, dtype)
 
 
 def spconv_scan(x, z, offsets, order=None, h0=None, out=None, workspace=None):
@@ -712,19 +723,14 @@ def spconv_scan(x, z, offsets, order=None, h0=None, out=None, workspace=None):
     dt, N, C, B, dev, x, z, offsets, order, h0 = _scan_args(x, z, offsets, order, h0)
     h = _out(out, (N, C), x.dtype, dev, "out")
     last = torch.empty((B, C), dtype=torch.float32, device=dev)
-    ws = _workspace(workspace, spconv_scan_workspace_size(N, C, dt), dev, "spconv_scan_workspace_size")
-    with torch.cuda.device(dev):
-        rc = load_library().spconv_scan(_ptr(x), _ptr(z), _ptr(offsets), _ptr(order), _ptr(h0), _ptr(ws),
-                                        ws.numel(), _ptr(h), _ptr(last), N, C, B, dt, _stream(dev))
-    _check(rc, "spconv_scan")
+    ws, n = _workspace(workspace, spconv_scan_workspace_size(N, C, dt), dev, "spconv_scan_workspace_size")
+    _call("spconv_scan", dev, _at(x), _at(z), _at(offsets), _at(order), _at(h0), _at(ws), n, _at(h), _at(last), N, C,
+          B, dt)
     return h, last
 
 
 def spconv_scan_grad_workspace_size(N: int, C: int, dtype: int) -> int:
-    n = ctypes.c_size_t(0)
-    _check(load_library().spconv_scan_grad_workspace_size(N, C, dtype, ctypes.byref(n)),
-           "spconv_scan_grad_workspace_size")
-    return n.value
+    return _size("spconv_scan_grad_workspace_size", N, C, dtype)
 
 
 def spconv_scan_grad(dout, x, z, offsets, order=None, h0=None, dlast=None, workspace=None):
@@ -742,10 +748,7 @@ def spconv_scan_grad(dout, x, z, offsets, order=None, h0=None, dlast=None, works
     dx = torch.empty_like(x)
     dz = torch.empty_like(x)
     dh0 = torch.empty_like(h0) if h0 is not None else None
-    ws = _workspace(workspace, spconv_scan_grad_workspace_size(N, C, dt), dev, "spconv_scan_grad_workspace_size")
-    with torch.cuda.device(dev):
-        rc = load_library().spconv_scan_grad(_ptr(dout), _ptr(x), _ptr(z), _ptr(offsets), _ptr(order), _ptr(h0),
-                                             _ptr(dlast), _ptr(ws), ws.numel(), _ptr(dx), _ptr(dz), _ptr(dh0),
-                                             N, C, B, dt, _stream(dev))
-    _check(rc, "spconv_scan_grad")
+    ws, n = _workspace(workspace, spconv_scan_grad_workspace_size(N, C, dt), dev, "spconv_scan_grad_workspace_size")
+    _call("spconv_scan_grad", dev, _at(dout), _at(x), _at(z), _at(offsets), _at(order), _at(h0), _at(dlast), _at(ws),
+          n, _at(dx), _at(dz), _at(dh0), N, C, B, dt)
     return dx, dz, dh0

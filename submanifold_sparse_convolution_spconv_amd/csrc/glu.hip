@@ -270,18 +270,42 @@ __device__ __forceinline__ void clear_blocks(f32x4r_t (&acc)[NM][NN]) {
         for (int j = 0; j < NN; ++j) acc[i][j] = f32x4r_t{0.f, 0.f, 0.f, 0.f};
 }
 
+// Workgroups go round the 8 XCDs, each of which has its own L2.  Blocks that
+// read the same rows (`inner` of them to each of `outer`) stand 8 apart, so
+// that they run on one XCD, where there are enough of the outer ones to give
+// every XCD several; else in a row.  False: no such block.
+constexpr int kXcds = 8;
+__host__ __device__ __forceinline__ bool by_xcd(int64_t outer) { return outer >= 2 * kXcds; }
+__device__ __forceinline__ bool place_block(int64_t id, int64_t outer, int inner, int64_t& o, int& i) {
+    if (by_xcd(outer)) {
+        const int64_t k = id / kXcds;
+        o = k / inner * kXcds + id % kXcds;
+        i = (int)(k % inner);
+    } else {
+        o = id / inner;
+        i = (int)(id % inner);
+    }
+    return o < outer;
+}
+unsigned block_count(int64_t outer, int64_t inner) {
+    return (unsigned)((by_xcd(outer) ? round_up(outer, kXcds) : outer) * inner);
+}
+
 // TILE rows x TILE / 2 hidden features, both projections: h, or (GRAD) da and
 // db with their sums over the tile's rows.
 template <typename T, int ACT, bool GRAD, int TILE>
-__global__ void __launch_bounds__(Shape<TILE>::THREADS, 4) k_glu_project(GluParams p) {
+__global__ void __launch_bounds__(Shape<TILE>::THREADS, TILE == 128 ? 4 : 3) k_glu_project(GluParams p) {
     constexpr int NM = Shape<TILE>::NM, NN = Shape<TILE>::NN, WN = Shape<TILE>::WN, FT = TILE / 2;
     __shared__ __align__(16) char smem[kProductBytes<T, false, true, TILE>];
     __shared__ float bsum[WN][2][FT];
     const int wave = threadIdx.x >> 6, wm = wave & 1, wn = wave >> 1;
     const int a = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
     const int C = p.C, F = p.F;
-    const int ft = (F + FT - 1) / FT, f0 = (int)(blockIdx.x % ft) * FT;
-    const int64_t tile = blockIdx.x / ft, r0 = tile * TILE;
+    int64_t tile;
+    int f0;
+    if (!place_block(blockIdx.x, (p.N + TILE - 1) / TILE, (F + FT - 1) / FT, tile, f0)) return;
+    f0 *= FT;
+    const int64_t r0 = tile * TILE;
     const T* x = (const T*)p.x;
     const T* w = (const T*)p.w;
     Operand<T, false, TILE> A(w + f0, [&](int m) { return (uint32_t)(m / FT) * C * F + m % FT; },
@@ -396,8 +420,11 @@ __device__ __forceinline__ void glu_dx_tile(const GluParams& p, int64_t block, c
     const int wave = threadIdx.x >> 6, wm = wave & 1, wn = wave >> 1;
     const int a = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
     const int C = p.C, F = p.F;
-    const int ct = (C + TILE - 1) / TILE, c0 = (int)(block % ct) * TILE;
-    const int64_t r0 = block / ct * TILE;
+    int64_t r0;
+    int c0;
+    if (!place_block(block, (p.N + TILE - 1) / TILE, (C + TILE - 1) / TILE, r0, c0)) return;
+    r0 *= TILE;
+    c0 *= TILE;
     f32x4r_t acc[NM][NN];
     clear_blocks(acc);
 #pragma unroll 1
@@ -431,8 +458,10 @@ __device__ __forceinline__ void glu_dw_tile(const GluParams& p, int64_t block, c
     const int a = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
     const int C = p.C, F = p.F, F2 = 2 * F;
     const int mt = (F2 + TILE - 1) / TILE, ct = (C + TILE - 1) / TILE;
-    const int m0 = (int)(block % mt) * TILE, c0 = (int)(block / mt % ct) * TILE;
-    const int64_t split = block / mt / ct;
+    int64_t split;
+    int at;
+    if (!place_block(block, (p.N + p.rows_per_split - 1) / p.rows_per_split, mt * ct, split, at)) return;
+    const int m0 = at % mt * TILE, c0 = at / mt * TILE;
     const int64_t k0 = split * p.rows_per_split, k1 = min(p.N, k0 + p.rows_per_split);
     Operand<T, false, TILE> A((const T*)p.dab + m0, [&](int m) { return (uint32_t)m; },
                               [&](int m) { return m0 + m < F2; }, m0 + TILE <= F2, F2);
@@ -463,7 +492,7 @@ __device__ __forceinline__ void glu_dw_tile(const GluParams& p, int64_t block, c
 // Both products of the gradient: they need the same da and db and nothing of
 // each other.
 template <typename T, int TILE>
-__global__ void __launch_bounds__(Shape<TILE>::THREADS, 4) k_glu_products(GluParams p, unsigned dx_blocks) {
+__global__ void __launch_bounds__(Shape<TILE>::THREADS, TILE == 128 ? 4 : 3) k_glu_products(GluParams p, unsigned dx_blocks) {
     __shared__ __align__(16) char smem[kMostBytes<T, TILE>];
     if (blockIdx.x < dx_blocks)
         glu_dx_tile<T, TILE>(p, blockIdx.x, smem);
@@ -541,7 +570,7 @@ GluLayout glu_layout(int64_t N, int C, int F, int dtype) {
 
 template <typename T, int ACT>
 hipError_t glu_project(const GluParams& p, bool grad, const GluLayout& l, hipStream_t st) {
-    const unsigned blocks = (unsigned)(l.tiles * tiles_of(p.F, l.ptile / 2));
+    const unsigned blocks = block_count(l.tiles, tiles_of(p.F, l.ptile / 2));
     const int threads = l.ptile == 128 ? Shape<128>::THREADS : Shape<64>::THREADS;
     auto fn = grad ? k_glu_project<T, ACT, true, 64> : k_glu_project<T, ACT, false, 64>;
     if constexpr (sizeof(T) == 2) {
@@ -553,8 +582,8 @@ hipError_t glu_project(const GluParams& p, bool grad, const GluLayout& l, hipStr
 
 template <typename T>
 hipError_t glu_products(const GluParams& p, const GluLayout& l, hipStream_t st) {
-    const unsigned dx = (unsigned)(tiles_of(p.N, l.tile) * tiles_of(p.C, l.tile));
-    const unsigned dw = (unsigned)(tiles_of(2 * p.F, l.tile) * tiles_of(p.C, l.tile) * l.splits);
+    const unsigned dx = block_count(tiles_of(p.N, l.tile), tiles_of(p.C, l.tile));
+    const unsigned dw = block_count(l.splits, tiles_of(2 * p.F, l.tile) * tiles_of(p.C, l.tile));
     const int threads = l.tile == 128 ? Shape<128>::THREADS : Shape<64>::THREADS;
     auto fn = k_glu_products<T, 64>;
     if constexpr (sizeof(T) == 2) {
