@@ -86,7 +86,7 @@ hipError_t launch_glu_rows(const GluParams& p, int act, hipStream_t st);
 hipError_t launch_glu_rows_dx(const GluParams& p, int act, hipStream_t st);
 // dw's and dbias' partial sums: `splits` splits of rows_per_split rows; the
 // number of splits that fills the card.
-int glu_rows_splits(int64_t N, int F);
+int glu_rows_splits(int64_t N, int C, int F);
 hipError_t launch_glu_rows_dw(const GluParams& p, int act, int splits, hipStream_t st);
 
 }  // namespace spc

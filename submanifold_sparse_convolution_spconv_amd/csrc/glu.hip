@@ -541,7 +541,7 @@ GluLayout glu_layout(int64_t N, int C, int F, int dtype) {
     GluLayout l{};
     l.rows = use_rows(N, C, dtype);
     if (l.rows) {
-        const int want = glu_rows_splits(N, F);
+        const int want = glu_rows_splits(N, C, F);
         l.rows_per_split = round_up((N + want - 1) / want, 64);
         l.splits = (int)((N + l.rows_per_split - 1) / l.rows_per_split);
         l.tiles = l.splits;

@@ -18,6 +18,7 @@
 #include "glu.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace spc {
 
@@ -273,24 +274,24 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p) {
     }
 }
 
-// dw and dbias of one split of the rows and 128 features, 16 per wave: 64 rows
-// at a time, x shared through LDS, dout (of its own features) per wave.
+// dw and dbias of one split of the rows and 16 features per wave: 64 rows at a
+// time, x shared through LDS, dout (of its own features) per wave.
 //
 // Here the projections are D = x w: a lane gets four consecutive rows of one
 // feature, so da and db, rounded, are the transposed operand of x^T da with
 // its reduction (32 rows) numbered 4 g + e (rows of the first 16) and 16 + 4 g
 // + e; x is read back transposed in the same order, dout too.
-constexpr int kDwFeatures = 128;
+constexpr int kDwWaves = 8;
 constexpr int kDwRows = 64;
+constexpr int kDwXBytes = kDwRows * 256, kDwDBytes = kDwRows * 32;      // of one buffer; dout: per wave
 
-// x tile: row r, 16-byte unit u of 16 at u ^ swz(r): conflict-free for 16
-// rows' unit u and for two units of four consecutive rows
+// x tile: rows of 256 bytes, 16-byte unit u of row r at u ^ swizzle_row(r):
+// conflict-free for 16 rows' unit u and for two units of four consecutive rows
 __device__ __forceinline__ int swizzle_row(int r) { return ((r & 7) << 1) | ((r >> 3) & 1); }
 
 template <int KC, int ACT>
-__global__ void __launch_bounds__(kRowThreads) k_glu_rows_dw(GluParams p, int slabs) {
-    __shared__ __align__(16) __bf16 lx[2][kDwRows * 128];
-    __shared__ __align__(16) __bf16 ld[kRowWaves][2][kDwRows * 16];
+__global__ void __launch_bounds__(kDwWaves * 64) k_glu_rows_dw(GluParams p, int slabs, int spread) {
+    __shared__ __align__(16) char smem[2 * kDwXBytes + 2 * kDwWaves * kDwDBytes];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, a = lane & 15, g = lane >> 4;
     const int C = p.C, F = p.F;
     // the slabs of one split on one XCD (workgroups go round the 8 in turn)
@@ -298,7 +299,8 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows_dw(GluParams p, int sl
     const int64_t split = (int64_t)(blockIdx.x >> 3) / slabs * 8 + (blockIdx.x & 7);
     const int64_t k0 = split * p.rows_per_split, k1 = min(p.N, k0 + p.rows_per_split);
     if (k0 >= p.N) return;
-    const int f = slab * kDwFeatures + wave * 16;      // this wave's first feature
+    const int f = (slab * spread + wave) * 16;         // this wave's first feature
+    const bool works = wave < spread && f < F;         // else it only helps to load x
     const __bf16* w = (const __bf16*)p.w;
 
     // weights as operands: feature f + a, channels 32 s + 8 g ..
@@ -316,25 +318,54 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows_dw(GluParams p, int sl
             }
     const float ba = p.bias && f + a < F ? p.bias[f + a] : 0.f, bb = p.bias && f + a < F ? p.bias[F + f + a] : 0.f;
 
-    // 64 rows of x: 1024 16-byte units, two per thread; of dout: 128 units per wave
-    bf16x8r_t rx[2], rd[2];
+    // Byte offsets in LDS, to which buffer, half and tile add constants.  Unit
+    // 4 s + g of row a; pieces of four channels of rows 4 g + (a >> 2).
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_bf16x4r_t*)smem;
+    uint32_t xa[KC], xt[2 * KC];
+#pragma unroll
+    for (int s = 0; s < KC; ++s) xa[s] = lds0 + a * 256 + ((4 * s + g) ^ swizzle_row(a)) * 16;
+    const int rt = 4 * g + (a >> 2);
+#pragma unroll
+    for (int i = 0; i < 2 * KC; ++i)
+        xt[i] = lds0 + rt * 256 + ((2 * i + ((a & 3) >> 1)) ^ swizzle_row(rt)) * 16 + 8 * (a & 1);
+    const uint32_t d0 = lds0 + 2 * kDwXBytes + wave * 2 * kDwDBytes;
+    const uint32_t dt = d0 + rt * 32 + 8 * (a & 3);
+
+    // x's 64 rows: units of KC * 32 channels, PER of them per thread (half of
+    // the threads' for 32 channels); dout's: 128 units per wave
+    constexpr int UNITS = KC * 4, PER = (kDwRows * UNITS + kDwWaves * 64 - 1) / (kDwWaves * 64);
+    constexpr int RSTEP = kDwWaves * 64 / UNITS;       // rows from unit to unit of a thread
+    const int xr = threadIdx.x / UNITS, xu = threadIdx.x % UNITS;
+    const bool loads = xr < kDwRows && 8 * xu < C;
+    bf16x8r_t rx[PER], rd[2];
     auto fetch = [&](int64_t k) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int e = threadIdx.x + kRowThreads * j, r = e >> 4, u = e & 15;
-            rx[j] = load8((const __bf16*)p.x + min(k + r, k1 - 1) * C + (8 * u < C ? 8 * u : 0));
-            const int q = lane + 64 * j, rr = q >> 1, h = q & 1;
-            rd[j] = load8((const __bf16*)p.dout + min(k + rr, k1 - 1) * F + (f + 8 * h < F ? f + 8 * h : 0));
-        }
-    };
-    auto put = [&](int b, int64_t k) {
+        for (int j = 0; j < PER; ++j)
+            rx[j] = load8((const __bf16*)p.x + min(k + xr + RSTEP * j, k1 - 1) * C + (loads ? 8 * xu : 0));
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int e = threadIdx.x + kRowThreads * j, r = e >> 4, u = e & 15;
-            *(bf16x8r_t*)(lx[b] + (r * 16 + (u ^ swizzle_row(r))) * 8) = keep(rx[j], k + r < k1 && 8 * u < C);
-            const int q = lane + 64 * j, rr = q >> 1, h = q & 1;
-            *(bf16x8r_t*)(ld[wave][b] + q * 8) = keep(rd[j], k + rr < k1 && f + 8 * h < F);
+        for (int j = 0; j < 2; ++j)
+            rd[j] = load8((const __bf16*)p.dout + min(k + (lane >> 1) + 32 * j, k1 - 1) * F +
+                          (f + 8 * (lane & 1) < F ? f + 8 * (lane & 1) : 0));
+    };
+    // Channels past C were cleared once and are never written; features past F
+    // keep to their own columns, which are not stored; rows past the split are
+    // zero, in its last block.
+    const uint32_t px = lds0 + xr * 256 + (xu ^ swizzle_row(xr)) * 16, pd = d0 + lane * 16;
+    auto put = [&](auto buffer, int64_t k) {
+        constexpr uint32_t B = decltype(buffer)::value;
+        if (k + kDwRows > k1) {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) rx[j] = keep(rx[j], k + xr + RSTEP * j < k1);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) rd[j] = keep(rd[j], k + (lane >> 1) + 32 * j < k1);
         }
+        if (loads) {
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                *(lds_bf16x8r_t*)(uintptr_t)(px + B * kDwXBytes + j * RSTEP * 256) = rx[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) *(lds_bf16x8r_t*)(uintptr_t)(pd + B * kDwDBytes + j * 1024) = rd[j];
     };
     f32x4r_t dw[2][2 * KC];
 #pragma unroll
@@ -342,54 +373,71 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows_dw(GluParams p, int sl
 #pragma unroll
         for (int i = 0; i < 2 * KC; ++i) dw[s][i] = f32x4r_t{0.f, 0.f, 0.f, 0.f};
     float sa = 0.f, sb = 0.f;
-    fetch(k0);
-    put(0, k0);
-    int b = 0;
-    for (int64_t k = k0; k < k1; k += kDwRows, b ^= 1) {
-        fetch(min(k + kDwRows, k1 - 1));
-        __syncthreads();
+    auto block = [&](auto buffer) {
+        constexpr uint32_t B = decltype(buffer)::value;
+        if (!works) return;
         float ua = 0.f, ub = 0.f;         // this block's sums first: short chains
 #pragma unroll
         for (int hf = 0; hf < kDwRows / 32; ++hf) {
             bf16x4r_t da[2], db[2];
 #pragma unroll
-            for (int rt = 0; rt < 2; ++rt) {
-                const int r = 32 * hf + 16 * rt + a;
+            for (int t = 0; t < 2; ++t) {
+                const uint32_t tile = 32 * hf + 16 * t;
                 f32x4r_t va = {ba, ba, ba, ba}, vb = {bb, bb, bb, bb};
 #pragma unroll
                 for (int s = 0; s < KC; ++s) {
-                    const bf16x8r_t xf = *(const bf16x8r_t*)(lx[b] + (r * 16 + ((4 * s + g) ^ swizzle_row(r))) * 8);
+                    const bf16x8r_t xf = read_unit(xa[s] + B * kDwXBytes + tile * 256);
                     va = mma(xf, wt[0][s], va);
                     vb = mma(xf, wt[1][s], vb);
                 }
-                const int rd0 = 32 * hf + 16 * rt + 4 * g + (a >> 2);
-                const bf16x4r_t dh = read_tr(ld[wave][b] + rd0 * 16 + 4 * (a & 3));
+                const bf16x4r_t dh = read_tr(dt + B * kDwDBytes + tile * 32);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const Act t = activation<ACT>(va[e]);
+                    const Act q = activation<ACT>(va[e]);
                     const float d = (float)dh[e];
-                    const float u = d * vb[e] * t.d, v = d * t.v;
+                    const float u = d * vb[e] * q.d, v = d * q.v;
                     ua += u;
                     ub += v;
-                    da[rt][e] = (__bf16)u;
-                    db[rt][e] = (__bf16)v;
+                    da[t][e] = (__bf16)u;
+                    db[t][e] = (__bf16)v;
                 }
+                keep_order();
             }
             const bf16x8r_t fa = join8(da[0], da[1]), fb = join8(db[0], db[1]);
-            const int r = 32 * hf + 4 * g + (a >> 2);
+            auto channels = [&](int i) {
+                const uint32_t q = xt[i] + B * kDwXBytes + 32 * hf * 256;
+                return join8(read_tr(q), read_tr(q + 16 * 256));
+            };
+            bf16x8r_t xf[2] = {channels(0), channels(1)};
 #pragma unroll
             for (int i = 0; i < 2 * KC; ++i) {
-                const int u = 2 * i + ((a & 3) >> 1), h = 4 * (a & 1);
-                const bf16x8r_t xt = join8(read_tr(lx[b] + (r * 16 + (u ^ swizzle_row(r))) * 8 + h),
-                                           read_tr(lx[b] + ((r + 16) * 16 + (u ^ swizzle_row(r + 16))) * 8 + h));
-                dw[0][i] = mma(fa, xt, dw[0][i]);
-                dw[1][i] = mma(fb, xt, dw[1][i]);
+                const bf16x8r_t x0 = xf[i & 1];
+                if (i + 2 < 2 * KC) xf[i & 1] = channels(i + 2);
+                dw[0][i] = mma(fa, x0, dw[0][i]);
+                dw[1][i] = mma(fb, x0, dw[1][i]);
+                keep_order();
             }
         }
         sa += ua;
         sb += ub;
-        put(b ^ 1, k + kDwRows);
+    };
+    for (int e = threadIdx.x; e < 2 * kDwXBytes / 16; e += kDwWaves * 64) *(bf16x8r_t*)(smem + 16 * e) = bf16x8r_t{};
+    constexpr std::integral_constant<uint32_t, 0> b0{};
+    constexpr std::integral_constant<uint32_t, 1> b1{};
+    fetch(k0);
+    __syncthreads();
+    put(b0, k0);
+    for (int64_t k = k0; k < k1; k += 2 * kDwRows) {
+        fetch(min(k + kDwRows, k1 - 1));
+        __syncthreads();
+        block(b0);
+        put(b1, k + kDwRows);
+        fetch(min(k + 2 * kDwRows, k1 - 1));
+        __syncthreads();
+        block(b1);                        // zeros past the last row
+        put(b0, k + 2 * kDwRows);
     }
+    if (!works) return;
     // output m = 4 g + e: feature f + m; channel 16 i + a
     float* part = p.wpart + split * C * 2 * F;
 #pragma unroll
@@ -412,11 +460,27 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows_dw(GluParams p, int sl
     }
 }
 
+// The features in slabs of at most 8 waves' worth, as even as they go, and the
+// splits of the rows that fill the card.
+struct DwShape {
+    int spread, slabs, splits;
+};
+DwShape dw_shape(int64_t N, int C, int F) {
+    DwShape s;
+    const int tiles = (F + 15) / 16;
+    s.slabs = (tiles + kDwWaves - 1) / kDwWaves;
+    s.spread = (tiles + s.slabs - 1) / s.slabs;
+    const int64_t groups = (int64_t)kCUs * (C <= 32 ? 2 : 1);      // workgroups that the registers hold
+    s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(groups / s.slabs, (N + kDwRows - 1) / kDwRows));
+    return s;
+}
+
 template <int KC, int ACT>
 hipError_t rows_go(const GluParams& p, int what, int splits, hipStream_t st) {
     if (what == 2) {
-        const int slabs = (p.F + kDwFeatures - 1) / kDwFeatures;
-        k_glu_rows_dw<KC, ACT><<<(unsigned)((splits + 7) / 8 * 8 * slabs), kRowThreads, 0, st>>>(p, slabs);
+        const DwShape s = dw_shape(p.N, p.C, p.F);
+        k_glu_rows_dw<KC, ACT><<<(unsigned)((splits + 7) / 8 * 8 * s.slabs), kDwWaves * 64, 0, st>>>(p, s.slabs,
+                                                                                                             s.spread);
         return hipGetLastError();
     }
     const size_t lds = (size_t)kSlabElems * 2 + (size_t)2 * kSlab<KC> * 4;
@@ -443,11 +507,7 @@ hipError_t rows_act(const GluParams& p, int act, int what, int splits, hipStream
 
 hipError_t launch_glu_rows(const GluParams& p, int act, hipStream_t st) { return rows_act(p, act, 0, 0, st); }
 hipError_t launch_glu_rows_dx(const GluParams& p, int act, hipStream_t st) { return rows_act(p, act, 1, 0, st); }
-int glu_rows_splits(int64_t N, int F) {
-    // a workgroup holds a CU's registers: one each
-    const int64_t slabs = (F + kDwFeatures - 1) / kDwFeatures;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(kCUs / slabs, (N + kDwRows - 1) / kDwRows));
-}
+int glu_rows_splits(int64_t N, int C, int F) { return dw_shape(N, C, F).splits; }
 hipError_t launch_glu_rows_dw(const GluParams& p, int act, int splits, hipStream_t st) {
     return rows_act(p, act, 2, splits, st);
 }
