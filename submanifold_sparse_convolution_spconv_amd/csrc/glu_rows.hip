@@ -107,11 +107,11 @@ __device__ __forceinline__ void load_slab(__bf16* lw, float* lb, const GluParams
 
 // The rows of a wave as operands: x[n][s] holds channels 32 s + 8 g .. of row
 // 16 n + a (channel 0 on where those are past C, the last row past the rows).
-template <int KC>
-__device__ __forceinline__ void load_rows(bf16x8r_t (&x)[NT][KC], const GluParams& p, int64_t r0) {
+template <int KC, int ROWS>
+__device__ __forceinline__ void load_rows(bf16x8r_t (&x)[ROWS][KC], const GluParams& p, int64_t r0) {
     const int a = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int n = 0; n < ROWS; ++n) {
         const __bf16* row = (const __bf16*)p.x + min(r0 + 16 * n + a, p.N - 1) * p.C;
 #pragma unroll
         for (int s = 0; s < KC; ++s) x[n][s] = load8(row + (32 * s + 8 * g < p.C ? 32 * s + 8 * g : 0));
@@ -142,15 +142,20 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p) {
         load_slab<KC>(lw, lb, p, 0);
         __syncthreads();
     }
-    bf16x8r_t x[NT][KC], xn[NT][KC];
-    load_rows<KC>(xn, p, (int64_t)blockIdx.x * kBlockRows + wave * kWaveRows);
+    // The next rows: the forward loads them a whole block ahead; dx, whose sums
+    // need the registers, into the operands themselves after their last use.
+    bf16x8r_t x[NT][KC], xn[DX ? 1 : NT][KC];
+    if constexpr (DX)
+        load_rows(x, p, (int64_t)blockIdx.x * kBlockRows + wave * kWaveRows);
+    else
+        load_rows(xn, p, (int64_t)blockIdx.x * kBlockRows + wave * kWaveRows);
     for (int64_t blk = blockIdx.x; blk < blocks; blk += gridDim.x) {
         const int64_t r0 = blk * kBlockRows + wave * kWaveRows;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int s = 0; s < KC; ++s) x[n][s] = keep(xn[n][s], 32 * s + 8 * g < C);
-        load_rows<KC>(xn, p, r0 + (int64_t)gridDim.x * kBlockRows);
+            for (int s = 0; s < KC; ++s) x[n][s] = keep(DX ? x[n][s] : xn[DX ? 0 : n][s], 32 * s + 8 * g < C);
+        if constexpr (!DX) load_rows(xn, p, r0 + (int64_t)gridDim.x * kBlockRows);
         f32x4r_t dx[DX ? 2 * KC : 1][NT];
         if constexpr (DX) {
 #pragma unroll
@@ -201,18 +206,21 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p) {
                     w[0] = join8(read_tr(q), read_tr(q + 8 * PITCH));
                     w[1] = join8(read_tr(q + 2 * FS), read_tr(q + 2 * FS + 8 * PITCH));
                 };
-                bf16x8r_t wf[2][2];
-                read1(0, wf[0]);
+                constexpr int STEPS = 2 * KC, AHEAD = STEPS < 3 ? STEPS : 3;      // operands on their way
+                bf16x8r_t wf[AHEAD][2];
 #pragma unroll
-                for (int i = 0; i < 2 * KC; ++i) {
-                    if (i + 1 < 2 * KC) read1(i + 1, wf[(i + 1) & 1]);
+                for (int i = 0; i < AHEAD - 1; ++i) read1(i, wf[i]);
+#pragma unroll
+                for (int i = 0; i < STEPS; ++i) {
+                    if (i + AHEAD - 1 < STEPS) read1(i + AHEAD - 1, wf[(i + AHEAD - 1) % AHEAD]);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        pa[i & 1][n] = mma(wf[i & 1][0], x[n][i >> 1], pa[i & 1][n]);
-                        pb[i & 1][n] = mma(wf[i & 1][1], x[n][i >> 1], pb[i & 1][n]);
+                        pa[i & 1][n] = mma(wf[i % AHEAD][0], x[n][i >> 1], pa[i & 1][n]);
+                        pb[i & 1][n] = mma(wf[i % AHEAD][1], x[n][i >> 1], pb[i & 1][n]);
                     }
                     keep_order();
                 }
+                if (DX && f0 + fl + 32 >= F) load_rows(x, p, r0 + (int64_t)gridDim.x * kBlockRows);
                 if constexpr (!DX) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
@@ -225,16 +233,6 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p) {
                             store_unit((__bf16*)p.h + r * F + f0 + fl + 8 * g, o, p.stream);
                     }
                 } else {
-                    bf16x8r_t da[NT], db[NT];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const Act t = activation<ACT>(pa[e >> 2][n][e & 3]);
-                            const float d = (float)dh[n][e];
-                            da[n][e] = (__bf16)(d * pb[e >> 2][n][e & 3] * t.d);
-                            db[n][e] = (__bf16)(d * t.v);
-                        }
                     // output m of tile i: channel 32 (i / 2) + 8 (m >> 2) + 4 (i & 1) + (m & 3)
                     const uint32_t q2 = w2 + ((fl * 2) ^ x2);
                     uint32_t q2h = q2 + 0x10000;
@@ -245,14 +243,27 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p) {
                         w[0] = read_unit(q);
                         w[1] = read_unit(q + 2 * FS);
                     };
-                    read2(0, wf[0]);
+                    // (asked for before the activations)
 #pragma unroll
-                    for (int i = 0; i < 2 * KC; ++i) {
-                        if (i + 1 < 2 * KC) read2(i + 1, wf[(i + 1) & 1]);
+                    for (int i = 0; i < AHEAD - 1; ++i) read2(i, wf[i]);
+                    keep_order();
+                    bf16x8r_t da[NT], db[NT];
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) dx[i][n] = mma(wf[i & 1][0], da[n], dx[i][n]);
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) dx[i][n] = mma(wf[i & 1][1], db[n], dx[i][n]);
+                        for (int e = 0; e < 8; ++e) {
+                            const Act t = activation<ACT>(pa[e >> 2][n][e & 3]);
+                            const float d = (float)dh[n][e];
+                            da[n][e] = (__bf16)(d * pb[e >> 2][n][e & 3] * t.d);
+                            db[n][e] = (__bf16)(d * t.v);
+                        }
+#pragma unroll
+                    for (int i = 0; i < STEPS; ++i) {
+                        if (i + AHEAD - 1 < STEPS) read2(i + AHEAD - 1, wf[(i + AHEAD - 1) % AHEAD]);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) dx[i][n] = mma(wf[i % AHEAD][0], da[n], dx[i][n]);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) dx[i][n] = mma(wf[i % AHEAD][1], db[n], dx[i][n]);
                         keep_order();
                     }
                 }
@@ -332,11 +343,13 @@ __global__ void __launch_bounds__(kDwWaves * 64) k_glu_rows_dw(GluParams p, int 
     const uint32_t dt = d0 + rt * 32 + 8 * (a & 3);
 
     // x's 64 rows: units of KC * 32 channels, PER of them per thread (half of
-    // the threads' for 32 channels); dout's: 128 units per wave
+    // the threads' for 32 channels); dout's: 16 units of the slab's features,
+    // two per thread, a wave's two features' units side by side in LDS
     constexpr int UNITS = KC * 4, PER = (kDwRows * UNITS + kDwWaves * 64 - 1) / (kDwWaves * 64);
     constexpr int RSTEP = kDwWaves * 64 / UNITS;       // rows from unit to unit of a thread
     const int xr = threadIdx.x / UNITS, xu = threadIdx.x % UNITS;
     const bool loads = xr < kDwRows && 8 * xu < C;
+    const int dr = threadIdx.x >> 4, du = threadIdx.x & 15, df = slab * spread * 16 + 8 * du;
     bf16x8r_t rx[PER], rd[2];
     auto fetch = [&](int64_t k) {
 #pragma unroll
@@ -344,20 +357,20 @@ __global__ void __launch_bounds__(kDwWaves * 64) k_glu_rows_dw(GluParams p, int 
             rx[j] = load8((const __bf16*)p.x + min(k + xr + RSTEP * j, k1 - 1) * C + (loads ? 8 * xu : 0));
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            rd[j] = load8((const __bf16*)p.dout + min(k + (lane >> 1) + 32 * j, k1 - 1) * F +
-                          (f + 8 * (lane & 1) < F ? f + 8 * (lane & 1) : 0));
+            rd[j] = load8((const __bf16*)p.dout + min(k + dr + 32 * j, k1 - 1) * F + (df < F ? df : 0));
     };
     // Channels past C were cleared once and are never written; features past F
     // keep to their own columns, which are not stored; rows past the split are
     // zero, in its last block.
-    const uint32_t px = lds0 + xr * 256 + (xu ^ swizzle_row(xr)) * 16, pd = d0 + lane * 16;
+    const uint32_t px = lds0 + xr * 256 + (xu ^ swizzle_row(xr)) * 16;
+    const uint32_t pd = lds0 + 2 * kDwXBytes + (du >> 1) * 2 * kDwDBytes + dr * 32 + (du & 1) * 16;
     auto put = [&](auto buffer, int64_t k) {
         constexpr uint32_t B = decltype(buffer)::value;
         if (k + kDwRows > k1) {
 #pragma unroll
             for (int j = 0; j < PER; ++j) rx[j] = keep(rx[j], k + xr + RSTEP * j < k1);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) rd[j] = keep(rd[j], k + (lane >> 1) + 32 * j < k1);
+            for (int j = 0; j < 2; ++j) rd[j] = keep(rd[j], k + dr + 32 * j < k1);
         }
         if (loads) {
 #pragma unroll
@@ -373,46 +386,60 @@ __global__ void __launch_bounds__(kDwWaves * 64) k_glu_rows_dw(GluParams p, int 
 #pragma unroll
         for (int i = 0; i < 2 * KC; ++i) dw[s][i] = f32x4r_t{0.f, 0.f, 0.f, 0.f};
     float sa = 0.f, sb = 0.f;
+    // One block: four tiles of 16 rows, the products with x after each second
+    // one.  What a step reads from LDS is asked for before the work of the step
+    // before it.
     auto block = [&](auto buffer) {
         constexpr uint32_t B = decltype(buffer)::value;
         if (!works) return;
         float ua = 0.f, ub = 0.f;         // this block's sums first: short chains
+        bf16x8r_t xf[2][KC];
+        bf16x4r_t dh[2];
+        auto read_tile = [&](int t) {
 #pragma unroll
-        for (int hf = 0; hf < kDwRows / 32; ++hf) {
-            bf16x4r_t da[2], db[2];
+            for (int s = 0; s < KC; ++s) xf[t & 1][s] = read_unit(xa[s] + B * kDwXBytes + t * 16 * 256);
+            dh[t & 1] = read_tr(dt + B * kDwDBytes + t * 16 * 32);
+        };
+        auto channels = [&](int t, int i) {
+            const uint32_t q = xt[i] + B * kDwXBytes + (t >> 1) * 32 * 256;
+            return join8(read_tr(q), read_tr(q + 16 * 256));
+        };
+        constexpr int AHEAD = 2 * KC < 4 ? 2 * KC : 4;
+        bf16x8r_t xc[AHEAD];
+        bf16x4r_t da[2], db[2];
+        read_tile(0);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const uint32_t tile = 32 * hf + 16 * t;
-                f32x4r_t va = {ba, ba, ba, ba}, vb = {bb, bb, bb, bb};
+        for (int t = 0; t < kDwRows / 16; ++t) {
+            f32x4r_t va = {ba, ba, ba, ba}, vb = {bb, bb, bb, bb};
 #pragma unroll
-                for (int s = 0; s < KC; ++s) {
-                    const bf16x8r_t xf = read_unit(xa[s] + B * kDwXBytes + tile * 256);
-                    va = mma(xf, wt[0][s], va);
-                    vb = mma(xf, wt[1][s], vb);
-                }
-                const bf16x4r_t dh = read_tr(dt + B * kDwDBytes + tile * 32);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const Act q = activation<ACT>(va[e]);
-                    const float d = (float)dh[e];
-                    const float u = d * vb[e] * q.d, v = d * q.v;
-                    ua += u;
-                    ub += v;
-                    da[t][e] = (__bf16)u;
-                    db[t][e] = (__bf16)v;
-                }
-                keep_order();
+            for (int s = 0; s < KC; ++s) {
+                va = mma(xf[t & 1][s], wt[0][s], va);
+                vb = mma(xf[t & 1][s], wt[1][s], vb);
             }
+            if (t & 1) {
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) xc[i] = channels(t, i);
+            } else {
+                read_tile(t + 1);
+            }
+            keep_order();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const Act q = activation<ACT>(va[e]);
+                const float d = (float)dh[t & 1][e];
+                const float u = d * vb[e] * q.d, v = d * q.v;
+                ua += u;
+                ub += v;
+                da[t & 1][e] = (__bf16)u;
+                db[t & 1][e] = (__bf16)v;
+            }
+            if (!(t & 1)) continue;
             const bf16x8r_t fa = join8(da[0], da[1]), fb = join8(db[0], db[1]);
-            auto channels = [&](int i) {
-                const uint32_t q = xt[i] + B * kDwXBytes + 32 * hf * 256;
-                return join8(read_tr(q), read_tr(q + 16 * 256));
-            };
-            bf16x8r_t xf[2] = {channels(0), channels(1)};
 #pragma unroll
             for (int i = 0; i < 2 * KC; ++i) {
-                const bf16x8r_t x0 = xf[i & 1];
-                if (i + 2 < 2 * KC) xf[i & 1] = channels(i + 2);
+                const bf16x8r_t x0 = xc[i % AHEAD];
+                if (i + AHEAD < 2 * KC) xc[i % AHEAD] = channels(t, i + AHEAD);
+                if (i + 1 == 2 * KC && t + 1 < kDwRows / 16) read_tile(t + 1);
                 dw[0][i] = mma(fa, x0, dw[0][i]);
                 dw[1][i] = mma(fb, x0, dw[1][i]);
                 keep_order();
