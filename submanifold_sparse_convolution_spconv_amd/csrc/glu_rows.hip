@@ -93,11 +93,24 @@ __device__ __forceinline__ void load_slab(__bf16* lw, float* lb, const GluParams
     constexpr int FS = kSlab<KC>, UNITS = FS / 8;
     const __bf16* w = (const __bf16*)p.w;
     const int n = min((p.F - f0 + 31) / 32 * 4, UNITS);    // units with features
-    for (int e = threadIdx.x; e < KC * 32 * 2 * n; e += kRowThreads) {
-        const int c = e / (2 * n), u = e % (2 * n), s = u >= n, ul = u - s * n, f = f0 + ul * 8;
-        const bool in = c < p.C && f < p.F;
-        const bf16x8r_t v = keep(load8(w + (in ? ((int64_t)s * p.C + c) * p.F + f : 0)), in);
-        *(bf16x8r_t*)(lw + (c * 2 * UNITS + s * UNITS + (ul ^ swizzle(c))) * 8) = v;
+    // eight units at a time, all loads before the first store
+    constexpr int B = 8;
+    const int total = KC * 32 * 2 * n;
+    for (int e0 = threadIdx.x; e0 < total; e0 += B * kRowThreads) {
+        bf16x8r_t v[B];
+        int at[B];
+        bool in[B];
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+            const int e = min(e0 + j * kRowThreads, total - 1);
+            const int c = e / (2 * n), u = e - c * 2 * n, s = u >= n, ul = u - s * n, f = f0 + ul * 8;
+            in[j] = c < p.C && f < p.F;
+            v[j] = load8(w + (in[j] ? ((int64_t)s * p.C + c) * p.F + f : 0));
+            at[j] = (c * 2 * UNITS + s * UNITS + (ul ^ swizzle(c))) * 8;
+        }
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+            if (e0 + j * kRowThreads < total) *(bf16x8r_t*)(lw + at[j]) = keep(v[j], in[j]);
     }
     for (int e = threadIdx.x; e < 2 * FS; e += kRowThreads) {
         const int s = e >= FS, f = f0 + e - s * FS;
@@ -207,7 +220,7 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p) {
                     w[1] = join8(read_tr(q + 2 * FS), read_tr(q + 2 * FS + 8 * PITCH));
                 };
                 constexpr int STEPS = 2 * KC, AHEAD = STEPS < 3 ? STEPS : 3;      // operands on their way
-                bf16x8r_t wf[AHEAD][2];
+                bf16x8r_t wf[4][2];
 #pragma unroll
                 for (int i = 0; i < AHEAD - 1; ++i) read1(i, wf[i]);
 #pragma unroll
@@ -244,8 +257,8 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p) {
                         w[1] = read_unit(q + 2 * FS);
                     };
                     // (asked for before the activations)
-#pragma unroll
-                    for (int i = 0; i < AHEAD - 1; ++i) read2(i, wf[i]);
+                    read2(0, wf[0]);
+                    read2(1, wf[1]);
                     keep_order();
                     bf16x8r_t da[NT], db[NT];
 #pragma unroll
@@ -257,13 +270,19 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p) {
                             da[n][e] = (__bf16)(d * pb[e >> 2][n][e & 3] * t.d);
                             db[n][e] = (__bf16)(d * t.v);
                         }
+                    // two steps at a time: eight products before a sum is needed again
 #pragma unroll
-                    for (int i = 0; i < STEPS; ++i) {
-                        if (i + AHEAD - 1 < STEPS) read2(i + AHEAD - 1, wf[(i + AHEAD - 1) % AHEAD]);
+                    for (int i = 0; i < STEPS; i += 2) {
+                        if (i + 2 < STEPS) {
+                            read2(i + 2, wf[(i + 2) % 4]);
+                            read2(i + 3, wf[(i + 3) % 4]);
+                        }
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) dx[i][n] = mma(wf[i % AHEAD][0], da[n], dx[i][n]);
+                        for (int s = 0; s < 2; ++s)
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) dx[i][n] = mma(wf[i % AHEAD][1], db[n], dx[i][n]);
+                            for (int q = i; q < i + 2; ++q)
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) dx[q][n] = mma(wf[q % 4][s], s ? db[n] : da[n], dx[q][n]);
                         keep_order();
                     }
                 }
@@ -386,8 +405,8 @@ __global__ void __launch_bounds__(kDwWaves * 64) k_glu_rows_dw(GluParams p, int 
 #pragma unroll
         for (int i = 0; i < 2 * KC; ++i) dw[s][i] = f32x4r_t{0.f, 0.f, 0.f, 0.f};
     float sa = 0.f, sb = 0.f;
-    // One block: four tiles of 16 rows, the products with x after each second
-    // one.  What a step reads from LDS is asked for before the work of the step
+    // One block: two pairs of tiles of 16 rows, each followed by its products
+    // with x.  What a step reads from LDS is asked for before the work of the step
     // before it.
     auto block = [&](auto buffer) {
         constexpr uint32_t B = decltype(buffer)::value;
@@ -395,51 +414,59 @@ __global__ void __launch_bounds__(kDwWaves * 64) k_glu_rows_dw(GluParams p, int 
         float ua = 0.f, ub = 0.f;         // this block's sums first: short chains
         bf16x8r_t xf[2][KC];
         bf16x4r_t dh[2];
-        auto read_tile = [&](int t) {
+        auto read_tiles = [&](int hf) {
 #pragma unroll
-            for (int s = 0; s < KC; ++s) xf[t & 1][s] = read_unit(xa[s] + B * kDwXBytes + t * 16 * 256);
-            dh[t & 1] = read_tr(dt + B * kDwDBytes + t * 16 * 32);
+            for (int s = 0; s < KC; ++s)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    xf[t][s] = read_unit(xa[s] + B * kDwXBytes + (32 * hf + 16 * t) * 256);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) dh[t] = read_tr(dt + B * kDwDBytes + (32 * hf + 16 * t) * 32);
         };
-        auto channels = [&](int t, int i) {
-            const uint32_t q = xt[i] + B * kDwXBytes + (t >> 1) * 32 * 256;
+        auto channels = [&](int hf, int i) {
+            const uint32_t q = xt[i] + B * kDwXBytes + 32 * hf * 256;
             return join8(read_tr(q), read_tr(q + 16 * 256));
         };
         constexpr int AHEAD = 2 * KC < 4 ? 2 * KC : 4;
         bf16x8r_t xc[AHEAD];
-        bf16x4r_t da[2], db[2];
-        read_tile(0);
+        read_tiles(0);
 #pragma unroll
-        for (int t = 0; t < kDwRows / 16; ++t) {
-            f32x4r_t va = {ba, ba, ba, ba}, vb = {bb, bb, bb, bb};
+        for (int hf = 0; hf < kDwRows / 32; ++hf) {
+            f32x4r_t va[2], vb[2];
+            bf16x4r_t da[2], db[2];
 #pragma unroll
-            for (int s = 0; s < KC; ++s) {
-                va = mma(xf[t & 1][s], wt[0][s], va);
-                vb = mma(xf[t & 1][s], wt[1][s], vb);
+            for (int t = 0; t < 2; ++t) {
+                va[t] = f32x4r_t{ba, ba, ba, ba};
+                vb[t] = f32x4r_t{bb, bb, bb, bb};
             }
-            if (t & 1) {
 #pragma unroll
-                for (int i = 0; i < AHEAD; ++i) xc[i] = channels(t, i);
-            } else {
-                read_tile(t + 1);
-            }
+            for (int s = 0; s < KC; ++s)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    va[t] = mma(xf[t][s], wt[0][s], va[t]);
+                    vb[t] = mma(xf[t][s], wt[1][s], vb[t]);
+                }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) xc[i] = channels(hf, i);
             keep_order();
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const Act q = activation<ACT>(va[e]);
-                const float d = (float)dh[t & 1][e];
-                const float u = d * vb[e] * q.d, v = d * q.v;
-                ua += u;
-                ub += v;
-                da[t & 1][e] = (__bf16)u;
-                db[t & 1][e] = (__bf16)v;
-            }
-            if (!(t & 1)) continue;
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const Act q = activation<ACT>(va[t][e]);
+                    const float d = (float)dh[t][e];
+                    const float u = d * vb[t][e] * q.d, v = d * q.v;
+                    ua += u;
+                    ub += v;
+                    da[t][e] = (__bf16)u;
+                    db[t][e] = (__bf16)v;
+                }
             const bf16x8r_t fa = join8(da[0], da[1]), fb = join8(db[0], db[1]);
 #pragma unroll
             for (int i = 0; i < 2 * KC; ++i) {
                 const bf16x8r_t x0 = xc[i % AHEAD];
-                if (i + AHEAD < 2 * KC) xc[i % AHEAD] = channels(t, i + AHEAD);
-                if (i + 1 == 2 * KC && t + 1 < kDwRows / 16) read_tile(t + 1);
+                if (i + AHEAD < 2 * KC) xc[i % AHEAD] = channels(hf, i + AHEAD);
+                if (i + 2 == 2 * KC && hf + 1 < kDwRows / 32) read_tiles(hf + 1);
                 dw[0][i] = mma(fa, x0, dw[0][i]);
                 dw[1][i] = mma(fb, x0, dw[1][i]);
                 keep_order();
