@@ -149,26 +149,44 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p) {
     const uint32_t x1 = (swizzle(8 * g + (a >> 2)) ^ (a & 3)) * 16;
     const uint32_t w2 = w0 + (8 * (a >> 2) + (a & 3)) * PITCH * 2;
     const uint32_t x2 = (swizzle(8 * (a >> 2) + (a & 3)) ^ g) * 16;
-    const int64_t blocks = (p.N + kBlockRows - 1) / kBlockRows;
+    // The workgroup's tiles of 32 rows, numbered through its blocks.  With one
+    // slab its waves take them from a counter: of the two on a SIMD one runs
+    // ahead of the other, and with even shares it would leave the SIMD half
+    // idle for the last quarter (finishing after 213 us where the other took
+    // 294).  Which wave computes a tile does not change it.
+    int* taken = (int*)(lb + 2 * FS);
+    auto tile_row = [&](int i) {
+        return ((int64_t)(i / kRowWaves) * gridDim.x + blockIdx.x) * kBlockRows + i % kRowWaves * kWaveRows;
+    };
     const bool whole = FS >= F;
     if (whole) {
+        if (threadIdx.x == 0) *taken = kRowWaves;
         load_slab<KC>(lw, lb, p, 0);
         __syncthreads();
     }
+    auto next_tile = [&](int i) {
+        if (!whole) return i + kRowWaves;
+        int t = 0;
+        if ((threadIdx.x & 63) == 0) t = atomicAdd(taken, 1);
+        return __builtin_amdgcn_readfirstlane(t);
+    };
     // The next rows: the forward loads them a whole block ahead; dx, whose sums
     // need the registers, into the operands themselves after their last use.
     bf16x8r_t x[NT][KC], xn[DX ? 1 : NT][KC];
+    int tile = wave;
     if constexpr (DX)
-        load_rows(x, p, (int64_t)blockIdx.x * kBlockRows + wave * kWaveRows);
+        load_rows(x, p, tile_row(tile));
     else
-        load_rows(xn, p, (int64_t)blockIdx.x * kBlockRows + wave * kWaveRows);
-    for (int64_t blk = blockIdx.x; blk < blocks; blk += gridDim.x) {
-        const int64_t r0 = blk * kBlockRows + wave * kWaveRows;
+        load_rows(xn, p, tile_row(tile));
+    for (;;) {
+        const int64_t r0 = tile_row(tile);
+        if (whole ? r0 >= p.N : r0 - wave * kWaveRows >= p.N) break;      // (slabs: all waves together)
+        tile = next_tile(tile);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int s = 0; s < KC; ++s) x[n][s] = keep(DX ? x[n][s] : xn[DX ? 0 : n][s], 32 * s + 8 * g < C);
-        if constexpr (!DX) load_rows(xn, p, r0 + (int64_t)gridDim.x * kBlockRows);
+        if constexpr (!DX) load_rows(xn, p, tile_row(tile));
         f32x4r_t dx[DX ? 2 * KC : 1][NT];
         if constexpr (DX) {
 #pragma unroll
@@ -233,7 +251,7 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p) {
                     }
                     keep_order();
                 }
-                if (DX && f0 + fl + 32 >= F) load_rows(x, p, r0 + (int64_t)gridDim.x * kBlockRows);
+                if (DX && f0 + fl + 32 >= F) load_rows(x, p, tile_row(tile));
                 if constexpr (!DX) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
@@ -537,7 +555,7 @@ hipError_t rows_go(const GluParams& p, int what, int splits, hipStream_t st) {
                                                                                                              s.spread);
         return hipGetLastError();
     }
-    const size_t lds = (size_t)kSlabElems * 2 + (size_t)2 * kSlab<KC> * 4;
+    const size_t lds = (size_t)kSlabElems * 2 + (size_t)2 * kSlab<KC> * 4 + 16;
     const unsigned grid = (unsigned)std::min<int64_t>((p.N + kBlockRows - 1) / kBlockRows, kCUs);
     const auto fn = what ? k_glu_rows<KC, ACT, true> : k_glu_rows<KC, ACT, false>;
     const hipError_t e = hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
