@@ -153,8 +153,9 @@ __device__ __forceinline__ void forget_uses(Q& q) {
 
 // ---- chunks ---------------------------------------------------------------
 constexpr int kChunkGroup = 64;       // chunks per group
-constexpr int kCarryChannels = 64;    // channels per workgroup of k_scan_carry
+constexpr int kCarryChannels = 64;    // channels per workgroup of k_scan_groups and k_scan_carry
 constexpr int kCarryParts = kScanThreads / kCarryChannels;
+constexpr int kCarryPer = kChunkGroup / kCarryParts;
 
 // The maps w[0], w[stride], ... (n of them) composed after m, eight loads at a
 // time (the last again where fewer are left: no branch between the loads).
@@ -188,43 +189,62 @@ __device__ __forceinline__ float state_after(const Map* w, int64_t stride, int n
     return s;
 }
 
+// The chunks of a group as k_scan_groups and k_scan_carry share them: kCarryPer
+// for each of the workgroup's parts, all loaded together.
+struct CarryChunks {
+    Map m[kCarryPer];
+    int64_t at, step;      // of the first, from one to the next
+    int n;
+    __device__ __forceinline__ CarryChunks(const ScanParams& p, bool back, int part, int c, bool live) {
+        const int64_t first = (int64_t)blockIdx.x * kChunkGroup;
+        const int all = (int)min((int64_t)kChunkGroup, p.chunks - first), a = min(all, part * kCarryPer);
+        n = live ? min(kCarryPer, all - a) : 0;
+        step = back ? -p.C : p.C;
+        at = (back ? p.chunks + first + all - 1 - a : first + a) * p.C + c;
+#pragma unroll
+        for (int k = 0; k < kCarryPer; ++k) m[k] = k < n ? p.maps[at + k * step] : Map{1.f, 0.f};
+    }
+    __device__ __forceinline__ Map whole() const {
+        Map r = {1.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < kCarryPer; ++k) r = after(m[k], r);
+        return r;
+    }
+};
+
 // Maps of groups of chunks; blockIdx.z: the direction.
-__global__ void __launch_bounds__(256) k_scan_groups(ScanParams p) {
-    const int c = blockIdx.y * 256 + threadIdx.x;
-    if (c >= p.C) return;
+__global__ void __launch_bounds__(kScanThreads) k_scan_groups(ScanParams p) {
+    constexpr int CT = kCarryChannels;
+    __shared__ Map join[kScanThreads];
+    const int cl = threadIdx.x % CT, part = threadIdx.x / CT, c = blockIdx.y * CT + cl;
     const bool back = blockIdx.z;
-    const int64_t first = (int64_t)blockIdx.x * kChunkGroup;
-    const int n = (int)min((int64_t)kChunkGroup, p.chunks - first);
-    const int64_t dir = back ? p.chunks : 0;
-    const Map* w = p.maps + (dir + first) * p.C + c;
-    if (back) w += (int64_t)(n - 1) * p.C;
-    const Map m = compose_maps(w, back ? -p.C : p.C, n, {1.f, 0.f});
+    join[threadIdx.x] = CarryChunks(p, back, part, c, c < p.C).whole();
+    __syncthreads();
+    if (part || c >= p.C) return;
+    Map m = {1.f, 0.f};
+#pragma unroll
+    for (int q = 0; q < kCarryParts; ++q) m = after(join[q * CT + cl], m);
     p.groups[((back ? gridDim.x : 0) + blockIdx.x) * (int64_t)p.C + c] = m;
 }
 
 // States that enter the chunks of one group: the groups before it, then the
 // chunks before each of its own.
 __global__ void __launch_bounds__(kScanThreads) k_scan_carry(ScanParams p) {
-    constexpr int CT = kCarryChannels, PER = kChunkGroup / kCarryParts;
+    constexpr int CT = kCarryChannels;
     __shared__ Map join[kScanThreads], own[kScanThreads];
     const int cl = threadIdx.x % CT, part = threadIdx.x / CT;
     const int c = blockIdx.y * CT + cl;
     const bool back = blockIdx.z, live = c < p.C;
-    const int64_t step = back ? -p.C : p.C;
     const Map* g = p.groups + (back ? 2 * (int64_t)gridDim.x - 1 : 0) * p.C + c;
     const int before = back ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x;
-    // this part's chunks, in the direction's order
-    const int64_t first = (int64_t)blockIdx.x * kChunkGroup;
-    const int n = (int)min((int64_t)kChunkGroup, p.chunks - first);
-    const int a = min(n, part * PER), e = min(n, a + PER);
-    const int64_t at = ((back ? p.chunks + first + n - 1 - a : first + a)) * p.C + c;
-    own[part * CT + cl] = live ? compose_maps(p.maps + at, step, e - a, {1.f, 0.f}) : Map{1.f, 0.f};
-    float s = state_after<CT>(g, step, before, live, join);
+    const CarryChunks chunks(p, back, part, c, live);
+    own[threadIdx.x] = chunks.whole();
+    float s = state_after<CT>(g, back ? -p.C : p.C, before, live, join);
     for (int q = 0; q < part; ++q) s = apply(own[q * CT + cl], s);
-    if (!live) return;
-    for (int k = 0; k < e - a; ++k) {
-        p.carry[at + k * step] = s;
-        s = apply(p.maps[at + k * step], s);
+#pragma unroll
+    for (int k = 0; k < kCarryPer; ++k) {
+        if (k < chunks.n) p.carry[chunks.at + k * chunks.step] = s;
+        s = apply(chunks.m[k], s);
     }
 }
 
@@ -371,6 +391,10 @@ __device__ __forceinline__ Map scan_waves(Map* wave_maps, int c) {
     return all;
 }
 
+// Rows whose scenes' states are asked for together (a row at a time, each
+// would wait for its own: 64 scenes of one row took 18 us).
+constexpr int kSceneRows = 4;
+
 // Rows of a workgroup's chunk, and what its scenes need of them.
 template <typename T, int G, int L, bool WHOLE>
 struct Chunk {
@@ -389,9 +413,16 @@ struct Chunk {
     __device__ __forceinline__ typename Quad<T>::vec load(const void* t, int l, int C) const {
         return load_quad<T, WHOLE>((const T*)t, row[l], C, c0);
     }
-    // element i of a scene's state, 0 without states
-    __device__ __forceinline__ float of_scene(const float* t, int b, int i, int C) const {
-        return t ? t[(int64_t)b * C + min(c0 + i, C - 1)] : 0.f;
+    // The states t of up to four rows' scenes b (0 where a row has none, or
+    // without states), all loads in flight together.
+    __device__ __forceinline__ void of_scenes(const float* t, const int* b, float (&s)[kSceneRows][V], int C) const {
+#pragma unroll
+        for (int l = 0; l < kSceneRows; ++l) {
+            typename Quad<float>::vec v = {};
+            if (t) v = load_quad<float, WHOLE>(t, b[l], C, c0);
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[l][i] = v[i];
+        }
     }
 };
 
@@ -423,19 +454,24 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_maps(ScanParams p) {
     auto compose = [&](auto mk) {
 #pragma unroll
         for (int i = 0; i < V; ++i) m[i] = mb[i] = {1.f, 0.f};
+        float h0[kSceneRows][V], dl[kSceneRows][V];
 #pragma unroll
         for (int l = 0; l < L; ++l) {
             const int b = decltype(mk)::value ? marks.first[k.seg * L + l] : -1;
             const int e = decltype(mk)::value && GRAD ? marks.last[k.seg * L + l] : -1;
+            if (decltype(mk)::value && l % kSceneRows == 0) {
+                k.of_scenes(p.h0, marks.first + k.seg * L + l, h0, p.C);
+                if (GRAD) k.of_scenes(p.dlast, marks.last + k.seg * L + l, dl, p.C);
+            }
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const Step g = gate((float)z[l][i]);
                 const float v = g.n * (float)x[l][i];
                 float t = GRAD ? (float)d[l][i] : 0.f;
                 if (decltype(mk)::value) {
-                    if (GRAD && e >= 0) t += k.of_scene(p.dlast, e, i, p.C);
+                    if (GRAD && e >= 0) t += dl[l % kSceneRows][i];
                     if (b >= 0) {
-                        m[i] = {kForget, fmaf(g.f, k.of_scene(p.h0, b, i, p.C), v)};
+                        m[i] = {kForget, fmaf(g.f, h0[l % kSceneRows][i], v)};
                         if (GRAD) mb[i] = after(mb[i], {kForget, 0.f});
                     } else {
                         m[i] = after({g.f, v}, m[i]);
@@ -500,15 +536,18 @@ __global__ void __launch_bounds__(kScanThreads) k_scan(ScanParams p) {
     auto compose = [&](auto mk) {
 #pragma unroll
         for (int i = 0; i < V; ++i) pre[i] = {1.f, 0.f};
+        float h0[kSceneRows][V];
 #pragma unroll
         for (int l = 0; l < L; ++l) {
             const int b = decltype(mk)::value ? marks.first[k.seg * L + l] : -1;
+            if (decltype(mk)::value && l % kSceneRows == 0)
+                k.of_scenes(p.h0, marks.first + k.seg * L + l, h0, p.C);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const Step g = gate((float)z[l][i]);
                 const float v = g.n * (float)x[l][i];
                 if (decltype(mk)::value)
-                    pre[i] = b >= 0 ? Map{kForget, fmaf(g.f, k.of_scene(p.h0, b, i, p.C), v)} : after({g.f, v}, pre[i]);
+                    pre[i] = b >= 0 ? Map{kForget, fmaf(g.f, h0[l % kSceneRows][i], v)} : after({g.f, v}, pre[i]);
                 else
                     pre[i] = {g.f * pre[i].F, fmaf(g.f, pre[i].V, v)};
             }
@@ -534,13 +573,16 @@ __global__ void __launch_bounds__(kScanThreads) k_scan(ScanParams p) {
         forget_uses(x[l]);
     }
     auto walk = [&](auto mk) {
+        float h0[kSceneRows][V];
 #pragma unroll
         for (int l = 0; l < L; ++l) {
             const int b = decltype(mk)::value ? marks.first[k.seg * L + l] : -1;
             const int e = decltype(mk)::value ? marks.last[k.seg * L + l] : -1;
+            if (decltype(mk)::value && l % kSceneRows == 0)
+                k.of_scenes(p.h0, marks.first + k.seg * L + l, h0, p.C);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                if (decltype(mk)::value && b >= 0) s[i] = k.of_scene(p.h0, b, i, p.C);
+                if (decltype(mk)::value && b >= 0) s[i] = h0[l % kSceneRows][i];
                 const Step g = gate((float)z[l][i]);
                 s[i] = fmaf(g.f, s[i], g.n * (float)x[l][i]);
                 if (decltype(mk)::value && e >= 0 && i < k.nv) p.last[(int64_t)e * p.C + k.c0 + i] = s[i];
@@ -594,6 +636,11 @@ __global__ void __launch_bounds__(kScanThreads, 4) k_scan_grad(ScanParams p) {
     auto compose = [&](auto mk) {
 #pragma unroll
         for (int i = 0; i < V; ++i) m[i] = mb[i] = {1.f, 0.f};
+        float h0[kSceneRows][V], dl[kSceneRows][V];
+        if (decltype(mk)::value) {
+            k.of_scenes(p.h0, marks.first + k.seg * L, h0, p.C);
+            k.of_scenes(p.dlast, marks.last + k.seg * L, dl, p.C);
+        }
 #pragma unroll
         for (int l = 0; l < L; ++l) {
             const int b = decltype(mk)::value ? marks.first[k.seg * L + l] : -1;
@@ -606,9 +653,9 @@ __global__ void __launch_bounds__(kScanThreads, 4) k_scan_grad(ScanParams p) {
                 n[l][i] = g.n;
                 float t = (float)d[l][i];
                 if (decltype(mk)::value) {
-                    if (e >= 0) t += k.of_scene(p.dlast, e, i, p.C);
+                    if (e >= 0) t += dl[l][i];
                     if (b >= 0) {
-                        m[i] = {kForget, fmaf(g.f, k.of_scene(p.h0, b, i, p.C), v)};
+                        m[i] = {kForget, fmaf(g.f, h0[l][i], v)};
                         mb[i] = after(mb[i], {kForget, 0.f});
                     } else {
                         m[i] = after({g.f, v}, m[i]);
@@ -643,17 +690,26 @@ __global__ void __launch_bounds__(kScanThreads, 4) k_scan_grad(ScanParams p) {
         s[i] = apply(m[i], apply(wave_maps[0][at], state[0][k.lane * V + i]));
         y[i] = apply(mb[i], apply(wave_maps[1][at], state[1][k.lane * V + i]));
     }
+    static_assert(L == kSceneRows, "one group of rows");
+    auto states = [&](auto mk) {
+        float h0[kSceneRows][V];
+        if (decltype(mk)::value) k.of_scenes(p.h0, marks.first + k.seg * L, h0, p.C);
 #pragma unroll
-    for (int l = 0; l < L; ++l) {
-        const int b = marked ? marks.first[k.seg * L + l] : -1;
+        for (int l = 0; l < L; ++l) {
+            const int b = decltype(mk)::value ? marks.first[k.seg * L + l] : -1;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float xv = (float)x[l][i];
-            if (b >= 0) s[i] = k.of_scene(p.h0, b, i, p.C);
-            q[l][i] = (s[i] - xv) * (f[l][i] * n[l][i]);
-            s[i] = fmaf(f[l][i], s[i], n[l][i] * xv);
+            for (int i = 0; i < V; ++i) {
+                const float xv = (float)x[l][i];
+                if (decltype(mk)::value && b >= 0) s[i] = h0[l][i];
+                q[l][i] = (s[i] - xv) * (f[l][i] * n[l][i]);
+                s[i] = fmaf(f[l][i], s[i], n[l][i] * xv);
+            }
         }
-    }
+    };
+    if (marked)
+        states(std::true_type{});
+    else
+        states(std::false_type{});
 #pragma unroll
     for (int l = L - 1; l >= 0; --l) {
         const int b = marked ? marks.first[k.seg * L + l] : -1;
@@ -724,7 +780,8 @@ hipError_t scan_go(ScanParams p, bool grad, const ScanLayout& l, char* ws, hipSt
             k_scan_maps<T, G, kScanRows, WHOLE, false><<<grid, kScanThreads, 0, st>>>(p);
     }
     if (l.groups > 1) {
-        k_scan_groups<<<dim3((unsigned)l.groups, (p.C + 255) / 256, l.dirs), 256, 0, st>>>(p);
+        k_scan_groups<<<dim3((unsigned)l.groups, (p.C + kCarryChannels - 1) / kCarryChannels, l.dirs), kScanThreads, 0,
+                        st>>>(p);
         k_scan_carry<<<dim3((unsigned)l.groups, (p.C + kCarryChannels - 1) / kCarryChannels, l.dirs), kScanThreads, 0,
                        st>>>(p);
     }
