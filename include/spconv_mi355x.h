@@ -335,7 +335,8 @@ int spconv_glu_grad(const void* dout, const void* x, const void* w, const float*
                     int dtype, void* stream);
 
 /* Gated linear recurrence over the voxels of each scene, in a given order
- * (the map's schedule order from spconv_nmap_export is a space-filling curve):
+ * (the map's schedule order from spconv_nmap_export follows a space-filling
+ * curve, 128 voxels at a time):
  *   h[t] = f[t] h[t-1] + (1 - f[t]) x[t],   f[t] = sigmoid(z[t])
  * per channel, along the positions t = offsets[b] .. offsets[b+1] - 1 of scene
  * b, from h0[b] before the first.

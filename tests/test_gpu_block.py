@@ -1,0 +1,79 @@
+"""The example's block, forward and backward, against autograd of the same
+formulas in 64 bits.
+
+The longest sum has 27 C = 864 terms, six operators stand in a row, and each
+rounds to float32: an output's norm is off by at most about 6 * 864 * 2^-24 =
+3.1e-4 of itself.
+"""
+import importlib.util
+import os
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import submanifold_sparse_convolution_spconv_amd as sp
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+C = 32
+TOL = 6 * 27 * C * 2.0 ** -24
+
+
+def example():
+    spec = importlib.util.spec_from_file_location("voxel_block", os.path.join(ROOT, "examples", "voxel_block.py"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+def conv(u, nbr, w):
+    pad = torch.cat([u, u.new_zeros(1, u.shape[1])])
+    return sum(pad[nbr[k]] @ w[k] for k in range(w.shape[0]))
+
+
+def block64(p, x, nbr, order):
+    """The block's formulas on the host in 64 bits."""
+    dev = x - x.mean(1, keepdim=True)
+    u = dev / torch.sqrt(dev.square().mean(1, keepdim=True) + 1e-5) * p["norm_w"] + p["norm_b"]
+    v, z = conv(u, nbr, p["w_value"]), conv(u, nbr, p["w_gate"])
+    f, s, h = torch.sigmoid(z), torch.zeros_like(x[0]), [None] * x.shape[0]
+    for r in order.tolist():
+        s = f[r] * s + (1 - f[r]) * v[r]
+        h[r] = s
+    a, b = (torch.stack(h) @ p["w_glu"][i] + p["b_glu"][i] for i in range(2))
+    return x + a * torch.sigmoid(a) * b
+
+
+def close(got, want, what):
+    err = float((got.double().cpu() - want).norm() / want.norm())
+    assert err <= TOL, f"{what}: {err:.3g} of its norm off, {TOL:.3g} allowed"
+
+
+def test_block_and_its_gradient():
+    rng = np.random.default_rng(3)
+    coords = np.argwhere(rng.random((9, 9, 9)) < 0.4).astype(np.int32)
+    coords = coords[rng.permutation(coords.shape[0])]
+    N = coords.shape[0]
+    nm = sp.spconv_build_nmap(torch.from_numpy(coords).cuda(), 27, 1)
+    _, order = nm.export()
+    offsets = torch.tensor([0, N], dtype=torch.int32, device="cuda")
+    block = example().VoxelBlock(C, dtype=torch.float32)
+    g = torch.Generator().manual_seed(4)
+    x, dy = torch.randn(N, C, generator=g), torch.randn(N, C, generator=g)
+    block.params["norm_w"] += 0.2 * torch.randn(C, generator=g).cuda()
+    block.params["b_glu"] += 0.2 * torch.randn(2, C, generator=g).cuda()
+
+    y, saved = block.forward(x.cuda(), nm, order, offsets)
+    dx, grads = block.backward(dy.cuda(), saved, nm, order, offsets)
+
+    p = {k: v.double().cpu().requires_grad_() for k, v in block.params.items()}
+    x64 = x.double().requires_grad_()
+    nbr = torch.from_numpy(oracle.nmap(coords, 27, 1)).long()
+    want = block64(p, x64, nbr, order.cpu())
+    want.backward(dy.double())
+    close(y, want.detach(), "y")
+    close(dx, x64.grad, "dx")
+    for name, v in p.items():
+        close(grads[name], v.grad, name)
