@@ -57,6 +57,31 @@ __device__ __forceinline__ void opaque(uint32_t& v) { asm volatile("" : "+v"(v))
 // Matrix instructions and LDS reads stay on their sides of this, so that the
 // next step's operands are read before this step's products, not after.
 __device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0x416); }
+// Consecutive rows as a buffer: a load's place costs one 32-bit offset (bytes),
+// and past the rows it reads zeros.
+constexpr uint32_t kOutside = 0x7FFFFFF0u;
+struct RowBuffer {
+    __amdgpu_buffer_rsrc_t r;
+    __device__ __forceinline__ RowBuffer(const __bf16* p, int elems)
+        : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<__bf16*>(p), (short)0, elems * 2, 0x00020000)) {}
+    __device__ __forceinline__ bf16x8r_t load8(uint32_t offset, uint32_t step = 0) const {
+        const auto w = __builtin_amdgcn_raw_buffer_load_b128(r, offset, step, 0);
+        bf16x8r_t v;
+        __builtin_memcpy(&v, &w, 16);
+        return v;
+    }
+};
+// One activation's instructions stand between four matrix instructions, whose
+// operands' reads come first.
+__device__ __forceinline__ void interleave() {
+    __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x402, 4, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+}
 __device__ __forceinline__ void store_unit(__bf16* p, bf16x8r_t v, bool stream) {
     if (stream)
         __builtin_nontemporal_store(v, (bf16x8r_t*)p);
@@ -332,6 +357,8 @@ __global__ void __launch_bounds__(kRowThreads) k_glu_rows(GluParams p) {
 constexpr int kDwWaves = 8;
 constexpr int kDwRows = 64;
 constexpr int kDwXBytes = kDwRows * 256, kDwDBytes = kDwRows * 32;      // of one buffer; dout: per wave
+constexpr int kDwBuffers = 3;
+constexpr int kDwLds = kDwBuffers * (kDwXBytes + kDwWaves * kDwDBytes);
 
 // x tile: rows of 256 bytes, 16-byte unit u of row r at u ^ swizzle_row(r):
 // conflict-free for 16 rows' unit u and for two units of four consecutive rows
@@ -339,7 +366,7 @@ __device__ __forceinline__ int swizzle_row(int r) { return ((r & 7) << 1) | ((r 
 
 template <int KC, int ACT>
 __global__ void __launch_bounds__(kDwWaves * 64) k_glu_rows_dw(GluParams p, int slabs, int spread) {
-    __shared__ __align__(16) char smem[2 * kDwXBytes + 2 * kDwWaves * kDwDBytes];
+    extern __shared__ __align__(16) char smem[];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, a = lane & 15, g = lane >> 4;
     const int C = p.C, F = p.F;
     // the slabs of one split on one XCD (workgroups go round the 8 in turn)
@@ -376,7 +403,7 @@ __global__ void __launch_bounds__(kDwWaves * 64) k_glu_rows_dw(GluParams p, int 
 #pragma unroll
     for (int i = 0; i < 2 * KC; ++i)
         xt[i] = lds0 + rt * 256 + ((2 * i + ((a & 3) >> 1)) ^ swizzle_row(rt)) * 16 + 8 * (a & 1);
-    const uint32_t d0 = lds0 + 2 * kDwXBytes + wave * 2 * kDwDBytes;
+    const uint32_t d0 = lds0 + kDwBuffers * kDwXBytes + wave * kDwBuffers * kDwDBytes;
     const uint32_t dt = d0 + rt * 32 + 8 * (a & 3);
 
     // x's 64 rows: units of KC * 32 channels, PER of them per thread (half of
@@ -388,27 +415,26 @@ __global__ void __launch_bounds__(kDwWaves * 64) k_glu_rows_dw(GluParams p, int 
     const bool loads = xr < kDwRows && 8 * xu < C;
     const int dr = threadIdx.x >> 4, du = threadIdx.x & 15, df = slab * spread * 16 + 8 * du;
     bf16x8r_t rx[PER], rd[2];
+    uint32_t ox[PER], od[2];                           // bytes from the block's first row
+#pragma unroll
+    for (int j = 0; j < PER; ++j) ox[j] = loads ? ((xr + RSTEP * j) * C + 8 * xu) * 2 : kOutside;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) od[j] = df < F ? ((dr + 32 * j) * F + df) * 2 : kOutside;
+    // (rows past the split read as zeros)
     auto fetch = [&](int64_t k) {
+        const int rows = (int)max((int64_t)0, min((int64_t)kDwRows, k1 - k));
+        const RowBuffer bx((const __bf16*)p.x + k * C, rows * C), bd((const __bf16*)p.dout + k * F, rows * F);
 #pragma unroll
-        for (int j = 0; j < PER; ++j)
-            rx[j] = load8((const __bf16*)p.x + min(k + xr + RSTEP * j, k1 - 1) * C + (loads ? 8 * xu : 0));
+        for (int j = 0; j < PER; ++j) rx[j] = bx.load8(ox[j]);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            rd[j] = load8((const __bf16*)p.dout + min(k + dr + 32 * j, k1 - 1) * F + (df < F ? df : 0));
+        for (int j = 0; j < 2; ++j) rd[j] = bd.load8(od[j]);
     };
     // Channels past C were cleared once and are never written; features past F
-    // keep to their own columns, which are not stored; rows past the split are
-    // zero, in its last block.
+    // are zero.
     const uint32_t px = lds0 + xr * 256 + (xu ^ swizzle_row(xr)) * 16;
-    const uint32_t pd = lds0 + 2 * kDwXBytes + (du >> 1) * 2 * kDwDBytes + dr * 32 + (du & 1) * 16;
-    auto put = [&](auto buffer, int64_t k) {
+    const uint32_t pd = lds0 + kDwBuffers * kDwXBytes + (du >> 1) * kDwBuffers * kDwDBytes + dr * 32 + (du & 1) * 16;
+    auto put = [&](auto buffer) {
         constexpr uint32_t B = decltype(buffer)::value;
-        if (k + kDwRows > k1) {
-#pragma unroll
-            for (int j = 0; j < PER; ++j) rx[j] = keep(rx[j], k + xr + RSTEP * j < k1);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) rd[j] = keep(rd[j], k + dr + 32 * j < k1);
-        }
         if (loads) {
 #pragma unroll
             for (int j = 0; j < PER; ++j)
@@ -422,92 +448,98 @@ __global__ void __launch_bounds__(kDwWaves * 64) k_glu_rows_dw(GluParams p, int 
     for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int i = 0; i < 2 * KC; ++i) dw[s][i] = f32x4r_t{0.f, 0.f, 0.f, 0.f};
+    // Three things of 32 rows each are under way at once: the projections of
+    // the next rows, the activations of these, the products of the last ones
+    // with x.  They need nothing of each other, so that a wave's matrix
+    // instructions run in the shadow of its activations.
     float sa = 0.f, sb = 0.f;
-    // One block: two pairs of tiles of 16 rows, each followed by its products
-    // with x.  What a step reads from LDS is asked for before the work of the step
-    // before it.
-    auto block = [&](auto buffer) {
-        constexpr uint32_t B = decltype(buffer)::value;
+    f32x4r_t va[2] = {}, vb[2] = {};      // projections, by tile of 16 rows
+    bf16x4r_t dh[2] = {};                 // dout of their rows
+    bf16x8r_t fa = {}, fb = {};           // da and db of the rows before
+    // Both halves of the block in buffer B are projected; what is left of the
+    // block before, in buffer P, is finished.
+    auto block = [&](auto cur, auto prev) {
+        constexpr uint32_t B = decltype(cur)::value, P = decltype(prev)::value;
         if (!works) return;
+        constexpr int STEPS = 2 * KC, EACH = 8 / STEPS, AHEAD = 3;
         float ua = 0.f, ub = 0.f;         // this block's sums first: short chains
-        bf16x8r_t xf[2][KC];
-        bf16x4r_t dh[2];
-        auto read_tiles = [&](int hf) {
-#pragma unroll
-            for (int s = 0; s < KC; ++s)
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    xf[t][s] = read_unit(xa[s] + B * kDwXBytes + (32 * hf + 16 * t) * 256);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) dh[t] = read_tr(dt + B * kDwDBytes + (32 * hf + 16 * t) * 32);
+        // operands of step i: unit s = i / 2 % KC of tile i % 2 of half i / STEPS;
+        // channels i % STEPS of the half, transposed
+        bf16x8r_t xf[AHEAD], xc[AHEAD];
+        auto ask = [&](int i) {
+            const int hf = i / STEPS, q = i % STEPS;
+            xf[i % AHEAD] = read_unit(xa[q >> 1] + B * kDwXBytes + (32 * hf + 16 * (q & 1)) * 256);
+            const uint32_t t = xt[q] + P * kDwXBytes + 32 * hf * 256;
+            xc[i % AHEAD] = join8(read_tr(t), read_tr(t + 16 * 256));
         };
-        auto channels = [&](int hf, int i) {
-            const uint32_t q = xt[i] + B * kDwXBytes + 32 * hf * 256;
-            return join8(read_tr(q), read_tr(q + 16 * 256));
-        };
-        constexpr int AHEAD = 2 * KC < 4 ? 2 * KC : 4;
-        bf16x8r_t xc[AHEAD];
-        read_tiles(0);
+#pragma unroll
+        for (int i = 0; i < AHEAD - 1; ++i) ask(i);
 #pragma unroll
         for (int hf = 0; hf < kDwRows / 32; ++hf) {
-            f32x4r_t va[2], vb[2];
-            bf16x4r_t da[2], db[2];
+            bf16x4r_t dn[2], da[2], db[2];
+            f32x4r_t na[2], nb[2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                va[t] = f32x4r_t{ba, ba, ba, ba};
-                vb[t] = f32x4r_t{bb, bb, bb, bb};
+                dn[t] = read_tr(dt + B * kDwDBytes + (32 * hf + 16 * t) * 32);
+                na[t] = f32x4r_t{ba, ba, ba, ba};
+                nb[t] = f32x4r_t{bb, bb, bb, bb};
             }
 #pragma unroll
-            for (int s = 0; s < KC; ++s)
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    va[t] = mma(xf[t][s], wt[0][s], va[t]);
-                    vb[t] = mma(xf[t][s], wt[1][s], vb[t]);
+            for (int c = 0; c < 8; ++c) {
+                const int i = hf * STEPS + c / EACH, q = i % STEPS;
+                if (c % EACH == 0) {
+                    if (i + AHEAD - 1 < 2 * STEPS) ask(i + AHEAD - 1);
+                    const bf16x8r_t x1 = xf[i % AHEAD], x0 = xc[i % AHEAD];
+                    na[q & 1] = mma(x1, wt[0][q >> 1], na[q & 1]);
+                    nb[q & 1] = mma(x1, wt[1][q >> 1], nb[q & 1]);
+                    dw[0][q] = mma(fa, x0, dw[0][q]);
+                    dw[1][q] = mma(fb, x0, dw[1][q]);
                 }
+                const int t = c / 4, e = c % 4;
+                const Act act = activation<ACT>(va[t][e]);
+                const float d = (float)dh[t][e];
+                const float u = d * vb[t][e] * act.d, v = d * act.v;
+                ua += u;
+                ub += v;
+                da[t][e] = (__bf16)u;
+                db[t][e] = (__bf16)v;
+                interleave();
+            }
+            fa = join8(da[0], da[1]);
+            fb = join8(db[0], db[1]);
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) xc[i] = channels(hf, i);
-            keep_order();
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const Act q = activation<ACT>(va[t][e]);
-                    const float d = (float)dh[t][e];
-                    const float u = d * vb[t][e] * q.d, v = d * q.v;
-                    ua += u;
-                    ub += v;
-                    da[t][e] = (__bf16)u;
-                    db[t][e] = (__bf16)v;
-                }
-            const bf16x8r_t fa = join8(da[0], da[1]), fb = join8(db[0], db[1]);
-#pragma unroll
-            for (int i = 0; i < 2 * KC; ++i) {
-                const bf16x8r_t x0 = xc[i % AHEAD];
-                if (i + AHEAD < 2 * KC) xc[i % AHEAD] = channels(hf, i + AHEAD);
-                if (i + 2 == 2 * KC && hf + 1 < kDwRows / 32) read_tiles(hf + 1);
-                dw[0][i] = mma(fa, x0, dw[0][i]);
-                dw[1][i] = mma(fb, x0, dw[1][i]);
-                keep_order();
+            for (int t = 0; t < 2; ++t) {
+                va[t] = na[t];
+                vb[t] = nb[t];
+                dh[t] = dn[t];
             }
         }
         sa += ua;
         sb += ub;
     };
-    for (int e = threadIdx.x; e < 2 * kDwXBytes / 16; e += kDwWaves * 64) *(bf16x8r_t*)(smem + 16 * e) = bf16x8r_t{};
+    for (int e = threadIdx.x; e < kDwBuffers * kDwXBytes / 16; e += kDwWaves * 64)
+        *(bf16x8r_t*)(smem + 16 * e) = bf16x8r_t{};
     constexpr std::integral_constant<uint32_t, 0> b0{};
     constexpr std::integral_constant<uint32_t, 1> b1{};
+    constexpr std::integral_constant<uint32_t, 2> b2{};
     fetch(k0);
     __syncthreads();
-    put(b0, k0);
-    for (int64_t k = k0; k < k1; k += 2 * kDwRows) {
-        fetch(min(k + kDwRows, k1 - 1));
-        __syncthreads();
-        block(b0);
-        put(b1, k + kDwRows);
-        fetch(min(k + 2 * kDwRows, k1 - 1));
-        __syncthreads();
-        block(b1);                        // zeros past the last row
-        put(b0, k + 2 * kDwRows);
+    put(b0);
+    // One block past the last row (zeros) finishes the last.  A block is written
+    // where the one before the last was: no wave reads that any more.
+    const int64_t ke = k1 + kDwRows;
+    for (int64_t k = k0;;) {
+        auto one = [&](auto cur, auto prev, auto next) {
+            fetch(k + kDwRows);
+            __syncthreads();
+            block(cur, prev);
+            put(next);
+            k += kDwRows;
+            return k < ke;
+        };
+        if (!one(b0, b2, b1)) break;
+        if (!one(b1, b0, b2)) break;
+        if (!one(b2, b1, b0)) break;
     }
     if (!works) return;
     // output m = 4 g + e: feature f + m; channel 16 i + a
@@ -542,7 +574,7 @@ DwShape dw_shape(int64_t N, int C, int F) {
     const int tiles = (F + 15) / 16;
     s.slabs = (tiles + kDwWaves - 1) / kDwWaves;
     s.spread = (tiles + s.slabs - 1) / s.slabs;
-    const int64_t groups = (int64_t)kCUs * (C <= 32 ? 2 : 1);      // workgroups that the registers hold
+    const int64_t groups = kCUs;      // one workgroup per CU
     s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(groups / s.slabs, (N + kDwRows - 1) / kDwRows));
     return s;
 }
@@ -551,8 +583,11 @@ template <int KC, int ACT>
 hipError_t rows_go(const GluParams& p, int what, int splits, hipStream_t st) {
     if (what == 2) {
         const DwShape s = dw_shape(p.N, p.C, p.F);
-        k_glu_rows_dw<KC, ACT><<<(unsigned)((splits + 7) / 8 * 8 * s.slabs), kDwWaves * 64, 0, st>>>(p, s.slabs,
-                                                                                                             s.spread);
+        const hipError_t e = hipFuncSetAttribute((const void*)k_glu_rows_dw<KC, ACT>,
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, kDwLds);
+        if (e != hipSuccess) return e;
+        k_glu_rows_dw<KC, ACT><<<(unsigned)((splits + 7) / 8 * 8 * s.slabs), kDwWaves * 64, kDwLds, st>>>(p, s.slabs,
+                                                                                                         s.spread);
         return hipGetLastError();
     }
     const size_t lds = (size_t)kSlabElems * 2 + (size_t)2 * kSlab<KC> * 4 + 16;
