@@ -521,11 +521,24 @@ def spconv_wgrad(feats, dout, nmap: NMap, out=None, workspace=None):
 
 # The row operators' calls are short (a single voxel's takes a few microseconds
 # on the GPU), so what stands around them here is kept short too: addresses as
-# plain integers, a device guard only where another device is current.
+# plain integers, torch looked up once, a device guard only where another device
+# is current, outputs made like the inputs.
+_torch = None
+_row_codes = {}
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _row_codes.update({torch.float32: SPCONV_F32, torch.bfloat16: SPCONV_BF16})
+    _torch = torch
+
+
 def _row_dtype(x, name="x"):
     """The dtype code of a feature tensor (N, C)."""
-    import torch
-    dt = SPCONV_F32 if x.dtype == torch.float32 else SPCONV_BF16 if x.dtype == torch.bfloat16 else None
+    if _torch is None:
+        _load_torch()
+    dt = _row_codes.get(x.dtype)
     if dt is None or x.dim() != 2 or not x.is_cuda:
         raise ValueError(f"{name} must be a float32 or bfloat16 (N, C) CUDA tensor")
     return dt
@@ -537,13 +550,13 @@ def _at(t):
 
 def _call(name, dev, *args):
     """The C function on the current stream of dev."""
-    import torch
     fn = getattr(_lib or load_library(), name)
-    if torch.cuda.current_device() == dev.index:
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    index = dev.index
+    if _torch._C._cuda_getDevice() == index:
+        rc = fn(*args, _torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+        with _torch.cuda.device(dev):
+            rc = fn(*args, _torch._C._cuda_getCurrentRawStream(index))
     if rc:
         _check(rc, name)
 
@@ -565,22 +578,22 @@ def _like(t, shape, dtype, device, name):
     return t.contiguous()
 
 
-def _out(out, shape, dtype, device, name):
-    import torch
+def _out(out, shape, like, name):
+    """The output of this shape, of like's type and device: the caller's,
+    checked, or a new one."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if out.shape != shape or out.dtype != dtype or out.device != device or not out.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} {tuple(shape)} tensor on the features' device")
+        return _torch.empty_like(like) if like.shape == shape else like.new_empty(shape)
+    if out.shape != shape or out.dtype != like.dtype or out.device != like.device or not out.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {like.dtype} {tuple(shape)} tensor on the features' device")
     return out
 
 
 def _workspace(workspace, n, device, size_name):
     """The workspace and its bytes: the caller's, checked, or one of n bytes
     (none for 0)."""
-    import torch
     if workspace is None:
-        return (torch.empty(n, dtype=torch.uint8, device=device) if n else None), n
-    if workspace.dtype != torch.uint8 or workspace.numel() < n or workspace.device != device \
+        return (_torch.empty(n, dtype=_torch.uint8, device=device) if n else None), n
+    if workspace.dtype != _torch.uint8 or workspace.numel() < n or workspace.device != device \
             or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {size_name} bytes")
     return workspace, workspace.numel()
@@ -590,16 +603,15 @@ def spconv_layernorm(x, weight=None, bias=None, eps: float = 1e-5, stats: bool =
     """Layer norm over each row's channels: x (N, C) float32 or bfloat16, CUDA,
     C <= 4096; weight, bias float32 (C,) or None.  Returns y in x's dtype, with
     ``stats`` (y, mean, rstd), float32 (N,) each, for the gradient."""
-    import torch
     dt = _row_dtype(x)
     N, C = x.shape
     dev = x.device
     x = x.contiguous()
-    weight = _like(weight, (C,), torch.float32, dev, "weight")
-    bias = _like(bias, (C,), torch.float32, dev, "bias")
-    y = _out(out, (N, C), x.dtype, dev, "out")
-    mean = torch.empty(N, dtype=torch.float32, device=dev) if stats else None
-    rstd = torch.empty(N, dtype=torch.float32, device=dev) if stats else None
+    weight = _like(weight, (C,), _torch.float32, dev, "weight")
+    bias = _like(bias, (C,), _torch.float32, dev, "bias")
+    y = _out(out, x.shape, x, "out")
+    mean = _torch.empty(N, dtype=_torch.float32, device=dev) if stats else None
+    rstd = _torch.empty(N, dtype=_torch.float32, device=dev) if stats else None
     _call("spconv_layernorm", dev, _at(x), _at(weight), _at(bias), _at(y), _at(mean), _at(rstd), N, C, eps, dt)
     return (y, mean, rstd) if stats else y
 
@@ -614,25 +626,24 @@ def spconv_layernorm_grad(dout, x, mean, rstd, weight=None, out=None, workspace=
     dbias float32 (C,), or None both where weight is None.  workspace: a uint8
     tensor of at least spconv_layernorm_grad_workspace_size bytes (allocated
     when None)."""
-    import torch
     dt = _row_dtype(x)
     N, C = x.shape
     dev = x.device
     x = x.contiguous()
     dout = _like(dout, (N, C), x.dtype, dev, "dout")
-    mean = _like(mean, (N,), torch.float32, dev, "mean")
-    rstd = _like(rstd, (N,), torch.float32, dev, "rstd")
+    mean = _like(mean, (N,), _torch.float32, dev, "mean")
+    rstd = _like(rstd, (N,), _torch.float32, dev, "rstd")
     if dout is None or mean is None or rstd is None:
         raise ValueError("dout, mean and rstd must be given")
-    weight = _like(weight, (C,), torch.float32, dev, "weight")
-    dx = _out(out, (N, C), x.dtype, dev, "out")
+    weight = _like(weight, (C,), _torch.float32, dev, "weight")
+    dx = _out(out, x.shape, x, "out")
     ws = dweight = dbias = None
     n = 0
     if weight is not None:
         ws, n = _workspace(workspace, spconv_layernorm_grad_workspace_size(N, C, dt), dev,
                            "spconv_layernorm_grad_workspace_size")
-        dweight = torch.empty(C, dtype=torch.float32, device=dev)
-        dbias = torch.empty(C, dtype=torch.float32, device=dev)
+        dweight = _torch.empty_like(weight)
+        dbias = _torch.empty_like(weight)
     _call("spconv_layernorm_grad", dev, _at(dout), _at(x), _at(mean), _at(rstd), _at(weight), _at(ws), n, _at(dx),
           _at(dweight), _at(dbias), N, C, dt)
     return dx, dweight, dbias
@@ -642,7 +653,6 @@ _ACTS = {"silu": SPCONV_SILU, "gelu": SPCONV_GELU}
 
 
 def _glu_args(x, w, bias, act):
-    import torch
     dt = _row_dtype(x)
     N, C = x.shape
     dev = x.device
@@ -651,7 +661,7 @@ def _glu_args(x, w, bias, act):
     if act not in _ACTS:
         raise ValueError(f"act must be one of {sorted(_ACTS)}")
     F = w.shape[2]
-    bias = _like(bias, (2, F), torch.float32, dev, "bias")
+    bias = _like(bias, (2, F), _torch.float32, dev, "bias")
     return dt, N, C, F, dev, x.contiguous(), w.contiguous(), bias, _ACTS[act]
 
 
@@ -660,9 +670,8 @@ def spconv_glu(x, w, bias=None, act: str = "silu", out=None):
     and w (2, C, F), both float32 or both bfloat16, CUDA; bias float32 (2, F) or
     None; act "silu" or "gelu" (erf); C and F multiples of 8 up to 4096.
     Returns h (N, F) in their dtype."""
-    import torch
     dt, N, C, F, dev, x, w, bias, a = _glu_args(x, w, bias, act)
-    h = _out(out, (N, F), x.dtype, dev, "out")
+    h = _out(out, (N, F), x, "out")
     _call("spconv_glu", dev, _at(x), _at(w), _at(bias), _at(h), N, C, F, a, dt)
     return h
 
@@ -676,14 +685,13 @@ def spconv_glu_grad(dout, x, w, bias=None, act: str = "silu", workspace=None):
     (N, C), dw (2, C, F), dbias float32 (2, F), or None where bias is None).
     workspace: a uint8 tensor of at least spconv_glu_grad_workspace_size bytes
     (allocated when None)."""
-    import torch
     dt, N, C, F, dev, x, w, bias, a = _glu_args(x, w, bias, act)
     dout = _like(dout, (N, F), x.dtype, dev, "dout")
     if dout is None:
         raise ValueError("dout must be given")
-    dx = torch.empty_like(x)
-    dw = torch.empty_like(w)
-    dbias = torch.empty_like(bias) if bias is not None else None
+    dx = _torch.empty_like(x)
+    dw = _torch.empty_like(w)
+    dbias = _torch.empty_like(bias) if bias is not None else None
     ws, n = _workspace(workspace, spconv_glu_grad_workspace_size(N, C, F, dt), dev, "spconv_glu_grad_workspace_size")
     _call("spconv_glu_grad", dev, _at(dout), _at(x), _at(w), _at(bias), _at(ws), n, _at(dx), _at(dw), _at(dbias), N,
           C, F, a, dt)
@@ -691,19 +699,18 @@ def spconv_glu_grad(dout, x, w, bias=None, act: str = "silu", workspace=None):
 
 
 def _scan_args(x, z, offsets, order, h0):
-    import torch
     dt = _row_dtype(x)
     N, C = x.shape
     dev = x.device
     if z is None or offsets is None:
         raise ValueError("z and offsets must be given")
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or offsets.device != dev:
+    if offsets.dtype != _torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or offsets.device != dev:
         raise ValueError("offsets must be an int32 (scenes + 1,) tensor on the features' device")
     B = offsets.numel() - 1
     x = x.contiguous()
     z = _like(z, (N, C), x.dtype, dev, "z")
-    order = _like(order, (N,), torch.int32, dev, "order")
-    h0 = _like(h0, (B, C), torch.float32, dev, "h0")
+    order = _like(order, (N,), _torch.int32, dev, "order")
+    h0 = _like(h0, (B, C), _torch.float32, dev, "h0")
     return dt, N, C, B, dev, x, z, offsets.contiguous(), order, h0
 
 
@@ -719,10 +726,9 @@ def spconv_scan(x, z, offsets, order=None, h0=None, out=None, workspace=None):
     start from (None: zero).  Returns (h (N, C) in the caller's row order, last
     (scenes, C) float32: each scene's last state).  workspace: a uint8 tensor of
     at least spconv_scan_workspace_size bytes (allocated when None)."""
-    import torch
     dt, N, C, B, dev, x, z, offsets, order, h0 = _scan_args(x, z, offsets, order, h0)
-    h = _out(out, (N, C), x.dtype, dev, "out")
-    last = torch.empty((B, C), dtype=torch.float32, device=dev)
+    h = _out(out, x.shape, x, "out")
+    last = _torch.empty((B, C), dtype=_torch.float32, device=dev)
     ws, n = _workspace(workspace, spconv_scan_workspace_size(N, C, dt), dev, "spconv_scan_workspace_size")
     _call("spconv_scan", dev, _at(x), _at(z), _at(offsets), _at(order), _at(h0), _at(ws), n, _at(h), _at(last), N, C,
           B, dt)
@@ -739,15 +745,14 @@ def spconv_scan_grad(dout, x, z, offsets, order=None, h0=None, dlast=None, works
     dh0 float32 (scenes, C), or None where h0 is None.  workspace: a uint8
     tensor of at least spconv_scan_grad_workspace_size bytes (allocated when
     None)."""
-    import torch
     dt, N, C, B, dev, x, z, offsets, order, h0 = _scan_args(x, z, offsets, order, h0)
     dout = _like(dout, (N, C), x.dtype, dev, "dout")
     if dout is None:
         raise ValueError("dout must be given")
-    dlast = _like(dlast, (B, C), torch.float32, dev, "dlast")
-    dx = torch.empty_like(x)
-    dz = torch.empty_like(x)
-    dh0 = torch.empty_like(h0) if h0 is not None else None
+    dlast = _like(dlast, (B, C), _torch.float32, dev, "dlast")
+    dx = _torch.empty_like(x)
+    dz = _torch.empty_like(x)
+    dh0 = _torch.empty_like(h0) if h0 is not None else None
     ws, n = _workspace(workspace, spconv_scan_grad_workspace_size(N, C, dt), dev, "spconv_scan_grad_workspace_size")
     _call("spconv_scan_grad", dev, _at(dout), _at(x), _at(z), _at(offsets), _at(order), _at(h0), _at(dlast), _at(ws),
           n, _at(dx), _at(dz), _at(dh0), N, C, B, dt)

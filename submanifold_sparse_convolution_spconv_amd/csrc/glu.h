@@ -19,9 +19,11 @@ struct GluParams {
     void* dw;
     float* bpart;      // [row tiles][2][F] partial sums of dbias; or NULL
     float* wpart;      // [splits][C][2 F] partial sums of dw; NULL: one split, into dw
+    float* xpart;      // [dx splits][N][C] partial sums of dx; NULL: one split, into dx
     int64_t N;
     int C, F;
     int64_t rows_per_split;
+    int dx_splits, dx_per;      // of dx's reduction (2 F), and its length
     bool stream;       // outputs past the caches
 };
 

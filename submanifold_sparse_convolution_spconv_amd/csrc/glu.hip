@@ -23,14 +23,14 @@ namespace spc {
 
 namespace {
 
-// Tiles of TILE x TILE outputs: two waves along the first operand, WN along the
+// Tiles of TILE x TILE outputs: WM waves along the first operand, WN along the
 // second; a wave holds NM x NN blocks of 16 x 16.  Eight waves share the large
 // tile rather than four: with half the accumulators each, four fit on a SIMD,
 // and short reductions spend less of their time waiting.
 template <int TILE>
 struct Shape {
-    static constexpr int WN = TILE / 32, THREADS = 128 * WN;
-    static constexpr int NM = TILE / 32, NN = TILE / 16 / WN;
+    static constexpr int WM = TILE >= 64 ? 2 : 1, WN = TILE >= 64 ? TILE / 32 : 2, THREADS = 64 * WM * WN;
+    static constexpr int NM = TILE / 16 / WM, NN = TILE / 16 / WN;
 };
 
 template <typename V>
@@ -296,9 +296,10 @@ unsigned block_count(int64_t outer, int64_t inner) {
 template <typename T, int ACT, bool GRAD, int TILE>
 __global__ void __launch_bounds__(Shape<TILE>::THREADS, TILE == 128 ? 4 : 3) k_glu_project(GluParams p) {
     constexpr int NM = Shape<TILE>::NM, NN = Shape<TILE>::NN, WN = Shape<TILE>::WN, FT = TILE / 2;
+    constexpr int FW = FT / Shape<TILE>::WM;      // features of a wave
     __shared__ __align__(16) char smem[kProductBytes<T, false, true, TILE>];
     __shared__ float bsum[WN][2][FT];
-    const int wave = threadIdx.x >> 6, wm = wave & 1, wn = wave >> 1;
+    const int wave = threadIdx.x >> 6, wm = wave % Shape<TILE>::WM, wn = wave / Shape<TILE>::WM;
     const int a = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
     const int C = p.C, F = p.F;
     int64_t tile;
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(Shape<TILE>::THREADS, TILE == 128 ? 4 : 3) k_g
                               [&](int m) { return f0 + m % FT < F; }, f0 + FT <= F, F);
     Operand<T, true, TILE> B(x + r0 * C, [&](int n) { return (uint32_t)n * C; },
                              [&](int n) { return r0 + n < p.N; }, r0 + TILE <= p.N, 0);
-    // A lane's features: E in a row (of the wave's FT / 2: 4 from each block, 8
+    // A lane's features: E in a row (of the wave's FW: 4 from each block, 8
     // from each pair of blocks).
     constexpr int PAIR = NM / 2 >= 2 ? 2 : 1, E = 4 * PAIR, NP = NM / 2 / PAIR;
     typedef typename Group<T, E>::vec group;
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(Shape<TILE>::THREADS, TILE == 128 ? 4 : 3) k_g
     group dh[GRAD ? NP : 1][NN];
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-        f[i] = f0 + FT / 2 * wm + 16 * PAIR * i + E * g;
+        f[i] = f0 + FW * wm + 16 * PAIR * i + E * g;
 #pragma unroll
         for (int q = 0; q < PAIR; ++q) {
             const int at = f[i] < F ? f[i] + 4 * q : 0;
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(Shape<TILE>::THREADS, TILE == 128 ? 4 : 3) k_g
         acc, A, B, 0, C, smem,
         [&](int i) {
             const int k = i % (NM / 2);
-            return FT * (2 * i / NM) + FT / 2 * wm + 16 * PAIR * (k / PAIR) + 4 * (k % PAIR);
+            return FT * (2 * i / NM) + FW * wm + 16 * PAIR * (k / PAIR) + 4 * (k % PAIR);
         },
         [&](int j) { return 16 * NN * wn + 16 * j; });
 #pragma unroll
@@ -413,27 +414,31 @@ __global__ void __launch_bounds__(Shape<TILE>::THREADS, TILE == 128 ? 4 : 3) k_g
     }
 }
 
-// dx: TILE rows x TILE channels, reduced over both halves of dab.
+// dx: TILE rows x TILE channels, reduced over both halves of dab, or over one
+// split of them as a partial sum.
 template <typename T, int TILE>
 __device__ __forceinline__ void glu_dx_tile(const GluParams& p, int64_t block, char* smem) {
     constexpr int NM = Shape<TILE>::NM, NN = Shape<TILE>::NN;
-    const int wave = threadIdx.x >> 6, wm = wave & 1, wn = wave >> 1;
+    const int wave = threadIdx.x >> 6, wm = wave % Shape<TILE>::WM, wn = wave / Shape<TILE>::WM;
     const int a = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
     const int C = p.C, F = p.F;
     int64_t r0;
-    int c0;
-    if (!place_block(block, (p.N + TILE - 1) / TILE, (C + TILE - 1) / TILE, r0, c0)) return;
+    int at;
+    const int ct = (C + TILE - 1) / TILE;
+    if (!place_block(block, (p.N + TILE - 1) / TILE, ct * p.dx_splits, r0, at)) return;
     r0 *= TILE;
-    c0 *= TILE;
+    const int c0 = at % ct * TILE, split = at / ct;
     f32x4r_t acc[NM][NN];
     clear_blocks(acc);
 #pragma unroll 1
     for (int s = 0; s < 2; ++s) {
+        const int k0 = max(split * p.dx_per - s * F, 0), k1 = min((split + 1) * p.dx_per - s * F, F);
+        if (k0 >= k1) continue;
         Operand<T, true, TILE> A((const T*)p.w + ((int64_t)s * C + c0) * F, [&](int m) { return (uint32_t)m * F; },
                                  [&](int m) { return c0 + m < C; }, c0 + TILE <= C, 0);
         Operand<T, true, TILE> B((const T*)p.dab + r0 * 2 * F + s * F, [&](int n) { return (uint32_t)n * 2 * F; },
                                  [&](int n) { return r0 + n < p.N; }, r0 + TILE <= p.N, 0);
-        tile_product<T, true, true, TILE>(acc, A, B, 0, F, smem, [&](int i) { return 16 * NM * wm + 16 * i; },
+        tile_product<T, true, true, TILE>(acc, A, B, k0, k1, smem, [&](int i) { return 16 * NM * wm + 16 * i; },
                                           [&](int j) { return 16 * NN * wn + 16 * j; });
     }
 #pragma unroll
@@ -443,8 +448,12 @@ __device__ __forceinline__ void glu_dx_tile(const GluParams& p, int64_t block, c
         for (int j = 0; j < NN; ++j) {
             const int64_t r = r0 + 16 * NN * wn + 16 * j + a;
             if (r >= p.N || c >= C) continue;
-            const float o[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-            store_four((T*)p.dx + r * C + c, o);
+            if (p.xpart) {
+                *(f32x4r_t*)(p.xpart + (split * p.N + r) * C + c) = acc[i][j];
+            } else {
+                const float o[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                store_four((T*)p.dx + r * C + c, o);
+            }
         }
     }
 }
@@ -454,7 +463,7 @@ __device__ __forceinline__ void glu_dx_tile(const GluParams& p, int64_t block, c
 template <typename T, int TILE>
 __device__ __forceinline__ void glu_dw_tile(const GluParams& p, int64_t block, char* smem) {
     constexpr int NM = Shape<TILE>::NM, NN = Shape<TILE>::NN;
-    const int wave = threadIdx.x >> 6, wm = wave & 1, wn = wave >> 1;
+    const int wave = threadIdx.x >> 6, wm = wave % Shape<TILE>::WM, wn = wave / Shape<TILE>::WM;
     const int a = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
     const int C = p.C, F = p.F, F2 = 2 * F;
     const int mt = (F2 + TILE - 1) / TILE, ct = (C + TILE - 1) / TILE;
@@ -500,11 +509,24 @@ __global__ void __launch_bounds__(Shape<TILE>::THREADS, TILE == 128 ? 4 : 3) k_g
         glu_dw_tile<T, TILE>(p, blockIdx.x - dx_blocks, smem);
 }
 
-// The partial sums of dw (splits, C, 2 F) and dbias (tiles, 2 F) added in
-// their order and rounded once; the first w_blocks workgroups serve dw.
+// The partial sums of dw (splits, C, 2 F), dbias (tiles, 2 F) and dx (splits,
+// N, C) added in their order and rounded once; the first w_blocks workgroups
+// serve dw, the next b_blocks dbias.
 template <typename T>
 __global__ void __launch_bounds__(kJoinCols * 16) k_glu_join(GluParams p, int splits, int64_t tiles, float* dbias,
-                                                             unsigned w_blocks) {
+                                                             unsigned w_blocks, unsigned b_blocks) {
+    if (blockIdx.x >= w_blocks + b_blocks) {
+        // few splits: a lane adds four columns by itself
+        const int64_t n = p.N * p.C;
+        const int64_t e = ((int64_t)(blockIdx.x - w_blocks - b_blocks) * (kJoinCols * 16) + threadIdx.x) * 4;
+        if (e >= n) return;
+        f32x4r_t t = *(const f32x4r_t*)(p.xpart + e);
+#pragma unroll 4
+        for (int q = 1; q < p.dx_splits; ++q) t += *(const f32x4r_t*)(p.xpart + q * n + e);
+        const float o[4] = {t[0], t[1], t[2], t[3]};
+        store_four((T*)p.dx + e, o);
+        return;
+    }
     const int F = p.F;
     const bool w = blockIdx.x < w_blocks;
     const int64_t n = w ? (int64_t)p.C * 2 * F : 2 * F;
@@ -528,13 +550,15 @@ bool use_rows(int64_t N, int C, int dtype) { return dtype == SPCONV_BF16 && C <=
 // often), of 64 where they would not.
 int64_t tiles_of(int64_t n, int tile) { return (n + tile - 1) / tile; }
 // (fp32, whose matrix instructions take four times as long as their operands'
-// reads, only has the small ones.)
+// reads, has no use for those.)
 int big_tile(bool fills, int dtype) { return fills && dtype == SPCONV_BF16 ? 128 : 64; }
 
 struct GluLayout {
     size_t dab, bpart, wpart, total;
     int64_t tiles, rows_per_split;    // row tiles of the projections; rows per split of dw
     int splits, tile, ptile;          // tile of the products and of the projections
+    int dx_splits, dx_per;
+    size_t xpart;
     bool rows;
 };
 GluLayout glu_layout(int64_t N, int C, int F, int dtype) {
@@ -550,6 +574,11 @@ GluLayout glu_layout(int64_t N, int C, int F, int dtype) {
         return l;
     }
     l.ptile = big_tile(tiles_of(N, 128) * tiles_of(F, 64) >= 256, dtype);
+    // The projections' reduction is not split (the activations need all of it).
+    // In fp32 a tile of 64 is 32 cycles of matrix instructions for each channel:
+    // tiles of 32 where those of 64 leave CUs idle (one row, 1024 -> 4096: 32.5
+    // -> 23.3 us; a little slower where they do not).
+    if (dtype == SPCONV_F32 && tiles_of(N, 64) * tiles_of(F, 32) < 256) l.ptile = 32;
     l.tiles = tiles_of(N, l.ptile);
     l.tile = big_tile(tiles_of(N, 128) * tiles_of(C, 128) >= 192, dtype);
     // enough workgroups for two per CU, at least 128 rows each
@@ -564,6 +593,20 @@ GluLayout glu_layout(int64_t N, int C, int F, int dtype) {
     if (l.tiles > 1) at += align_up((size_t)l.tiles * 2 * F * 4, 256);
     l.wpart = at;
     if (l.splits > 1) at += align_up((size_t)l.splits * C * 2 * F * 4, 256);
+    // dx, where its tiles leave most of the card idle and its reduction is long
+    // (one row, 1024 -> 4096 fp32: 248 us unsplit): splits of at least four steps,
+    // or eight where only dx would need the sums to be joined
+    const int bk = dtype == SPCONV_BF16 ? kTileK<__bf16> : kTileK<float>, least = l.splits > 1 ? 4 : 8;
+    const int64_t dx = std::max<int64_t>(1, tiles_of(N, l.tile) * tiles_of(C, l.tile)), steps = tiles_of(2 * F, bk);
+    l.dx_splits = 1;
+    l.dx_per = 2 * F;
+    if (dx < 256 && steps >= 3 * least) {
+        const int64_t want = std::min<int64_t>((512 + dx - 1) / dx, steps / least);
+        l.dx_per = (int)tiles_of(steps, want) * bk;
+        l.dx_splits = (int)tiles_of(2 * F, l.dx_per);
+    }
+    l.xpart = at;
+    if (l.dx_splits > 1) at += align_up((size_t)l.dx_splits * N * C * 4, 256);
     l.total = at;
     return l;
 }
@@ -571,10 +614,16 @@ GluLayout glu_layout(int64_t N, int C, int F, int dtype) {
 template <typename T, int ACT>
 hipError_t glu_project(const GluParams& p, bool grad, const GluLayout& l, hipStream_t st) {
     const unsigned blocks = block_count(l.tiles, tiles_of(p.F, l.ptile / 2));
-    const int threads = l.ptile == 128 ? Shape<128>::THREADS : Shape<64>::THREADS;
+    int threads = Shape<64>::THREADS;
     auto fn = grad ? k_glu_project<T, ACT, true, 64> : k_glu_project<T, ACT, false, 64>;
     if constexpr (sizeof(T) == 2) {
-        if (l.ptile == 128) fn = grad ? k_glu_project<T, ACT, true, 128> : k_glu_project<T, ACT, false, 128>;
+        if (l.ptile == 128) {
+            fn = grad ? k_glu_project<T, ACT, true, 128> : k_glu_project<T, ACT, false, 128>;
+            threads = Shape<128>::THREADS;
+        }
+    } else if (l.ptile == 32) {
+        fn = grad ? k_glu_project<T, ACT, true, 32> : k_glu_project<T, ACT, false, 32>;
+        threads = Shape<32>::THREADS;
     }
     fn<<<blocks, threads, 0, st>>>(p);
     return hipGetLastError();
@@ -582,7 +631,7 @@ hipError_t glu_project(const GluParams& p, bool grad, const GluLayout& l, hipStr
 
 template <typename T>
 hipError_t glu_products(const GluParams& p, const GluLayout& l, hipStream_t st) {
-    const unsigned dx = block_count(tiles_of(p.N, l.tile), tiles_of(p.C, l.tile));
+    const unsigned dx = block_count(tiles_of(p.N, l.tile), tiles_of(p.C, l.tile) * l.dx_splits);
     const unsigned dw = block_count(l.splits, tiles_of(2 * p.F, l.tile) * tiles_of(p.C, l.tile));
     const int threads = l.tile == 128 ? Shape<128>::THREADS : Shape<64>::THREADS;
     auto fn = k_glu_products<T, 64>;
@@ -612,7 +661,9 @@ hipError_t glu_go(GluParams p, int act, bool grad, const GluLayout& l, float* db
     const bool w = p.wpart || p.N == 0, b = dbias && (p.bpart != dbias || p.N == 0);
     const unsigned wb = w ? (unsigned)tiles_of((int64_t)p.C * 2 * p.F, 4 * kJoinCols) : 0;
     const unsigned bb = b ? (unsigned)tiles_of(2 * p.F, 4 * kJoinCols) : 0;
-    if (wb + bb) k_glu_join<T><<<wb + bb, kJoinCols * 16, 0, st>>>(p, l.splits, l.tiles, dbias, wb);
+    const unsigned xb = p.xpart ? (unsigned)tiles_of(p.N * p.C, 4 * kJoinCols * 16) : 0;
+    if (wb + bb + xb)
+        k_glu_join<T><<<wb + bb + xb, kJoinCols * 16, 0, st>>>(p, l.splits, l.tiles, dbias, wb, bb);
     return hipGetLastError();
 }
 
@@ -637,6 +688,9 @@ hipError_t launch_glu(const GluArgs& a, bool grad, hipStream_t stream) {
         p.dab = ws + l.dab;
         if (a.dbias) p.bpart = l.rows || l.tiles > 1 ? (float*)(ws + l.bpart) : a.dbias;
         if (l.rows || l.splits > 1) p.wpart = (float*)(ws + l.wpart);
+        if (l.dx_splits > 1) p.xpart = (float*)(ws + l.xpart);
+        p.dx_splits = l.dx_splits;
+        p.dx_per = l.dx_per;
     }
     p.N = a.N;
     p.C = a.C;

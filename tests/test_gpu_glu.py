@@ -121,6 +121,15 @@ def test_many_rows(N, C, F, dt):
     check_grad(d, x, w, b, "silu")
 
 
+@DTS
+@pytest.mark.parametrize("N, C, F", [(5, 72, 1544), (130, 200, 2008), (1, 1024, 4096), (700, 64, 840), (260, 8, 392), (2100, 40, 1000)])
+def test_few_rows_of_wide_weights(N, C, F, dt):
+    """The input gradient's reduction in splits, which end inside the halves."""
+    for kind, bias in (("silu", False), ("gelu", True)):
+        x, w, b, d = inputs(N, C, F, dt, bias)
+        check_grad(d, x, w, b, kind)
+
+
 @pytest.mark.parametrize("N, C, F", [(32768, 128, 256), (40007, 128, 264), (33000, 8, 8), (50001, 40, 1000),
                                      (66000, 64, 72), (65537, 104, 512), (100003, 24, 136), (33333, 96, 2048)])
 def test_rows_with_few_channels(N, C, F):
