@@ -42,8 +42,11 @@ constexpr int kScanV = 4;            // channels per lane
 // then hold twice the rows, and joining the segments costs half as much for
 // each element.
 constexpr int kScanGroup = 32;
-constexpr int kScanRows = 8;         // rows per lane, forward
-constexpr int kScanGradRows = 4;     // and gradient, which holds more of each
+// Rows per lane, forward: eight, or for short sequences, whose time is a lane's
+// own, four where chunks are few (no groups of them, or not two per CU), and two
+// where one chunk has all rows (3,000 x 128: 18.5 us with eight, 15.6 with four).  Gradient, which holds more of each: four.
+constexpr int kScanRows = 8, kScanRowsShort = 4, kScanRowsOne = 2;
+constexpr int kScanGradRows = 4;
 
 struct Step {
     float f, n;      // sigmoid(z), sigmoid(-z)
@@ -307,14 +310,19 @@ __device__ __forceinline__ bool wave_marks(const SceneMarks<R>& m, int seg) {
     return __any(any);
 }
 
-// Scenes without rows: their state is what came in.  The lanes of the grid
-// share the scenes; one writes its scene's channels alone (they are few).
-__device__ __forceinline__ void empty_scenes(const ScanParams& p, const float* in, float* out, int channels) {
-    const int c0 = blockIdx.y * channels, c1 = min(p.C, c0 + channels);
-    for (int64_t b = (int64_t)blockIdx.x * kScanThreads + threadIdx.x; b < p.scenes;
-         b += (int64_t)gridDim.x * kScanThreads) {
-        if (p.offsets[b + 1] > p.offsets[b]) continue;
-        for (int c = c0; c < c1; ++c) out[b * p.C + c] = in ? in[b * p.C + c] : 0.f;
+// Scenes without rows: their state is what came in.  A wave looks at 64 scenes
+// at once, or at 8 where that reaches all of them, and writes the empty ones.
+__device__ __forceinline__ void empty_scenes(const ScanParams& p, int tile, const float* in, float* out, int channels) {
+    const int c0 = tile * channels, c1 = min(p.C, c0 + channels), lane = threadIdx.x & 63;
+    const int64_t waves = (int64_t)gridDim.x * kScanWaves;
+    const int per = p.scenes <= 8 * waves ? 8 : 64;
+    for (int64_t b0 = ((int64_t)blockIdx.x * kScanWaves + (threadIdx.x >> 6)) * per; b0 < p.scenes; b0 += waves * per) {
+        const int64_t b = b0 + lane, at = min(b, (int64_t)p.scenes - 1);
+        uint64_t empty = __ballot(lane < per && b < p.scenes && p.offsets[at + 1] <= p.offsets[at]);
+        for (; empty; empty &= empty - 1) {
+            const int64_t e = b0 + __builtin_ctzll(empty);
+            for (int c = c0 + lane; c < c1; c += 64) out[e * p.C + c] = in ? in[e * p.C + c] : 0.f;
+        }
     }
 }
 
@@ -393,7 +401,8 @@ __device__ __forceinline__ Map scan_waves(Map* wave_maps, int c) {
 
 // Rows whose scenes' states are asked for together (a row at a time, each
 // would wait for its own: 64 scenes of one row took 18 us).
-constexpr int kSceneRows = 4;
+template <int L>
+constexpr int kSceneRows = L < 4 ? L : 4;
 
 // Rows of a workgroup's chunk, and what its scenes need of them.
 template <typename T, int G, int L, bool WHOLE>
@@ -415,9 +424,9 @@ struct Chunk {
     }
     // The states t of up to four rows' scenes b (0 where a row has none, or
     // without states), all loads in flight together.
-    __device__ __forceinline__ void of_scenes(const float* t, const int* b, float (&s)[kSceneRows][V], int C) const {
+    __device__ __forceinline__ void of_scenes(const float* t, const int* b, float (&s)[kSceneRows<L>][V], int C) const {
 #pragma unroll
-        for (int l = 0; l < kSceneRows; ++l) {
+        for (int l = 0; l < kSceneRows<L>; ++l) {
             typename Quad<float>::vec v = {};
             if (t) v = load_quad<float, WHOLE>(t, b[l], C, c0);
 #pragma unroll
@@ -430,7 +439,7 @@ struct Chunk {
 template <typename T, int G, int L, bool WHOLE, bool GRAD>
 __global__ void __launch_bounds__(kScanThreads) k_scan_maps(ScanParams p) {
     using K = Chunk<T, G, L, WHOLE>;
-    constexpr int V = K::V;
+    constexpr int V = K::V, SR = kSceneRows<L>;
     __shared__ SceneMarks<K::R> marks;
     __shared__ Map wave_maps[GRAD ? 2 : 1][kScanWaves * K::CT];
     const int64_t chunk = blockIdx.x;
@@ -454,12 +463,12 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_maps(ScanParams p) {
     auto compose = [&](auto mk) {
 #pragma unroll
         for (int i = 0; i < V; ++i) m[i] = mb[i] = {1.f, 0.f};
-        float h0[kSceneRows][V], dl[kSceneRows][V];
+        float h0[SR][V], dl[SR][V];
 #pragma unroll
         for (int l = 0; l < L; ++l) {
             const int b = decltype(mk)::value ? marks.first[k.seg * L + l] : -1;
             const int e = decltype(mk)::value && GRAD ? marks.last[k.seg * L + l] : -1;
-            if (decltype(mk)::value && l % kSceneRows == 0) {
+            if (decltype(mk)::value && l % SR == 0) {
                 k.of_scenes(p.h0, marks.first + k.seg * L + l, h0, p.C);
                 if (GRAD) k.of_scenes(p.dlast, marks.last + k.seg * L + l, dl, p.C);
             }
@@ -469,9 +478,9 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_maps(ScanParams p) {
                 const float v = g.n * (float)x[l][i];
                 float t = GRAD ? (float)d[l][i] : 0.f;
                 if (decltype(mk)::value) {
-                    if (GRAD && e >= 0) t += dl[l % kSceneRows][i];
+                    if (GRAD && e >= 0) t += dl[l % SR][i];
                     if (b >= 0) {
-                        m[i] = {kForget, fmaf(g.f, h0[l % kSceneRows][i], v)};
+                        m[i] = {kForget, fmaf(g.f, h0[l % SR][i], v)};
                         if (GRAD) mb[i] = after(mb[i], {kForget, 0.f});
                     } else {
                         m[i] = after({g.f, v}, m[i]);
@@ -505,16 +514,15 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_maps(ScanParams p) {
 // The states, with the chunks' entering states known.  From the last chunk to
 // the first: the rows that k_scan_maps read last are still in the memory-side
 // cache.
-template <typename T, int G, bool WHOLE>
+template <typename T, int G, int L, bool WHOLE>
 __global__ void __launch_bounds__(kScanThreads) k_scan(ScanParams p) {
-    constexpr int L = kScanRows;
     using K = Chunk<T, G, L, WHOLE>;
-    constexpr int V = K::V, CT = K::CT;
+    constexpr int V = K::V, CT = K::CT, SR = kSceneRows<L>;
     __shared__ SceneMarks<K::R> marks;
     __shared__ Map wave_maps[kScanWaves * CT], join[kScanThreads];
     __shared__ float state[CT];
     if (p.N == 0) {              // nothing to read: the scenes' states alone
-        empty_scenes(p, p.h0, p.last, CT);
+        empty_scenes(p, blockIdx.y, p.h0, p.last, CT);
         return;
     }
     const int64_t chunk = p.chunks - 1 - blockIdx.x;
@@ -525,6 +533,7 @@ __global__ void __launch_bounds__(kScanThreads) k_scan(ScanParams p) {
         z[l] = k.load(p.z, l, p.C);
         x[l] = k.load(p.x, l, p.C);
     }
+    empty_scenes(p, blockIdx.y, p.h0, p.last, CT);      // (while the rows are on their way)
     entering_state<CT, false>(p, chunk, join, state);
     mark_scenes(marks, p, k.p0);
     if (any_missing(k.row)) {
@@ -536,18 +545,18 @@ __global__ void __launch_bounds__(kScanThreads) k_scan(ScanParams p) {
     auto compose = [&](auto mk) {
 #pragma unroll
         for (int i = 0; i < V; ++i) pre[i] = {1.f, 0.f};
-        float h0[kSceneRows][V];
+        float h0[SR][V];
 #pragma unroll
         for (int l = 0; l < L; ++l) {
             const int b = decltype(mk)::value ? marks.first[k.seg * L + l] : -1;
-            if (decltype(mk)::value && l % kSceneRows == 0)
+            if (decltype(mk)::value && l % SR == 0)
                 k.of_scenes(p.h0, marks.first + k.seg * L + l, h0, p.C);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const Step g = gate((float)z[l][i]);
                 const float v = g.n * (float)x[l][i];
                 if (decltype(mk)::value)
-                    pre[i] = b >= 0 ? Map{kForget, fmaf(g.f, h0[l % kSceneRows][i], v)} : after({g.f, v}, pre[i]);
+                    pre[i] = b >= 0 ? Map{kForget, fmaf(g.f, h0[l % SR][i], v)} : after({g.f, v}, pre[i]);
                 else
                     pre[i] = {g.f * pre[i].F, fmaf(g.f, pre[i].V, v)};
             }
@@ -573,16 +582,16 @@ __global__ void __launch_bounds__(kScanThreads) k_scan(ScanParams p) {
         forget_uses(x[l]);
     }
     auto walk = [&](auto mk) {
-        float h0[kSceneRows][V];
+        float h0[SR][V];
 #pragma unroll
         for (int l = 0; l < L; ++l) {
             const int b = decltype(mk)::value ? marks.first[k.seg * L + l] : -1;
             const int e = decltype(mk)::value ? marks.last[k.seg * L + l] : -1;
-            if (decltype(mk)::value && l % kSceneRows == 0)
+            if (decltype(mk)::value && l % SR == 0)
                 k.of_scenes(p.h0, marks.first + k.seg * L + l, h0, p.C);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                if (decltype(mk)::value && b >= 0) s[i] = h0[l % kSceneRows][i];
+                if (decltype(mk)::value && b >= 0) s[i] = h0[l % SR][i];
                 const Step g = gate((float)z[l][i]);
                 s[i] = fmaf(g.f, s[i], g.n * (float)x[l][i]);
                 if (decltype(mk)::value && e >= 0 && i < k.nv) p.last[(int64_t)e * p.C + k.c0 + i] = s[i];
@@ -594,7 +603,6 @@ __global__ void __launch_bounds__(kScanThreads) k_scan(ScanParams p) {
         walk(std::true_type{});
     else
         walk(std::false_type{});
-    empty_scenes(p, p.h0, p.last, CT);
 }
 
 // The gradient, with the states that enter the chunks known in both
@@ -603,12 +611,12 @@ template <typename T, int G, bool WHOLE>
 __global__ void __launch_bounds__(kScanThreads, 4) k_scan_grad(ScanParams p) {
     constexpr int L = kScanGradRows;
     using K = Chunk<T, G, L, WHOLE>;
-    constexpr int V = K::V, CT = K::CT;
+    constexpr int V = K::V, CT = K::CT, SR = kSceneRows<L>;
     __shared__ SceneMarks<K::R> marks;
     __shared__ Map wave_maps[2][kScanWaves * CT], join[2][kScanThreads];
     __shared__ float state[2][CT];
     if (p.N == 0) {
-        if (p.last) empty_scenes(p, p.dlast, p.last, CT);
+        if (p.last) empty_scenes(p, blockIdx.y, p.dlast, p.last, CT);
         return;
     }
     const int64_t chunk = p.chunks - 1 - blockIdx.x;
@@ -620,6 +628,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) k_scan_grad(ScanParams p) {
         x[l] = k.load(p.x, l, p.C);
         d[l] = k.load(p.dout, l, p.C);
     }
+    if (p.last) empty_scenes(p, blockIdx.y, p.dlast, p.last, CT);
     entering_state<CT, false>(p, chunk, join[0], state[0]);
     entering_state<CT, true>(p, chunk, join[1], state[1]);
     mark_scenes(marks, p, k.p0);
@@ -636,7 +645,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) k_scan_grad(ScanParams p) {
     auto compose = [&](auto mk) {
 #pragma unroll
         for (int i = 0; i < V; ++i) m[i] = mb[i] = {1.f, 0.f};
-        float h0[kSceneRows][V], dl[kSceneRows][V];
+        float h0[SR][V], dl[SR][V];
         if (decltype(mk)::value) {
             k.of_scenes(p.h0, marks.first + k.seg * L, h0, p.C);
             k.of_scenes(p.dlast, marks.last + k.seg * L, dl, p.C);
@@ -690,9 +699,9 @@ __global__ void __launch_bounds__(kScanThreads, 4) k_scan_grad(ScanParams p) {
         s[i] = apply(m[i], apply(wave_maps[0][at], state[0][k.lane * V + i]));
         y[i] = apply(mb[i], apply(wave_maps[1][at], state[1][k.lane * V + i]));
     }
-    static_assert(L == kSceneRows, "one group of rows");
+    static_assert(L == SR, "one group of rows");
     auto states = [&](auto mk) {
-        float h0[kSceneRows][V];
+        float h0[SR][V];
         if (decltype(mk)::value) k.of_scenes(p.h0, marks.first + k.seg * L, h0, p.C);
 #pragma unroll
         for (int l = 0; l < L; ++l) {
@@ -731,7 +740,6 @@ __global__ void __launch_bounds__(kScanThreads, 4) k_scan_grad(ScanParams p) {
         store_quad<T, WHOLE>((T*)p.h, k.row[l], p.C, k.c0, ox, p.stream);
         store_quad<T, WHOLE>((T*)p.dz, k.row[l], p.C, k.c0, oz, p.stream);
     }
-    if (p.last) empty_scenes(p, p.dlast, p.last, CT);
 }
 
 // Lanes per row: enough for its channels, kScanGroup at most (wider rows take
@@ -741,20 +749,28 @@ int scan_group(int C) {
     while (G < kScanGroup && G * kScanV < C) G *= 2;
     return G;
 }
-int64_t scan_chunks(int64_t N, int C, bool grad) {
-    const int64_t R = (int64_t)(kScanThreads / scan_group(C)) * (grad ? kScanGradRows : kScanRows);
+int64_t scan_chunks(int64_t N, int C, int rows) {
+    const int64_t R = (int64_t)(kScanThreads / scan_group(C)) * rows;
     return std::max<int64_t>(1, (N + R - 1) / R);
+}
+int scan_rows(int64_t N, int C, bool grad) {
+    if (grad) return kScanGradRows;
+    if (scan_chunks(N, C, kScanRowsOne) == 1) return kScanRowsOne;
+    const int64_t tiles = (C + scan_group(C) * kScanV - 1) / (scan_group(C) * kScanV);
+    return scan_chunks(N, C, kScanRowsShort) <= kChunkGroup || scan_chunks(N, C, kScanRows) * tiles < 512
+               ? kScanRowsShort : kScanRows;
 }
 // Workspace: the chunks' maps, the groups' maps and the entering states, each
 // for both directions in the gradient.
 struct ScanLayout {
     int64_t chunks, groups;
-    int tiles, dirs;
+    int rows, tiles, dirs;
     size_t group_at, carry_at, total;
 };
 ScanLayout scan_layout(int64_t N, int C, bool grad) {
     ScanLayout l{};
-    l.chunks = scan_chunks(N, C, grad);
+    l.rows = scan_rows(N, C, grad);
+    l.chunks = scan_chunks(N, C, l.rows);
     l.groups = (l.chunks + kChunkGroup - 1) / kChunkGroup;
     l.tiles = (C + scan_group(C) * kScanV - 1) / (scan_group(C) * kScanV);
     l.dirs = grad ? 2 : 1;
@@ -774,10 +790,11 @@ hipError_t scan_go(ScanParams p, bool grad, const ScanLayout& l, char* ws, hipSt
     p.groups = (Map*)(ws + l.group_at);
     p.carry = (float*)(ws + l.carry_at);
     if (l.chunks > 1) {
-        if (grad)
-            k_scan_maps<T, G, kScanGradRows, WHOLE, true><<<grid, kScanThreads, 0, st>>>(p);
-        else
-            k_scan_maps<T, G, kScanRows, WHOLE, false><<<grid, kScanThreads, 0, st>>>(p);
+        auto maps = k_scan_maps<T, G, kScanGradRows, WHOLE, true>;
+        if (!grad)
+            maps = l.rows == kScanRows ? k_scan_maps<T, G, kScanRows, WHOLE, false>
+                                       : k_scan_maps<T, G, kScanRowsShort, WHOLE, false>;
+        maps<<<grid, kScanThreads, 0, st>>>(p);
     }
     if (l.groups > 1) {
         k_scan_groups<<<dim3((unsigned)l.groups, (p.C + kCarryChannels - 1) / kCarryChannels, l.dirs), kScanThreads, 0,
@@ -785,10 +802,12 @@ hipError_t scan_go(ScanParams p, bool grad, const ScanLayout& l, char* ws, hipSt
         k_scan_carry<<<dim3((unsigned)l.groups, (p.C + kCarryChannels - 1) / kCarryChannels, l.dirs), kScanThreads, 0,
                        st>>>(p);
     }
-    if (grad)
-        k_scan_grad<T, G, WHOLE><<<grid, kScanThreads, 0, st>>>(p);
-    else
-        k_scan<T, G, WHOLE><<<grid, kScanThreads, 0, st>>>(p);
+    auto rows = k_scan_grad<T, G, WHOLE>;
+    if (!grad)
+        rows = l.rows == kScanRows        ? k_scan<T, G, kScanRows, WHOLE>
+               : l.rows == kScanRowsShort ? k_scan<T, G, kScanRowsShort, WHOLE>
+                                          : k_scan<T, G, kScanRowsOne, WHOLE>;
+    rows<<<grid, kScanThreads, 0, st>>>(p);
     return hipGetLastError();
 }
 
