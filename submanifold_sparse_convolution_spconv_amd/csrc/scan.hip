@@ -107,37 +107,59 @@ struct Quad<float> {
     typedef f32x4r_t vec;
     typedef f32x4ru_t uvec;
 };
-// WHOLE: rows have a multiple of four channels, so a lane has four or none.
-// The load is then the same instruction in every lane (a missing row's or
-// channel's reads row 0 or channel 0 instead), so that all of a segment's are
-// in flight together; a branch around each would end that.
-template <typename T, bool WHOLE>
+// Rows of a multiple of four channels: a lane has four or none.  Of more than
+// four: the last lane may have fewer; it reads the row's last four and moves its
+// own to the front.  Of fewer than four: one by one.
+enum RowEnd { kWholeQuads, kCutQuad, kSingles };
+template <typename Q>
+__device__ __forceinline__ Q move_down(Q q, int s) {
+    if constexpr (sizeof(Q) == 8) {
+        uint64_t w;
+        __builtin_memcpy(&w, &q, 8);
+        w >>= 16 * s;
+        __builtin_memcpy(&q, &w, 8);
+    } else {
+        const Q one = __builtin_shufflevector(q, q, 1, 2, 3, 3);
+#pragma unroll
+        for (int i = 0; i < kScanV; ++i) q[i] = s & 1 ? one[i] : q[i];
+        const Q two = __builtin_shufflevector(q, q, 2, 3, 3, 3);
+#pragma unroll
+        for (int i = 0; i < kScanV; ++i) q[i] = s & 2 ? two[i] : q[i];
+    }
+    return q;
+}
+// The load is the same instruction in every lane (a missing row's or channel's
+// reads row 0 or channel 0 instead), so that all of a segment's are in flight
+// together; a branch around each would end that.  Channels past the row's end
+// get some value.
+template <typename T, RowEnd END>
 __device__ __forceinline__ typename Quad<T>::vec load_quad(const T* base, int row, int C, int c0) {
     const int n = C - c0;
+    const T* p = base + (int64_t)max(row, 0) * C;
     typename Quad<T>::vec v;
-    if constexpr (WHOLE) {
-        v = *(const typename Quad<T>::uvec*)(base + (int64_t)max(row, 0) * C + (n > 0 ? c0 : 0));
-    } else {
-        const T* p = base + (int64_t)max(row, 0) * C;
+    if constexpr (END == kSingles) {
 #pragma unroll
         for (int i = 0; i < kScanV; ++i) v[i] = p[min(c0 + i, C - 1)];
+    } else {
+        v = *(const typename Quad<T>::uvec*)(p + (n > 0 ? min(c0, C - kScanV) : 0));
+        if constexpr (END == kCutQuad) v = move_down(v, n > 0 ? max(kScanV - n, 0) : 0);
     }
     return v;
 }
-template <typename T, bool WHOLE>
+template <typename T, RowEnd END>
 __device__ __forceinline__ void store_quad(T* base, int row, int C, int c0, const float (&f)[kScanV], bool stream) {
     const int n = row >= 0 ? C - c0 : 0;
     T* p = base + (int64_t)row * C + c0;
     typename Quad<T>::vec v;
 #pragma unroll
     for (int i = 0; i < kScanV; ++i) v[i] = (T)f[i];
-    if constexpr (WHOLE) {
+    if (END != kSingles && n >= kScanV) {
         typename Quad<T>::uvec* q = (typename Quad<T>::uvec*)p;
-        if (n > 0 && stream)
+        if (stream)
             __builtin_nontemporal_store((typename Quad<T>::uvec)v, q);
-        else if (n > 0)
+        else
             *q = v;
-    } else {
+    } else if (END != kWholeQuads) {
 #pragma unroll
         for (int i = 0; i < kScanV; ++i)
             if (i < n) p[i] = v[i];
@@ -421,7 +443,7 @@ template <int L>
 constexpr int kSceneRows = L < 4 ? L : 4;
 
 // Rows of a workgroup's chunk, and what its scenes need of them.
-template <typename T, int G, int L, bool WHOLE>
+template <typename T, int G, int L, RowEnd END>
 struct Chunk {
     static constexpr int V = kScanV, S = kScanThreads / G, R = S * L, CT = G * V;
     int lane, seg, c0, nv;
@@ -436,7 +458,7 @@ struct Chunk {
         segment_rows<L>(p, p0 + seg * L, row);
     }
     __device__ __forceinline__ typename Quad<T>::vec load(const void* t, int l, int C) const {
-        return load_quad<T, WHOLE>((const T*)t, row[l], C, c0);
+        return load_quad<T, END>((const T*)t, row[l], C, c0);
     }
     // The states t of up to four rows' scenes b (0 where a row has none, or
     // without states), all loads in flight together.
@@ -444,7 +466,7 @@ struct Chunk {
 #pragma unroll
         for (int l = 0; l < kSceneRows<L>; ++l) {
             typename Quad<float>::vec v = {};
-            if (t) v = load_quad<float, WHOLE>(t, b[l], C, c0);
+            if (t) v = load_quad<float, END>(t, b[l], C, c0);
 #pragma unroll
             for (int i = 0; i < V; ++i) s[l][i] = v[i];
         }
@@ -452,9 +474,9 @@ struct Chunk {
 };
 
 // Maps of the chunks: first to last, and with GRAD last to first.
-template <typename T, int G, int L, bool WHOLE, bool GRAD>
+template <typename T, int G, int L, RowEnd END, bool GRAD>
 __global__ void __launch_bounds__(kScanThreads) k_scan_maps(ScanParams p) {
-    using K = Chunk<T, G, L, WHOLE>;
+    using K = Chunk<T, G, L, END>;
     constexpr int V = K::V, SR = kSceneRows<L>;
     __shared__ SceneMarks<K::R> marks;
     __shared__ Map wave_maps[GRAD ? 2 : 1][kScanWaves * K::CT];
@@ -532,9 +554,9 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_maps(ScanParams p) {
 // The states, with the chunks' entering states known.  From the last chunk to
 // the first: the rows that k_scan_maps read last are still in the memory-side
 // cache.
-template <typename T, int G, int L, bool WHOLE>
+template <typename T, int G, int L, RowEnd END>
 __global__ void __launch_bounds__(kScanThreads) k_scan(ScanParams p) {
-    using K = Chunk<T, G, L, WHOLE>;
+    using K = Chunk<T, G, L, END>;
     constexpr int V = K::V, CT = K::CT, SR = kSceneRows<L>;
     __shared__ SceneMarks<K::R> marks;
     __shared__ Map wave_maps[kScanWaves * CT], join[kScanThreads];
@@ -616,7 +638,7 @@ __global__ void __launch_bounds__(kScanThreads) k_scan(ScanParams p) {
                 s[i] = fmaf(g.f, s[i], g.n * (float)x[l][i]);
                 if (decltype(mk)::value && e >= 0 && i < k.nv) p.last[(int64_t)e * p.C + k.c0 + i] = s[i];
             }
-            store_quad<T, WHOLE>((T*)p.h, k.row[l], p.C, k.c0, s, p.stream);
+            store_quad<T, END>((T*)p.h, k.row[l], p.C, k.c0, s, p.stream);
         }
     };
     if (marked)
@@ -627,10 +649,10 @@ __global__ void __launch_bounds__(kScanThreads) k_scan(ScanParams p) {
 
 // The gradient, with the states that enter the chunks known in both
 // directions; from the last chunk to the first, like k_scan.
-template <typename T, int G, bool WHOLE>
+template <typename T, int G, RowEnd END>
 __global__ void __launch_bounds__(kScanThreads, 4) k_scan_grad(ScanParams p) {
     constexpr int L = kScanGradRows;
-    using K = Chunk<T, G, L, WHOLE>;
+    using K = Chunk<T, G, L, END>;
     constexpr int V = K::V, CT = K::CT, SR = kSceneRows<L>;
     __shared__ SceneMarks<K::R> marks;
     __shared__ Map wave_maps[2][kScanWaves * CT], join[2][kScanThreads];
@@ -759,8 +781,8 @@ __global__ void __launch_bounds__(kScanThreads, 4) k_scan_grad(ScanParams p) {
                 y[i] = 0.f;
             }
         }
-        store_quad<T, WHOLE>((T*)p.h, k.row[l], p.C, k.c0, ox, p.stream);
-        store_quad<T, WHOLE>((T*)p.dz, k.row[l], p.C, k.c0, oz, p.stream);
+        store_quad<T, END>((T*)p.h, k.row[l], p.C, k.c0, ox, p.stream);
+        store_quad<T, END>((T*)p.dz, k.row[l], p.C, k.c0, oz, p.stream);
     }
 }
 
@@ -804,7 +826,7 @@ ScanLayout scan_layout(int64_t N, int C, bool grad) {
     return l;
 }
 
-template <typename T, int G, bool WHOLE>
+template <typename T, int G, RowEnd END>
 hipError_t scan_go(ScanParams p, bool grad, const ScanLayout& l, char* ws, hipStream_t st) {
     p.beside = l.tiles > 1 && p.C * sizeof(T) % 128 != 0;
     const unsigned grid = (unsigned)((p.beside ? round_up(l.chunks, 8) : l.chunks) * l.tiles);
@@ -814,10 +836,10 @@ hipError_t scan_go(ScanParams p, bool grad, const ScanLayout& l, char* ws, hipSt
     p.groups = (Map*)(ws + l.group_at);
     p.carry = (float*)(ws + l.carry_at);
     if (l.chunks > 1) {
-        auto maps = k_scan_maps<T, G, kScanGradRows, WHOLE, true>;
+        auto maps = k_scan_maps<T, G, kScanGradRows, END, true>;
         if (!grad)
-            maps = l.rows == kScanRows ? k_scan_maps<T, G, kScanRows, WHOLE, false>
-                                       : k_scan_maps<T, G, kScanRowsShort, WHOLE, false>;
+            maps = l.rows == kScanRows ? k_scan_maps<T, G, kScanRows, END, false>
+                                       : k_scan_maps<T, G, kScanRowsShort, END, false>;
         maps<<<grid, kScanThreads, 0, st>>>(p);
     }
     if (l.groups > 1) {
@@ -826,30 +848,32 @@ hipError_t scan_go(ScanParams p, bool grad, const ScanLayout& l, char* ws, hipSt
         k_scan_carry<<<dim3((unsigned)l.groups, (p.C + kCarryChannels - 1) / kCarryChannels, l.dirs), kScanThreads, 0,
                        st>>>(p);
     }
-    auto rows = k_scan_grad<T, G, WHOLE>;
+    auto rows = k_scan_grad<T, G, END>;
     if (!grad)
-        rows = l.rows == kScanRows        ? k_scan<T, G, kScanRows, WHOLE>
-               : l.rows == kScanRowsShort ? k_scan<T, G, kScanRowsShort, WHOLE>
-                                          : k_scan<T, G, kScanRowsOne, WHOLE>;
+        rows = l.rows == kScanRows        ? k_scan<T, G, kScanRows, END>
+               : l.rows == kScanRowsShort ? k_scan<T, G, kScanRowsShort, END>
+                                          : k_scan<T, G, kScanRowsOne, END>;
     rows<<<grid, kScanThreads, 0, st>>>(p);
     return hipGetLastError();
 }
 
 template <typename T, int G>
-hipError_t scan_whole(const ScanParams& p, bool grad, const ScanLayout& l, char* ws, hipStream_t st) {
-    return p.C % kScanV ? scan_go<T, G, false>(p, grad, l, ws, st) : scan_go<T, G, true>(p, grad, l, ws, st);
+hipError_t scan_ends(const ScanParams& p, bool grad, const ScanLayout& l, char* ws, hipStream_t st) {
+    if (p.C % kScanV == 0) return scan_go<T, G, kWholeQuads>(p, grad, l, ws, st);
+    // (a group of one lane serves up to four channels, a larger one more)
+    return scan_go<T, G, G == 1 ? kSingles : kCutQuad>(p, grad, l, ws, st);
 }
 
 template <typename T>
 hipError_t scan_dispatch(const ScanParams& p, bool grad, char* ws, hipStream_t st) {
     const ScanLayout l = scan_layout(p.N, p.C, grad);
     switch (scan_group(p.C)) {
-        case 1: return scan_whole<T, 1>(p, grad, l, ws, st);
-        case 2: return scan_whole<T, 2>(p, grad, l, ws, st);
-        case 4: return scan_whole<T, 4>(p, grad, l, ws, st);
-        case 8: return scan_whole<T, 8>(p, grad, l, ws, st);
-        case 16: return scan_whole<T, 16>(p, grad, l, ws, st);
-        default: return scan_whole<T, 32>(p, grad, l, ws, st);
+        case 1: return scan_ends<T, 1>(p, grad, l, ws, st);
+        case 2: return scan_ends<T, 2>(p, grad, l, ws, st);
+        case 4: return scan_ends<T, 4>(p, grad, l, ws, st);
+        case 8: return scan_ends<T, 8>(p, grad, l, ws, st);
+        case 16: return scan_ends<T, 16>(p, grad, l, ws, st);
+        default: return scan_ends<T, 32>(p, grad, l, ws, st);
     }
 }
 
