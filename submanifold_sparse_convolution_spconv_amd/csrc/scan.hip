@@ -84,7 +84,6 @@ struct ScanParams {
     int C, scenes, tiles;
     int64_t chunks;
     bool stream;       // outputs past the caches
-    bool beside;       // tiles of a chunk stand side by side in the grid
     // [directions][chunks][C] maps of the chunks, first to last and (gradient) last to
     // first; the same of groups of chunks; the states that enter the chunks
     Map* maps;
@@ -292,17 +291,23 @@ __device__ __forceinline__ void entering_state(const ScanParams& p, int64_t chun
 }
 
 // The chunk (in the grid's order) and the tile of channels of this workgroup.
-// Where rows end inside cache lines, the tiles of one chunk follow each other on
-// one XCD (workgroups go round the 8): the lines at their borders are then read
-// once (gradient of 400,000 x 200 bf16: 521 -> 381 us).  Else the chunks of one
-// tile do (29,000 x 1,024 forward: 73 us against 77).
+// Workgroups go round the 8 XCDs: the tiles of one chunk follow each other on one
+// of them, so that the cache lines at their borders are read once (gradient of
+// 400,000 x 200 bf16: 519 -> 379 us; rows that end with their lines do not mind).
 struct Place {
     int64_t chunk;
     int tile;
     __device__ __forceinline__ explicit Place(const ScanParams& p) {
-        const uint32_t k = blockIdx.x / 8;
-        chunk = p.beside ? (int64_t)(k / p.tiles) * 8 + blockIdx.x % 8 : blockIdx.x % (uint32_t)p.chunks;
-        tile = p.beside ? k % p.tiles : blockIdx.x / (uint32_t)p.chunks;
+        if (p.tiles == 1) {
+            chunk = blockIdx.x;
+            tile = 0;
+        } else {
+            // (a quotient is the same in every lane, which the compiler has to be
+            // told: as a vector it costs 25 us at 1,006,716 x 128)
+            const uint32_t k = blockIdx.x / 8, q = __builtin_amdgcn_readfirstlane(k / p.tiles);
+            chunk = (int64_t)q * 8 + blockIdx.x % 8;
+            tile = k - q * p.tiles;
+        }
     }
 };
 
@@ -828,8 +833,7 @@ ScanLayout scan_layout(int64_t N, int C, bool grad) {
 
 template <typename T, int G, RowEnd END>
 hipError_t scan_go(ScanParams p, bool grad, const ScanLayout& l, char* ws, hipStream_t st) {
-    p.beside = l.tiles > 1 && p.C * sizeof(T) % 128 != 0;
-    const unsigned grid = (unsigned)((p.beside ? round_up(l.chunks, 8) : l.chunks) * l.tiles);
+    const unsigned grid = (unsigned)(l.tiles > 1 ? round_up(l.chunks, 8) * l.tiles : l.chunks);
     p.chunks = l.chunks;
     p.tiles = l.tiles;
     p.maps = (Map*)ws;
