@@ -293,7 +293,8 @@ __device__ __forceinline__ void entering_state(const ScanParams& p, int64_t chun
 // The chunk (in the grid's order) and the tile of channels of this workgroup.
 // Workgroups go round the 8 XCDs: the tiles of one chunk follow each other on one
 // of them, so that the cache lines at their borders are read once (gradient of
-// 400,000 x 200 bf16: 519 -> 379 us; rows that end with their lines do not mind).
+// 400,000 x 200 bf16: 519 -> 379 us; of 29,000 x 1,024, whose rows end with their
+// lines: 99 -> 106).
 struct Place {
     int64_t chunk;
     int tile;
