@@ -77,3 +77,47 @@ def test_block_and_its_gradient():
     close(dx, x64.grad, "dx")
     for name, v in p.items():
         close(grads[name], v.grad, name)
+
+
+@pytest.mark.parametrize("N, dt", [(37, torch.float32), (1500, torch.bfloat16), (33000, torch.bfloat16)])
+def test_operators_in_a_graph(N, dt):
+    """Captured once, replayed on new inputs with eager work between: the bits of
+    the eager calls."""
+    C, F, B = 128, 200, 5
+    g = torch.Generator().manual_seed(N)
+
+    def make():
+        n = [torch.randn(N, C, generator=g).to(dt).cuda() for _ in range(3)]
+        return n + [torch.randn(N, F, generator=g).to(dt).cuda(), torch.randn(B, C, generator=g).cuda()]
+
+    w = (torch.randn(2, C, F, generator=g) / 12).to(dt).cuda()
+    nw, nb = torch.rand(C, generator=g).cuda(), torch.randn(C, generator=g).cuda()
+    gb = torch.randn(2, F, generator=g).cuda()
+    off = torch.tensor([0, N // 3, N // 3, N - 1, N, N], dtype=torch.int32).cuda()
+    order = torch.randperm(N, generator=g).to(torch.int32).cuda()
+
+    def calls(x, z, d, e, h0):
+        y, mean, rstd = sp.spconv_layernorm(x, nw, nb, stats=True)
+        out = [y, mean, rstd, *sp.spconv_layernorm_grad(d, x, mean, rstd, nw)]
+        out += [sp.spconv_glu(x, w, gb), *sp.spconv_glu_grad(e, x, w, gb)]
+        out += [*sp.spconv_scan(x, z, off, order, h0), *sp.spconv_scan_grad(d, x, z, off, order, h0, h0)]
+        return out
+
+    held = make()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls(*held)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = calls(*held)
+    for _ in range(4):
+        new = make()
+        want = calls(*new)
+        for a, b in zip(held, new):
+            a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(got, want)):
+            assert torch.equal(a, b), f"output {i}"

@@ -142,6 +142,22 @@ def test_many_chunks_and_wide_rows(dt):
     check(130, 4096, dt, [0, 70, 130], order=True, h0=True)
 
 
+@DTS
+@pytest.mark.parametrize("C", [1021, 1024])
+def test_long_and_wide(C, dt):
+    """Enough chunks for the most rows per lane, tiles of channels side by side."""
+    check(8200, C, dt, [0, 0, 5000, 5001, 8200], order=True, h0=True)
+
+
+@DTS
+@pytest.mark.parametrize("C", [1, 2, 3, 5, 6, 7, 11, 130])
+def test_row_ends(C, dt):
+    """Rows that are no multiple of four channels, with scenes' states, and many
+    scenes without rows around and between."""
+    off = [0] * 70 + [3] * 9 + [40] + [41] * 100 + [90, 90]
+    check(90, C, dt, off, order=True, h0=True)
+
+
 def test_no_rows():
     x = torch.empty(0, 16, device=DEV)
     o = torch.zeros(4, dtype=torch.int32, device=DEV)
