@@ -40,7 +40,9 @@ __device__ __forceinline__ Act activation(float a) {
     if constexpr (ACT == SPCONV_SILU) {
         const float s = fast_sigmoid(a);
         const float v = a * s;
-        return {v, fmaf(-s, v, s) + v};       // s (1 + a (1 - s))
+        // s (1 + a (1 - s)): 1 - s is exact from s = 1/2 on and 0 where s is 1, so
+        // that the 1 is not lost next to a large a
+        return {v, fmaf(v, 1.f - s, s)};
     } else {
         // The normal distribution from erfc(x) = t P(t) e^(-x^2) + 1.5e-7 at
         // most, t = 1 / (1 + 0.3275911 x) (Abramowitz and Stegun, 7.1.26); the
