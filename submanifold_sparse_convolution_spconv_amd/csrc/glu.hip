@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kJoinCols * 16) k_glu_join(GluParams p, int sp
     const int64_t e = (block * kJoinCols + threadIdx.x) * 4;
     if (threadIdx.x >= kJoinCols || e >= n) return;
     if (!w) {
-        *(f32x4r_t*)(dbias + e) = f32x4r_t{t.f[0], t.f[1], t.f[2], t.f[3]};
+        *(f32x4ru_t*)(dbias + e) = f32x4ru_t{t.f[0], t.f[1], t.f[2], t.f[3]};    // aligned to its elements only
         return;
     }
     const int64_t c = e / (2 * F);

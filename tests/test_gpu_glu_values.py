@@ -13,6 +13,8 @@ density, what the kernels round:
         reciprocal.  value: |a| ds + u; slope s + a s (1 - s): its derivative
         by s is 1 + a (1 - 2 s); its own roundings are 4 u of the terms.
 """
+import ctypes
+
 import pytest
 import torch
 
@@ -121,3 +123,29 @@ def test_single_precision_follows_the_tail(N, kind):
     for k, (g, e) in enumerate(((s, es), (v, ev))):
         within(dw[k, 0], g, e + 2 * U * g.abs() + TINY, f"dw[{k}]", a)
         within(db[k], g, e + 2 * U * g.abs() + TINY, f"dbias[{k}]", a)
+
+
+@pytest.mark.parametrize("dt, N, C, F", [(F32, 3, 16, 24), (F32, 300, 16, 24), (BF16, 700, 136, 72), (BF16, 33000, 32, 40),
+                                         (F32, 0, 16, 24)])
+def test_bias_gradient_inside_a_packed_buffer(dt, N, C, F):
+    """The C entry point takes bias and dbias at any element of a buffer, in
+    calls of one tile of rows, of several, of many rows, and of none."""
+    g = torch.Generator().manual_seed(N)
+    x, d = torch.randn(N, C, generator=g).to(dt).to(DEV), torch.randn(N, F, generator=g).to(dt).to(DEV)
+    w, b = (torch.randn(2, C, F, generator=g) / 8).to(dt).to(DEV), torch.randn(2, F, generator=g).to(DEV)
+    want = sp.spconv_glu_grad(d, x, w, b)
+    code = sp.SPCONV_BF16 if dt == BF16 else sp.SPCONV_F32
+    n = sp.spconv_glu_grad_workspace_size(N, C, F, code)
+    ws = torch.empty(max(n, 256), dtype=torch.uint8, device=DEV)
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    for at in (1, 2, 3):
+        packed = torch.full((2, 2 * F + 8), 7.0, device=DEV)
+        packed[0, at:at + 2 * F] = b.reshape(-1)
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        rc = sp.load_library().spconv_glu_grad(p(d), p(x), p(w), p(packed[0, at:]), p(ws), n, p(dx), p(dw),
+                                               p(packed[1, at:]), N, C, F, sp.SPCONV_SILU, code,
+                                               ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        assert rc == 0
+        assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+        assert torch.equal(packed[1, at:at + 2 * F], want[2].reshape(-1))
+        assert (packed[1, :at] == 7).all() and (packed[1, at + 2 * F:] == 7).all()
