@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(Shape<TILE>::THREADS, TILE == 128 ? 4 : 3) k_g
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const float va = acc[PAIR * i + e / 4][j][e % 4], vb = acc[NM / 2 + PAIR * i + e / 4][j][e % 4];
-                const Act t = activation<ACT>(va);
+                const Act t = activation<ACT, sizeof(T) == 4>(va);
                 if constexpr (!GRAD) {
                     o[e] = (T)(t.v * vb);
                 } else {

@@ -12,8 +12,13 @@ density, what the kernels round:
         3 u s, and 0 from a = 17.4 on, where 1 + e is 1 and so is its
         reciprocal.  value: |a| ds + u; slope s + a s (1 - s): its derivative
         by s is 1 + a (1 - 2 s); its own roundings are 4 u of the terms.
+  gelu  q from one exponential of a^2: exponent off by 3 u of a^2 / 2, the
+        polynomial in 1 / (1 + p x) and its argument by at most 32 u: q (2 a^2 +
+        32) u; 1 - q rounds once.  The density: phi (2 a^2 + 8) u.  In bfloat16
+        q comes from a shorter polynomial, off by 1.5e-7 / 2.
 """
 import ctypes
+import math
 
 import pytest
 import torch
@@ -58,10 +63,18 @@ def problem(values, N, C, dt):
 
 def act64(a, kind, dt):
     """Value and slope, and how far the kernels' may be off."""
-    s, n = torch.sigmoid(a), torch.sigmoid(-a)
-    v, d = a * s, s + a * s * n
-    ds = torch.where(a < 17.4, s * n * (2 * a.abs() + 2) * U + 3 * U * s, 0.0)
-    return v, d, a.abs() * ds + U * v.abs(), ds * (1 + a.abs() * (n - s).abs()) + 4 * U * (s + v.abs() * n)
+    if kind == "silu":
+        s, n = torch.sigmoid(a), torch.sigmoid(-a)
+        v, d = a * s, s + a * s * n
+        ds = torch.where(a < 17.4, s * n * (2 * a.abs() + 2) * U + 3 * U * s, 0.0)
+        return v, d, a.abs() * ds + U * v.abs(), ds * (1 + a.abs() * (n - s).abs()) + 4 * U * (s + v.abs() * n)
+    q = 0.5 * torch.special.erfc(a.abs() / math.sqrt(2))
+    phi = torch.exp(-a * a / 2) / math.sqrt(2 * math.pi)
+    cdf = torch.where(a < 0, q, 1 - q)
+    eq = q * (2 * a * a + 32) * U + (1.5e-7 / 2 if dt == BF16 else 0.0)
+    ec = torch.where(a < 0, eq, eq + U)
+    return a * cdf, cdf + a * phi, a.abs() * ec + U * (a * cdf).abs(), ec + a.abs() * phi * (2 * a * a + 8) * U + 2 * U * (
+        cdf + (a * phi).abs())
 
 
 def within(got, want, tol, what, values):
@@ -75,7 +88,7 @@ def within(got, want, tol, what, values):
 SIZES = [(F32, 5, 8), (F32, 1000, 72), (BF16, 5, 8), (BF16, 1000, 136), (BF16, 66000, 40), (BF16, 66000, 128)]
 
 
-@pytest.mark.parametrize("kind", ["silu"])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
 @pytest.mark.parametrize("dt, N, C", SIZES)
 def test_far_arguments(dt, N, C, kind):
     """Both signs, from small to where 1 is lost next to the argument: h, dw,
@@ -108,7 +121,7 @@ def test_far_arguments(dt, N, C, kind):
         assert torch.count_nonzero(dx[:N // 3]) == 0 and torch.count_nonzero(dx[N // 3 + 1:]) == 0
 
 
-@pytest.mark.parametrize("kind", ["silu"])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
 @pytest.mark.parametrize("N", [1, 70])
 def test_single_precision_follows_the_tail(N, kind):
     """fp32 from -12 to 12: relative precision where the value is small."""
