@@ -352,6 +352,8 @@ int spconv_glu_grad(const void* dout, const void* x, const void* w, const float*
  *           a scene without positions)
  *   workspace (dev) spconv_scan_workspace_size bytes, 256-byte aligned (may
  *           be NULL when that is 0)
+ * An infinite state stays infinite until a gate is 0 in 32 bits (z below -87),
+ * which makes it NaN; neither leaves its scene and channel.
  * The contents of offsets and order are not checked: bad values give wrong
  * states, never an access outside the given arrays. */
 int spconv_scan_workspace_size(int64_t N, int C, int dtype, size_t* bytes);

@@ -12,7 +12,9 @@
 // (composed from the maps in a fixed order), and the rows again with those
 // states.  A scene's first row forgets what came before: its
 // map is marked F = kForget, and composing selects instead of multiplying, so
-// infinities and NaN of one scene stay in it.
+// infinities and NaN of one scene stay in it.  Products of factors above zero
+// stay above zero (the smallest number where they would underflow), so that an
+// infinite state stays infinite through a composed map as it does step by step.
 //
 // The gradient runs the same maps backwards: with g[t] the derivative at h[t],
 //   y[t] = f[t] g[t]                what row t hands to row t - 1
@@ -66,11 +68,12 @@ __device__ __forceinline__ Step gate(float z) {
 struct Map {
     float F, V;
 };
-// b after a
+// b after a.  A product that would round to 0 without a factor of 0 becomes the
+// smallest number, 2^-149: 0 times an infinite state would be NaN.
 __device__ __forceinline__ Map after(Map b, Map a) {
     Map r;
     r.V = b.F < 0.f ? b.V : fmaf(b.F, a.V, b.V);
-    r.F = b.F < 0.f || a.F < 0.f ? kForget : b.F * a.F;
+    r.F = b.F < 0.f || a.F < 0.f ? kForget : fmaxf(b.F * a.F, fminf(fminf(b.F, a.F), 0x1p-149f));
     return r;
 }
 __device__ __forceinline__ float apply(Map m, float s) { return m.F < 0.f ? m.V : fmaf(m.F, s, m.V); }
@@ -408,6 +411,42 @@ __device__ __forceinline__ void missing_row(int row, typename Quad<T>::vec& z, t
     }
 }
 
+// Whether some gate of a channel is 0 in 32 bits: z below -87.33, where the
+// exponential vanishes.  As whole numbers the bits of negative z grow as z falls,
+// above those of every other: one maximum for two elements.
+template <typename T>
+struct Shut {
+    typedef std::conditional_t<sizeof(T) == 2, uint16_t, uint32_t> word;
+    typedef word vec __attribute__((ext_vector_type(kScanV)));
+    static constexpr word kBorder = sizeof(T) == 2 ? (word)0xC2AE : (word)0xC2AEAC50;
+    vec most = {};
+    __device__ __forceinline__ void add(typename Quad<T>::vec z) {
+        vec w;
+        __builtin_memcpy(&w, &z, sizeof w);
+        most = __builtin_elementwise_max(most, w);
+    }
+    // Plain products of gates leave 0 for an underflow too: such a factor becomes
+    // the smallest number, unless a gate is 0.  True: some factor of the wave was 0.
+    __device__ __forceinline__ bool lift(Map (&m)[kScanV]) const {
+        int any = 0;
+#pragma unroll
+        for (int i = 0; i < kScanV; ++i) {
+            const bool zero = m[i].F == 0.f;
+            any |= zero;
+            if (zero && most[i] <= kBorder) m[i].F = 0x1p-149f;
+        }
+        return __any(any);
+    }
+};
+// Whether a row's gradient met a factor of 0 in the plain products: infinite ones
+// have become NaN there.
+__device__ __forceinline__ bool any_nan(const Map (&m)[kScanV]) {
+    int any = 0;
+#pragma unroll
+    for (int i = 0; i < kScanV; ++i) any |= m[i].V != m[i].V;
+    return __any(any);
+}
+
 // A scan of the lanes' maps over the workgroup's segments.  Within a wave
 // here: m becomes the composition of the wave's segments before the lane's own
 // (BACK: behind it), the whole wave's goes to wave_maps[wave][channel].
@@ -512,6 +551,7 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_maps(ScanParams p) {
         }
     }
     Map m[V], mb[V];
+    Shut<T> shut;
     auto compose = [&](auto mk) {
 #pragma unroll
         for (int i = 0; i < V; ++i) m[i] = mb[i] = {1.f, 0.f};
@@ -520,6 +560,7 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_maps(ScanParams p) {
         for (int l = 0; l < L; ++l) {
             const int b = decltype(mk)::value ? marks.first[k.seg * L + l] : -1;
             const int e = decltype(mk)::value && GRAD ? marks.last[k.seg * L + l] : -1;
+            if (!decltype(mk)::value) shut.add(z[l]);
             if (decltype(mk)::value && l % SR == 0) {
                 k.of_scenes(p.h0, marks.first + k.seg * L + l, h0, p.C);
                 if (GRAD) k.of_scenes(p.dlast, marks.last + k.seg * L + l, dl, p.C);
@@ -539,18 +580,21 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_maps(ScanParams p) {
                         if (GRAD) mb[i] = after(mb[i], {g.f, g.f * t});
                     }
                 } else {
-                    // the product of the factors serves both directions
+                    // (the product of the factors serves both directions)
                     if (GRAD) mb[i].V = fmaf(m[i].F, g.f * t, mb[i].V);
                     m[i] = {g.f * m[i].F, fmaf(g.f, m[i].V, v)};
-                    mb[i].F = m[i].F;
                 }
             }
         }
     };
-    if (wave_marks<L>(marks, k.seg))
-        compose(std::true_type{});
-    else
+    bool by_maps = wave_marks<L>(marks, k.seg);
+    if (!by_maps) {
         compose(std::false_type{});
+        by_maps = shut.lift(m) && GRAD && any_nan(mb);
+#pragma unroll
+        for (int i = 0; i < V; ++i) mb[i].F = m[i].F;
+    }
+    if (by_maps) compose(std::true_type{});
     scan_wave<G, false>(m, wave_maps[0]);
     if constexpr (GRAD) scan_wave<G, true>(mb, wave_maps[1]);
     __syncthreads();
@@ -596,6 +640,7 @@ __global__ void __launch_bounds__(kScanThreads) k_scan(ScanParams p) {
     }
     const bool marked = wave_marks<L>(marks, k.seg);
     Map pre[V];
+    Shut<T> shut;
     auto compose = [&](auto mk) {
 #pragma unroll
         for (int i = 0; i < V; ++i) pre[i] = {1.f, 0.f};
@@ -603,6 +648,7 @@ __global__ void __launch_bounds__(kScanThreads) k_scan(ScanParams p) {
 #pragma unroll
         for (int l = 0; l < L; ++l) {
             const int b = decltype(mk)::value ? marks.first[k.seg * L + l] : -1;
+            if (!decltype(mk)::value) shut.add(z[l]);
             if (decltype(mk)::value && l % SR == 0)
                 k.of_scenes(p.h0, marks.first + k.seg * L + l, h0, p.C);
 #pragma unroll
@@ -616,10 +662,12 @@ __global__ void __launch_bounds__(kScanThreads) k_scan(ScanParams p) {
             }
         }
     };
-    if (marked)
+    if (marked) {
         compose(std::true_type{});
-    else
+    } else {
         compose(std::false_type{});
+        shut.lift(pre);
+    }
     scan_wave<G, false>(pre, wave_maps);
     __syncthreads();
     if (threadIdx.x < CT) scan_waves<CT, false>(wave_maps, threadIdx.x);
@@ -698,6 +746,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) k_scan_grad(ScanParams p) {
     const bool marked = wave_marks<L>(marks, k.seg);
     Map m[V], mb[V];
     float f[L][V], n[L][V], dh[L][V];
+    Shut<T> shut;
     auto compose = [&](auto mk) {
 #pragma unroll
         for (int i = 0; i < V; ++i) m[i] = mb[i] = {1.f, 0.f};
@@ -710,6 +759,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) k_scan_grad(ScanParams p) {
         for (int l = 0; l < L; ++l) {
             const int b = decltype(mk)::value ? marks.first[k.seg * L + l] : -1;
             const int e = decltype(mk)::value ? marks.last[k.seg * L + l] : -1;
+            if (!decltype(mk)::value) shut.add(z[l]);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const Step g = gate((float)z[l][i]);
@@ -729,16 +779,19 @@ __global__ void __launch_bounds__(kScanThreads, 4) k_scan_grad(ScanParams p) {
                 } else {
                     mb[i].V = fmaf(m[i].F, g.f * t, mb[i].V);
                     m[i] = {g.f * m[i].F, fmaf(g.f, m[i].V, v)};
-                    mb[i].F = m[i].F;
                 }
                 dh[l][i] = t;
             }
         }
     };
-    if (marked)
-        compose(std::true_type{});
-    else
+    bool by_maps = marked;
+    if (!by_maps) {
         compose(std::false_type{});
+        by_maps = shut.lift(m) && any_nan(mb);
+#pragma unroll
+        for (int i = 0; i < V; ++i) mb[i].F = m[i].F;
+    }
+    if (by_maps) compose(std::true_type{});
     scan_wave<G, false>(m, wave_maps[0]);
     scan_wave<G, true>(mb, wave_maps[1]);
     __syncthreads();
