@@ -1,0 +1,151 @@
+"""Long recurrences on the GPU: many chunks and groups of chunks, against a
+blocked walk in 64 bits on the GPU.
+
+Tolerances, u = 2^-24.  The smaller of f and 1 - f is off by r = (2 |z| + 8) u
+of itself (the exponent's product with log2 e, the exponential, 1 + e, the
+reciprocal, a product), the larger by that and one rounding of a number below
+one.  So a step adds m r (|s| + |x|) + 3 u (f |s| + n |x|), m = min(f, n), and
+earlier errors decay with f as the state does.  Composing steps into maps
+rounds the same products, once each.
+"""
+import math
+
+import pytest
+import torch
+
+import submanifold_sparse_convolution_spconv_amd as sp
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+U = 2.0 ** -24
+TINY = 1e-30
+F32, BF16 = torch.float32, torch.bfloat16
+DTS = pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+
+
+def half(dt):
+    return torch.finfo(dt).eps / 2
+
+
+def blocked(f, v):
+    """y[t] = f[t] y[t-1] + v[t] from zero: runs of the sequence side by side,
+    first from zero, then from the end of the run before."""
+    n, C = f.shape
+    L = max(1, math.isqrt(n))
+    P = -(-n // L)
+    pad = P * L - n
+    f, v = (torch.cat([t, t.new_zeros(pad, C)]).view(P, L, C) for t in (f, v))
+    end, prod = torch.zeros_like(v[:, 0]), torch.ones_like(v[:, 0])
+    for i in range(L):
+        end = f[:, i] * end + v[:, i]
+        prod = prod * f[:, i]
+    s = torch.zeros_like(end)
+    for p in range(1, P):
+        s[p] = prod[p - 1] * s[p - 1] + end[p - 1]
+    out = torch.empty_like(v)
+    for i in range(L):
+        s = f[:, i] * s + v[:, i]
+        out[:, i] = s
+    return out.view(P * L, C)[:n]
+
+
+def reference(x, z, off, perm, h0, d, dl):
+    """Values and bounds by name, rows in the caller's order."""
+    N, C = x.shape
+    rows = perm.long() if perm is not None else torch.arange(N, device=DEV)
+    x, z, d = x.double()[rows], z.double()[rows], d.double()[rows]
+    f, n = torch.sigmoid(z), torch.sigmoid(-z)
+    m, r = torch.minimum(f, n), (2 * z.abs() + 8) * U
+    o = torch.tensor(off, device=DEV)
+    full = o[1:] > o[:-1]
+    lo, hi = o[:-1][full], o[1:][full] - 1
+    start = h0.double() if h0 is not None else torch.zeros(len(off) - 1, C, dtype=torch.float64, device=DEV)
+    begin = torch.zeros(N, 1, dtype=torch.bool, device=DEV)
+    begin[lo] = True
+    into = torch.zeros_like(x)
+    into[lo] = start[full]
+    link = torch.where(begin, 0.0, f)
+
+    def before(t, first):
+        return torch.where(begin, first, torch.cat([torch.zeros_like(t[:1]), t[:-1]]))
+
+    h, H = blocked(link, f * into + n * x), blocked(link, f * into.abs() + n * x.abs())
+    prev, prevH = before(h, into), before(H, into.abs())
+    E = blocked(link, m * r * (prevH + x.abs()) + 3 * U * H)
+    prevE = before(E, torch.zeros_like(x))
+    last, lastE = start.clone(), torch.zeros_like(start)
+    last[full], lastE[full] = h[hi], E[hi]
+    d[hi] += dl.double()[full]
+    nxt = torch.cat([link[1:], torch.zeros_like(link[:1])])
+
+    def back(v):
+        return blocked(nxt.flip(0), v.flip(0)).flip(0)
+
+    g, G = back(d), back(d.abs())
+    step = (m * r + 3 * U * f) * G               # what handing a row's gradient on adds
+    Eg = back(2 * U * G + torch.cat([torch.where(begin, 0.0, step)[1:], torch.zeros_like(step[:1])]))
+    W = prevH + x.abs()
+    dh0, dh0E = dl.double().clone(), torch.zeros_like(start)
+    dh0[full], dh0E[full] = (f * g)[lo], (f * Eg + step)[lo]
+
+    def caller(t):
+        out = torch.empty_like(t)
+        out[rows] = t
+        return out
+
+    return {"h": (caller(h), caller(E)), "last": (last, lastE), "dx": (caller(n * g), caller(n * (Eg + (r + 3 * U) * G))),
+            "dz": (caller(g * (prev - x) * f * n), caller(f * n * (Eg * W + G * prevE + (2 * r + 8 * U) * G * W))),
+            "dh0": (dh0, dh0E)}
+
+
+def check(x, z, d, off, perm, h0, dl):
+    want = reference(x, z, off, perm, h0, d, dl)
+    o = torch.tensor(off, dtype=torch.int32, device=DEV)
+    got = dict(zip(("h", "last"), sp.spconv_scan(x, z, o, order=perm, h0=h0)))
+    got.update(zip(("dx", "dz", "dh0"), sp.spconv_scan_grad(d, x, z, o, order=perm, h0=h0, dlast=dl)))
+    assert (got["dh0"] is None) == (h0 is None)
+    for name, t in got.items():
+        if t is None:
+            continue
+        v, e = want[name]
+        err = (t.double() - v).abs_()
+        tol = half(t.dtype) * (v.abs() + e) + e + TINY
+        bad = ~(err <= tol)
+        assert not bad.any(), (f"{name}: {int(bad.sum())} of {bad.numel()} off, first at {bad.nonzero()[0].tolist()}, "
+                               f"worst {float((err / tol).max()):.3g} of the tolerance")
+
+
+def waves(N, C, reach, dt, seed):
+    """Inputs whose states show where they came from: slow waves under the
+    noise, gates of channel c open for about e^reach steps, falling with c."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+
+    def rand(*s):
+        return torch.randn(*s, generator=g, device=DEV)
+
+    t = torch.arange(N, device=DEV)[:, None] / N
+    c = torch.arange(C, device=DEV)[None] / C
+    x = (torch.cos(40 * t * (1 + c)) + 0.2 * rand(N, C)).to(dt)
+    z = (reach - 4 * c + 0.3 * rand(N, C)).to(dt)
+    d = (torch.sin(35 * t * (1 + c)) + 0.2 * rand(N, C)).to(dt)
+    perm = torch.randperm(N, generator=g, device=DEV).to(torch.int32)
+    return x, z, d, perm, rand
+
+
+@DTS
+@pytest.mark.parametrize("N, C", [(3000, 128), (4096, 128), (4095, 100), (2900, 260)])
+def test_up_to_64_chunks(N, C, dt):
+    """One scene through all chunks, whose states are composed in shares of up
+    to 16 maps."""
+    x, z, d, perm, rand = waves(N, C, 8.0, dt, N + C)
+    check(x, z, d, [0, N], None, rand(1, C), rand(1, C))
+    check(x, z, d, [0, 0, N - 1, N], perm, None, rand(3, C))
+
+
+@DTS
+@pytest.mark.parametrize("N, C", [(600001, 128), (530000, 72)])
+def test_more_than_64_groups_of_chunks(N, C, dt):
+    x, z, d, perm, rand = waves(N, C, 11.0, dt, N + C)
+    check(x, z, d, [0, N], perm, rand(1, C), rand(1, C))
+    if dt == F32:
+        check(x, z, d, [0, 7, N - 5, N - 5, N], None, rand(4, C), rand(4, C))
