@@ -352,6 +352,8 @@ int spconv_glu_grad(const void* dout, const void* x, const void* w, const float*
  *           a scene without positions)
  *   workspace (dev) spconv_scan_workspace_size bytes, 256-byte aligned (may
  *           be NULL when that is 0)
+ * f is a number of 32 bits too: a state kept by a constant open gate is off by
+ * up to 2^-24 of itself per step.
  * An infinite state stays infinite until a gate is 0 in 32 bits (z below -87),
  * which makes it NaN; neither leaves its scene and channel.
  * The contents of offsets and order are not checked: bad values give wrong

@@ -23,9 +23,13 @@
 // i.e. s -> f s + f dout from the last row to the first.
 //
 // With e = exp(-|z|), the smaller of f and 1 - f is e / (1 + e), in its own
-// relative precision, and the larger is one minus it: rounded once and without
-// a bias (the reciprocal's would add up over the thousands of steps that an
-// open gate remembers).  States, maps and sums are fp32.
+// relative precision, and the larger is one minus it.  That is rounded once, to a
+// multiple of 2^-24 below one: over varying gates to either side (a reciprocal's
+// error would lean to one), but a gate that stays open at one value repeats its
+// error at every step.  Then 1 - f, as the state decays, is off by up to 2^-25: 3%
+// of it at z = 15, 44% at 17 (f = 1 - 2^-24), all of it from 17.4 on (f = 1); and a
+// state kept for t steps by up to t 2^-24 of itself, the products' rounding
+// included (0.5% after 300,000 steps at z = 17).  States, maps and sums are fp32.
 //
 // Long sequences are bound by memory, at the price of reading the rows twice:
 // 1,006,716 x 128 bf16 takes 273 us forward (1.29 GB, 4.7 TB/s) and 466 us for the

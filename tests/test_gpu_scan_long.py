@@ -1,5 +1,5 @@
 """Long recurrences on the GPU: many chunks and groups of chunks, against a
-blocked walk in 64 bits on the GPU.
+blocked walk in 64 bits on the GPU; gates that stay open.
 
 Tolerances, u = 2^-24.  The smaller of f and 1 - f is off by r = (2 |z| + 8) u
 of itself (the exponent's product with log2 e, the exponential, 1 + e, the
@@ -149,3 +149,22 @@ def test_more_than_64_groups_of_chunks(N, C, dt):
     check(x, z, d, [0, N], perm, rand(1, C), rand(1, C))
     if dt == F32:
         check(x, z, d, [0, 7, N - 5, N - 5, N], None, rand(4, C), rand(4, C))
+
+
+@pytest.mark.parametrize("C", [4, 128])
+def test_gates_that_stay_open(C):
+    """x = 0 under a constant gate: h[t] = f^t h0.  f and each product of the
+    factors round by at most 2^-25 below one, so a state is off by t 2^-24 of
+    what it was."""
+    N = 300000
+    o = torch.tensor([0, N], dtype=torch.int32, device=DEV)
+    zero, one = torch.zeros(N, C, device=DEV), torch.ones(1, C, device=DEV)
+    t = torch.arange(1, N + 1, device=DEV, dtype=torch.float64)[:, None]
+    for v in (9.0, 12.0, 14.0, 15.0, 16.0, 17.0, 20.0):
+        h, last = sp.spconv_scan(zero, torch.full_like(zero, v), o, h0=one)
+        want = torch.exp(-t * math.log1p(math.exp(-v)))
+        rel = (2 * v + 8) * U * math.exp(-v)            # of 1 - f
+        # the factors of t steps together: t (2^-24 + rel), as long as the state is there to be off
+        tol = want * torch.expm1(t * (U + rel)) + U * want + TINY
+        assert ((h.double() - want).abs() <= tol).all(), v
+        assert abs(float(last[0, 0]) - float(want[-1])) <= float(tol[-1]), v
