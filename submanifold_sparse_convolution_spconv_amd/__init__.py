@@ -27,7 +27,7 @@ Functions carry the C entry points' names:
     spconv_wgrad(feats, dout, nmap) -> dw
 Row-wise operators of a voxel block, on (N, C) feature rows:
     spconv_layernorm(x, weight=None, bias=None, eps=1e-5, stats=False) -> y, or (y, mean, rstd)
-    spconv_layernorm_grad(dout, x, mean, rstd, weight=None) -> (dx, dweight, dbias)
+    spconv_layernorm_grad(dout, x, mean, rstd, weight=None, sums=None) -> (dx, dweight, dbias)
     spconv_glu(x, w, bias=None, act="silu") -> h
     spconv_glu_grad(dout, x, w, bias=None, act="silu") -> (dx, dw, dbias)
     spconv_scan(x, z, offsets, order=None, h0=None) -> (h, last)
@@ -620,12 +620,13 @@ def spconv_layernorm_grad_workspace_size(N: int, C: int, dtype: int) -> int:
     return _size("spconv_layernorm_grad_workspace_size", N, C, dtype)
 
 
-def spconv_layernorm_grad(dout, x, mean, rstd, weight=None, out=None, workspace=None):
+def spconv_layernorm_grad(dout, x, mean, rstd, weight=None, out=None, workspace=None, sums=None):
     """Gradient of spconv_layernorm: dout and x (N, C), the statistics that the
-    forward returned, its weight.  Returns (dx, dweight, dbias), dweight and
-    dbias float32 (C,), or None both where weight is None.  workspace: a uint8
-    tensor of at least spconv_layernorm_grad_workspace_size bytes (allocated
-    when None)."""
+    forward returned, its weight.  ``sums``: whether dweight and dbias are wanted
+    (None: where weight is given; True also serves a norm with a bias and no
+    weight).  Returns (dx, dweight, dbias), dweight and dbias float32 (C,), or
+    None both.  workspace: a uint8 tensor of at least
+    spconv_layernorm_grad_workspace_size bytes (allocated when None)."""
     dt = _row_dtype(x)
     N, C = x.shape
     dev = x.device
@@ -639,11 +640,11 @@ def spconv_layernorm_grad(dout, x, mean, rstd, weight=None, out=None, workspace=
     dx = _out(out, x.shape, x, "out")
     ws = dweight = dbias = None
     n = 0
-    if weight is not None:
+    if weight is not None if sums is None else sums:
         ws, n = _workspace(workspace, spconv_layernorm_grad_workspace_size(N, C, dt), dev,
                            "spconv_layernorm_grad_workspace_size")
-        dweight = _torch.empty_like(weight)
-        dbias = _torch.empty_like(weight)
+        dweight = _torch.empty(C, dtype=_torch.float32, device=dev)
+        dbias = _torch.empty(C, dtype=_torch.float32, device=dev)
     _call("spconv_layernorm_grad", dev, _at(dout), _at(x), _at(mean), _at(rstd), _at(weight), _at(ws), n, _at(dx),
           _at(dweight), _at(dbias), N, C, dt)
     return dx, dweight, dbias
