@@ -669,7 +669,9 @@ def _glu_args(x, w, bias, act):
 def spconv_glu(x, w, bias=None, act: str = "silu", out=None):
     """Gated linear unit h = act(x w[0] + bias[0]) * (x w[1] + bias[1]): x (N, C)
     and w (2, C, F), both float32 or both bfloat16, CUDA; bias float32 (2, F) or
-    None; act "silu" or "gelu" (erf); C and F multiples of 8 up to 4096.
+    None; act "silu" or "gelu" (erf); C and F multiples of 8 up to 4096.  Like
+    the convolution's operands, x, w and out start at 16-byte addresses; others
+    (contiguous views into a buffer) raise SpconvError, SPCONV_E_INVALID.
     Returns h (N, F) in their dtype."""
     dt, N, C, F, dev, x, w, bias, a = _glu_args(x, w, bias, act)
     h = _out(out, (N, F), x, "out")
@@ -682,7 +684,8 @@ def spconv_glu_grad_workspace_size(N: int, C: int, F: int, dtype: int) -> int:
 
 
 def spconv_glu_grad(dout, x, w, bias=None, act: str = "silu", workspace=None):
-    """Gradient of spconv_glu: dout (N, F), the forward's inputs.  Returns (dx
+    """Gradient of spconv_glu: dout (N, F), at a 16-byte address like x and w, the
+    forward's inputs.  Returns (dx
     (N, C), dw (2, C, F), dbias float32 (2, F), or None where bias is None).
     workspace: a uint8 tensor of at least spconv_glu_grad_workspace_size bytes
     (allocated when None)."""

@@ -162,3 +162,22 @@ def test_bias_gradient_inside_a_packed_buffer(dt, N, C, F):
         assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
         assert torch.equal(packed[1, at:at + 2 * F], want[2].reshape(-1))
         assert (packed[1, :at] == 7).all() and (packed[1, at + 2 * F:] == 7).all()
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_refuses_rows_between_16_byte_addresses(dt):
+    """Contiguous views one element into a buffer, as the convolution does; a
+    view that is copied (not contiguous) is taken wherever it starts."""
+    x, w, d = (torch.zeros(s, dtype=dt, device=DEV) for s in ((4, 16), (2, 16, 24), (4, 24)))
+
+    def moved(t):
+        return torch.zeros(t.numel() + 1, dtype=dt, device=DEV)[1:].view(t.shape)
+
+    for bad in (lambda: sp.spconv_glu(moved(x), w), lambda: sp.spconv_glu(x, moved(w)), lambda: sp.spconv_glu(x, w, out=moved(d)),
+                lambda: sp.spconv_glu_grad(moved(d), x, w), lambda: sp.spconv_glu_grad(d, moved(x), w),
+                lambda: sp.spconv_glu_grad(d, x, moved(w))):
+        with pytest.raises(sp.SpconvError) as e:
+            bad()
+        assert e.value.code == -1 and "16-byte" in str(e.value)
+    wide = torch.zeros(4, 17, dtype=dt, device=DEV)[:, 1:]
+    assert wide.data_ptr() % 16 and sp.spconv_glu(wide, w).shape == (4, 24)
