@@ -24,6 +24,7 @@ struct GluParams {
     int C, F;
     int64_t rows_per_split;
     int dx_splits, dx_per;      // of dx's reduction (2 F), and its length
+    int64_t first_block;        // of this launch (tiles: a call may need several)
     bool stream;       // outputs past the caches
 };
 

@@ -291,8 +291,21 @@ __device__ __forceinline__ bool place_block(int64_t id, int64_t outer, int inner
     }
     return o < outer;
 }
-unsigned block_count(int64_t outer, int64_t inner) {
-    return (unsigned)((by_xcd(outer) ? round_up(outer, kXcds) : outer) * inner);
+int64_t block_count(int64_t outer, int64_t inner) { return (by_xcd(outer) ? round_up(outer, kXcds) : outer) * inner; }
+
+// A launch's threads are counted in 32 bits: at 2^32 it is refused, above it runs
+// only what is left of the number.  Calls with more (fp32, h of 137 GB; rows of 8
+// channels from 2^30 on) take several launches, of whole rounds of the XCDs.
+constexpr int64_t kLaunchThreads = (int64_t)1 << 31;
+template <class L>
+hipError_t launch_blocks(GluParams& p, int64_t blocks, int threads, L launch) {
+    const int64_t most = kLaunchThreads / threads;
+    for (p.first_block = 0; p.first_block < blocks; p.first_block += most) {
+        launch((unsigned)std::min(most, blocks - p.first_block));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 // TILE rows x TILE / 2 hidden features, both projections: h, or (GRAD) da and
@@ -308,7 +321,7 @@ __global__ void __launch_bounds__(Shape<TILE>::THREADS, TILE == 128 ? 4 : 3) k_g
     const int C = p.C, F = p.F;
     int64_t tile;
     int f0;
-    if (!place_block(blockIdx.x, (p.N + TILE - 1) / TILE, (F + FT - 1) / FT, tile, f0)) return;
+    if (!place_block(p.first_block + blockIdx.x, (p.N + TILE - 1) / TILE, (F + FT - 1) / FT, tile, f0)) return;
     f0 *= FT;
     const int64_t r0 = tile * TILE;
     const T* x = (const T*)p.x;
@@ -505,12 +518,13 @@ __device__ __forceinline__ void glu_dw_tile(const GluParams& p, int64_t block, c
 // Both products of the gradient: they need the same da and db and nothing of
 // each other.
 template <typename T, int TILE>
-__global__ void __launch_bounds__(Shape<TILE>::THREADS, TILE == 128 ? 4 : 3) k_glu_products(GluParams p, unsigned dx_blocks) {
+__global__ void __launch_bounds__(Shape<TILE>::THREADS, TILE == 128 ? 4 : 3) k_glu_products(GluParams p, int64_t dx_blocks) {
     __shared__ __align__(16) char smem[kMostBytes<T, TILE>];
-    if (blockIdx.x < dx_blocks)
-        glu_dx_tile<T, TILE>(p, blockIdx.x, smem);
+    const int64_t block = p.first_block + blockIdx.x;
+    if (block < dx_blocks)
+        glu_dx_tile<T, TILE>(p, block, smem);
     else
-        glu_dw_tile<T, TILE>(p, blockIdx.x - dx_blocks, smem);
+        glu_dw_tile<T, TILE>(p, block - dx_blocks, smem);
 }
 
 // The partial sums of dw (splits, C, 2 F), dbias (tiles, 2 F) and dx (splits,
@@ -616,8 +630,8 @@ GluLayout glu_layout(int64_t N, int C, int F, int dtype) {
 }
 
 template <typename T, int ACT>
-hipError_t glu_project(const GluParams& p, bool grad, const GluLayout& l, hipStream_t st) {
-    const unsigned blocks = block_count(l.tiles, tiles_of(p.F, l.ptile / 2));
+hipError_t glu_project(GluParams p, bool grad, const GluLayout& l, hipStream_t st) {
+    const int64_t blocks = block_count(l.tiles, tiles_of(p.F, l.ptile / 2));
     int threads = Shape<64>::THREADS;
     auto fn = grad ? k_glu_project<T, ACT, true, 64> : k_glu_project<T, ACT, false, 64>;
     if constexpr (sizeof(T) == 2) {
@@ -629,21 +643,19 @@ hipError_t glu_project(const GluParams& p, bool grad, const GluLayout& l, hipStr
         fn = grad ? k_glu_project<T, ACT, true, 32> : k_glu_project<T, ACT, false, 32>;
         threads = Shape<32>::THREADS;
     }
-    fn<<<blocks, threads, 0, st>>>(p);
-    return hipGetLastError();
+    return launch_blocks(p, blocks, threads, [&](unsigned n) { fn<<<n, threads, 0, st>>>(p); });
 }
 
 template <typename T>
-hipError_t glu_products(const GluParams& p, const GluLayout& l, hipStream_t st) {
-    const unsigned dx = block_count(tiles_of(p.N, l.tile), tiles_of(p.C, l.tile) * l.dx_splits);
-    const unsigned dw = block_count(l.splits, tiles_of(2 * p.F, l.tile) * tiles_of(p.C, l.tile));
+hipError_t glu_products(GluParams p, const GluLayout& l, hipStream_t st) {
+    const int64_t dx = block_count(tiles_of(p.N, l.tile), tiles_of(p.C, l.tile) * l.dx_splits);
+    const int64_t dw = block_count(l.splits, tiles_of(2 * p.F, l.tile) * tiles_of(p.C, l.tile));
     const int threads = l.tile == 128 ? Shape<128>::THREADS : Shape<64>::THREADS;
     auto fn = k_glu_products<T, 64>;
     if constexpr (sizeof(T) == 2) {
         if (l.tile == 128) fn = k_glu_products<T, 128>;
     }
-    fn<<<dx + dw, threads, 0, st>>>(p, dx);
-    return hipGetLastError();
+    return launch_blocks(p, dx + dw, threads, [&](unsigned n) { fn<<<n, threads, 0, st>>>(p, dx); });
 }
 
 template <typename T>
