@@ -356,6 +356,8 @@ int spconv_glu_grad(const void* dout, const void* x, const void* w, const float*
  * up to 2^-24 of itself per step.
  * An infinite state stays infinite until a gate is 0 in 32 bits (z below -87),
  * which makes it NaN; neither leaves its scene and channel.
+ * Calls of more than 2^32 threads (the gradient from N C = 3.5e10 at the widths
+ * that use their threads least) give SPCONV_E_UNSUPPORTED.
  * The contents of offsets and order are not checked: bad values give wrong
  * states, never an access outside the given arrays. */
 int spconv_scan_workspace_size(int64_t N, int C, int dtype, size_t* bytes);

@@ -650,6 +650,8 @@ static int scan_size(int64_t N, int C, int dtype, bool grad, size_t* bytes) {
     if (!bytes) return fail(SPCONV_E_INVALID, "bytes pointer is NULL");
     int rc = check_rows(N, C, dtype, "C");
     if (rc) return rc;
+    if (!spc::scan_fits(N, C, grad))
+        return fail(SPCONV_E_UNSUPPORTED, "N=%lld rows of C=%d channels need more than 2^32 threads", (long long)N, C);
     *bytes = spc::scan_workspace_bytes(N, C, dtype, grad);
     return SPCONV_OK;
 }

@@ -895,9 +895,13 @@ ScanLayout scan_layout(int64_t N, int C, bool grad) {
     return l;
 }
 
+unsigned scan_blocks(const ScanLayout& l) {
+    return (unsigned)(l.tiles > 1 ? round_up(l.chunks, 8) * l.tiles : l.chunks);
+}
+
 template <typename T, int G, RowEnd END>
 hipError_t scan_go(ScanParams p, bool grad, const ScanLayout& l, char* ws, hipStream_t st) {
-    const unsigned grid = (unsigned)(l.tiles > 1 ? round_up(l.chunks, 8) * l.tiles : l.chunks);
+    const unsigned grid = scan_blocks(l);
     p.chunks = l.chunks;
     p.tiles = l.tiles;
     p.maps = (Map*)ws;
@@ -947,6 +951,9 @@ hipError_t scan_dispatch(const ScanParams& p, bool grad, char* ws, hipStream_t s
 
 }  // namespace
 
+bool scan_fits(int64_t N, int C, bool grad) {
+    return (uint64_t)scan_blocks(scan_layout(N, C, grad)) * kScanThreads < (uint64_t)1 << 32;
+}
 size_t scan_workspace_bytes(int64_t N, int C, int, bool grad) { return scan_layout(N, C, grad).total; }
 
 hipError_t launch_scan(const ScanArgs& a, bool grad, hipStream_t stream) {

@@ -266,6 +266,8 @@ struct ScanArgs {
     int64_t N;
     int C, scenes, dtype;
 };
+// A launch's threads are counted in 32 bits: false where a kernel would need more.
+bool scan_fits(int64_t N, int C, bool grad);
 size_t scan_workspace_bytes(int64_t N, int C, int dtype, bool grad);
 hipError_t launch_scan(const ScanArgs& a, bool grad, hipStream_t stream);
 
