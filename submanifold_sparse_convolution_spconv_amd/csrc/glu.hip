@@ -561,8 +561,23 @@ __global__ void __launch_bounds__(kJoinCols * 16) k_glu_join(GluParams p, int sp
     store_four((T*)p.dw + (m < F ? c * F + m : (p.C + c) * F + (m - F)), t.f);
 }
 
-// Few channels and enough rows to give every CU a block of them: glu_rows.hip.
-bool use_rows(int64_t N, int C, int dtype) { return dtype == SPCONV_BF16 && C <= kGluRowC && N >= 32768; }
+// Few channels and enough rows: glu_rows.hip.  Its blocks have 256 rows and one of
+// them fills a CU, so that a call takes the same time up to 65,536 rows, while the
+// tiles' time grows with the rows.  The two cross at about 49,152 rows forward and
+// 32,768 in the gradient, which reads and writes da and db with tiles.  us, rows
+// against tiles:
+//                    forward                                 gradient
+//   C -> F       32,768       49,152       65,536       24,576       32,768       49,152
+//   32 -> 256    11.9/10.3    12.7/13.7    13.5/16.9    29.9/34.9    31.7/41.4    34.2/51.3
+//   64 -> 512    21.9/16.9    22.5/22.3    22.8/28.3    52.2/58.9    56.2/66.3    62.1/84.9
+//   128 -> 256   17.1/12.0    18.1/16.6    19.3/21.0    50.6/44.5    54.1/53.4    57.9/65.5
+//   128 -> 1024  49.8/36.5    51.5/52.5    56.2/68.7   121.1/108.8  129.1/124.4  148.1/187.7
+// Weights that take several slabs of LDS (128 -> 344 and wider), loaded again for
+// every block, do not turn this: 131,072 rows 128 -> 344 49/52 and 180/218 us,
+// 128 -> 1024 117/163 and 324/541.
+bool use_rows(int64_t N, int C, int dtype, bool grad) {
+    return dtype == SPCONV_BF16 && C <= kGluRowC && N >= (grad ? 32768 : 49152);
+}
 
 // Tiles of 128 where they fill the card (the operands are then read half as
 // often), of 64 where they would not.
@@ -579,9 +594,9 @@ struct GluLayout {
     size_t xpart;
     bool rows;
 };
-GluLayout glu_layout(int64_t N, int C, int F, int dtype) {
+GluLayout glu_layout(int64_t N, int C, int F, int dtype, bool grad) {
     GluLayout l{};
-    l.rows = use_rows(N, C, dtype);
+    l.rows = use_rows(N, C, dtype, grad);
     if (l.rows) {
         const int want = glu_rows_splits(N, C, F);
         l.rows_per_split = round_up((N + want - 1) / want, 64);
@@ -685,11 +700,11 @@ hipError_t glu_go(GluParams p, int act, bool grad, const GluLayout& l, float* db
 
 }  // namespace
 
-size_t glu_grad_workspace_bytes(int64_t N, int C, int F, int dtype) { return glu_layout(N, C, F, dtype).total; }
+size_t glu_grad_workspace_bytes(int64_t N, int C, int F, int dtype) { return glu_layout(N, C, F, dtype, true).total; }
 
 hipError_t launch_glu(const GluArgs& a, bool grad, hipStream_t stream) {
     if (a.N == 0 && !grad) return hipSuccess;
-    const GluLayout l = glu_layout(a.N, a.C, a.F, a.dtype);
+    const GluLayout l = glu_layout(a.N, a.C, a.F, a.dtype, grad);
     GluParams p{};
     p.x = a.x;
     p.w = a.w;
