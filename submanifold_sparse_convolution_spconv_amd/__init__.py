@@ -525,12 +525,16 @@ def spconv_wgrad(feats, dout, nmap: NMap, out=None, workspace=None):
 # is current, outputs made like the inputs.
 _torch = None
 _row_codes = {}
+_current_device = _raw_stream = None
 
 
 def _load_torch():
-    global _torch
+    global _torch, _current_device, _raw_stream
     import torch
     _row_codes.update({torch.float32: SPCONV_F32, torch.bfloat16: SPCONV_BF16})
+    # torch's own short cuts, where this torch has them
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
     _torch = torch
 
 
@@ -552,11 +556,11 @@ def _call(name, dev, *args):
     """The C function on the current stream of dev."""
     fn = getattr(_lib or load_library(), name)
     index = dev.index
-    if _torch._C._cuda_getDevice() == index:
-        rc = fn(*args, _torch._C._cuda_getCurrentRawStream(index))
+    if _current_device() == index:
+        rc = fn(*args, _raw_stream(index))
     else:
         with _torch.cuda.device(dev):
-            rc = fn(*args, _torch._C._cuda_getCurrentRawStream(index))
+            rc = fn(*args, _raw_stream(index))
     if rc:
         _check(rc, name)
 
