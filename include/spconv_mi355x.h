@@ -282,7 +282,8 @@ int spconv_wgrad(const void* feats, const void* dout, const spconv_nmap* nmap,
  * are fp32, each output is rounded once, two calls with the same inputs give
  * bit-identical outputs.  C up to 4096.  Asynchronous on `stream`, no
  * allocation, no synchronisation; N = 0 enqueues nothing but the zeros of
- * outputs that sum over rows.  The row operators' conventions on errors are
+ * outputs that sum over rows.  Outputs do not overlap inputs or the workspace
+ * (but spconv_layernorm's y may be x).  The row operators' conventions on errors are
  * the library's. */
 
 /* Layer norm over each row's channels.

@@ -14,9 +14,14 @@
 // axis is not contiguous in memory is read back with the transposing LDS read
 // (bf16) or one word per lane (fp32).
 //
-// Gradient of 29,578 rows, 256 -> 680 bf16: 55 us for da and db (the activations),
-// 75 us for both products (547 TFLOP/s; LDS reads take 47% of the time), 7 us to
-// join the partial sums.
+// With bfloat16, da and db are rounded to it once, since the matrix instructions
+// take operands of that type (two-part operands would double the products): the
+// gradients' error against 64 bits is 2.3e-3 of their norm where unrounded ones give
+// 1.7e-3, the outputs' own rounding.
+//
+// Gradient of 29,578 rows, 256 -> 680 bf16 (averages of ten): 58 us for da and db (the
+// activations), 80 us for both products (513 TFLOP/s; LDS reads take 47% of the time),
+// 8 us to join the partial sums.  In fp32 197 us forward (104 TFLOP/s), 705 us gradient.
 #include "glu.h"
 #include "join.h"
 

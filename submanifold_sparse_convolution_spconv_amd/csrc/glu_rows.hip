@@ -10,8 +10,11 @@
 // operations, where writing da and db and reading them twice would be 12 N F
 // bytes, which takes longer below about 300 channels.
 //
-// 1,006,716 rows, 128 -> 256, silu: 188 us forward (4.1 TB/s), 615 us gradient (860
-// TFLOP/s with what is computed again).  The gradient's kernels are bound by issue:
+// 1,006,716 rows, 128 -> 256, silu: 188 to 200 us forward, card by card (3.9 to 4.1
+// TB/s), 613 to 636 us gradient (830 to 860 TFLOP/s with what is computed again).  With
+// fewer channels the forward's time follows its activations, not its bytes: 100,000
+// rows 32 -> 256 take 18 us (3.1 TB/s), 64 -> 512 34 us (3.3).  The gradient's kernels
+// are bound by issue:
 // vector instructions (the activations) fill 55% of the slots, matrix instructions
 // keep their unit busy for 41% of the time, at a clock that the load lowers.
 //
@@ -31,7 +34,8 @@ namespace {
 
 // Two waves per SIMD, one workgroup per CU.  (The forward's registers would
 // allow three waves; they take 215 us where two take 182 at 1,006,716 rows,
-// 128 -> 256: the LDS reads of the weights get in each other's way.)
+// 128 -> 256, the one width where both were measured: the LDS reads of the weights
+// get in each other's way.)
 constexpr int kRowThreads = 512;
 constexpr int kRowWaves = kRowThreads / 64;
 constexpr int NT = 2;                 // 16-row tiles per wave

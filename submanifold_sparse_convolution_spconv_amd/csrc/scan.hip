@@ -32,8 +32,8 @@
 // included (0.5% after 300,000 steps at z = 17).  States, maps and sums are fp32.
 //
 // Long sequences are bound by memory, at the price of reading the rows twice:
-// 1,006,716 x 128 bf16 takes 273 us forward (1.29 GB, 4.7 TB/s) and 466 us for the
-// gradient (2.06 GB, 4.4 TB/s).  Workgroups that keep their rows and wait for the
+// 1,006,716 x 128 bf16 takes 274 to 288 us forward, card by card (1.29 GB, 4.5 to 4.7
+// TB/s), and 472 to 490 us for the gradient (2.06 GB, 4.2 to 4.4 TB/s).  Workgroups that keep their rows and wait for the
 // states before them took 323 and 867 us.  Short sequences are a chain of reads:
 // 64 scenes of one row, 7.6 us.
 #include "rowops.h"
