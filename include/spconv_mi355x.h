@@ -54,7 +54,13 @@ enum spconv_dtype {
 
 enum spconv_act {
     SPCONV_SILU = 0,            /* a sigmoid(a)                                            */
-    SPCONV_GELU = 1             /* a (1 + erf(a / sqrt 2)) / 2                             */
+    SPCONV_GELU = 1,            /* a (1 + erf(a / sqrt 2)) / 2                             */
+    SPCONV_LINEAR = 2           /* a (group norm only)                                     */
+};
+
+enum spconv_layout {
+    SPCONV_HALF = 0,            /* pair i of P: elements i and i + P                       */
+    SPCONV_INTERLEAVED = 1      /* pair i: elements 2 i and 2 i + 1                        */
 };
 
 /* Opaque host-side handle of a built neighbour map.  The map's device data
@@ -380,6 +386,141 @@ int spconv_scan_grad_workspace_size(int64_t N, int C, int dtype, size_t* bytes);
 int spconv_scan_grad(const void* dout, const void* x, const void* z, const int32_t* offsets, const int32_t* order,
                      const float* h0, const float* dlast, void* workspace, size_t workspace_bytes, void* dx,
                      void* dz, float* dh0, int64_t N, int C, int scenes, int dtype, void* stream);
+
+/* ---- Operators that mix the voxels of a scene ----------------------------
+ * Attention among the rows of packed sequences, rotary positions of its
+ * queries and keys, and the group norm that stands before a convolution.
+ * Rows lie one after the other, sequence b (a scene, or a run of the map's
+ * schedule order) at the positions offsets[b] .. offsets[b+1] - 1; 0 =
+ * offsets[0] <= ... <= offsets[B] <= N, and sequences without positions may
+ * stand anywhere.  Rows behind the last sequence are neither read nor
+ * written: outputs stay there as they were.  The contents of offsets and
+ * orders are not checked: bad values give wrong results, never an access
+ * outside the given arrays.  Sums, statistics and softmax are fp32, each output
+ * is rounded once, two calls with the same inputs give bit-identical
+ * outputs.  Asynchronous on `stream`, no allocation, no synchronisation.
+ * Outputs do not overlap inputs or the workspace (but spconv_rotary's y may be
+ * x, and spconv_groupnorm's too).
+ *
+ * Heads: a tensor of N rows and H heads of D elements may be strided, so that
+ * the parts of one projection (N, 3, H, D) are used where they lie.  `strides`
+ * (host) holds, for each tensor in the order that the call states, two
+ * numbers: elements from row to row and from head to head; NULL: all
+ * contiguous.  A head's elements are consecutive. */
+
+/* Frequencies of rotary positions (host; freqs is host memory of `pairs`
+ * doubles, to be copied to the device by the caller), in radians per step of a
+ * position: the pairs are divided evenly over the axes, and pair j of an axis'
+ * n = pairs / axes turns by base^(-j / n).  For contexts longer than a
+ * model has seen, by factor > 1:
+ *   original = 0   every frequency divided by factor
+ *   original > 0   by parts: a pair that makes r turns over `original` positions
+ *                  is divided by factor where r <= 1, kept where r >= 32, and
+ *                  between them mixed linearly in r
+ * axes in 1..8, pairs a multiple of it, base > 1, factor >= 1, original >= 0. */
+int spconv_rotary_freqs(int pairs, int axes, double base, double factor, double original, double* freqs);
+
+/* Rotary positions.  For each row n, head and pair i of the first 2 pairs
+ * elements of a head (which they are: enum spconv_layout), turned by
+ * t = positions[n, i / (pairs / axes)] freqs[i]:
+ *   (a, b) -> gain (a cos t - b sin t, b cos t + a sin t)
+ * The elements from 2 pairs on are copied.
+ *   x, y      (dev) (N, H, D) of dtype, aligned to their elements; y may be x
+ *             (with the same strides)
+ *   positions (dev) int32, rows of `axes` values, pos_stride elements apart:
+ *             coordinates of voxels as spconv_build_nmap takes them, or places
+ *             along a sequence; any int32
+ *   freqs     (dev) float64 (pairs,), aligned to 8 bytes
+ *   gain      of the turned elements, cosines and sines alike (long contexts
+ *             ask for one next to the frequencies)
+ *   strides   x, y
+ * Angles are taken in 64 bits, so that positions far along lose nothing.
+ * H, D up to 4096.  spconv_rotary_grad is the adjoint: dx from dout (in the
+ * places of y and x), the turn the other way. */
+int spconv_rotary(const void* x, const int32_t* positions, int64_t pos_stride, const double* freqs, void* y,
+                  const int64_t* strides, int64_t N, int H, int D, int pairs, int axes, int layout, float gain,
+                  int dtype, void* stream);
+int spconv_rotary_grad(const void* dout, const int32_t* positions, int64_t pos_stride, const double* freqs, void* dx,
+                       const int64_t* strides, int64_t N, int H, int D, int pairs, int axes, int layout, float gain,
+                       int dtype, void* stream);
+
+/* Group norm of each scene's rows with an activation, channels last.
+ *   y = act((x - mean) rstd weight + bias),  rstd = 1 / sqrt(var + eps),
+ * mean and var (the mean squared deviation) over a scene's rows and the C /
+ * groups consecutive channels of a group.
+ *   x, y     (dev) (N, C) of dtype, aligned to their elements; y may be x
+ *   offsets  (dev) int32 (scenes + 1,)
+ *   weight, bias (dev) float32 (C,), or NULL for 1 and 0
+ *   mean, rstd   (dev) float32 (scenes, groups) written, or both NULL; 0 and
+ *            1 / sqrt(eps) for a scene without rows
+ *   act      SPCONV_SILU, SPCONV_GELU or SPCONV_LINEAR
+ *   workspace (dev) spconv_groupnorm_workspace_size bytes, 256-byte aligned
+ * C up to 4096, a multiple of groups; eps >= 0.  Calls of more than 2^32
+ * threads (from 1.6e7 scenes and groups on) give SPCONV_E_UNSUPPORTED. */
+int spconv_groupnorm_workspace_size(int64_t N, int C, int scenes, int groups, int dtype, size_t* bytes);
+int spconv_groupnorm(const void* x, const int32_t* offsets, const float* weight, const float* bias, void* workspace,
+                     size_t workspace_bytes, void* y, float* mean, float* rstd, int64_t N, int C, int scenes,
+                     int groups, float eps, int act, int dtype, void* stream);
+
+/* Gradient of spconv_groupnorm, from the statistics that it wrote.  With
+ * xhat = (x - mean) rstd, dz = dout act'(xhat weight + bias), g = dz weight and
+ * means over a scene's rows and a group's channels:
+ *   dx      = rstd (g - mean(g) - xhat mean(g xhat))      (N, C), dtype
+ *   dweight = sum_n dz xhat,  dbias = sum_n dz            float32 (C,), over all
+ *             scenes; written, or both NULL
+ *   weight, bias  as given to the forward
+ *   workspace (dev) spconv_groupnorm_workspace_size bytes, 256-byte aligned. */
+int spconv_groupnorm_grad(const void* dout, const void* x, const int32_t* offsets, const float* mean,
+                          const float* rstd, const float* weight, const float* bias, void* workspace,
+                          size_t workspace_bytes, void* dx, float* dweight, float* dbias, int64_t N, int C,
+                          int scenes, int groups, int act, int dtype, void* stream);
+
+/* Attention within packed sequences.
+ *   out[i, h] = sum_j p[i, j] v[j, h'],  p[i, :] = softmax over j of scale q[i, h] k[j, h']
+ *   lse[i, h] = log sum_j exp(scale q[i, h] k[j, h'])
+ * for the queries i and keys j of one sequence, h' = h / (H / HK): runs of H / HK
+ * heads of queries share a head of keys and values.  With Lq queries and Lk
+ * keys, `causal` lets query i see the keys j <= i + Lk - Lq: the last query sees
+ * all of them (a new voxel the keys of those before it).  A query that sees no
+ * key gives out 0 and lse -inf.  A key that a query does not see has no effect
+ * on it, whatever it holds.
+ *   q        (dev) (N, H, D);  k, v (dev) (M, HK, D);  out (dev) (N, H, D)
+ *            written; of dtype, 16-byte aligned, strides multiples of 16 bytes
+ *   offsets  (dev) int32 (B + 1,): the sequences' queries
+ *   koffsets (dev) int32 (B + 1,): their keys; or NULL: the queries' own rows (then
+ *            M = N, and order holds for the keys too)
+ *   order    (dev) int32 (N,): the row of a position (as in spconv_scan), each
+ *            row once; or NULL.  korder (dev) int32 (M,): the keys', with koffsets
+ *   strides  q, k, v, out
+ *   lse      (dev) float32 (N, H) written, or NULL
+ *   workspace (dev) spconv_attention_workspace_size bytes, 256-byte aligned (may
+ *            be NULL when that is 0)
+ * D a multiple of 8 up to 128, H and HK up to 4096, H a multiple of HK, scale >
+ * 0.  Scores and sums are fp32; with SPCONV_BF16 the weights p (before their
+ * division by the sum) are rounded to bfloat16 once, as the operand of the
+ * second product.  Calls of more than 2^32 threads give SPCONV_E_UNSUPPORTED. */
+int spconv_attention_workspace_size(int64_t N, int64_t M, int B, int H, int HK, int D, int dtype, size_t* bytes);
+int spconv_attention(const void* q, const void* k, const void* v, const int32_t* offsets, const int32_t* koffsets,
+                     const int32_t* order, const int32_t* korder, const int64_t* strides, void* workspace,
+                     size_t workspace_bytes, void* out, float* lse, int64_t N, int64_t M, int B, int H, int HK, int D,
+                     float scale, int causal, int dtype, void* stream);
+
+/* Gradient of spconv_attention, from its output and lse.
+ *   ds[i, j] = p[i, j] (dout[i] v[j] - dout[i] out[i])
+ *   dq[i] = scale sum_j ds[i, j] k[j],  dk[j] = scale sum_i ds[i, j] q[i],
+ *   dv[j] = sum_i p[i, j] dout[i]      (dk and dv over all heads that share them)
+ *   dout, out, dq as q;  dk, dv as k;  all of dtype
+ *   strides  q, k, v, out, dout, dq, dk, dv
+ *   workspace (dev) spconv_attention_grad_workspace_size bytes, 256-byte aligned
+ * With SPCONV_BF16, p and ds are rounded to bfloat16 once, as operands.  Other
+ * arguments, and what is said about them, are spconv_attention's. */
+int spconv_attention_grad_workspace_size(int64_t N, int64_t M, int B, int H, int HK, int D, int dtype,
+                                         size_t* bytes);
+int spconv_attention_grad(const void* dout, const void* q, const void* k, const void* v, const void* out,
+                          const float* lse, const int32_t* offsets, const int32_t* koffsets, const int32_t* order,
+                          const int32_t* korder, const int64_t* strides, void* workspace, size_t workspace_bytes,
+                          void* dq, void* dk, void* dv, int64_t N, int64_t M, int B, int H, int HK, int D, float scale,
+                          int causal, int dtype, void* stream);
 
 /* Release a handle (host memory only; the arena stays the caller's). */
 void spconv_nmap_destroy(spconv_nmap* h);

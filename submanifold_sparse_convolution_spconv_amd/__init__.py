@@ -32,6 +32,17 @@ Row-wise operators of a voxel block, on (N, C) feature rows:
     spconv_glu_grad(dout, x, w, bias=None, act="silu") -> (dx, dw, dbias)
     spconv_scan(x, z, offsets, order=None, h0=None) -> (h, last)
     spconv_scan_grad(dout, x, z, offsets, order=None, h0=None, dlast=None) -> (dx, dz, dh0)
+Operators that mix the voxels of a scene, on packed rows with offsets:
+    spconv_groupnorm(x, offsets, groups, weight=None, bias=None, eps=1e-5, act=None, stats=False)
+        -> y, or (y, mean, rstd)
+    spconv_groupnorm_grad(dout, x, offsets, groups, mean, rstd, weight=None, bias=None, act=None)
+        -> (dx, dweight, dbias)
+    spconv_rotary_freqs(pairs, axes=1, base=10000.0, factor=1.0, original=0.0, device="cuda") -> freqs
+    spconv_rotary(x, positions, freqs, layout="half", gain=1.0) -> y
+    spconv_rotary_grad(dout, positions, freqs, layout="half", gain=1.0) -> dx
+    spconv_attention(q, k, v, offsets, koffsets=None, order=None, korder=None, causal=False, scale=None, stats=False)
+        -> out, or (out, lse)
+    spconv_attention_grad(dout, q, k, v, out, lse, offsets, ...) -> (dq, dk, dv)
 """
 from __future__ import annotations
 
@@ -50,6 +61,10 @@ __all__ = [
     "spconv_layernorm", "spconv_layernorm_grad_workspace_size", "spconv_layernorm_grad",
     "spconv_glu", "spconv_glu_grad_workspace_size", "spconv_glu_grad", "SPCONV_SILU", "SPCONV_GELU",
     "spconv_scan_workspace_size", "spconv_scan", "spconv_scan_grad_workspace_size", "spconv_scan_grad",
+    "spconv_groupnorm_workspace_size", "spconv_groupnorm", "spconv_groupnorm_grad", "SPCONV_LINEAR",
+    "spconv_rotary_freqs", "spconv_rotary", "spconv_rotary_grad", "SPCONV_HALF", "SPCONV_INTERLEAVED",
+    "spconv_attention_workspace_size", "spconv_attention", "spconv_attention_grad_workspace_size",
+    "spconv_attention_grad",
     "SPCONV_F32", "SPCONV_BF16", "STATUS",
 ]
 
@@ -61,6 +76,9 @@ SPCONV_F32 = 0
 SPCONV_BF16 = 1
 SPCONV_SILU = 0
 SPCONV_GELU = 1
+SPCONV_LINEAR = 2
+SPCONV_HALF = 0
+SPCONV_INTERLEAVED = 1
 STATUS = {0: "SPCONV_OK", -1: "SPCONV_E_INVALID", -2: "SPCONV_E_UNSUPPORTED",
           -3: "SPCONV_E_COORD_RANGE", -4: "SPCONV_E_DUPLICATE", -5: "SPCONV_E_WORKSPACE",
           -6: "SPCONV_E_HIP"}
@@ -131,6 +149,25 @@ def load_library():
     lib.spconv_scan.argtypes = [vp, vp, vp, vp, vp, vp, sz, vp, vp, i64, i32, i32, i32, vp]
     lib.spconv_scan_grad_workspace_size.argtypes = [i64, i32, i32, szp]
     lib.spconv_scan_grad.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp, vp, i64, i32, i32, i32, vp]
+    f64 = ctypes.c_double
+    rotary = [vp, vp, i64, vp, vp, vp, i64, i32, i32, i32, i32, i32, f32, i32, vp]
+    lib.spconv_rotary_freqs.argtypes = [i32, i32, f64, f64, f64, vp]
+    lib.spconv_rotary.argtypes = rotary
+    lib.spconv_rotary_grad.argtypes = rotary
+    lib.spconv_groupnorm_workspace_size.argtypes = [i64, i32, i32, i32, i32, szp]
+    lib.spconv_groupnorm.argtypes = [vp, vp, vp, vp, vp, sz, vp, vp, vp, i64, i32, i32, i32, f32, i32, i32, vp]
+    lib.spconv_groupnorm_grad.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp, vp, i64, i32, i32, i32, i32,
+                                          i32, vp]
+    lib.spconv_attention_workspace_size.argtypes = [i64, i64, i32, i32, i32, i32, i32, szp]
+    lib.spconv_attention.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp, i64, i64, i32, i32, i32, i32, f32,
+                                     i32, i32, vp]
+    lib.spconv_attention_grad_workspace_size.argtypes = [i64, i64, i32, i32, i32, i32, i32, szp]
+    lib.spconv_attention_grad.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp, vp, i64, i64, i32,
+                                          i32, i32, i32, f32, i32, i32, vp]
+    for f in (lib.spconv_rotary_freqs, lib.spconv_rotary, lib.spconv_rotary_grad, lib.spconv_groupnorm_workspace_size,
+              lib.spconv_groupnorm, lib.spconv_groupnorm_grad, lib.spconv_attention_workspace_size,
+              lib.spconv_attention, lib.spconv_attention_grad_workspace_size, lib.spconv_attention_grad):
+        f.restype = i32
     for f in (lib.spconv_glu, lib.spconv_glu_grad_workspace_size, lib.spconv_glu_grad,
               lib.spconv_scan_workspace_size, lib.spconv_scan, lib.spconv_scan_grad_workspace_size,
               lib.spconv_scan_grad, lib.spconv_layernorm, lib.spconv_layernorm_grad_workspace_size, lib.spconv_layernorm_grad):
@@ -765,3 +802,273 @@ def spconv_scan_grad(dout, x, z, offsets, order=None, h0=None, dlast=None, works
     _call("spconv_scan_grad", dev, _at(dout), _at(x), _at(z), _at(offsets), _at(order), _at(h0), _at(dlast), _at(ws),
           n, _at(dx), _at(dz), _at(dh0), N, C, B, dt)
     return dx, dz, dh0
+
+
+# Operators that mix the voxels of a scene: group norm over its rows, rotary
+# positions and attention within packed sequences.
+_GROUP_ACTS = {None: SPCONV_LINEAR, "silu": SPCONV_SILU, "gelu": SPCONV_GELU}
+
+
+def _offsets(t, dev, name):
+    if t is None or t.dtype != _torch.int32 or t.dim() != 1 or t.numel() < 2 or t.device != dev:
+        raise ValueError(f"{name} must be an int32 (sequences + 1,) tensor on the features' device")
+    return t.contiguous()
+
+
+def spconv_groupnorm_workspace_size(N: int, C: int, scenes: int, groups: int, dtype: int) -> int:
+    return _size("spconv_groupnorm_workspace_size", N, C, scenes, groups, dtype)
+
+
+def _group_args(x, offsets, groups, weight, bias, act):
+    dt = _row_dtype(x)
+    N, C = x.shape
+    dev = x.device
+    offsets = _offsets(offsets, dev, "offsets")
+    if act not in _GROUP_ACTS:
+        raise ValueError("act must be None, 'silu' or 'gelu'")
+    weight = _like(weight, (C,), _torch.float32, dev, "weight")
+    bias = _like(bias, (C,), _torch.float32, dev, "bias")
+    B = offsets.numel() - 1
+    return dt, N, C, B, dev, x.contiguous(), offsets, weight, bias, _GROUP_ACTS[act], \
+        spconv_groupnorm_workspace_size(N, C, B, groups, dt)
+
+
+def spconv_groupnorm(x, offsets, groups: int, weight=None, bias=None, eps: float = 1e-5, act=None,
+                     stats: bool = False, out=None, workspace=None):
+    """Group norm with an activation over each scene's rows: x (N, C) float32 or
+    bfloat16, CUDA, C <= 4096, a multiple of groups; offsets int32 (scenes + 1,),
+    the scenes' rows; weight, bias float32 (C,) or None; act None, "silu" or
+    "gelu" (erf).  Returns y in x's dtype, with ``stats`` (y, mean, rstd), float32
+    (scenes, groups) each, for the gradient.  Rows behind the last scene are not
+    read, and not written in ``out`` (in a new output they hold anything).
+    workspace: a uint8 tensor of at least spconv_groupnorm_workspace_size bytes
+    (allocated when None)."""
+    dt, N, C, B, dev, x, offsets, weight, bias, a, n = _group_args(x, offsets, groups, weight, bias, act)
+    y = _out(out, x.shape, x, "out")
+    mean = _torch.empty((B, groups), dtype=_torch.float32, device=dev) if stats else None
+    rstd = _torch.empty((B, groups), dtype=_torch.float32, device=dev) if stats else None
+    ws, n = _workspace(workspace, n, dev, "spconv_groupnorm_workspace_size")
+    _call("spconv_groupnorm", dev, _at(x), _at(offsets), _at(weight), _at(bias), _at(ws), n, _at(y), _at(mean),
+          _at(rstd), N, C, B, groups, eps, a, dt)
+    return (y, mean, rstd) if stats else y
+
+
+def spconv_groupnorm_grad(dout, x, offsets, groups: int, mean, rstd, weight=None, bias=None, act=None, out=None,
+                          workspace=None, sums=None):
+    """Gradient of spconv_groupnorm: dout and x (N, C), the statistics that the
+    forward returned, its weight, bias and act.  ``sums``: whether dweight and
+    dbias are wanted (None: where weight or bias is given).  Returns (dx, dweight,
+    dbias), dweight and dbias float32 (C,), or None both.  workspace: as the
+    forward's."""
+    dt, N, C, B, dev, x, offsets, weight, bias, a, n = _group_args(x, offsets, groups, weight, bias, act)
+    dout = _like(dout, (N, C), x.dtype, dev, "dout")
+    mean = _like(mean, (B, groups), _torch.float32, dev, "mean")
+    rstd = _like(rstd, (B, groups), _torch.float32, dev, "rstd")
+    if dout is None or mean is None or rstd is None:
+        raise ValueError("dout, mean and rstd must be given")
+    dx = _out(out, x.shape, x, "out")
+    dweight = dbias = None
+    if (weight is not None or bias is not None) if sums is None else sums:
+        dweight = _torch.empty(C, dtype=_torch.float32, device=dev)
+        dbias = _torch.empty(C, dtype=_torch.float32, device=dev)
+    ws, n = _workspace(workspace, n, dev, "spconv_groupnorm_workspace_size")
+    _call("spconv_groupnorm_grad", dev, _at(dout), _at(x), _at(offsets), _at(mean), _at(rstd), _at(weight), _at(bias),
+          _at(ws), n, _at(dx), _at(dweight), _at(dbias), N, C, B, groups, a, dt)
+    return dx, dweight, dbias
+
+
+_LAYOUTS = {"half": SPCONV_HALF, "interleaved": SPCONV_INTERLEAVED}
+
+
+def _heads(t, name, like=None, shape=None):
+    """The dtype code of a tensor of heads (rows, heads, D), checked against
+    another's type, device and a shape."""
+    if _torch is None:
+        _load_torch()
+    if t is None:
+        raise ValueError(f"{name} must be given")
+    dt = _row_codes.get(t.dtype)
+    if dt is None or t.dim() != 3 or not t.is_cuda:
+        raise ValueError(f"{name} must be a float32 or bfloat16 (rows, heads, D) CUDA tensor")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must have {like.dtype} on the other tensors' device")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}")
+    return dt
+
+
+def _strides(*tensors):
+    # (a contiguous tensor's strides along a dimension of one are anything)
+    s = [n for t in tensors for n in ((t.shape[1] * t.shape[2], t.shape[2]) if t.is_contiguous()
+                                      else (t.stride(0), t.stride(1)))]
+    return (ctypes.c_int64 * len(s))(*s)
+
+
+def spconv_rotary_freqs(pairs: int, axes: int = 1, base: float = 10000.0, factor: float = 1.0, original: float = 0.0,
+                        device="cuda"):
+    """Frequencies for spconv_rotary, float64 (pairs,) on the device: the pairs
+    divided evenly over the axes, pair j of an axis' n turning by base^(-j / n)
+    per step; with factor > 1 for contexts that many times longer: all divided
+    by it, or, with the original context's length, by parts (pairs that turn 32
+    times and more over it are kept, those that turn once at most divided, those
+    between mixed)."""
+    import torch
+    f = torch.empty(max(pairs, 0), dtype=torch.float64)
+    _check(load_library().spconv_rotary_freqs(pairs, axes, base, factor, original, f.data_ptr() or None),
+           "spconv_rotary_freqs")
+    return f.to(device)
+
+
+def _rotary(name, x, positions, freqs, layout, gain, out):
+    dt = _heads(x, "dout" if name.endswith("grad") else "x")
+    N, H, D = x.shape
+    dev = x.device
+    if layout not in _LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}")
+    if positions is None or positions.dtype != _torch.int32 or positions.dim() not in (1, 2) \
+            or positions.shape[0] != N or positions.device != dev:
+        raise ValueError("positions must be an int32 (N,) or (N, axes) tensor on the features' device")
+    if freqs is None or freqs.dtype != _torch.float64 or freqs.dim() != 1 or freqs.device != dev:
+        raise ValueError("freqs must be a float64 (pairs,) tensor on the features' device")
+    if x.stride(2) != 1:
+        x = x.contiguous()
+    axes = 1
+    if positions.dim() == 2:
+        axes = positions.shape[1]
+        if axes > 1 and positions.stride(1) != 1:
+            positions = positions.contiguous()
+    if out is None:
+        out = _torch.empty((N, H, D), dtype=x.dtype, device=dev)
+    else:
+        _heads(out, "out", x, x.shape)
+        if out.stride(2) != 1:
+            raise ValueError("out must have its last dimension contiguous")
+    _call(name, dev, _at(x), _at(positions), positions.stride(0), _at(freqs.contiguous()), _at(out),
+          None if x.is_contiguous() and out.is_contiguous() else _strides(x, out), N, H, D, freqs.numel(), axes,
+          _LAYOUTS[layout], gain, dt)
+    return out
+
+
+def spconv_rotary(x, positions, freqs, layout: str = "half", gain: float = 1.0, out=None):
+    """Rotary positions: x (N, H, D) float32 or bfloat16, CUDA, H, D <= 4096 (a
+    strided view of a projection's output is used as it lies); positions int32
+    (N,) or (N, axes), such as voxel coordinates; freqs float64 (pairs,), 2 pairs
+    <= D, in radians per step (spconv_rotary_freqs).  The first 2 pairs elements
+    of each head turn, pair i being elements i and i + pairs (layout "half") or
+    2 i and 2 i + 1 ("interleaved"), and are multiplied by gain; the others are
+    copied.  Returns y (N, H, D); out may be x."""
+    return _rotary("spconv_rotary", x, positions, freqs, layout, gain, out)
+
+
+def spconv_rotary_grad(dout, positions, freqs, layout: str = "half", gain: float = 1.0, out=None):
+    """Gradient of spconv_rotary with the same positions, freqs, layout and gain:
+    dx (N, H, D) from dout; out may be dout."""
+    return _rotary("spconv_rotary_grad", dout, positions, freqs, layout, gain, out)
+
+
+def spconv_attention_workspace_size(N: int, M: int, B: int, H: int, HK: int, D: int, dtype: int) -> int:
+    return _size("spconv_attention_workspace_size", N, M, B, H, HK, D, dtype)
+
+
+def spconv_attention_grad_workspace_size(N: int, M: int, B: int, H: int, HK: int, D: int, dtype: int) -> int:
+    return _size("spconv_attention_grad_workspace_size", N, M, B, H, HK, D, dtype)
+
+
+def _lies_well(t):
+    """Whether rows and heads start at multiples of 16 bytes and heads lie in one piece."""
+    unit = 16 // t.element_size()
+    return t.is_contiguous() or t.stride(2) == 1 and t.stride(0) % unit == 0 and t.stride(1) % unit == 0
+
+
+def _head_input(t):
+    return t if _lies_well(t) else t.contiguous()
+
+
+def _head_output(out, shape, like, name):
+    if out is None:
+        return _torch.empty(shape, dtype=like.dtype, device=like.device)
+    _heads(out, name, like, shape)
+    if not _lies_well(out):
+        raise ValueError(f"{name} must have contiguous heads that start at multiples of 16 bytes")
+    return out
+
+
+def _attention_args(q, k, v, offsets, koffsets, order, korder, scale):
+    dt = _heads(q, "q")
+    _heads(k, "k", q)
+    _heads(v, "v", q, k.shape)
+    N, H, D = q.shape
+    M, HK = k.shape[:2]
+    dev = q.device
+    if k.shape[2] != D or HK == 0 or H % HK:
+        raise ValueError("k and v must be (M, HK, D) with q's D and H a multiple of HK")
+    offsets = _offsets(offsets, dev, "offsets")
+    B = offsets.numel() - 1
+    if koffsets is None:
+        if M != N or korder is not None:
+            raise ValueError("without koffsets the keys are the queries' rows: as many, and no korder")
+    else:
+        koffsets = _offsets(koffsets, dev, "koffsets")
+        if koffsets.numel() != B + 1:
+            raise ValueError("koffsets must have as many sequences as offsets")
+    order = _like(order, (N,), _torch.int32, dev, "order")
+    korder = _like(korder, (M,), _torch.int32, dev, "korder")
+    scale = D ** -0.5 if scale is None else scale
+    return dt, N, M, B, H, HK, D, dev, _head_input(q), _head_input(k), _head_input(v), offsets, koffsets, order, \
+        korder, scale
+
+
+def spconv_attention(q, k, v, offsets, koffsets=None, order=None, korder=None, causal: bool = False, scale=None,
+                     stats: bool = False, out=None, workspace=None):
+    """Attention within packed sequences: q (N, H, D), k and v (M, HK, D), all
+    float32 or all bfloat16, CUDA, D a multiple of 8 up to 128, H a multiple of HK
+    (runs of H / HK heads share keys); strided views with contiguous heads at
+    multiples of 16 bytes are used as they lie, and tensors start at 16-byte
+    addresses (others raise SpconvError, SPCONV_E_INVALID).  offsets int32
+    (sequences + 1,): the queries' positions of each sequence; koffsets: the
+    keys', None: the queries' rows are the keys'.  order int32 (N,): the row of
+    each position (the keys' too without koffsets); korder int32 (M,) with
+    koffsets.  ``causal``: the last query of a sequence sees all its keys, the one
+    before it all but one, and so on.  scale: of the scores, > 0 (None: D^-0.5).
+    Returns out (N, H, D), with ``stats`` (out, lse), lse float32 (N, H), for the
+    gradient; a query without keys gives 0 and -inf.  Rows behind the last
+    sequence are not read, and not written in ``out`` (in a new output they hold
+    anything).  workspace: a uint8 tensor of at least
+    spconv_attention_workspace_size bytes (allocated when None)."""
+    dt, N, M, B, H, HK, D, dev, q, k, v, offsets, koffsets, order, korder, scale = _attention_args(
+        q, k, v, offsets, koffsets, order, korder, scale)
+    o = _head_output(out, (N, H, D), q, "out")
+    lse = _torch.empty((N, H), dtype=_torch.float32, device=dev) if stats else None
+    ws, n = _workspace(workspace, spconv_attention_workspace_size(N, M, B, H, HK, D, dt), dev,
+                       "spconv_attention_workspace_size")
+    _call("spconv_attention", dev, _at(q), _at(k), _at(v), _at(offsets), _at(koffsets), _at(order), _at(korder),
+          _strides(q, k, v, o), _at(ws), n, _at(o), _at(lse), N, M, B, H, HK, D, scale, causal, dt)
+    return (o, lse) if stats else o
+
+
+def spconv_attention_grad(dout, q, k, v, out, lse, offsets, koffsets=None, order=None, korder=None,
+                          causal: bool = False, scale=None, grads=None, workspace=None):
+    """Gradient of spconv_attention: dout (N, H, D), the forward's arguments, its
+    output and lse.  Returns (dq, dk, dv) in their dtype, dk and dv summed over
+    the heads that share them.  ``grads``: the three tensors to write into, such as
+    views of one projection's gradient (rows behind the last sequence stay as
+    they were).  workspace: a uint8 tensor of at least
+    spconv_attention_grad_workspace_size bytes (allocated when None)."""
+    dt, N, M, B, H, HK, D, dev, q, k, v, offsets, koffsets, order, korder, scale = _attention_args(
+        q, k, v, offsets, koffsets, order, korder, scale)
+    _heads(dout, "dout", q, q.shape)
+    _heads(out, "out", q, q.shape)
+    lse = _like(lse, (N, H), _torch.float32, dev, "lse")
+    if lse is None:
+        raise ValueError("lse must be given")
+    dout, out = _head_input(dout), _head_input(out)
+    dq, dk, dv = (None, None, None) if grads is None else grads
+    dq = _head_output(dq, (N, H, D), q, "dq")
+    dk = _head_output(dk, (M, HK, D), q, "dk")
+    dv = _head_output(dv, (M, HK, D), q, "dv")
+    ws, n = _workspace(workspace, spconv_attention_grad_workspace_size(N, M, B, H, HK, D, dt), dev,
+                       "spconv_attention_grad_workspace_size")
+    _call("spconv_attention_grad", dev, _at(dout), _at(q), _at(k), _at(v), _at(out), _at(lse), _at(offsets),
+          _at(koffsets), _at(order), _at(korder), _strides(q, k, v, out, dout, dq, dk, dv), _at(ws), n, _at(dq), _at(dk),
+          _at(dv), N, M, B, H, HK, D, scale, causal, dt)
+    return dq, dk, dv

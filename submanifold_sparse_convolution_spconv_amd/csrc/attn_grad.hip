@@ -1,0 +1,486 @@
+// Gradient of the attention within packed sequences, for gfx950.
+//
+// With p = exp(scale q k - lse) and delta[i] = dout[i] out[i]:
+//   ds[i, j] = p[i, j] (dout[i] v[j] - delta[i])
+//   dq[i] = scale sum_j ds[i, j] k[j]
+//   dk[j] = scale sum_i ds[i, j] q[i],   dv[j] = sum_i p[i, j] dout[i]
+//
+// Two kernels, so that every sum has one owner and a fixed order: one over the
+// queries (dq, and delta for the other), one over the keys (dk and dv, summed
+// over the heads that share them).  Each computes p and ds again: 7 products
+// where 5 are needed, against atomics in dq.  As in the forward the results of
+// the first products are the operands of the next as they lie in the
+// registers: (key, query) tiles for dq, (query, key) tiles for dk and dv; p
+// and ds are rounded to bf16 there, all sums are fp32.
+#include "attn.h"
+
+#include <algorithm>
+
+namespace spc {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// KS: the waves of a workgroup take turns at the long axis for 32 rows instead
+// of sharing its tiles for 32 rows each.
+template <typename T, int DP, bool KS>
+struct GradShape {
+    static constexpr int ES = sizeof(T);
+    static constexpr int KT = ES == 2 && !KS ? 64 : 32;             // rows per tile of the long axis
+    static constexpr int NW = KS && ES == 4 && DP > 64 ? 2 : 4;
+    static constexpr int TR = KS ? 32 : 32 * NW;                    // rows that a workgroup owns
+    static constexpr int TILE = KT * DP * ES;
+    static constexpr int STATS = 2 * KT * 4;                        // lse and delta of a tile of queries
+    static constexpr int WAVE = 4 * TILE + 2 * STATS;               // two buffers
+    static constexpr int LDS = WAVE * (KS ? NW : 1);
+};
+
+// lse in powers of two; rows without keys: p = 2^-inf = 0
+__device__ __forceinline__ float stat2(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
+
+template <typename T, int DP, bool KS>
+__global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW)) k_attn_dq(AttnParams p) {
+    using S = GradShape<T, DP, KS>;
+    using O = Operand<T, DP>;
+    constexpr int KT = S::KT, NW = S::NW, NDT = DP / 32;
+    extern __shared__ __align__(16) uint8_t smem[];
+
+    const int64_t id = xcd_order(blockIdx.x);
+    if (id >= p.items * p.HK * p.splits) return;
+    const int split = (int)(id % p.splits);
+    const int hk = (int)(id / p.splits / p.items);
+    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6), h = lane >> 5;
+    QueryRows qr;
+    if (!qr.find(p, S::TR, KS ? 0 : 32 * wave, hk, id / p.splits % p.items)) return;
+    RowFrag<T, DP> qf[O::STEPS], df[O::STEPS];
+    // delta with the matrix instructions that give dout v below: where a query
+    // has one key, out is v and their difference is 0
+    f32x16_t dd = zero16();
+#pragma unroll
+    for (int s = 0; s < O::STEPS; ++s) {
+        qf[s] = O::row(p.q + qr.row * p.qs[0] + qr.head * p.qs[1], s, p.D);
+        df[s] = O::row(p.dout + qr.row * p.dos[0] + qr.head * p.dos[1], s, p.D);
+        dd = O::mma(O::row(p.out + qr.row * p.os[0] + qr.head * p.os[1], s, p.D), df[s], dd);
+    }
+    // the diagonal: row16(i, h) = lane & 31
+    float delta = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) delta = row16(i, h) == (lane & 31) ? dd[i] : delta;
+    const float other = __shfl_xor(delta, 32);
+    delta = ((lane >> 2) & 1) == h ? delta : other;
+    const float lse2 = stat2(p.lse[qr.row * p.H + qr.head]);
+    if (qr.valid && h == 0 && split == 0 && (!KS || wave == 0)) p.delta[qr.row * p.H + qr.head] = delta;
+
+    const int nt = (qr.longest + KT - 1) / KT;
+    const int t0 = (int)((int64_t)nt * split / p.splits), t1 = (int)((int64_t)nt * (split + 1) / p.splits);
+    constexpr int STEP = KS ? NW : 1;
+    const int begin = t0 + (KS ? wave : 0);
+    lds_u8* buf = (lds_u8*)smem + (KS ? wave * S::WAVE : 0);
+    KeyStager<T, DP, KT, KS ? 64 : 64 * NW> keys(p, qr.pl, hk, KS ? lane : t);
+
+    f32x16_t acc[NDT];
+#pragma unroll
+    for (int d = 0; d < NDT; ++d) acc[d] = zero16();
+
+    auto compute = [&](int tl, int b, auto masked) {
+        constexpr bool MASKED = decltype(masked)::value;
+        const lds_u8* kt = buf + b * 2 * S::TILE;
+        const lds_u8* vt = kt + S::TILE;
+#pragma unroll
+        for (int u = 0; u < KT / 32; ++u) {
+            f32x16_t s = zero16(), dp = zero16();
+#pragma unroll
+            for (int c = 0; c < O::STEPS; ++c) {
+                s = O::mma(O::along(kt, 32 * u, c), qf[c], s);
+                dp = O::mma(O::along(vt, 32 * u, c), df[c], dp);
+            }
+            uint32_t seen = 0xFFFFu;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float e = __builtin_amdgcn_exp2f(fmaf(s[i], p.scale2, -lse2));
+                s[i] = e * (dp[i] - delta);
+                if constexpr (MASKED) {
+                    const bool see = tl * KT + 32 * u + row16(i, h) < qr.limit;
+                    seen = see ? seen : seen & ~(1u << i);
+                    s[i] = see ? s[i] : 0.f;
+                }
+            }
+            add_rows<T, DP, MASKED>(acc, kt, 32 * u, s, seen);
+        }
+    };
+
+    if (begin < t1) {
+        keys.look_up(begin);
+        keys.load(buf, buf + S::TILE);
+        keys.look_up(begin + STEP);
+    }
+    wait_loads();
+    if constexpr (!KS) __syncthreads();
+    int b = 0;
+    for (int tl = begin; tl < t1; tl += STEP, b ^= 1) {
+        if (tl + STEP < t1) {
+            if constexpr (KS) wait_reads();
+            keys.load(buf + (b ^ 1) * 2 * S::TILE, buf + (b ^ 1) * 2 * S::TILE + S::TILE);
+            keys.look_up(tl + 2 * STEP);
+        }
+        if (tl * KT < qr.most) {
+            if ((tl + 1) * KT > qr.least)
+                compute(tl, b, std::true_type{});
+            else
+                compute(tl, b, std::false_type{});
+        }
+        wait_loads();
+        if constexpr (!KS) __syncthreads();
+    }
+
+    if constexpr (KS) {
+        __syncthreads();
+        if (wave > 0) {
+            float* mine = (float*)(smem + wave * S::WAVE);
+#pragma unroll
+            for (int d = 0; d < NDT; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) mine[(32 * d + row16(i, h)) * 32 + (lane & 31)] = acc[d][i];
+        }
+        __syncthreads();
+        if (wave > 0) return;
+        for (int w = 1; w < NW; ++w) {
+            const float* o = (const float*)(smem + w * S::WAVE);
+#pragma unroll
+            for (int d = 0; d < NDT; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[d][i] += o[(32 * d + row16(i, h)) * 32 + (lane & 31)];
+        }
+    }
+    if (!qr.valid) return;
+    if (p.splits > 1) {
+        float* o = p.part + ((split * p.N + qr.pl.q0 + qr.rh.pos) * p.H + qr.head) * p.D;
+#pragma unroll
+        for (int d = 0; d < NDT; ++d) store_col<float>((uint8_t*)o, acc[d], p.scale, d, p.D);
+        return;
+    }
+    uint8_t* o = p.dq + qr.row * p.dqs[0] + qr.head * p.dqs[1];
+#pragma unroll
+    for (int d = 0; d < NDT; ++d) store_col<T>(o, acc[d], p.scale, d, p.D);
+}
+
+template <typename T, int DP, bool KS>
+__global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW)) k_attn_dkv(AttnParams p) {
+    using S = GradShape<T, DP, KS>;
+    using O = Operand<T, DP>;
+    constexpr int KT = S::KT, NW = S::NW, NDT = DP / 32;
+    constexpr int THR = KS ? 64 : 64 * NW;
+    using St = Stager<T, DP, KT, THR>;
+    extern __shared__ __align__(16) uint8_t smem[];
+
+    const int64_t id = xcd_order(blockIdx.x);
+    if (id >= p.items * p.HK * p.splits) return;
+    const int split = (int)(id % p.splits);
+    const int hk = (int)(id / p.splits / p.items);
+    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6), h = lane >> 5;
+    const int st = KS ? lane : t;
+
+    // the sequence by its keys
+    Place pl = find_place(p.koffsets ? p.koffsets : p.offsets, p.B, p.M, 1, S::TR, id / p.splits % p.items);
+    if (pl.tile < 0) return;
+    pl.k0 = pl.q0;
+    pl.Lk = pl.Lq;
+    if (p.koffsets) {
+        pl.q0 = clamp_to(p.offsets[pl.b], 0, p.N);
+        pl.Lq = (int)(clamp_to(p.offsets[pl.b + 1], pl.q0, p.N) - pl.q0);
+    }
+    const int R = pl.Lq * p.G;
+    const int first = pl.tile * S::TR + (KS ? 0 : 32 * wave);
+    const bool valid = first + (lane & 31) < pl.Lk;
+    const int key = min(first + (lane & 31), pl.Lk - 1);
+    // the first query row that sees a key
+    const auto seen_from = [&](int k) {
+        const int64_t r = p.causal ? (int64_t)max(0, k - (pl.Lk - pl.Lq)) * p.G : 0;
+        return (int)min(r, (int64_t)R);
+    };
+    const int from = seen_from(key);
+    const int wave_first = first < pl.Lk ? seen_from(first) : R, wave_last = seen_from(min(first + 31, pl.Lk - 1));
+    const int64_t krow = row_of(p.korder, pl.k0 + key, p.M);
+    RowFrag<T, DP> kf[O::STEPS], vf[O::STEPS];
+#pragma unroll
+    for (int s = 0; s < O::STEPS; ++s) {
+        kf[s] = O::row(p.k + krow * p.ks[0] + hk * p.ks[1], s, p.D);
+        vf[s] = O::row(p.v + krow * p.vs[0] + hk * p.vs[1], s, p.D);
+    }
+
+    const int tb = seen_from(pl.tile * S::TR) / KT, nt = (R + KT - 1) / KT - tb;
+    const int t0 = tb + (int)((int64_t)nt * split / p.splits), t1 = tb + (int)((int64_t)nt * (split + 1) / p.splits);
+    constexpr int STEP = KS ? NW : 1;
+    const int begin = t0 + (KS ? wave : 0);
+    lds_u8* buf = (lds_u8*)smem + (KS ? wave * S::WAVE : 0);
+    float* stats = (float*)(smem + (KS ? wave * S::WAVE : 0) + 4 * S::TILE);
+
+    // rows of the queries' tiles, looked up one tile before they are loaded
+    int64_t qrow[St::NP];
+    int qhead[St::NP];
+    float lse = INFINITY, delta = 0.f;
+    auto look_up = [&](int tl) {
+#pragma unroll
+        for (int i = 0; i < St::NP; ++i) {
+            const int r = tl * KT + St::row(i, st);
+            qrow[i] = -1;
+            qhead[i] = 0;
+            if (r < R) {
+                const RowHead rh = split_row(r, p.G, p.magic);
+                qrow[i] = row_of(p.order, pl.q0 + rh.pos, p.N);
+                qhead[i] = hk * p.G + rh.head;
+            }
+        }
+        if (st < KT) {
+            const int r = tl * KT + st;
+            lse = INFINITY;
+            delta = 0.f;
+            if (r < R) {
+                const RowHead rh = split_row(r, p.G, p.magic);
+                const int64_t at = row_of(p.order, pl.q0 + rh.pos, p.N) * p.H + hk * p.G + rh.head;
+                lse = p.lse[at];
+                delta = p.delta[at];
+            }
+        }
+    };
+    auto load = [&](int b) {
+        lds_u8* qt = buf + b * 2 * S::TILE;
+#pragma unroll
+        for (int i = 0; i < St::NP; ++i) {
+            const int by = St::byte(i, st, p.D);
+            const bool in = qrow[i] >= 0 && by >= 0;
+            St::load(in ? p.q + qrow[i] * p.qs[0] + qhead[i] * p.qs[1] + by : (const uint8_t*)kAttnZeros, qt, i, st);
+            St::load(in ? p.dout + qrow[i] * p.dos[0] + qhead[i] * p.dos[1] + by : (const uint8_t*)kAttnZeros,
+                     qt + S::TILE, i, st);
+        }
+        if (st < KT) {
+            stats[b * 2 * KT + st] = stat2(lse);
+            stats[b * 2 * KT + KT + st] = delta;
+        }
+    };
+
+    f32x16_t dk[NDT], dv[NDT];
+#pragma unroll
+    for (int d = 0; d < NDT; ++d) dk[d] = dv[d] = zero16();
+
+    auto compute = [&](int tl, int b, auto masked) {
+        constexpr bool MASKED = decltype(masked)::value;
+        const lds_u8* qt = buf + b * 2 * S::TILE;
+        const lds_u8* dt = qt + S::TILE;
+#pragma unroll
+        for (int u = 0; u < KT / 32; ++u) {
+            f32x16_t s = zero16(), dp = zero16();
+#pragma unroll
+            for (int c = 0; c < O::STEPS; ++c) {
+                s = O::mma(O::along(qt, 32 * u, c), kf[c], s);
+                dp = O::mma(O::along(dt, 32 * u, c), vf[c], dp);
+            }
+            const float* l2 = stats + b * 2 * KT + 32 * u;
+            uint32_t seen = 0xFFFFu;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float e = __builtin_amdgcn_exp2f(fmaf(s[i], p.scale2, -l2[row16(i, h)]));
+                dp[i] = e * (dp[i] - l2[KT + row16(i, h)]);
+                s[i] = e;
+                if constexpr (MASKED) {
+                    const bool see = tl * KT + 32 * u + row16(i, h) >= from;
+                    seen = see ? seen : seen & ~(1u << i);
+                    s[i] = see ? s[i] : 0.f;
+                    dp[i] = see ? dp[i] : 0.f;
+                }
+            }
+            add_rows<T, DP, MASKED>(dv, dt, 32 * u, s, seen);
+            add_rows<T, DP, MASKED>(dk, qt, 32 * u, dp, seen);
+        }
+    };
+
+    if (begin < t1) {
+        look_up(begin);
+        load(0);
+        look_up(begin + STEP);
+    }
+    wait_loads();
+    if constexpr (!KS) __syncthreads();
+    int b = 0;
+    for (int tl = begin; tl < t1; tl += STEP, b ^= 1) {
+        if (tl + STEP < t1) {
+            if constexpr (KS) wait_reads();
+            load(b ^ 1);
+            look_up(tl + 2 * STEP);
+        }
+        if ((tl + 1) * KT > wave_first) {
+            if (tl * KT < wave_last)
+                compute(tl, b, std::true_type{});
+            else
+                compute(tl, b, std::false_type{});
+        }
+        wait_loads();
+        if constexpr (!KS) __syncthreads();
+    }
+
+    if constexpr (KS) {
+        static_assert(DP * 32 * 4 * 2 <= 4 * S::TILE);
+        __syncthreads();
+        if (wave > 0) {
+            float* mine = (float*)(smem + wave * S::WAVE);
+#pragma unroll
+            for (int d = 0; d < NDT; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    mine[(32 * d + row16(i, h)) * 32 + (lane & 31)] = dk[d][i];
+                    mine[(DP + 32 * d + row16(i, h)) * 32 + (lane & 31)] = dv[d][i];
+                }
+        }
+        __syncthreads();
+        if (wave > 0) return;
+        for (int w = 1; w < NW; ++w) {
+            const float* o = (const float*)(smem + w * S::WAVE);
+#pragma unroll
+            for (int d = 0; d < NDT; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    dk[d][i] += o[(32 * d + row16(i, h)) * 32 + (lane & 31)];
+                    dv[d][i] += o[(DP + 32 * d + row16(i, h)) * 32 + (lane & 31)];
+                }
+        }
+    }
+    if (!valid) return;
+    if (p.splits > 1) {
+        float* o = p.part + ((split * p.M + pl.k0 + key) * p.HK + hk) * p.D;
+        const int64_t all = p.splits * p.M * p.HK * p.D;
+#pragma unroll
+        for (int d = 0; d < NDT; ++d) {
+            store_col<float>((uint8_t*)o, dk[d], p.scale, d, p.D);
+            store_col<float>((uint8_t*)(o + all), dv[d], 1.f, d, p.D);
+        }
+        return;
+    }
+#pragma unroll
+    for (int d = 0; d < NDT; ++d) {
+        store_col<T>(p.dk + krow * p.dks[0] + hk * p.dks[1], dk[d], p.scale, d, p.D);
+        store_col<T>(p.dv + krow * p.dvs[0] + hk * p.dvs[1], dv[d], 1.f, d, p.D);
+    }
+}
+
+// Sums of the splits' parts in their order: four elements of a (position, head)
+// per thread.
+template <typename T>
+__global__ void __launch_bounds__(256) k_attn_sum(const float* part, int splits, const int32_t* offsets, int B,
+                                                  const int32_t* order, int64_t n, int heads, int D, uint8_t* out,
+                                                  int64_t rs, int64_t hs) {
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x, quads = D / 4, all = n * heads * quads;
+    if (e >= all) return;
+    const int64_t pos = e / quads / heads;
+    const int64_t begin = clamp_to(offsets[0], 0, n);
+    if (pos < begin || pos >= clamp_to(offsets[B], begin, n)) return;
+    f32x4r_t s = {};
+#pragma unroll 8
+    for (int k = 0; k < splits; ++k) s += *(const f32x4r_t*)(part + 4 * (k * all + e));
+    typedef T vec __attribute__((ext_vector_type(4)));
+    vec r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = (T)s[j];
+    *(vec*)(out + row_of(order, pos, n) * rs + e / quads % heads * hs + e % quads * 4 * (int)sizeof(T)) = r;
+}
+
+// A gradient kernel owns rows (queries or keys) of one axis and sums over the
+// other: the waves' share and the splits from both axes' sizes.
+AttnPlan side_plan(int64_t n, int64_t per, int64_t B, int64_t HK, int64_t along) {
+    const int64_t seqs = std::max<int64_t>(1, std::min(B, n));
+    AttnPlan r;
+    const int64_t shared = attn_places(n, per, 128, seqs) * HK;
+    r.ks = n * per / seqs <= 32 || shared < 512;
+    const int64_t blocks = std::max<int64_t>(1, r.ks ? attn_places(n, per, 32, seqs) * HK : shared);
+    const int64_t splits = blocks >= 512 ? 1 : std::min((1024 + blocks - 1) / blocks, along / 512);
+    r.splits = (int)std::max<int64_t>(1, std::min<int64_t>(splits, 256));
+    if (attn_places(n, per, 32, B) * HK * r.splits > (1 << 20)) r.splits = 1;     // (many empty sequences)
+    return r;
+}
+AttnPlan dq_plan(const AttnArgs& a) {
+    return side_plan(a.N, a.H / a.HK, a.B, a.HK, a.M / std::max<int64_t>(1, std::min<int64_t>(a.B, a.M)));
+}
+AttnPlan dkv_plan(const AttnArgs& a) {
+    return side_plan(a.M, 1, a.B, a.HK, a.N * (a.H / a.HK) / std::max<int64_t>(1, std::min<int64_t>(a.B, a.N)));
+}
+size_t delta_bytes(const AttnArgs& a) { return align_up((size_t)a.N * a.H * 4, 256); }
+
+template <typename T, int DP, bool KS>
+hipError_t dq_go(AttnParams p, hipStream_t st) {
+    using S = GradShape<T, DP, KS>;
+    p.items = attn_places(p.N, p.G, S::TR, p.B);
+    hipError_t e = hipFuncSetAttribute((const void*)k_attn_dq<T, DP, KS>,
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, S::LDS);
+    if (e != hipSuccess) return e;
+    k_attn_dq<T, DP, KS><<<(unsigned)xcd_blocks(p.items * p.HK * p.splits), 64 * S::NW, S::LDS, st>>>(p);
+    return hipGetLastError();
+}
+template <typename T, int DP, bool KS>
+hipError_t dkv_go(AttnParams p, hipStream_t st) {
+    using S = GradShape<T, DP, KS>;
+    p.items = attn_places(p.M, 1, S::TR, p.B);
+    hipError_t e = hipFuncSetAttribute((const void*)k_attn_dkv<T, DP, KS>,
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, S::LDS);
+    if (e != hipSuccess) return e;
+    k_attn_dkv<T, DP, KS><<<(unsigned)xcd_blocks(p.items * p.HK * p.splits), 64 * S::NW, S::LDS, st>>>(p);
+    return hipGetLastError();
+}
+
+template <typename T, int DP>
+hipError_t grad_width(const AttnArgs& a, AttnParams p, hipStream_t st) {
+    const auto sum = [&](const float* part, const int32_t* offs, const int32_t* order, int64_t n, int heads,
+                         uint8_t* out, const int64_t(&s)[2]) {
+        const int64_t quads = n * heads * (p.D / 4);
+        k_attn_sum<T><<<(unsigned)((quads + 255) / 256), 256, 0, st>>>(part, p.splits, offs, p.B, order, n, heads, p.D,
+                                                                     out, s[0], s[1]);
+        return hipGetLastError();
+    };
+    hipError_t e = hipSuccess;
+    if (p.N > 0) {
+        const AttnPlan r = dq_plan(a);
+        p.splits = r.splits;
+        e = r.ks ? dq_go<T, DP, true>(p, st) : dq_go<T, DP, false>(p, st);
+        if (e == hipSuccess && r.splits > 1) e = sum(p.part, p.offsets, p.order, p.N, p.H, p.dq, p.dqs);
+        if (e != hipSuccess) return e;
+    }
+    if (p.M > 0) {
+        const AttnPlan r = dkv_plan(a);
+        p.splits = r.splits;
+        e = r.ks ? dkv_go<T, DP, true>(p, st) : dkv_go<T, DP, false>(p, st);
+        if (e == hipSuccess && r.splits > 1) {
+            const int32_t* offs = p.koffsets ? p.koffsets : p.offsets;
+            e = sum(p.part, offs, p.korder, p.M, p.HK, p.dk, p.dks);
+            if (e == hipSuccess)
+                e = sum(p.part + r.splits * p.M * p.HK * p.D, offs, p.korder, p.M, p.HK, p.dv, p.dvs);
+        }
+    }
+    return e;
+}
+template <typename T>
+hipError_t grad_type(const AttnArgs& a, const AttnParams& p, hipStream_t st) {
+    switch ((p.D + 31) / 32) {
+        case 1: return grad_width<T, 32>(a, p, st);
+        case 2: return grad_width<T, 64>(a, p, st);
+        case 3: return grad_width<T, 96>(a, p, st);
+        default: return grad_width<T, 128>(a, p, st);
+    }
+}
+
+}  // namespace
+
+size_t attn_grad_workspace_bytes(const AttnArgs& a) {
+    const AttnPlan q = dq_plan(a), k = dkv_plan(a);
+    size_t part = 0;
+    if (q.splits > 1) part = (size_t)q.splits * a.N * a.H * a.D * 4;
+    if (k.splits > 1) part = std::max(part, (size_t)k.splits * a.M * a.HK * a.D * 8);
+    return delta_bytes(a) + align_up(part, 256);
+}
+
+hipError_t launch_attn_grad(const AttnArgs& a, hipStream_t stream) {
+    AttnParams p = attn_params(a);
+    p.delta = (float*)a.workspace;
+    p.part = (float*)((uint8_t*)a.workspace + delta_bytes(a));
+    return a.dtype == SPCONV_BF16 ? grad_type<__bf16>(a, p, stream) : grad_type<float>(a, p, stream);
+}
+
+}  // namespace spc

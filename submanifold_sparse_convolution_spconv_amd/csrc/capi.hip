@@ -5,6 +5,8 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
+#include <cmath>
 #include <mutex>
 #include <new>
 
@@ -706,6 +708,259 @@ int spconv_scan_grad(const void* dout, const void* x, const void* z, const int32
                      void* dz, float* dh0, int64_t N, int C, int scenes, int dtype, void* stream) {
     return scan_impl({x, z, dout, offsets, order, h0, dlast, workspace, dx, dz, dh0, N, C, scenes, dtype}, true,
                      workspace_bytes, stream, "spconv_scan_grad");
+}
+
+int spconv_rotary_freqs(int pairs, int axes, double base, double factor, double original, double* freqs) {
+    if (!freqs) return fail(SPCONV_E_INVALID, "freqs is NULL");
+    if (axes < 1 || axes > 8 || pairs < 1 || pairs > spc::kMaxRowChannels / 2 || pairs % axes)
+        return fail(SPCONV_E_INVALID, "pairs must be a multiple of axes (1..8) up to %d (got %d, %d)",
+                    spc::kMaxRowChannels / 2, pairs, axes);
+    if (!(base > 1.0) || !(factor >= 1.0) || !(original >= 0.0) || !std::isfinite(base) || !std::isfinite(factor) ||
+        !std::isfinite(original))
+        return fail(SPCONV_E_INVALID, "base must be > 1, factor >= 1 and original >= 0 (got %g, %g, %g)", base, factor,
+                    original);
+    const int n = pairs / axes;
+    for (int i = 0; i < pairs; ++i) {
+        const double f = std::pow(base, -(double)(i % n) / n);
+        const double turns = original * f / 6.283185307179586;
+        const double keep = original > 0 ? std::min(1.0, std::max(0.0, (turns - 1.0) / 31.0)) : 0.0;
+        freqs[i] = f / factor * (1.0 - keep) + f * keep;
+    }
+    return SPCONV_OK;
+}
+
+static int rotary_impl(const void* x, const int32_t* positions, int64_t pos_stride, const double* freqs, void* y,
+                       const int64_t* strides, int64_t N, int H, int D, int pairs, int axes, int layout, float gain,
+                       int dtype, void* stream, bool back, const char* name) {
+    int rc = check_rows(N, D, dtype, "D");
+    if (!rc) rc = check_rows(N, H, dtype, "H");
+    if (rc) return rc;
+    if (axes < 1 || axes > 8 || pairs < 1 || pairs % axes || 2 * (int64_t)pairs > D)
+        return fail(SPCONV_E_INVALID, "pairs must be a multiple of axes (1..8) and 2 pairs <= D (got %d, %d, D=%d)",
+                    pairs, axes, D);
+    if (layout != SPCONV_HALF && layout != SPCONV_INTERLEAVED)
+        return fail(SPCONV_E_INVALID, "layout must be SPCONV_HALF or SPCONV_INTERLEAVED (got %d)", layout);
+    if (N == 0) return SPCONV_OK;
+    if (!x || !positions || !freqs || !y) return fail(SPCONV_E_INVALID, "rows, positions and freqs must be non-NULL");
+    const size_t es = elem_size(dtype);
+    if (!aligned(x, es) || !aligned(y, es) || !aligned(positions, 4) || !aligned(freqs, 8))
+        return fail(SPCONV_E_INVALID, "rows, positions and freqs must be aligned to their elements");
+    spc::RotaryArgs a{x, positions, pos_stride, freqs, y, {(int64_t)H * D, D}, {(int64_t)H * D, D}, N, H, D,
+                      pairs, axes, layout, gain, dtype};
+    if (strides) {
+        for (int i = 0; i < 2; ++i) {
+            a.xs[i] = strides[i];
+            a.ys[i] = strides[2 + i];
+        }
+        if (x == y && (a.xs[0] != a.ys[0] || a.xs[1] != a.ys[1]))
+            return fail(SPCONV_E_INVALID, "in place, both strides must be the same");
+    }
+    hipError_t e = spc::launch_rotary(a, back, (hipStream_t)stream);
+    return e == hipSuccess ? SPCONV_OK : hip_fail(e, name);
+}
+
+int spconv_rotary(const void* x, const int32_t* positions, int64_t pos_stride, const double* freqs, void* y,
+                  const int64_t* strides, int64_t N, int H, int D, int pairs, int axes, int layout, float gain,
+                  int dtype, void* stream) {
+    return rotary_impl(x, positions, pos_stride, freqs, y, strides, N, H, D, pairs, axes, layout, gain, dtype, stream,
+                       false, "spconv_rotary");
+}
+
+int spconv_rotary_grad(const void* dout, const int32_t* positions, int64_t pos_stride, const double* freqs, void* dx,
+                       const int64_t* strides, int64_t N, int H, int D, int pairs, int axes, int layout, float gain,
+                       int dtype, void* stream) {
+    return rotary_impl(dout, positions, pos_stride, freqs, dx, strides, N, H, D, pairs, axes, layout, gain, dtype,
+                       stream, true, "spconv_rotary_grad");
+}
+
+int spconv_groupnorm_workspace_size(int64_t N, int C, int scenes, int groups, int dtype, size_t* bytes) {
+    if (!bytes) return fail(SPCONV_E_INVALID, "bytes pointer is NULL");
+    int rc = check_rows(N, C, dtype, "C");
+    if (rc) return rc;
+    if (scenes < 1) return fail(SPCONV_E_INVALID, "scenes must be >= 1 (got %d)", scenes);
+    if (groups < 1 || C % groups)
+        return fail(SPCONV_E_INVALID, "C must be a multiple of groups (got C=%d groups=%d)", C, groups);
+    if (!spc::group_fits(N, C, scenes, groups, dtype))
+        return fail(SPCONV_E_UNSUPPORTED, "%d scenes of %d groups need more than 2^32 threads", scenes, groups);
+    *bytes = spc::group_workspace_bytes(N, C, scenes, groups, dtype);
+    return SPCONV_OK;
+}
+
+// Checks of both directions.
+static int group_impl(const spc::GroupArgs& a, bool grad, size_t workspace_bytes, void* stream, const char* name) {
+    size_t need = 0;
+    int rc = spconv_groupnorm_workspace_size(a.N, a.C, a.scenes, a.groups, a.dtype, &need);
+    if (rc) return rc;
+    if (!(a.eps >= 0.f)) return fail(SPCONV_E_INVALID, "eps must be >= 0 (got %g)", (double)a.eps);
+    if (a.act != SPCONV_SILU && a.act != SPCONV_GELU && a.act != SPCONV_LINEAR)
+        return fail(SPCONV_E_INVALID, "act must be SPCONV_SILU, SPCONV_GELU or SPCONV_LINEAR (got %d)", a.act);
+    if (grad ? !a.mean || !a.rstd : !a.mean != !a.rstd)
+        return fail(SPCONV_E_INVALID, "mean and rstd must be given%s", grad ? "" : " together");
+    if (!a.dweight != !a.dbias) return fail(SPCONV_E_INVALID, "dweight and dbias must be given together");
+    if (!a.offsets) return fail(SPCONV_E_INVALID, "offsets is NULL");
+    if (!a.workspace) return fail(SPCONV_E_INVALID, "workspace is NULL");
+    if (a.N > 0 && (!a.x || !a.y || (grad && !a.dout)))
+        return fail(SPCONV_E_INVALID, "feature rows must be non-NULL");
+    const size_t es = elem_size(a.dtype);
+    if (!aligned(a.x, es) || !aligned(a.y, es) || !aligned(a.dout, es))
+        return fail(SPCONV_E_INVALID, "feature rows must be aligned to their elements");
+    if (!aligned(a.offsets, 4) || !aligned(a.weight, 4) || !aligned(a.bias, 4) || !aligned(a.mean, 4) ||
+        !aligned(a.rstd, 4) || !aligned(a.dweight, 4) || !aligned(a.dbias, 4))
+        return fail(SPCONV_E_INVALID, "offsets, weights and statistics must be 4-byte aligned");
+    if (!aligned(a.workspace, 256)) return fail(SPCONV_E_INVALID, "workspace must be 256-byte aligned");
+    if (workspace_bytes < need)
+        return fail(SPCONV_E_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    hipError_t e = spc::launch_group(a, grad, (hipStream_t)stream);
+    return e == hipSuccess ? SPCONV_OK : hip_fail(e, name);
+}
+
+int spconv_groupnorm(const void* x, const int32_t* offsets, const float* weight, const float* bias, void* workspace,
+                     size_t workspace_bytes, void* y, float* mean, float* rstd, int64_t N, int C, int scenes,
+                     int groups, float eps, int act, int dtype, void* stream) {
+    return group_impl({x, nullptr, offsets, weight, bias, workspace, y, mean, rstd, nullptr, nullptr, N, C, scenes,
+                       groups, eps, act, dtype},
+                      false, workspace_bytes, stream, "spconv_groupnorm");
+}
+
+int spconv_groupnorm_grad(const void* dout, const void* x, const int32_t* offsets, const float* mean,
+                          const float* rstd, const float* weight, const float* bias, void* workspace,
+                          size_t workspace_bytes, void* dx, float* dweight, float* dbias, int64_t N, int C,
+                          int scenes, int groups, int act, int dtype, void* stream) {
+    return group_impl({x, dout, offsets, weight, bias, workspace, dx, const_cast<float*>(mean),
+                       const_cast<float*>(rstd), dweight, dbias, N, C, scenes, groups, 0.f, act, dtype},
+                      true, workspace_bytes, stream, "spconv_groupnorm_grad");
+}
+
+// Sizes of an attention: rows, sequences, heads.
+static int check_attention(const spc::AttnArgs& a, bool grad) {
+    int rc = check_rows(a.N, a.H, a.dtype, "H");
+    if (!rc) rc = check_rows(a.M, a.HK, a.dtype, "HK");
+    if (rc) return rc;
+    if (a.B < 1) return fail(SPCONV_E_INVALID, "B must be >= 1 (got %d)", a.B);
+    if (a.H % a.HK) return fail(SPCONV_E_INVALID, "H must be a multiple of HK (got %d and %d)", a.H, a.HK);
+    if (a.D < 1) return fail(SPCONV_E_INVALID, "D must be >= 1 (got %d)", a.D);
+    if (a.D % 8 || a.D > spc::kMaxHeadDim)
+        return fail(SPCONV_E_UNSUPPORTED, "no kernel for D=%d (multiples of 8 up to %d)", a.D, spc::kMaxHeadDim);
+    if (!spc::attn_fits(a, grad))
+        return fail(SPCONV_E_UNSUPPORTED, "N=%lld M=%lld B=%d H=%d HK=%d need more than 2^32 threads",
+                    (long long)a.N, (long long)a.M, a.B, a.H, a.HK);
+    return SPCONV_OK;
+}
+static spc::AttnArgs attention_sizes(int64_t N, int64_t M, int B, int H, int HK, int D, int dtype) {
+    spc::AttnArgs a{};
+    a.N = N;
+    a.M = M;
+    a.B = B;
+    a.H = H;
+    a.HK = HK;
+    a.D = D;
+    a.dtype = dtype;
+    return a;
+}
+
+int spconv_attention_workspace_size(int64_t N, int64_t M, int B, int H, int HK, int D, int dtype, size_t* bytes) {
+    if (!bytes) return fail(SPCONV_E_INVALID, "bytes pointer is NULL");
+    const spc::AttnArgs a = attention_sizes(N, M, B, H, HK, D, dtype);
+    int rc = check_attention(a, false);
+    if (rc) return rc;
+    *bytes = spc::attn_workspace_bytes(a);
+    return SPCONV_OK;
+}
+
+int spconv_attention_grad_workspace_size(int64_t N, int64_t M, int B, int H, int HK, int D, int dtype,
+                                         size_t* bytes) {
+    if (!bytes) return fail(SPCONV_E_INVALID, "bytes pointer is NULL");
+    const spc::AttnArgs a = attention_sizes(N, M, B, H, HK, D, dtype);
+    int rc = check_attention(a, true);
+    if (rc) return rc;
+    *bytes = spc::attn_grad_workspace_bytes(a);
+    return SPCONV_OK;
+}
+
+// Checks of both directions, after the sizes; fills in the strides.
+static int attention_impl(spc::AttnArgs& a, bool grad, const int64_t* strides, size_t workspace_bytes, void* stream,
+                          const char* name) {
+    int rc = check_attention(a, grad);
+    if (rc) return rc;
+    if (!(a.scale > 0.f) || !std::isfinite(a.scale))
+        return fail(SPCONV_E_INVALID, "scale must be > 0 and finite (got %g)", (double)a.scale);
+    if (!a.offsets) return fail(SPCONV_E_INVALID, "offsets is NULL");
+    if (!a.koffsets && (a.M != a.N || a.korder))
+        return fail(SPCONV_E_INVALID, "without koffsets the keys are the queries' rows: M = N, no korder");
+    if (!aligned(a.offsets, 4) || !aligned(a.koffsets, 4) || !aligned(a.order, 4) || !aligned(a.korder, 4) ||
+        !aligned(a.lse, 4))
+        return fail(SPCONV_E_INVALID, "offsets, orders and lse must be 4-byte aligned");
+    if (a.N > 0 && (!a.q || !a.out || (grad && (!a.dout || !a.lse || !a.dq))))
+        return fail(SPCONV_E_INVALID, "%s must be non-NULL", grad ? "q, out, lse, dout and dq" : "q and out");
+    if (a.M > 0 && (!a.k || !a.v || (grad && (!a.dk || !a.dv))))
+        return fail(SPCONV_E_INVALID, "%s must be non-NULL", grad ? "k, v, dk and dv" : "k and v");
+    struct {
+        const void* t;
+        int64_t* s;
+        int heads;
+    } const tensors[] = {{a.q, a.qs, a.H},     {a.k, a.ks, a.HK},   {a.v, a.vs, a.HK},   {a.out, a.os, a.H},
+                         {a.dout, a.dos, a.H}, {a.dq, a.dqs, a.H}, {a.dk, a.dks, a.HK}, {a.dv, a.dvs, a.HK}};
+    const int unit = a.dtype == SPCONV_BF16 ? 8 : 4;
+    for (int i = 0; i < (grad ? 8 : 4); ++i) {
+        tensors[i].s[0] = strides ? strides[2 * i] : (int64_t)tensors[i].heads * a.D;
+        tensors[i].s[1] = strides ? strides[2 * i + 1] : a.D;
+        if (!aligned(tensors[i].t, 16) || tensors[i].s[0] % unit || tensors[i].s[1] % unit)
+            return fail(SPCONV_E_INVALID, "rows and heads must start at 16-byte addresses");
+    }
+    const size_t need = grad ? spc::attn_grad_workspace_bytes(a) : spc::attn_workspace_bytes(a);
+    if (need) {
+        if (!a.workspace) return fail(SPCONV_E_INVALID, "workspace is NULL");
+        if (!aligned(a.workspace, 256)) return fail(SPCONV_E_INVALID, "workspace must be 256-byte aligned");
+        if (workspace_bytes < need)
+            return fail(SPCONV_E_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    }
+    hipError_t e = grad ? spc::launch_attn_grad(a, (hipStream_t)stream) : spc::launch_attn(a, (hipStream_t)stream);
+    return e == hipSuccess ? SPCONV_OK : hip_fail(e, name);
+}
+
+int spconv_attention(const void* q, const void* k, const void* v, const int32_t* offsets, const int32_t* koffsets,
+                     const int32_t* order, const int32_t* korder, const int64_t* strides, void* workspace,
+                     size_t workspace_bytes, void* out, float* lse, int64_t N, int64_t M, int B, int H, int HK, int D,
+                     float scale, int causal, int dtype, void* stream) {
+    spc::AttnArgs a = attention_sizes(N, M, B, H, HK, D, dtype);
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.offsets = offsets;
+    a.koffsets = koffsets;
+    a.order = order;
+    a.korder = korder;
+    a.workspace = workspace;
+    a.out = out;
+    a.lse = lse;
+    a.scale = scale;
+    a.causal = causal != 0;
+    return attention_impl(a, false, strides, workspace_bytes, stream, "spconv_attention");
+}
+
+int spconv_attention_grad(const void* dout, const void* q, const void* k, const void* v, const void* out,
+                          const float* lse, const int32_t* offsets, const int32_t* koffsets, const int32_t* order,
+                          const int32_t* korder, const int64_t* strides, void* workspace, size_t workspace_bytes,
+                          void* dq, void* dk, void* dv, int64_t N, int64_t M, int B, int H, int HK, int D, float scale,
+                          int causal, int dtype, void* stream) {
+    spc::AttnArgs a = attention_sizes(N, M, B, H, HK, D, dtype);
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.offsets = offsets;
+    a.koffsets = koffsets;
+    a.order = order;
+    a.korder = korder;
+    a.dout = dout;
+    a.workspace = workspace;
+    a.out = const_cast<void*>(out);
+    a.lse = const_cast<float*>(lse);
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.scale = scale;
+    a.causal = causal != 0;
+    return attention_impl(a, true, strides, workspace_bytes, stream, "spconv_attention_grad");
 }
 
 void spconv_nmap_destroy(spconv_nmap* h) {

@@ -271,6 +271,77 @@ bool scan_fits(int64_t N, int C, bool grad);
 size_t scan_workspace_bytes(int64_t N, int C, int dtype, bool grad);
 hipError_t launch_scan(const ScanArgs& a, bool grad, hipStream_t stream);
 
+struct RotaryArgs {
+    const void* x;
+    const int32_t* positions;
+    int64_t pos_stride;        // elements from row to row
+    const double* freqs;
+    void* y;
+    int64_t xs[2], ys[2];      // elements from row to row and from head to head
+    int64_t N;
+    int H, D, pairs, axes, layout;
+    float gain;
+    int dtype;
+};
+hipError_t launch_rotary(const RotaryArgs& a, bool back, hipStream_t stream);
+
+struct GroupArgs {
+    const void* x;
+    const void* dout;          // gradient only
+    const int32_t* offsets;
+    const float* weight;       // or NULL: 1
+    const float* bias;         // or NULL: 0
+    void* workspace;           // group_workspace_bytes
+    void* y;                   // forward: y; gradient: dx
+    float* mean;               // forward: or NULL (then rstd too): statistics not kept
+    float* rstd;
+    float* dweight;            // gradient only; or NULL (then dbias too)
+    float* dbias;
+    int64_t N;
+    int C, scenes, groups;
+    float eps;
+    int act, dtype;
+};
+// A launch's threads are counted in 32 bits: false where a kernel would need more.
+bool group_fits(int64_t N, int C, int scenes, int groups, int dtype);
+size_t group_workspace_bytes(int64_t N, int C, int scenes, int groups, int dtype);
+hipError_t launch_group(const GroupArgs& a, bool grad, hipStream_t stream);
+
+// Attention: elements of a head up to this.
+constexpr int kMaxHeadDim = 128;
+
+struct AttnArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    const int32_t* offsets;
+    const int32_t* koffsets;   // or NULL: the keys are the queries' rows
+    const int32_t* order;      // or NULL
+    const int32_t* korder;     // or NULL
+    const void* dout;          // gradient only
+    void* workspace;
+    void* out;                 // forward: written; gradient: read
+    float* lse;                // likewise; forward: or NULL
+    void* dq;                  // gradient only
+    void* dk;
+    void* dv;
+    // elements from row to row and from head to head
+    int64_t qs[2], ks[2], vs[2], os[2], dos[2], dqs[2], dks[2], dvs[2];
+    int64_t N, M;
+    int B, H, HK, D;
+    float scale;
+    int causal, dtype;
+};
+// Places of tiles of `rows` query rows (positions times heads of a group): at
+// least as many as any partition into B sequences needs.
+constexpr int64_t attn_places(int64_t N, int64_t G, int64_t rows, int64_t B) { return N * G / rows + B; }
+// A launch's threads are counted in 32 bits: false where a kernel would need more.
+bool attn_fits(const AttnArgs& a, bool grad);
+size_t attn_workspace_bytes(const AttnArgs& a);
+size_t attn_grad_workspace_bytes(const AttnArgs& a);
+hipError_t launch_attn(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_attn_grad(const AttnArgs& a, hipStream_t stream);
+
 }  // namespace spc
 
 // Opaque handle of the public interface.

@@ -1,0 +1,219 @@
+"""Group norm with an activation over each scene against 64 bits.
+
+u = 2^-24, h half a step of the element type.  The mean of n elements, taken in
+batches and joined by counts, is off by d_m <= (c + 8) u mean |x| + (c + 8) u
+max |x - mean|-like terms; with c = 64 joins that is bounded by 80 u max |x|.  The
+variance from deviations of a mean that is off by d_m: off by 80 u var + d_m^2, so
+rstd by 80 u of itself (d_m^2 stays below u var at these spreads).  xhat is off by
+d_m rstd + 84 u |xhat|, z by |weight| times that and 2 u |z|; the activations are
+Lipschitz with 1.13 at most and right to 8 u of max(|z|, 1).  The gradient's sums
+over n elements are off by 80 u of the sums of their absolute values and by what
+their terms are.
+"""
+import pytest
+import torch
+
+import submanifold_sparse_convolution_spconv_amd as sp
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+U = 2.0 ** -24
+H = {F32: U, BF: 2.0 ** -8}
+
+
+def offs(lens):
+    return torch.tensor([0] + list(lens)).cumsum(0).to(torch.int32).cuda()
+
+
+def act64(z, kind):
+    if kind is None:
+        return z, torch.ones_like(z)
+    if kind == "silu":
+        s = torch.sigmoid(z)
+        return z * s, s + z * s * (1 - s)
+    c = 0.5 * torch.special.erfc(-z * 0.5 ** 0.5)
+    return z * c, c + z * torch.exp(-z * z / 2) / (2 * torch.pi) ** 0.5
+
+
+def reference(x, lens, G, w, b, eps, act, dout=None):
+    """{name: (value, bound)} in 64 bits on the host."""
+    h = H[x.dtype]
+    x = x.double().cpu()
+    N, C = x.shape
+    w64 = w.double().cpu() if w is not None else torch.ones(C, dtype=torch.float64)
+    b64 = b.double().cpu() if b is not None else torch.zeros(C, dtype=torch.float64)
+    y, ye, dx, dxe = (torch.full((N, C), float("nan"), dtype=torch.float64) for _ in range(4))
+    mean, me, rstd, re = (torch.zeros(len(lens), G, dtype=torch.float64) for _ in range(4))
+    sums = torch.zeros(4, C, dtype=torch.float64)
+    at, cg = 0, C // G
+    for s, n in enumerate(lens):
+        if n == 0:
+            rstd[s] = eps ** -0.5
+            re[s] = 4 * U * rstd[s]
+            continue
+        t = x[at:at + n].view(n, G, cg)
+        m = t.mean((0, 2))
+        dev = t - m[None, :, None]
+        var = dev.square().mean((0, 2))
+        r = (var + eps).rsqrt()
+        mean[s], rstd[s] = m, r
+        me[s] = 80 * U * t.abs().amax((0, 2))
+        re[s] = (80 * U + me[s] ** 2 * r ** 2) * r
+        assert bool((me[s] ** 2 <= 1e-3 * var + 1e-30).all())
+        unit = dev * r[None, :, None]
+        ue = (me[s] * r)[None, :, None] + (84 * U + me[s] ** 2 * r ** 2)[None, :, None] * unit.abs()
+        unit, ue = unit.reshape(n, C), ue.reshape(n, C)
+        z = unit * w64 + b64
+        ze = ue * w64.abs() + 2 * U * (z.abs() + b64.abs())
+        v, slope = act64(z, act)
+        y[at:at + n] = v
+        ye[at:at + n] = v.abs() * h + 1.13 * ze + 8 * U * z.abs().clamp(min=1)
+        if dout is not None:
+            do = dout[at:at + n].double().cpu()
+            dz = do * slope
+            dze = do.abs() * (1.13 * ze + 8 * U * z.abs().clamp(min=1)) + 2 * U * dz.abs()
+            sums[0] += (dz * unit).sum(0)
+            sums[1] += dz.sum(0)
+            sums[2] += (dze * unit.abs() + dz.abs() * ue + 80 * U * (dz * unit).abs()).sum(0)
+            sums[3] += (dze + 80 * U * dz.abs()).sum(0)
+            g, ge = dz * w64, dze * w64.abs() + U * (dz * w64).abs()
+            grp = lambda q: q.view(n, G, cg).mean((0, 2))[None, :, None].expand(n, G, cg).reshape(n, C)
+            m1, m2 = grp(g), grp(g * unit)
+            m1e = grp(ge + 80 * U * g.abs())
+            m2e = grp(ge * unit.abs() + g.abs() * ue + 80 * U * (g * unit).abs())
+            rr = r[None, :, None].expand(n, G, cg).reshape(n, C)
+            d = (g - m1 - unit * m2) * rr
+            dx[at:at + n] = d
+            dxe[at:at + n] = rr * (ge + m1e + unit.abs() * m2e + ue * m2.abs()
+                                   + 4 * U * (g.abs() + m1.abs() + (unit * m2).abs())) + (84 * U + h) * d.abs()
+        at += n
+    out = {"y": (y, ye), "mean": (mean, me + U * mean.abs()), "rstd": (rstd, re)}
+    if dout is not None:
+        out.update(dx=(dx, dxe), dweight=(sums[0], sums[2]), dbias=(sums[1], sums[3]))
+    return out
+
+
+def check(got, want, what):
+    v, e = want
+    got = got.double().cpu()
+    inside = ~torch.isnan(v)
+    assert bool((got[~inside] == 7).all()), f"{what}: rows behind the scenes were written"
+    off = (got - v).abs()[inside] / (e[inside] + 1e-37)
+    assert bool(torch.isfinite(got[inside]).all())
+    if off.numel():
+        assert float(off.max()) <= 1, f"{what}: {float(off.max()):.3g} of the bound"
+
+
+def run(N, C, G, lens, dt, act, affine=True, eps=1e-5, shift=1.0, seed=0):
+    print(N, C, G, lens[:5], dt, act, flush=True)
+    g = torch.Generator().manual_seed(seed + N + C)
+    x = (torch.randn(N, C, generator=g) * (torch.rand(C, generator=g) + 0.5) + shift * torch.randn(C, generator=g)).to(
+        dt).cuda()
+    w = (1 + 0.2 * torch.randn(C, generator=g)).cuda() if affine else None
+    b = (0.2 * torch.randn(C, generator=g)).cuda() if affine else None
+    do = torch.randn(N, C, generator=g).to(dt).cuda()
+    o = offs(lens)
+    out = torch.full_like(x, 7)
+    y, mean, rstd = sp.spconv_groupnorm(x, o, G, w, b, eps=eps, act=act, stats=True, out=out)
+    torch.cuda.synchronize()
+    want = reference(x, lens, G, w, b, eps, act, do)
+    check(y, want["y"], "y")
+    check(mean, want["mean"], "mean")
+    check(rstd, want["rstd"], "rstd")
+    y2 = sp.spconv_groupnorm(x, o, G, w, b, eps=eps, act=act)
+    n = sum(lens)
+    assert torch.equal(y2[:n], y[:n])
+    dx, dw, db = sp.spconv_groupnorm_grad(do, x, o, G, mean, rstd, w, b, act=act, out=torch.full_like(x, 7))
+    torch.cuda.synchronize()
+    check(dx, want["dx"], "dx")
+    if affine:
+        check(dw, want["dweight"], "dweight")
+        check(db, want["dbias"], "dbias")
+    else:
+        assert dw is None and db is None
+    again = sp.spconv_groupnorm_grad(do, x, o, G, mean, rstd, w, b, act=act, sums=True)
+    assert torch.equal(again[0][:n], dx[:n])
+    check(again[1], want["dweight"], "dweight")
+    return y, dx
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("act", [None, "silu", "gelu"])
+@pytest.mark.parametrize("C, G", [(32, 8), (128, 32), (1, 1), (7, 7), (30, 3), (67, 1), (520, 8), (4096, 32)])
+def test_channels(dt, act, C, G):
+    run(150, C, G, [100, 0, 50], dt, act)
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("lens", [[1], [0, 1, 0], [1] * 70, [63, 64, 65], [5000], [3, 4000, 0, 1000, 1], [0, 0]],
+                         ids=str)
+def test_scenes(dt, lens):
+    run(sum(lens) + 20, 64, 16, lens, dt, "silu")
+    if sum(lens):
+        run(sum(lens), 24, 4, lens, dt, None, affine=False)
+
+
+def test_many_rows():
+    run(200000, 40, 8, [70001, 1, 129998], BF, "silu")
+    run(30000, 16, 2, [30000], F32, "gelu")
+
+
+def test_far_from_zero():
+    """Means a thousand times the spread: deviations, not squares, are summed."""
+    run(3000, 32, 4, [2000, 1000], F32, None, shift=1000.0)
+
+
+def test_lone_elements():
+    """Groups of one element: y is the bias, the gradient 0 to the bit."""
+    for dt in (BF, F32):
+        g = torch.Generator().manual_seed(2)
+        x, do = (torch.randn(40, 24, generator=g).to(dt).cuda() for _ in range(2))
+        w, b = torch.randn(24, generator=g).cuda(), torch.randn(24, generator=g).cuda()
+        o = offs([1] * 40)
+        y, mean, rstd = sp.spconv_groupnorm(x, o, 24, w, b, stats=True)
+        assert torch.equal(y, b.to(dt).expand(40, 24))
+        dx, _, _ = sp.spconv_groupnorm_grad(do, x, o, 24, mean, rstd, w, b, act="silu")
+        assert bool((dx == 0).all())
+
+
+def test_in_place_and_views():
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(500, 48, generator=g).to(BF).cuda()
+    o = offs([200, 300])
+    want = sp.spconv_groupnorm(x, o, 6, act="gelu")
+    wide = torch.zeros(500, 100, dtype=BF, device="cuda")
+    wide[:, 3:51] = x
+    assert torch.equal(sp.spconv_groupnorm(wide[:, 3:51], o, 6, act="gelu"), want)
+    flat = torch.zeros(500 * 48 + 1, dtype=BF, device="cuda")
+    odd = flat[1:].view(500, 48)
+    odd.copy_(x)
+    assert torch.equal(sp.spconv_groupnorm(odd, o, 6, act="gelu"), want)
+    sp.spconv_groupnorm(x, o, 6, act="gelu", out=x)
+    assert torch.equal(x, want)
+
+
+def test_nan_stays_in_its_scene_and_group():
+    x = torch.randn(60, 16).cuda()
+    x[25, 5] = float("nan")
+    y = sp.spconv_groupnorm(x, offs([20, 20, 20]), 4)
+    bad = torch.isnan(y)
+    assert bool(bad[20:40, 4:8].all()) and int(bad.sum()) == 80
+
+
+def test_gradient_against_differences():
+    g = torch.Generator().manual_seed(8)
+    x, do, d = (torch.randn(90, 24, generator=g).cuda() for _ in range(3))
+    w, b = (1 + torch.rand(24, generator=g)).cuda(), torch.randn(24, generator=g).cuda()
+    o = offs([40, 50])
+    for act in (None, "silu", "gelu"):
+        _, mean, rstd = sp.spconv_groupnorm(x, o, 6, w, b, act=act, stats=True)
+        dx, dw, db = sp.spconv_groupnorm_grad(do, x, o, 6, mean, rstd, w, b, act=act)
+        f = lambda *a: float((sp.spconv_groupnorm(a[0], o, 6, a[1], a[2], act=act).double() * do.double()).sum())
+        step = 1e-2
+        for i, got in enumerate((dx, dw, db)):
+            args, v = [x, w, b], d if i == 0 else d[0]
+            up, down = list(args), list(args)
+            up[i], down[i] = args[i] + step * v, args[i] - step * v
+            want = (f(*up) - f(*down)) / (2 * step)
+            size = float(do.double().norm()) * float(v.double().norm()) * (90 if i else 1) ** 0.5
+            assert abs(float((got.double() * v.double()).sum()) - want) <= size * (step ** 2 + 2 ** -24 * 8 / step)
