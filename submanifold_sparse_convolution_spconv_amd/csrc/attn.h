@@ -52,9 +52,6 @@ struct AttnPlan {
 AttnPlan attn_plan(const AttnArgs& a);
 AttnParams attn_params(const AttnArgs& a);
 
-// 16 zero bytes: where lanes without a row load from.
-static __device__ const uint32_t kAttnZeros[4] = {0, 0, 0, 0};
-
 __device__ __forceinline__ f32x16_t mfma32(bf16x8r_t a, bf16x8r_t b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
@@ -106,8 +103,9 @@ __device__ __forceinline__ void find_keys(const AttnParams& p, Place& pl) {
     }
 }
 
-// A wave's 32 query rows, one per lane (both halves), and the keys they see:
-// the lane's own first `limit`, and over the wave's and the workgroup's rows.
+// A wave's 32 query rows, one per lane (both halves), and the keys they see: the
+// lane's own first `limit`, at most `most` in the wave, and `least` to `longest`
+// over the workgroup.
 // Lanes past the sequence repeat its last row.
 struct QueryRows {
     Place pl;
@@ -134,7 +132,7 @@ struct QueryRows {
         head = hk * p.G + rh.head;
         row = row_of(p.order, pl.q0 + rh.pos, p.N);
         limit = sees(mine);
-        least = sees(first);
+        least = sees(tile * tq);
         most = first < R ? sees(first + 31) : 0;
         longest = sees(tile * tq + tq - 1);
         return true;
@@ -170,53 +168,106 @@ struct Tile {
     static __device__ __forceinline__ int at(int row, int unit) { return row * ROWB + ((unit ^ key(row)) << 4); }
 };
 
-// Rows into a tile, by THR threads, past the registers.  A lane's unit goes to
-// consecutive LDS addresses; which unit of which row it fetches carries the
-// permutation.
+typedef uint32_t u32x4a_t __attribute__((ext_vector_type(4)));
+
+// Rows into a tile by THR threads: each fetches 16-byte units into registers
+// while the tile before is worked on, and stores them to consecutive LDS
+// addresses; which unit of which row it fetches carries the permutation.
+// (Loads past the registers were slower: the compiler has the transposing reads
+// wait for all of them.)
+constexpr uint32_t kNoUnit = 0x80000000u;      // an offset past every buffer: zeros are read
 template <typename T, int DP, int ROWS, int THR>
 struct Stager {
     using L = Tile<T, DP>;
     static constexpr int NP = ROWS * L::U / THR;
     static_assert(ROWS * L::U % THR == 0 && THR % 64 == 0);
     static __device__ __forceinline__ int row(int i, int t) { return (i * THR + t) / L::U; }
-    // the byte in its row of thread t's unit i, or -1 past D
-    static __device__ __forceinline__ int byte(int i, int t, int D) {
+    // the byte in its row of thread t's unit i
+    static __device__ __forceinline__ int byte(int i, int t) {
         const int p = i * THR + t;
-        const int u = (p % L::U) ^ L::key(p / L::U);
-        return u * L::E < D ? u * 16 : -1;
+        return ((p % L::U) ^ L::key(p / L::U)) * 16;
     }
-    static __device__ __forceinline__ void load(const uint8_t* src, lds_u8* tile, int i, int t) {
-        __builtin_amdgcn_global_load_lds(src, tile + (i * THR + (t & ~63)) * 16, 16, 0, 0);
+    static __device__ __forceinline__ void store(const u32x4a_t (&r)[NP], lds_u8* tile, int t) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+            *(__attribute__((address_space(3))) u32x4a_t*)(tile + (i * THR + t) * 16) = r[i];
     }
 };
+__device__ __forceinline__ u32x4a_t fetch16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    return __builtin_bit_cast(u32x4a_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const uint8_t* p) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), (short)0, 0x7FFFFFFF, 0x00020000);
+}
+__device__ __forceinline__ u32x4a_t fetch16(const uint8_t* p, bool in) {
+    u32x4a_t r = {};
+    if (in) r = *(const u32x4a_t*)p;
+    return r;
+}
 
-// Keys' and values' rows of a sequence into tiles, ahead of their use: the rows'
-// places are looked up (through korder) one tile before they are loaded.
+// Keys' and values' rows of a sequence into tiles.  Rows one after the other
+// are a buffer whose start moves with the tile, so that a unit's offset stays
+// the same; through korder each row's place is looked up one tile before it
+// is fetched.
 template <typename T, int DP, int KT, int THR>
 struct KeyStager {
     using St = Stager<T, DP, KT, THR>;
+    static constexpr int NP = St::NP;
     const AttnParams& p;
-    const Place& pl;
     const uint8_t *k, *v;
-    int t;
-    int64_t row[St::NP];
+    int64_t k0;
+    int Lk, t;
+    uint32_t ok[NP], ov[NP];
+    int row[NP];
+    u32x4a_t rk[NP], rv[NP];
     __device__ __forceinline__ KeyStager(const AttnParams& p, const Place& pl, int hk, int t)
-        : p(p), pl(pl), k(p.k + hk * p.ks[1]), v(p.v + hk * p.vs[1]), t(t) {}
-    __device__ __forceinline__ void look_up(int tile) {
+        : p(p), k(p.k + hk * p.ks[1]), v(p.v + hk * p.vs[1]), k0(pl.k0), Lk(pl.Lk), t(t) {
 #pragma unroll
-        for (int i = 0; i < St::NP; ++i) {
-            const int j = tile * KT + St::row(i, t);
-            row[i] = j < pl.Lk ? row_of(p.korder, pl.k0 + j, p.M) : -1;
+        for (int i = 0; i < NP; ++i) {
+            const int by = St::byte(i, t);
+            const bool in = by < p.D * (int)sizeof(T);
+            ok[i] = !in ? kNoUnit : p.korder ? by : by + St::row(i, t) * (uint32_t)p.ks[0];
+            ov[i] = !in ? kNoUnit : p.korder ? by : by + St::row(i, t) * (uint32_t)p.vs[0];
         }
     }
-    __device__ __forceinline__ void load(lds_u8* kt, lds_u8* vt) const {
+    __device__ __forceinline__ void look_up(int tile) {
+        if (!p.korder) return;
 #pragma unroll
-        for (int i = 0; i < St::NP; ++i) {
-            const int by = St::byte(i, t, p.D);
-            const bool in = row[i] >= 0 && by >= 0;
-            St::load(in ? k + row[i] * p.ks[0] + by : (const uint8_t*)kAttnZeros, kt, i, t);
-            St::load(in ? v + row[i] * p.vs[0] + by : (const uint8_t*)kAttnZeros, vt, i, t);
+        for (int i = 0; i < NP; ++i) {
+            const int j = tile * KT + St::row(i, t);
+            row[i] = j < Lk ? (int)row_of(p.korder, k0 + j, p.M) : -1;
         }
+    }
+    __device__ __forceinline__ void fetch(int tile) {
+        if (p.korder) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const bool in = row[i] >= 0 && ok[i] != kNoUnit;
+                rk[i] = fetch16(k + row[i] * p.ks[0] + ok[i], in);
+                rv[i] = fetch16(v + row[i] * p.vs[0] + ov[i], in);
+            }
+            return;
+        }
+        const int64_t at = k0 + (int64_t)tile * KT;
+        const auto bk = rows_at(k + at * p.ks[0]), bv = rows_at(v + at * p.vs[0]);
+        const int left = Lk - tile * KT;
+        if (left >= KT) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                rk[i] = fetch16(bk, ok[i]);
+                rv[i] = fetch16(bv, ov[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                rk[i] = fetch16(bk, St::row(i, t) < left ? ok[i] : kNoUnit);
+                rv[i] = fetch16(bv, St::row(i, t) < left ? ov[i] : kNoUnit);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(lds_u8* kt) const {
+        St::store(rk, kt, t);
+        St::store(rv, kt + KT * St::L::ROWB, t);
     }
 };
 
@@ -267,17 +318,29 @@ struct Operand<__bf16, DP> {
     // the rows that the lane's element j of instruction c stands for
     static constexpr int ROWS = 8;
     static __device__ __forceinline__ int index(int c, int j) { return 8 * c + j; }
-    static __device__ __forceinline__ bool bad(frag f) {
-        uint32_t w[4], t = 0;
-        __builtin_memcpy(w, &f, 16);
+    // the infinite and NaN elements, the others 0
+    static __device__ __forceinline__ frag bad(frag f) {
+        u32x4a_t w = __builtin_bit_cast(u32x4a_t, f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) t |= (w[j] & 0x7F807F80u) + 0x00800080u;
-        return t & 0x80008000u;
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t top = ((w[j] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;    // exponents of ones
+            w[j] &= (top >> 15) * 0xFFFFu;
+        }
+        return __builtin_bit_cast(frag, w);
     }
+    static __device__ __forceinline__ bool any(frag f) {
+        const u32x4a_t w = __builtin_bit_cast(u32x4a_t, f);
+        return w[0] | w[1] | w[2] | w[3];
+    }
+    static __device__ __forceinline__ frag without(frag f, frag g) {       // g: some of f's elements
+        return __builtin_bit_cast(frag, __builtin_bit_cast(u32x4a_t, f) ^ __builtin_bit_cast(u32x4a_t, g));
+    }
+    // element j where `mine`, else 0
     static __device__ __forceinline__ frag only(frag f, int j, bool mine) {
+        u32x4a_t w = __builtin_bit_cast(u32x4a_t, f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = mine && e == j ? f[e] : (__bf16)0.f;
-        return f;
+        for (int e = 0; e < 4; ++e) w[e] = mine && e == (j >> 1) ? w[e] & (0xFFFFu << (16 * (j & 1))) : 0u;
+        return __builtin_bit_cast(frag, w);
     }
 };
 
@@ -314,7 +377,13 @@ struct Operand<float, DP> {
     static __device__ __forceinline__ f32x16_t mma(frag a, frag b, f32x16_t c) { return mfma32(a, b, c); }
     static constexpr int ROWS = 1;
     static __device__ __forceinline__ int index(int c, int) { return c; }
-    static __device__ __forceinline__ bool bad(frag f) { return (__float_as_uint(f) & 0x7F800000u) == 0x7F800000u; }
+    static __device__ __forceinline__ frag bad(frag f) {
+        return (__float_as_uint(f) & 0x7F800000u) == 0x7F800000u ? f : 0.f;
+    }
+    static __device__ __forceinline__ bool any(frag f) { return __float_as_uint(f) != 0; }
+    static __device__ __forceinline__ frag without(frag f, frag g) {
+        return __uint_as_float(__float_as_uint(f) ^ __float_as_uint(g));
+    }
     static __device__ __forceinline__ frag only(frag f, int, bool mine) { return mine ? f : 0.f; }
 };
 // a row's operand has the type of along()
@@ -323,47 +392,49 @@ using RowFrag = decltype(Operand<T, DP>::row((const uint8_t*)nullptr, 0, 0));
 
 // acc[dt] += (rows' transpose) x w for 32 rows of a tile, w a 32 x 32 result
 // whose hidden entries (bit i of `seen` clear) are zero.  A zero times an infinite
-// or NaN element of the tile would still be NaN, so a tile that holds some
-// (masked tiles only are looked at) goes row by row: every other row's
-// elements zeroed, and the sum taken over only by the columns that see the row.
+// or NaN element of the tile would still be NaN, so masked tiles multiply the
+// others only, and where there are some, these are added row by row, to the
+// columns that see the row.
 template <typename T, int DP, bool MASKED>
 __device__ __forceinline__ void add_rows(f32x16_t (&acc)[DP / 32], const lds_u8* tile, int row0, const f32x16_t& w,
                                          uint32_t seen) {
     using O = Operand<T, DP>;
-    if constexpr (MASKED) {
-        bool bad = false;
-#pragma unroll
-        for (int c = 0; c < O::CROSS; ++c)
-#pragma unroll
-            for (int dt = 0; dt < DP / 32; ++dt) bad |= O::bad(O::across(tile, row0, c, dt));
-        if (__ballot(bad)) {
-            const int h = (threadIdx.x >> 5) & 1;
-#pragma unroll
-            for (int c = 0; c < O::CROSS; ++c)
-#pragma unroll
-                for (int dt = 0; dt < DP / 32; ++dt) {
-                    const auto a = O::across(tile, row0, c, dt);
-                    const auto b = O::pack(w, c);
-#pragma unroll 1
-                    for (int j = 0; j < O::ROWS; ++j)
-#pragma unroll 1
-                        for (int half = 0; half < 2; ++half) {
-                            const f32x16_t t = O::mma(O::only(a, j, h == half), O::only(b, j, h == half), acc[dt]);
-                            // a column's two lane halves see different rows: ask the half that holds it
-                            const uint32_t other = (uint32_t)__shfl_xor((int)seen, 32);
-                            const bool see = ((h == half ? seen : other) >> O::index(c, j)) & 1;
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) acc[dt][i] = see ? t[i] : acc[dt][i];
-                        }
-                }
-            return;
-        }
-    }
+    bool some = false;
 #pragma unroll
     for (int c = 0; c < O::CROSS; ++c) {
         const auto b = O::pack(w, c);
 #pragma unroll
-        for (int dt = 0; dt < DP / 32; ++dt) acc[dt] = O::mma(O::across(tile, row0, c, dt), b, acc[dt]);
+        for (int dt = 0; dt < DP / 32; ++dt) {
+            auto a = O::across(tile, row0, c, dt);
+            if constexpr (MASKED) {
+                const auto x = O::bad(a);
+                some |= O::any(x);
+                a = O::without(a, x);
+            }
+            acc[dt] = O::mma(a, b, acc[dt]);
+        }
+    }
+    if (MASKED && __builtin_expect(__ballot(some) != 0, 0)) {
+        const int h = (threadIdx.x >> 5) & 1;
+        // a column's two lane halves see different rows: ask the half that holds it
+        const uint32_t other = (uint32_t)__shfl_xor((int)seen, 32);
+#pragma unroll
+        for (int c = 0; c < O::CROSS; ++c) {
+            const auto b = O::pack(w, c);
+#pragma unroll 1
+            for (int j = 0; j < 2 * O::ROWS; ++j) {
+                const int half = j & 1, e = j >> 1;
+                const bool see = ((h == half ? seen : other) >> O::index(c, e)) & 1;
+#pragma unroll
+                for (int dt = 0; dt < DP / 32; ++dt) {
+                    const auto x = O::only(O::bad(O::across(tile, row0, c, dt)), e, h == half);
+                    const f32x16_t t = O::mma(x, O::only(b, e, h == half), zero16());
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[dt][i] += see ? t[i] : 0.f;
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        }
     }
 }
 
@@ -384,15 +455,18 @@ __device__ __forceinline__ void store_col(uint8_t* row, const f32x16_t& v, float
     }
 }
 
-// All of this wave's loads into LDS have landed.
-__device__ __forceinline__ void wait_loads() {
-    __builtin_amdgcn_s_waitcnt(0x0F70);
-    asm volatile("" ::: "memory");
-}
-// Every LDS read of this wave has returned.
-__device__ __forceinline__ void wait_reads() {
-    __builtin_amdgcn_s_waitcnt(0xC07F);
-    asm volatile("" ::: "memory");
+// Everything loaded so far has arrived: said before a loop, so that the loop does
+// not wait for it (and with it for its own loads) every time.
+__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+
+// Between the tiles: the workgroup's waves together, or, where a wave has tiles of
+// its own, its own LDS operations (which the hardware keeps in order).
+template <bool OWN>
+__device__ __forceinline__ void next_tile() {
+    if constexpr (OWN)
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    else
+        __syncthreads();
 }
 
 }  // namespace spc

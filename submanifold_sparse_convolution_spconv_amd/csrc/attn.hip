@@ -10,10 +10,12 @@
 // already that of the second product's operand (rounded to bf16 there; sums and
 // references stay fp32).  Values are read transposed from LDS.
 //
-// The reference a query's exponentials are taken against moves only where the
-// maximum has grown by more than 2^8 since: exponentials and sums stay far
-// inside fp32's range either way, and the sums so far are rescaled a few
-// times instead of once a tile.
+// The reference that a query's exponentials are taken against is the maximum of
+// the first 32 keys, so that the largest weight is 1 at least; larger ones do
+// floating point no harm until they leave its range.  No maximum is needed on
+// the way, and nothing rescaled (which cost a fifth of the time, most of it in
+// copies of the sums around the branch).  Where the sum reaches 2^64, or a
+// result is not finite, the tile is done again with the maximum of all keys.
 #include "attn.h"
 
 #include <algorithm>
@@ -23,7 +25,7 @@ namespace spc {
 namespace {
 
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr float kSlack = 8.f;       // powers of two that the maximum may outgrow the reference by
+constexpr float kMost = 0x1p64f;    // a query's sum from which its reference is taken again
 
 // KS: the workgroup's waves take turns at the keys of one tile of 32 queries
 // (each with tiles of its own, joined at the end) instead of sharing the
@@ -36,10 +38,11 @@ struct FwdShape {
     static constexpr int TQ = KS ? 32 : 32 * NW;                    // query rows per workgroup
     static constexpr int TILE = KT * DP * ES;
     static constexpr int LDS = 4 * TILE * (KS ? NW : 1);            // two buffers of keys and values
+    static constexpr int OCC = ES == 2 && DP <= 64 ? (DP == 32 ? 4 : 3) : ES == 2 || DP <= (KS ? 32 : 64) ? 2 : 1;   // waves of a SIMD that registers are for
 };
 
 template <typename T, int DP, bool KS>
-__global__ void __launch_bounds__((64 * FwdShape<T, DP, KS>::NW)) k_attn(AttnParams p) {
+__global__ void __launch_bounds__((64 * FwdShape<T, DP, KS>::NW), (FwdShape<T, DP, KS>::OCC)) k_attn(AttnParams p) {
     using S = FwdShape<T, DP, KS>;
     using O = Operand<T, DP>;
     constexpr int KT = S::KT, NW = S::NW, NSUB = KT / 32, NDT = DP / 32;
@@ -64,89 +67,110 @@ __global__ void __launch_bounds__((64 * FwdShape<T, DP, KS>::NW)) k_attn(AttnPar
     KeyStager<T, DP, KT, KS ? 64 : 64 * NW> keys(p, qr.pl, hk, KS ? lane : t);
 
     f32x16_t acc[NDT];
-#pragma unroll
-    for (int d = 0; d < NDT; ++d) acc[d] = zero16();
-    float ref = -INFINITY, sum = 0.f;
+    // the reference of the lane's query (a score, -inf if it sees no key here), and
+    // what it takes off exponents (in bf16 powers of two)
+    float ref = -INFINITY, base = 0.f, sum;
 
-    auto compute = [&](int tl, int b, auto masked) {
-        constexpr bool MASKED = decltype(masked)::value;
+    // scores of 32 keys of a tile
+    const auto scores = [&](int tl, int b, int u, auto masked, uint32_t& seen) {
         const lds_u8* kt = buf + b * 2 * S::TILE;
-        const lds_u8* vt = kt + S::TILE;
-        f32x16_t s[NSUB];
-        uint32_t seen[NSUB];
+        f32x16_t s = zero16();
 #pragma unroll
-        for (int u = 0; u < NSUB; ++u) {
-            s[u] = zero16();
+        for (int c = 0; c < O::STEPS; ++c) s = O::mma(O::along(kt, 32 * u, c), qf[c], s);
+        if constexpr (decltype(masked)::value) {
+            seen = 0;
 #pragma unroll
-            for (int c = 0; c < O::STEPS; ++c) s[u] = O::mma(O::along(kt, 32 * u, c), qf[c], s[u]);
-            seen[u] = 0xFFFFu;
-            if constexpr (MASKED) {
-                seen[u] = 0;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const bool see = tl * KT + 32 * u + row16(i, h) < qr.limit;
-                    seen[u] |= (uint32_t)see << i;
-                    s[u][i] = see ? s[u][i] : -INFINITY;
-                }
+            for (int i = 0; i < 16; ++i) {
+                const bool see = tl * KT + 32 * u + row16(i, h) < qr.limit;
+                seen |= (uint32_t)see << i;
+                s[i] = see ? s[i] : -INFINITY;
             }
         }
-        float mx = s[0][0];
+        return s;
+    };
+    const auto raise = [&](int tl, int b, int u) {
+        uint32_t seen;
+        const f32x16_t s = scores(tl, b, u, std::true_type{}, seen);
 #pragma unroll
-        for (int u = 0; u < NSUB; ++u)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[u][i]);
-        mx = half_max(mx);
-        const bool grow = (mx - ref) * p.scale2 > kSlack;
-        if (__ballot(grow)) {
-            const float f = grow ? __builtin_amdgcn_exp2f((ref - mx) * p.scale2) : 1.f;
-            ref = grow ? mx : ref;
-            sum *= f;
-#pragma unroll
-            for (int d = 0; d < NDT; ++d)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) acc[d][i] *= f;
-        }
-        const float base = ref == -INFINITY ? 0.f : ref;
-        const float base2 = -base * p.scale2;
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < 16; ++i) ref = fmaxf(ref, s[i]);
+    };
+    const auto set_base = [&]() {
+        ref = half_max(ref);
+        base = ref == -INFINITY ? 0.f : S::ES == 4 ? ref : ref * p.scale2;
+    };
+    const auto compute = [&](int tl, int b, auto masked) {
+        constexpr bool MASKED = decltype(masked)::value;
 #pragma unroll
         for (int u = 0; u < NSUB; ++u) {
+            uint32_t seen = 0xFFFFu;
+            f32x16_t s = scores(tl, b, u, masked, seen);
+            float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 // fp32: the reference's own weight is 1 to the bit, so that one key's
                 // value comes out as it is; in bf16 the rounding sees to that
-                s[u][i] = __builtin_amdgcn_exp2f(S::ES == 4 ? (s[u][i] - base) * p.scale2
-                                                          : fmaf(s[u][i], p.scale2, base2));
-                part[i & 3] += s[u][i];
+                s[i] = __builtin_amdgcn_exp2f(S::ES == 4 ? (s[i] - base) * p.scale2 : fmaf(s[i], p.scale2, -base));
+                part[i & 3] += s[i];
             }
+            sum += (part[0] + part[1]) + (part[2] + part[3]);
+            add_rows<T, DP, MASKED>(acc, buf + b * 2 * S::TILE + S::TILE, 32 * u, s, seen);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        sum += (part[0] + part[1]) + (part[2] + part[3]);
-#pragma unroll
-        for (int u = 0; u < NSUB; ++u) add_rows<T, DP, MASKED>(acc, vt, 32 * u, s[u], seen[u]);
     };
 
-    if (begin < t1) {
-        keys.look_up(begin);
-        keys.load(buf, buf + S::TILE);
-        keys.look_up(begin + STEP);
-    }
-    wait_loads();
-    if constexpr (!KS) __syncthreads();
-    int b = 0;
-    for (int tl = begin; tl < t1; tl += STEP, b ^= 1) {
-        if (tl + STEP < t1) {
-            if constexpr (KS) wait_reads();
-            keys.load(buf + (b ^ 1) * 2 * S::TILE, buf + (b ^ 1) * 2 * S::TILE + S::TILE);
-            keys.look_up(tl + 2 * STEP);
-        }
-        if (tl * KT < qr.most) {
-            if ((tl + 1) * KT > qr.least)
-                compute(tl, b, std::true_type{});
-            else
-                compute(tl, b, std::false_type{});
+    // all tiles: `first` before them, when the first has arrived; `each` on those
+    // that every query sees whole, then on those that some do not
+    const auto sweep = [&](auto first, auto each) {
+        if (begin < t1) {
+            keys.look_up(begin);
+            keys.fetch(begin);
+            keys.store(buf);
+            keys.look_up(begin + STEP);
         }
         wait_loads();
-        if constexpr (!KS) __syncthreads();
+        next_tile<KS>();
+        if (begin < t1 && begin * KT < qr.most) first();
+        int b = 0, tl = begin;
+        const auto run = [&](int end, auto masked) {
+            for (; tl < end; tl += STEP, b ^= 1) {
+                if (tl + STEP < t1) {
+                    keys.fetch(tl + STEP);
+                    keys.look_up(tl + 2 * STEP);
+                }
+                if (tl * KT < qr.most) each(tl, b, masked);
+                if (tl + STEP < t1) keys.store(buf + (b ^ 1) * 2 * S::TILE);
+                next_tile<KS>();
+            }
+        };
+        run(min(t1, qr.least / KT), std::false_type{});
+        run(t1, std::true_type{});
+    };
+    const auto clear = [&]() {
+        sum = 0.f;
+#pragma unroll
+        for (int d = 0; d < NDT; ++d) acc[d] = zero16();
+    };
+    clear();
+    sweep(
+        [&]() {
+            raise(begin, 0, 0);
+            set_base();
+        },
+        compute);
+    bool again = !(sum < kMost);
+#pragma unroll
+    for (int d = 0; d < NDT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) again |= !(fabsf(acc[d][i]) < INFINITY);
+    if (__builtin_expect(KS ? __ballot(again) != 0 : __syncthreads_or(again), 0)) {
+        sweep([]() {},
+              [&](int tl, int b, auto) {
+#pragma unroll 1
+                  for (int u = 0; u < NSUB; ++u) raise(tl, b, u);
+              });
+        set_base();
+        clear();
+        sweep([]() {}, compute);
     }
     sum = half_sum(sum);
 

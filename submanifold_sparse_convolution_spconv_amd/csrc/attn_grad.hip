@@ -34,13 +34,15 @@ struct GradShape {
     static constexpr int STATS = 2 * KT * 4;                        // lse and delta of a tile of queries
     static constexpr int WAVE = 4 * TILE + 2 * STATS;               // two buffers
     static constexpr int LDS = WAVE * (KS ? NW : 1);
+    static constexpr int DQ_OCC = ES == 2 && DP == 32 ? 4 : DP <= 32 || (ES == 2 && DP == 64) ? 2 : 1;   // waves of a SIMD that registers are for
+    static constexpr int DKV_OCC = DP <= 64 ? 2 : 1;
 };
 
 // lse in powers of two; rows without keys: p = 2^-inf = 0
 __device__ __forceinline__ float stat2(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
 
 template <typename T, int DP, bool KS>
-__global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW)) k_attn_dq(AttnParams p) {
+__global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T, DP, KS>::DQ_OCC)) k_attn_dq(AttnParams p) {
     using S = GradShape<T, DP, KS>;
     using O = Operand<T, DP>;
     constexpr int KT = S::KT, NW = S::NW, NDT = DP / 32;
@@ -54,8 +56,6 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW)) k_attn_dq(Att
     QueryRows qr;
     if (!qr.find(p, S::TR, KS ? 0 : 32 * wave, hk, id / p.splits % p.items)) return;
     RowFrag<T, DP> qf[O::STEPS], df[O::STEPS];
-    // delta with the matrix instructions that give dout v below: where a query
-    // has one key, out is v and their difference is 0
     f32x16_t dd = zero16();
 #pragma unroll
     for (int s = 0; s < O::STEPS; ++s) {
@@ -71,6 +71,11 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW)) k_attn_dq(Att
     delta = ((lane >> 2) & 1) == h ? delta : other;
     const float lse2 = stat2(p.lse[qr.row * p.H + qr.head]);
     if (qr.valid && h == 0 && split == 0 && (!KS || wave == 0)) p.delta[qr.row * p.H + qr.head] = delta;
+
+    // where the sums of dout v start: -delta
+    f32x16_t less;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) less[i] = -delta;
 
     const int nt = (qr.longest + KT - 1) / KT;
     const int t0 = (int)((int64_t)nt * split / p.splits), t1 = (int)((int64_t)nt * (split + 1) / p.splits);
@@ -89,7 +94,7 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW)) k_attn_dq(Att
         const lds_u8* vt = kt + S::TILE;
 #pragma unroll
         for (int u = 0; u < KT / 32; ++u) {
-            f32x16_t s = zero16(), dp = zero16();
+            f32x16_t s = zero16(), dp = less;
 #pragma unroll
             for (int c = 0; c < O::STEPS; ++c) {
                 s = O::mma(O::along(kt, 32 * u, c), qf[c], s);
@@ -99,7 +104,7 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW)) k_attn_dq(Att
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const float e = __builtin_amdgcn_exp2f(fmaf(s[i], p.scale2, -lse2));
-                s[i] = e * (dp[i] - delta);
+                s[i] = e * dp[i];
                 if constexpr (MASKED) {
                     const bool see = tl * KT + 32 * u + row16(i, h) < qr.limit;
                     seen = see ? seen : seen & ~(1u << i);
@@ -107,32 +112,33 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW)) k_attn_dq(Att
                 }
             }
             add_rows<T, DP, MASKED>(acc, kt, 32 * u, s, seen);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
 
     if (begin < t1) {
         keys.look_up(begin);
-        keys.load(buf, buf + S::TILE);
+        keys.fetch(begin);
+        keys.store(buf);
         keys.look_up(begin + STEP);
     }
     wait_loads();
-    if constexpr (!KS) __syncthreads();
-    int b = 0;
-    for (int tl = begin; tl < t1; tl += STEP, b ^= 1) {
-        if (tl + STEP < t1) {
-            if constexpr (KS) wait_reads();
-            keys.load(buf + (b ^ 1) * 2 * S::TILE, buf + (b ^ 1) * 2 * S::TILE + S::TILE);
-            keys.look_up(tl + 2 * STEP);
+    next_tile<KS>();
+    // tiles that every query sees whole, then those that some do not
+    int b = 0, tl = begin;
+    const auto sweep = [&](int end, auto masked) {
+        for (; tl < end; tl += STEP, b ^= 1) {
+            if (tl + STEP < t1) {
+                keys.fetch(tl + STEP);
+                keys.look_up(tl + 2 * STEP);
+            }
+            if (tl * KT < qr.most) compute(tl, b, masked);
+            if (tl + STEP < t1) keys.store(buf + (b ^ 1) * 2 * S::TILE);
+            next_tile<KS>();
         }
-        if (tl * KT < qr.most) {
-            if ((tl + 1) * KT > qr.least)
-                compute(tl, b, std::true_type{});
-            else
-                compute(tl, b, std::false_type{});
-        }
-        wait_loads();
-        if constexpr (!KS) __syncthreads();
-    }
+    };
+    sweep(min(t1, qr.least / KT), std::false_type{});
+    sweep(t1, std::true_type{});
 
     if constexpr (KS) {
         __syncthreads();
@@ -154,19 +160,21 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW)) k_attn_dq(Att
         }
     }
     if (!qr.valid) return;
+    // (the weight of a single key is 1, whatever its score)
+    const float scale = qr.limit > 1 ? p.scale : 0.f;
     if (p.splits > 1) {
         float* o = p.part + ((split * p.N + qr.pl.q0 + qr.rh.pos) * p.H + qr.head) * p.D;
 #pragma unroll
-        for (int d = 0; d < NDT; ++d) store_col<float>((uint8_t*)o, acc[d], p.scale, d, p.D);
+        for (int d = 0; d < NDT; ++d) store_col<float>((uint8_t*)o, acc[d], scale, d, p.D);
         return;
     }
     uint8_t* o = p.dq + qr.row * p.dqs[0] + qr.head * p.dqs[1];
 #pragma unroll
-    for (int d = 0; d < NDT; ++d) store_col<T>(o, acc[d], p.scale, d, p.D);
+    for (int d = 0; d < NDT; ++d) store_col<T>(o, acc[d], scale, d, p.D);
 }
 
 template <typename T, int DP, bool KS>
-__global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW)) k_attn_dkv(AttnParams p) {
+__global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T, DP, KS>::DKV_OCC)) k_attn_dkv(AttnParams p) {
     using S = GradShape<T, DP, KS>;
     using O = Operand<T, DP>;
     constexpr int KT = S::KT, NW = S::NW, NDT = DP / 32;
@@ -200,7 +208,8 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW)) k_attn_dkv(At
         return (int)min(r, (int64_t)R);
     };
     const int from = seen_from(key);
-    const int wave_first = first < pl.Lk ? seen_from(first) : R, wave_last = seen_from(min(first + 31, pl.Lk - 1));
+    const int wave_first = first < pl.Lk ? seen_from(first) : R;
+    const int block_last = seen_from(min((pl.tile + 1) * S::TR, pl.Lk) - 1);
     const int64_t krow = row_of(p.korder, pl.k0 + key, p.M);
     RowFrag<T, DP> kf[O::STEPS], vf[O::STEPS];
 #pragma unroll
@@ -216,47 +225,79 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW)) k_attn_dkv(At
     lds_u8* buf = (lds_u8*)smem + (KS ? wave * S::WAVE : 0);
     float* stats = (float*)(smem + (KS ? wave * S::WAVE : 0) + 4 * S::TILE);
 
-    // rows of the queries' tiles, looked up one tile before they are loaded
-    int64_t qrow[St::NP];
-    int qhead[St::NP];
-    float lse = INFINITY, delta = 0.f;
-    auto look_up = [&](int tl) {
+    // The queries' rows.  Where a tile is a whole number of positions, and those one
+    // after the other, as the keys are fetched; else each row's place is looked
+    // up one tile before.
+    constexpr int NP = St::NP;
+    const bool plain = !p.order && KT % p.G == 0;
+    uint32_t oq[NP], od[NP];
+    int qrow[NP], qhead[NP];
+    u32x4a_t rq[NP], rd[NP];
+    float lse = INFINITY, delta = 0.f, lse_next = INFINITY, delta_next = 0.f;
+    const uint8_t* qh = p.q + hk * p.G * p.qs[1];
+    const uint8_t* dh = p.dout + hk * p.G * p.dos[1];
 #pragma unroll
-        for (int i = 0; i < St::NP; ++i) {
-            const int r = tl * KT + St::row(i, st);
-            qrow[i] = -1;
-            qhead[i] = 0;
-            if (r < R) {
-                const RowHead rh = split_row(r, p.G, p.magic);
-                qrow[i] = row_of(p.order, pl.q0 + rh.pos, p.N);
-                qhead[i] = hk * p.G + rh.head;
+    for (int i = 0; i < NP; ++i) {
+        const int by = St::byte(i, st);
+        const RowHead rh = plain ? split_row(St::row(i, st), p.G, p.magic) : RowHead{0, 0};
+        const bool in = by < p.D * (int)sizeof(T);
+        oq[i] = in ? (uint32_t)(by + rh.pos * p.qs[0] + rh.head * p.qs[1]) : kNoUnit;
+        od[i] = in ? (uint32_t)(by + rh.pos * p.dos[0] + rh.head * p.dos[1]) : kNoUnit;
+    }
+    auto look_up = [&](int tl) {
+        if (!plain) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const int r = tl * KT + St::row(i, st);
+                qrow[i] = -1;
+                qhead[i] = 0;
+                if (r < R) {
+                    const RowHead rh = split_row(r, p.G, p.magic);
+                    qrow[i] = (int)row_of(p.order, pl.q0 + rh.pos, p.N);
+                    qhead[i] = rh.head;
+                }
             }
         }
         if (st < KT) {
             const int r = tl * KT + st;
-            lse = INFINITY;
-            delta = 0.f;
+            lse_next = INFINITY;
+            delta_next = 0.f;
             if (r < R) {
                 const RowHead rh = split_row(r, p.G, p.magic);
                 const int64_t at = row_of(p.order, pl.q0 + rh.pos, p.N) * p.H + hk * p.G + rh.head;
-                lse = p.lse[at];
-                delta = p.delta[at];
+                lse_next = p.lse[at];
+                delta_next = p.delta[at];
             }
         }
     };
-    auto load = [&](int b) {
-        lds_u8* qt = buf + b * 2 * S::TILE;
+    auto fetch = [&](int tl) {
+        lse = lse_next;
+        delta = delta_next;
+        if (!plain) {
 #pragma unroll
-        for (int i = 0; i < St::NP; ++i) {
-            const int by = St::byte(i, st, p.D);
-            const bool in = qrow[i] >= 0 && by >= 0;
-            St::load(in ? p.q + qrow[i] * p.qs[0] + qhead[i] * p.qs[1] + by : (const uint8_t*)kAttnZeros, qt, i, st);
-            St::load(in ? p.dout + qrow[i] * p.dos[0] + qhead[i] * p.dos[1] + by : (const uint8_t*)kAttnZeros,
-                     qt + S::TILE, i, st);
+            for (int i = 0; i < NP; ++i) {
+                const bool in = qrow[i] >= 0 && oq[i] != kNoUnit;
+                rq[i] = fetch16(qh + qrow[i] * p.qs[0] + qhead[i] * p.qs[1] + oq[i], in);
+                rd[i] = fetch16(dh + qrow[i] * p.dos[0] + qhead[i] * p.dos[1] + od[i], in);
+            }
+            return;
         }
+        const int64_t at = pl.q0 + (int64_t)tl * (KT / p.G);
+        const auto bq = rows_at(qh + at * p.qs[0]), bd = rows_at(dh + at * p.dos[0]);
+        const int left = R - tl * KT;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            rq[i] = fetch16(bq, left >= KT || St::row(i, st) < left ? oq[i] : kNoUnit);
+            rd[i] = fetch16(bd, left >= KT || St::row(i, st) < left ? od[i] : kNoUnit);
+        }
+    };
+    auto store = [&](int b) {
+        lds_u8* qt = buf + b * 2 * S::TILE;
+        St::store(rq, qt, st);
+        St::store(rd, qt + S::TILE, st);
         if (st < KT) {
             stats[b * 2 * KT + st] = stat2(lse);
-            stats[b * 2 * KT + KT + st] = delta;
+            stats[b * 2 * KT + KT + st] = -delta;
         }
     };
 
@@ -270,18 +311,20 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW)) k_attn_dkv(At
         const lds_u8* dt = qt + S::TILE;
 #pragma unroll
         for (int u = 0; u < KT / 32; ++u) {
-            f32x16_t s = zero16(), dp = zero16();
+            const float* l2 = stats + b * 2 * KT + 32 * u;
+            f32x16_t s = zero16(), dp;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) dp[i] = l2[KT + row16(i, h)];
 #pragma unroll
             for (int c = 0; c < O::STEPS; ++c) {
                 s = O::mma(O::along(qt, 32 * u, c), kf[c], s);
                 dp = O::mma(O::along(dt, 32 * u, c), vf[c], dp);
             }
-            const float* l2 = stats + b * 2 * KT + 32 * u;
             uint32_t seen = 0xFFFFu;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const float e = __builtin_amdgcn_exp2f(fmaf(s[i], p.scale2, -l2[row16(i, h)]));
-                dp[i] = e * (dp[i] - l2[KT + row16(i, h)]);
+                dp[i] *= e;
                 s[i] = e;
                 if constexpr (MASKED) {
                     const bool see = tl * KT + 32 * u + row16(i, h) >= from;
@@ -292,32 +335,33 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW)) k_attn_dkv(At
             }
             add_rows<T, DP, MASKED>(dv, dt, 32 * u, s, seen);
             add_rows<T, DP, MASKED>(dk, qt, 32 * u, dp, seen);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
 
     if (begin < t1) {
         look_up(begin);
-        load(0);
+        fetch(begin);
+        store(0);
         look_up(begin + STEP);
     }
     wait_loads();
-    if constexpr (!KS) __syncthreads();
-    int b = 0;
-    for (int tl = begin; tl < t1; tl += STEP, b ^= 1) {
-        if (tl + STEP < t1) {
-            if constexpr (KS) wait_reads();
-            load(b ^ 1);
-            look_up(tl + 2 * STEP);
+    next_tile<KS>();
+    // tiles that some keys are hidden from, then those that see every key
+    int b = 0, tl = begin;
+    const auto sweep = [&](int end, auto masked) {
+        for (; tl < end; tl += STEP, b ^= 1) {
+            if (tl + STEP < t1) {
+                fetch(tl + STEP);
+                look_up(tl + 2 * STEP);
+            }
+            if ((tl + 1) * KT > wave_first) compute(tl, b, masked);
+            if (tl + STEP < t1) store(b ^ 1);
+            next_tile<KS>();
         }
-        if ((tl + 1) * KT > wave_first) {
-            if (tl * KT < wave_last)
-                compute(tl, b, std::true_type{});
-            else
-                compute(tl, b, std::false_type{});
-        }
-        wait_loads();
-        if constexpr (!KS) __syncthreads();
-    }
+    };
+    sweep(min(t1, (block_last + KT - 1) / KT), std::true_type{});
+    sweep(t1, std::false_type{});
 
     if constexpr (KS) {
         static_assert(DP * 32 * 4 * 2 <= 4 * S::TILE);
@@ -346,19 +390,20 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW)) k_attn_dkv(At
         }
     }
     if (!valid) return;
+    const float scale = pl.Lk > 1 ? p.scale : 0.f;     // (a single key's weight is 1)
     if (p.splits > 1) {
         float* o = p.part + ((split * p.M + pl.k0 + key) * p.HK + hk) * p.D;
         const int64_t all = p.splits * p.M * p.HK * p.D;
 #pragma unroll
         for (int d = 0; d < NDT; ++d) {
-            store_col<float>((uint8_t*)o, dk[d], p.scale, d, p.D);
+            store_col<float>((uint8_t*)o, dk[d], scale, d, p.D);
             store_col<float>((uint8_t*)(o + all), dv[d], 1.f, d, p.D);
         }
         return;
     }
 #pragma unroll
     for (int d = 0; d < NDT; ++d) {
-        store_col<T>(p.dk + krow * p.dks[0] + hk * p.dks[1], dk[d], p.scale, d, p.D);
+        store_col<T>(p.dk + krow * p.dks[0] + hk * p.dks[1], dk[d], scale, d, p.D);
         store_col<T>(p.dv + krow * p.dvs[0] + hk * p.dvs[1], dv[d], 1.f, d, p.D);
     }
 }
@@ -390,7 +435,7 @@ AttnPlan side_plan(int64_t n, int64_t per, int64_t B, int64_t HK, int64_t along)
     const int64_t seqs = std::max<int64_t>(1, std::min(B, n));
     AttnPlan r;
     const int64_t shared = attn_places(n, per, 128, seqs) * HK;
-    r.ks = n * per / seqs <= 32 || shared < 512;
+    r.ks = n * per / seqs <= 32 || shared < 256;
     const int64_t blocks = std::max<int64_t>(1, r.ks ? attn_places(n, per, 32, seqs) * HK : shared);
     const int64_t splits = blocks >= 512 ? 1 : std::min((1024 + blocks - 1) / blocks, along / 512);
     r.splits = (int)std::max<int64_t>(1, std::min<int64_t>(splits, 256));
