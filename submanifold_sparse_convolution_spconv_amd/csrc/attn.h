@@ -39,6 +39,7 @@ struct AttnParams {
     int H, HK, G, D, B;
     uint32_t magic;             // of a division by G
     int causal;
+    int near;                   // 1: rows are below 2 GiB from their tensor's start
     int splits;                 // of the long axis over workgroups
     float scale, scale2;        // of the scores; the same times log2 e
 };
@@ -103,16 +104,16 @@ __device__ __forceinline__ void find_keys(const AttnParams& p, Place& pl) {
     }
 }
 
-// A wave's 32 query rows, one per lane (both halves), and the keys they see: the
-// lane's own first `limit`, at most `most` in the wave, and `least` to `longest`
-// over the workgroup.
-// Lanes past the sequence repeat its last row.
+// A wave's 32 NB query rows, NB per lane (both halves), and the keys they see:
+// each lane's own first `limit`, at most `most` in the wave, and `least` to
+// `longest` over the workgroup.  Lanes past the sequence repeat its last row.
+template <int NB>
 struct QueryRows {
     Place pl;
-    RowHead rh;
-    int64_t row;
-    int head, limit, least, most, longest;
-    bool valid;
+    int pos[NB], head[NB], limit[NB];
+    uint32_t row[NB];
+    int least, most, longest;
+    bool valid[NB];
     // wave_row: the wave's first row in the tile of tq
     __device__ __forceinline__ bool find(const AttnParams& p, int tq, int wave_row, int hk, int64_t item) {
         pl = find_place(p.offsets, p.B, p.N, p.G, tq, item);
@@ -121,21 +122,30 @@ struct QueryRows {
         const int R = pl.Lq * p.G;
         // a causal sequence's long tiles first
         const int tile = p.causal ? (R - 1) / tq - pl.tile : pl.tile;
-        const int first = tile * tq + wave_row, mine = first + (threadIdx.x & 31);
+        const int first = tile * tq + wave_row;
         const int past = pl.Lk - pl.Lq + 1;
-        const auto sees = [&](int r) {
-            const int pos = split_row(min(r, R - 1), p.G, p.magic).pos;
-            return p.causal ? min(max(pos + past, 0), pl.Lk) : pl.Lk;
-        };
-        valid = mine < R;
-        rh = split_row(min(mine, R - 1), p.G, p.magic);
-        head = hk * p.G + rh.head;
-        row = row_of(p.order, pl.q0 + rh.pos, p.N);
-        limit = sees(mine);
-        least = sees(tile * tq);
-        most = first < R ? sees(first + 31) : 0;
-        longest = sees(tile * tq + tq - 1);
+        const auto sees = [&](int pos) { return p.causal ? min(max(pos + past, 0), pl.Lk) : pl.Lk; };
+        const auto pos_of = [&](int r) { return split_row(min(r, R - 1), p.G, p.magic).pos; };
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            const int mine = first + 32 * n + (threadIdx.x & 31);
+            const RowHead rh = split_row(min(mine, R - 1), p.G, p.magic);
+            valid[n] = mine < R;
+            pos[n] = rh.pos;
+            head[n] = hk * p.G + rh.head;
+            row[n] = row_of(p.order, pl.q0 + rh.pos, p.N);
+            limit[n] = sees(rh.pos);
+        }
+        least = sees(pos_of(tile * tq));
+        most = first < R ? sees(pos_of(first + 32 * NB - 1)) : 0;
+        longest = sees(pos_of(tile * tq + tq - 1));
         return true;
+    }
+    __device__ __forceinline__ const uint8_t* at(const uint8_t* t, const int64_t (&s)[2], int n) const {
+        return t + row[n] * s[0] + head[n] * s[1];
+    }
+    __device__ __forceinline__ uint8_t* at(uint8_t* t, const int64_t (&s)[2], int n) const {
+        return t + row[n] * s[0] + head[n] * s[1];
     }
 };
 
@@ -208,7 +218,8 @@ __device__ __forceinline__ u32x4a_t fetch16(const uint8_t* p, bool in) {
 // Keys' and values' rows of a sequence into tiles.  Rows one after the other
 // are a buffer whose start moves with the tile, so that a unit's offset stays
 // the same; through korder each row's place is looked up one tile before it
-// is fetched.
+// is fetched (in one buffer, where the tensors are below 2 GiB).  Rows past the
+// sequence, zeros or its last one again, are hidden from every query.
 template <typename T, int DP, int KT, int THR>
 struct KeyStager {
     using St = Stager<T, DP, KT, THR>;
@@ -234,17 +245,22 @@ struct KeyStager {
         if (!p.korder) return;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            const int j = tile * KT + St::row(i, t);
-            row[i] = j < Lk ? (int)row_of(p.korder, k0 + j, p.M) : -1;
+            row[i] = p.korder[k0 + min(tile * KT + St::row(i, t), Lk - 1)];
         }
     }
     __device__ __forceinline__ void fetch(int tile) {
         if (p.korder) {
+            const auto bk = rows_at(k), bv = rows_at(v);
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
-                const bool in = row[i] >= 0 && ok[i] != kNoUnit;
-                rk[i] = fetch16(k + row[i] * p.ks[0] + ok[i], in);
-                rv[i] = fetch16(v + row[i] * p.vs[0] + ov[i], in);
+                const uint32_t r = min((uint32_t)row[i], (uint32_t)p.M - 1);
+                if (p.near) {
+                    rk[i] = fetch16(bk, r * (uint32_t)p.ks[0] + ok[i]);
+                    rv[i] = fetch16(bv, r * (uint32_t)p.vs[0] + ov[i]);
+                } else {
+                    rk[i] = fetch16(k + r * p.ks[0] + ok[i], ok[i] != kNoUnit);
+                    rv[i] = fetch16(v + r * p.vs[0] + ov[i], ov[i] != kNoUnit);
+                }
             }
             return;
         }
@@ -390,19 +406,21 @@ struct Operand<float, DP> {
 template <typename T, int DP>
 using RowFrag = decltype(Operand<T, DP>::row((const uint8_t*)nullptr, 0, 0));
 
-// acc[dt] += (rows' transpose) x w for 32 rows of a tile, w a 32 x 32 result
+// acc[n][dt] += (rows' transpose) x w[n] for 32 rows of a tile, w 32 x 32 results
 // whose hidden entries (bit i of `seen` clear) are zero.  A zero times an infinite
 // or NaN element of the tile would still be NaN, so masked tiles multiply the
 // others only, and where there are some, these are added row by row, to the
 // columns that see the row.
-template <typename T, int DP, bool MASKED>
-__device__ __forceinline__ void add_rows(f32x16_t (&acc)[DP / 32], const lds_u8* tile, int row0, const f32x16_t& w,
-                                         uint32_t seen) {
+template <typename T, int DP, bool MASKED, int NB>
+__device__ __forceinline__ void add_rows(f32x16_t (&acc)[NB][DP / 32], const lds_u8* tile, int row0,
+                                         const f32x16_t (&w)[NB], const uint32_t (&seen)[NB]) {
     using O = Operand<T, DP>;
     bool some = false;
 #pragma unroll
     for (int c = 0; c < O::CROSS; ++c) {
-        const auto b = O::pack(w, c);
+        typename O::frag b[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) b[n] = O::pack(w[n], c);
 #pragma unroll
         for (int dt = 0; dt < DP / 32; ++dt) {
             auto a = O::across(tile, row0, c, dt);
@@ -411,27 +429,31 @@ __device__ __forceinline__ void add_rows(f32x16_t (&acc)[DP / 32], const lds_u8*
                 some |= O::any(x);
                 a = O::without(a, x);
             }
-            acc[dt] = O::mma(a, b, acc[dt]);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) acc[n][dt] = O::mma(a, b[n], acc[n][dt]);
         }
     }
     if (MASKED && __builtin_expect(__ballot(some) != 0, 0)) {
         const int h = (threadIdx.x >> 5) & 1;
-        // a column's two lane halves see different rows: ask the half that holds it
-        const uint32_t other = (uint32_t)__shfl_xor((int)seen, 32);
 #pragma unroll
-        for (int c = 0; c < O::CROSS; ++c) {
-            const auto b = O::pack(w, c);
+        for (int n = 0; n < NB; ++n) {
+            // a column's two lane halves see different rows: ask the half that holds it
+            const uint32_t other = (uint32_t)__shfl_xor((int)seen[n], 32);
+#pragma unroll
+            for (int c = 0; c < O::CROSS; ++c) {
+                const auto b = O::pack(w[n], c);
 #pragma unroll 1
-            for (int j = 0; j < 2 * O::ROWS; ++j) {
-                const int half = j & 1, e = j >> 1;
-                const bool see = ((h == half ? seen : other) >> O::index(c, e)) & 1;
+                for (int j = 0; j < 2 * O::ROWS; ++j) {
+                    const int half = j & 1, e = j >> 1;
+                    const bool see = ((h == half ? seen[n] : other) >> O::index(c, e)) & 1;
 #pragma unroll
-                for (int dt = 0; dt < DP / 32; ++dt) {
-                    const auto x = O::only(O::bad(O::across(tile, row0, c, dt)), e, h == half);
-                    const f32x16_t t = O::mma(x, O::only(b, e, h == half), zero16());
+                    for (int dt = 0; dt < DP / 32; ++dt) {
+                        const auto x = O::only(O::bad(O::across(tile, row0, c, dt)), e, h == half);
+                        const f32x16_t t = O::mma(x, O::only(b, e, h == half), zero16());
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[dt][i] += see ? t[i] : 0.f;
-                    __builtin_amdgcn_sched_barrier(0);
+                        for (int i = 0; i < 16; ++i) acc[n][dt][i] += see ? t[i] : 0.f;
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
                 }
             }
         }

@@ -30,20 +30,20 @@ constexpr float kMost = 0x1p64f;    // a query's sum from which its reference is
 // KS: the workgroup's waves take turns at the keys of one tile of 32 queries
 // (each with tiles of its own, joined at the end) instead of sharing the
 // keys' tiles for 32 queries each.
-template <typename T, int DP, bool KS>
+template <typename T, int DP, bool KS, int NB>
 struct FwdShape {
     static constexpr int ES = sizeof(T);
     static constexpr int KT = ES == 2 && !KS ? 64 : 32;             // keys per tile
     static constexpr int NW = KS && ES == 4 && DP > 64 ? 2 : 4;     // waves (LDS holds no more)
-    static constexpr int TQ = KS ? 32 : 32 * NW;                    // query rows per workgroup
+    static constexpr int TQ = KS ? 32 : 32 * NB * NW;               // query rows per workgroup
     static constexpr int TILE = KT * DP * ES;
     static constexpr int LDS = 4 * TILE * (KS ? NW : 1);            // two buffers of keys and values
-    static constexpr int OCC = ES == 2 && DP <= 64 ? (DP == 32 ? 4 : 3) : ES == 2 || DP <= (KS ? 32 : 64) ? 2 : 1;   // waves of a SIMD that registers are for
+    static constexpr int OCC = ES == 2 && DP <= 64 ? (DP == 32 ? 4 : 3) - (NB == 2) : ES == 2 || DP <= (KS ? 32 : 64) ? 2 : 1;   // waves of a SIMD that registers are for
 };
 
-template <typename T, int DP, bool KS>
-__global__ void __launch_bounds__((64 * FwdShape<T, DP, KS>::NW), (FwdShape<T, DP, KS>::OCC)) k_attn(AttnParams p) {
-    using S = FwdShape<T, DP, KS>;
+template <typename T, int DP, bool KS, int NB>
+__global__ void __launch_bounds__((64 * FwdShape<T, DP, KS, NB>::NW), (FwdShape<T, DP, KS, NB>::OCC)) k_attn(AttnParams p) {
+    using S = FwdShape<T, DP, KS, NB>;
     using O = Operand<T, DP>;
     constexpr int KT = S::KT, NW = S::NW, NSUB = KT / 32, NDT = DP / 32;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -53,11 +53,13 @@ __global__ void __launch_bounds__((64 * FwdShape<T, DP, KS>::NW), (FwdShape<T, D
     const int split = (int)(id % p.splits);
     const int hk = (int)(id / p.splits / p.items);
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6), h = lane >> 5;
-    QueryRows qr;
-    if (!qr.find(p, S::TQ, KS ? 0 : 32 * wave, hk, id / p.splits % p.items)) return;
-    RowFrag<T, DP> qf[O::STEPS];
+    QueryRows<NB> qr;
+    if (!qr.find(p, S::TQ, KS ? 0 : 32 * NB * wave, hk, id / p.splits % p.items)) return;
+    RowFrag<T, DP> qf[NB][O::STEPS];
 #pragma unroll
-    for (int s = 0; s < O::STEPS; ++s) qf[s] = O::row(p.q + qr.row * p.qs[0] + qr.head * p.qs[1], s, p.D);
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int s = 0; s < O::STEPS; ++s) qf[n][s] = O::row(qr.at(p.q, p.qs, n), s, p.D);
 
     const int nt = (qr.longest + KT - 1) / KT;
     const int t0 = (int)((int64_t)nt * split / p.splits), t1 = (int)((int64_t)nt * (split + 1) / p.splits);
@@ -66,54 +68,80 @@ __global__ void __launch_bounds__((64 * FwdShape<T, DP, KS>::NW), (FwdShape<T, D
     lds_u8* buf = (lds_u8*)smem + (KS ? wave * 4 * S::TILE : 0);
     KeyStager<T, DP, KT, KS ? 64 : 64 * NW> keys(p, qr.pl, hk, KS ? lane : t);
 
-    f32x16_t acc[NDT];
-    // the reference of the lane's query (a score, -inf if it sees no key here), and
-    // what it takes off exponents (in bf16 powers of two)
-    float ref = -INFINITY, base = 0.f, sum;
+    f32x16_t acc[NB][NDT];
+    // the references of the lane's queries (scores, -inf if they see no key here), and
+    // what they take off exponents (in bf16 powers of two)
+    float ref[NB], base[NB], sum[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        ref[n] = -INFINITY;
+        base[n] = 0.f;
+    }
 
     // scores of 32 keys of a tile
-    const auto scores = [&](int tl, int b, int u, auto masked, uint32_t& seen) {
+    const auto scores = [&](int tl, int b, int u, auto masked, f32x16_t(&s)[NB], uint32_t(&seen)[NB]) {
         const lds_u8* kt = buf + b * 2 * S::TILE;
-        f32x16_t s = zero16();
 #pragma unroll
-        for (int c = 0; c < O::STEPS; ++c) s = O::mma(O::along(kt, 32 * u, c), qf[c], s);
+        for (int n = 0; n < NB; ++n) {
+            s[n] = zero16();
+            seen[n] = 0xFFFFu;
+        }
+#pragma unroll
+        for (int c = 0; c < O::STEPS; ++c) {
+            const auto a = O::along(kt, 32 * u, c);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) s[n] = O::mma(a, qf[n][c], s[n]);
+        }
         if constexpr (decltype(masked)::value) {
-            seen = 0;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const bool see = tl * KT + 32 * u + row16(i, h) < qr.limit;
-                seen |= (uint32_t)see << i;
-                s[i] = see ? s[i] : -INFINITY;
+            for (int n = 0; n < NB; ++n) {
+                seen[n] = 0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const bool see = tl * KT + 32 * u + row16(i, h) < qr.limit[n];
+                    seen[n] |= (uint32_t)see << i;
+                    s[n][i] = see ? s[n][i] : -INFINITY;
+                }
             }
         }
-        return s;
     };
     const auto raise = [&](int tl, int b, int u) {
-        uint32_t seen;
-        const f32x16_t s = scores(tl, b, u, std::true_type{}, seen);
+        uint32_t seen[NB];
+        f32x16_t s[NB];
+        scores(tl, b, u, std::true_type{}, s, seen);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) ref = fmaxf(ref, s[i]);
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) ref[n] = fmaxf(ref[n], s[n][i]);
     };
     const auto set_base = [&]() {
-        ref = half_max(ref);
-        base = ref == -INFINITY ? 0.f : S::ES == 4 ? ref : ref * p.scale2;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            ref[n] = half_max(ref[n]);
+            base[n] = ref[n] == -INFINITY ? 0.f : S::ES == 4 ? ref[n] : ref[n] * p.scale2;
+        }
     };
     const auto compute = [&](int tl, int b, auto masked) {
         constexpr bool MASKED = decltype(masked)::value;
 #pragma unroll
         for (int u = 0; u < NSUB; ++u) {
-            uint32_t seen = 0xFFFFu;
-            f32x16_t s = scores(tl, b, u, masked, seen);
-            float part[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t seen[NB];
+            f32x16_t s[NB];
+            scores(tl, b, u, masked, s, seen);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                // fp32: the reference's own weight is 1 to the bit, so that one key's
-                // value comes out as it is; in bf16 the rounding sees to that
-                s[i] = __builtin_amdgcn_exp2f(S::ES == 4 ? (s[i] - base) * p.scale2 : fmaf(s[i], p.scale2, -base));
-                part[i & 3] += s[i];
+            for (int n = 0; n < NB; ++n) {
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    // fp32: the reference's own weight is 1 to the bit, so that one key's
+                    // value comes out as it is; in bf16 the rounding sees to that
+                    s[n][i] = __builtin_amdgcn_exp2f(S::ES == 4 ? (s[n][i] - base[n]) * p.scale2
+                                                                : fmaf(s[n][i], p.scale2, -base[n]));
+                    part[i & 3] += s[n][i];
+                }
+                sum[n] += (part[0] + part[1]) + (part[2] + part[3]);
             }
-            sum += (part[0] + part[1]) + (part[2] + part[3]);
-            add_rows<T, DP, MASKED>(acc, buf + b * 2 * S::TILE + S::TILE, 32 * u, s, seen);
+            add_rows<T, DP, MASKED, NB>(acc, buf + b * 2 * S::TILE + S::TILE, 32 * u, s, seen);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -146,9 +174,12 @@ __global__ void __launch_bounds__((64 * FwdShape<T, DP, KS>::NW), (FwdShape<T, D
         run(t1, std::true_type{});
     };
     const auto clear = [&]() {
-        sum = 0.f;
 #pragma unroll
-        for (int d = 0; d < NDT; ++d) acc[d] = zero16();
+        for (int n = 0; n < NB; ++n) {
+            sum[n] = 0.f;
+#pragma unroll
+            for (int d = 0; d < NDT; ++d) acc[n][d] = zero16();
+        }
     };
     clear();
     sweep(
@@ -157,11 +188,15 @@ __global__ void __launch_bounds__((64 * FwdShape<T, DP, KS>::NW), (FwdShape<T, D
             set_base();
         },
         compute);
-    bool again = !(sum < kMost);
+    bool again = false;
 #pragma unroll
-    for (int d = 0; d < NDT; ++d)
+    for (int n = 0; n < NB; ++n) {
+        again |= !(sum[n] < kMost);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) again |= !(fabsf(acc[d][i]) < INFINITY);
+        for (int d = 0; d < NDT; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) again |= !(fabsf(acc[n][d][i]) < INFINITY);
+    }
     if (__builtin_expect(KS ? __ballot(again) != 0 : __syncthreads_or(again), 0)) {
         sweep([]() {},
               [&](int tl, int b, auto) {
@@ -172,7 +207,8 @@ __global__ void __launch_bounds__((64 * FwdShape<T, DP, KS>::NW), (FwdShape<T, D
         clear();
         sweep([]() {}, compute);
     }
-    sum = half_sum(sum);
+#pragma unroll
+    for (int n = 0; n < NB; ++n) sum[n] = half_sum(sum[n]);
 
     if constexpr (KS) {
         // the waves' parts, in their order: (sum, reference) and the columns
@@ -184,54 +220,59 @@ __global__ void __launch_bounds__((64 * FwdShape<T, DP, KS>::NW), (FwdShape<T, D
 #pragma unroll
             for (int d = 0; d < NDT; ++d)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) mine[(32 * d + row16(i, h)) * 32 + (lane & 31)] = acc[d][i];
+                for (int i = 0; i < 16; ++i) mine[(32 * d + row16(i, h)) * 32 + (lane & 31)] = acc[0][d][i];
             if (h == 0) {
-                mine[DP * 32 + lane] = ref;
-                mine[DP * 32 + 32 + lane] = sum;
+                mine[DP * 32 + lane] = ref[0];
+                mine[DP * 32 + 32 + lane] = sum[0];
             }
         }
         __syncthreads();
         if (wave > 0) return;
-        float top = ref;
+        float top = ref[0];
         for (int w = 1; w < NW; ++w) top = fmaxf(top, ((float*)(smem + w * 4 * S::TILE))[DP * 32 + (lane & 31)]);
         const float base = top == -INFINITY ? 0.f : top;
-        const float f0 = __builtin_amdgcn_exp2f((ref - base) * p.scale2);
-        sum *= f0;
+        const float f0 = __builtin_amdgcn_exp2f((ref[0] - base) * p.scale2);
+        sum[0] *= f0;
 #pragma unroll
         for (int d = 0; d < NDT; ++d)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[d][i] *= f0;
+            for (int i = 0; i < 16; ++i) acc[0][d][i] *= f0;
         for (int w = 1; w < NW; ++w) {
             const float* o = (const float*)(smem + w * 4 * S::TILE);
             const float f = __builtin_amdgcn_exp2f((o[DP * 32 + (lane & 31)] - base) * p.scale2);
-            sum = fmaf(o[DP * 32 + 32 + (lane & 31)], f, sum);
+            sum[0] = fmaf(o[DP * 32 + 32 + (lane & 31)], f, sum[0]);
 #pragma unroll
             for (int d = 0; d < NDT; ++d)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    acc[d][i] = fmaf(o[(32 * d + row16(i, h)) * 32 + (lane & 31)], f, acc[d][i]);
+                    acc[0][d][i] = fmaf(o[(32 * d + row16(i, h)) * 32 + (lane & 31)], f, acc[0][d][i]);
         }
-        ref = top;
+        ref[0] = top;
     }
 
-    if (!qr.valid) return;
-    if (p.splits > 1) {
-        const int64_t NH = p.N * p.H, at = (int64_t)split * NH + (qr.pl.q0 + qr.rh.pos) * p.H + qr.head;
-        float* o = p.part + at * p.D;
 #pragma unroll
-        for (int d = 0; d < NDT; ++d) store_col<float>((uint8_t*)o, acc[d], 1.f, d, p.D);
-        if (h == 0) {
-            float* m = p.part + p.splits * NH * p.D + at * 2;
-            m[0] = ref * p.scale2;
-            m[1] = qr.limit > 0 ? sum : -1.f;
+    for (int n = 0; n < NB; ++n) {
+        if (!qr.valid[n]) continue;
+        const bool sees = qr.limit[n] > 0;
+        if (p.splits > 1) {
+            const int64_t NH = p.N * p.H, at = (int64_t)split * NH + (qr.pl.q0 + qr.pos[n]) * p.H + qr.head[n];
+            float* o = p.part + at * p.D;
+#pragma unroll
+            for (int d = 0; d < NDT; ++d) store_col<float>((uint8_t*)o, acc[n][d], 1.f, d, p.D);
+            if (h == 0) {
+                float* m = p.part + p.splits * NH * p.D + at * 2;
+                m[0] = ref[n] * p.scale2;
+                m[1] = sees ? sum[n] : -1.f;
+            }
+            continue;
         }
-        return;
-    }
-    const float f = qr.limit > 0 ? 1.f / sum : 0.f;
-    uint8_t* o = p.out + qr.row * p.os[0] + qr.head * p.os[1];
+        const float f = sees ? 1.f / sum[n] : 0.f;
+        uint8_t* o = qr.at(p.out, p.os, n);
 #pragma unroll
-    for (int d = 0; d < NDT; ++d) store_col<T>(o, acc[d], f, d, p.D);
-    if (p.lse && h == 0) p.lse[qr.row * p.H + qr.head] = qr.limit > 0 ? fmaf(ref, p.scale, logf(sum)) : -INFINITY;
+        for (int d = 0; d < NDT; ++d) store_col<T>(o, acc[n][d], f, d, p.D);
+        if (p.lse && h == 0)
+            p.lse[(int64_t)qr.row[n] * p.H + qr.head[n]] = sees ? fmaf(ref[n], p.scale, logf(sum[n])) : -INFINITY;
+    }
 }
 
 // The splits' parts of one (position, head) each block, added in their order
@@ -283,22 +324,23 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(AttnParams p) {
     if (p.lse && q == 0) p.lse[row * p.H + head] = none ? -INFINITY : (top + log2f(l)) * kLn2;
 }
 
-template <typename T, int DP, bool KS>
+template <typename T, int DP, bool KS, int NB>
 hipError_t attn_go(AttnParams p, hipStream_t st) {
-    using S = FwdShape<T, DP, KS>;
+    using S = FwdShape<T, DP, KS, NB>;
     p.items = attn_places(p.N, p.G, S::TQ, p.B);
     const int64_t blocks = xcd_blocks(p.items * p.HK * p.splits);
     const hipError_t e =
-        hipFuncSetAttribute((const void*)k_attn<T, DP, KS>, hipFuncAttributeMaxDynamicSharedMemorySize, S::LDS);
+        hipFuncSetAttribute((const void*)k_attn<T, DP, KS, NB>, hipFuncAttributeMaxDynamicSharedMemorySize, S::LDS);
     if (e != hipSuccess) return e;
-    k_attn<T, DP, KS><<<(unsigned)blocks, 64 * S::NW, S::LDS, st>>>(p);
+    k_attn<T, DP, KS, NB><<<(unsigned)blocks, 64 * S::NW, S::LDS, st>>>(p);
     if (p.splits > 1) k_attn_join<T><<<(unsigned)(p.N * p.H), kJoinThreads, 0, st>>>(p);
     return hipGetLastError();
 }
 
 template <typename T, int DP>
 hipError_t attn_width(const AttnParams& p, bool ks, hipStream_t st) {
-    return ks ? attn_go<T, DP, true>(p, st) : attn_go<T, DP, false>(p, st);
+    constexpr int NB = 1;
+    return ks ? attn_go<T, DP, true, 1>(p, st) : attn_go<T, DP, false, NB>(p, st);
 }
 template <typename T>
 hipError_t attn_type(const AttnParams& p, bool ks, hipStream_t st) {
@@ -380,6 +422,8 @@ AttnParams attn_params(const AttnArgs& a) {
     p.magic = (uint32_t)((1ull << 32) / p.G + 1);
     p.causal = a.causal;
     p.splits = 1;
+    const auto below = [&](const int64_t(&s)[2]) { return a.M * s[0] * es < (1ll << 31); };
+    p.near = below(a.ks) && below(a.vs);
     p.scale = a.scale;
     p.scale2 = a.scale * 1.4426950408889634f;
     return p;

@@ -53,15 +53,15 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
     const int split = (int)(id % p.splits);
     const int hk = (int)(id / p.splits / p.items);
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6), h = lane >> 5;
-    QueryRows qr;
+    QueryRows<1> qr;
     if (!qr.find(p, S::TR, KS ? 0 : 32 * wave, hk, id / p.splits % p.items)) return;
     RowFrag<T, DP> qf[O::STEPS], df[O::STEPS];
     f32x16_t dd = zero16();
 #pragma unroll
     for (int s = 0; s < O::STEPS; ++s) {
-        qf[s] = O::row(p.q + qr.row * p.qs[0] + qr.head * p.qs[1], s, p.D);
-        df[s] = O::row(p.dout + qr.row * p.dos[0] + qr.head * p.dos[1], s, p.D);
-        dd = O::mma(O::row(p.out + qr.row * p.os[0] + qr.head * p.os[1], s, p.D), df[s], dd);
+        qf[s] = O::row(qr.at(p.q, p.qs, 0), s, p.D);
+        df[s] = O::row(qr.at(p.dout, p.dos, 0), s, p.D);
+        dd = O::mma(O::row(qr.at((const uint8_t*)p.out, p.os, 0), s, p.D), df[s], dd);
     }
     // the diagonal: row16(i, h) = lane & 31
     float delta = 0.f;
@@ -69,8 +69,8 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
     for (int i = 0; i < 16; ++i) delta = row16(i, h) == (lane & 31) ? dd[i] : delta;
     const float other = __shfl_xor(delta, 32);
     delta = ((lane >> 2) & 1) == h ? delta : other;
-    const float lse2 = stat2(p.lse[qr.row * p.H + qr.head]);
-    if (qr.valid && h == 0 && split == 0 && (!KS || wave == 0)) p.delta[qr.row * p.H + qr.head] = delta;
+    const float lse2 = stat2(p.lse[(int64_t)qr.row[0] * p.H + qr.head[0]]);
+    if (qr.valid[0] && h == 0 && split == 0 && (!KS || wave == 0)) p.delta[(int64_t)qr.row[0] * p.H + qr.head[0]] = delta;
 
     // where the sums of dout v start: -delta
     f32x16_t less;
@@ -84,9 +84,9 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
     lds_u8* buf = (lds_u8*)smem + (KS ? wave * S::WAVE : 0);
     KeyStager<T, DP, KT, KS ? 64 : 64 * NW> keys(p, qr.pl, hk, KS ? lane : t);
 
-    f32x16_t acc[NDT];
+    f32x16_t acc[1][NDT];
 #pragma unroll
-    for (int d = 0; d < NDT; ++d) acc[d] = zero16();
+    for (int d = 0; d < NDT; ++d) acc[0][d] = zero16();
 
     auto compute = [&](int tl, int b, auto masked) {
         constexpr bool MASKED = decltype(masked)::value;
@@ -94,24 +94,24 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
         const lds_u8* vt = kt + S::TILE;
 #pragma unroll
         for (int u = 0; u < KT / 32; ++u) {
-            f32x16_t s = zero16(), dp = less;
+            f32x16_t s[1] = {zero16()}, dp = less;
 #pragma unroll
             for (int c = 0; c < O::STEPS; ++c) {
-                s = O::mma(O::along(kt, 32 * u, c), qf[c], s);
+                s[0] = O::mma(O::along(kt, 32 * u, c), qf[c], s[0]);
                 dp = O::mma(O::along(vt, 32 * u, c), df[c], dp);
             }
-            uint32_t seen = 0xFFFFu;
+            uint32_t seen[1] = {0xFFFFu};
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float e = __builtin_amdgcn_exp2f(fmaf(s[i], p.scale2, -lse2));
-                s[i] = e * dp[i];
+                const float e = __builtin_amdgcn_exp2f(fmaf(s[0][i], p.scale2, -lse2));
+                s[0][i] = e * dp[i];
                 if constexpr (MASKED) {
-                    const bool see = tl * KT + 32 * u + row16(i, h) < qr.limit;
-                    seen = see ? seen : seen & ~(1u << i);
-                    s[i] = see ? s[i] : 0.f;
+                    const bool see = tl * KT + 32 * u + row16(i, h) < qr.limit[0];
+                    seen[0] = see ? seen[0] : seen[0] & ~(1u << i);
+                    s[0][i] = see ? s[0][i] : 0.f;
                 }
             }
-            add_rows<T, DP, MASKED>(acc, kt, 32 * u, s, seen);
+            add_rows<T, DP, MASKED, 1>(acc, kt, 32 * u, s, seen);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
 #pragma unroll
             for (int d = 0; d < NDT; ++d)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) mine[(32 * d + row16(i, h)) * 32 + (lane & 31)] = acc[d][i];
+                for (int i = 0; i < 16; ++i) mine[(32 * d + row16(i, h)) * 32 + (lane & 31)] = acc[0][d][i];
         }
         __syncthreads();
         if (wave > 0) return;
@@ -156,21 +156,21 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
 #pragma unroll
             for (int d = 0; d < NDT; ++d)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) acc[d][i] += o[(32 * d + row16(i, h)) * 32 + (lane & 31)];
+                for (int i = 0; i < 16; ++i) acc[0][d][i] += o[(32 * d + row16(i, h)) * 32 + (lane & 31)];
         }
     }
-    if (!qr.valid) return;
+    if (!qr.valid[0]) return;
     // (the weight of a single key is 1, whatever its score)
-    const float scale = qr.limit > 1 ? p.scale : 0.f;
+    const float scale = qr.limit[0] > 1 ? p.scale : 0.f;
     if (p.splits > 1) {
-        float* o = p.part + ((split * p.N + qr.pl.q0 + qr.rh.pos) * p.H + qr.head) * p.D;
+        float* o = p.part + ((split * p.N + qr.pl.q0 + qr.pos[0]) * p.H + qr.head[0]) * p.D;
 #pragma unroll
-        for (int d = 0; d < NDT; ++d) store_col<float>((uint8_t*)o, acc[d], scale, d, p.D);
+        for (int d = 0; d < NDT; ++d) store_col<float>((uint8_t*)o, acc[0][d], scale, d, p.D);
         return;
     }
-    uint8_t* o = p.dq + qr.row * p.dqs[0] + qr.head * p.dqs[1];
+    uint8_t* o = qr.at(p.dq, p.dqs, 0);
 #pragma unroll
-    for (int d = 0; d < NDT; ++d) store_col<T>(o, acc[d], scale, d, p.D);
+    for (int d = 0; d < NDT; ++d) store_col<T>(o, acc[0][d], scale, d, p.D);
 }
 
 template <typename T, int DP, bool KS>
@@ -301,9 +301,9 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
         }
     };
 
-    f32x16_t dk[NDT], dv[NDT];
+    f32x16_t dk[1][NDT], dv[1][NDT];
 #pragma unroll
-    for (int d = 0; d < NDT; ++d) dk[d] = dv[d] = zero16();
+    for (int d = 0; d < NDT; ++d) dk[0][d] = dv[0][d] = zero16();
 
     auto compute = [&](int tl, int b, auto masked) {
         constexpr bool MASKED = decltype(masked)::value;
@@ -312,29 +312,29 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
 #pragma unroll
         for (int u = 0; u < KT / 32; ++u) {
             const float* l2 = stats + b * 2 * KT + 32 * u;
-            f32x16_t s = zero16(), dp;
+            f32x16_t s[1] = {zero16()}, dp[1];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) dp[i] = l2[KT + row16(i, h)];
+            for (int i = 0; i < 16; ++i) dp[0][i] = l2[KT + row16(i, h)];
 #pragma unroll
             for (int c = 0; c < O::STEPS; ++c) {
-                s = O::mma(O::along(qt, 32 * u, c), kf[c], s);
-                dp = O::mma(O::along(dt, 32 * u, c), vf[c], dp);
+                s[0] = O::mma(O::along(qt, 32 * u, c), kf[c], s[0]);
+                dp[0] = O::mma(O::along(dt, 32 * u, c), vf[c], dp[0]);
             }
-            uint32_t seen = 0xFFFFu;
+            uint32_t seen[1] = {0xFFFFu};
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float e = __builtin_amdgcn_exp2f(fmaf(s[i], p.scale2, -l2[row16(i, h)]));
-                dp[i] *= e;
-                s[i] = e;
+                const float e = __builtin_amdgcn_exp2f(fmaf(s[0][i], p.scale2, -l2[row16(i, h)]));
+                dp[0][i] *= e;
+                s[0][i] = e;
                 if constexpr (MASKED) {
                     const bool see = tl * KT + 32 * u + row16(i, h) >= from;
-                    seen = see ? seen : seen & ~(1u << i);
-                    s[i] = see ? s[i] : 0.f;
-                    dp[i] = see ? dp[i] : 0.f;
+                    seen[0] = see ? seen[0] : seen[0] & ~(1u << i);
+                    s[0][i] = see ? s[0][i] : 0.f;
+                    dp[0][i] = see ? dp[0][i] : 0.f;
                 }
             }
-            add_rows<T, DP, MASKED>(dv, dt, 32 * u, s, seen);
-            add_rows<T, DP, MASKED>(dk, qt, 32 * u, dp, seen);
+            add_rows<T, DP, MASKED, 1>(dv, dt, 32 * u, s, seen);
+            add_rows<T, DP, MASKED, 1>(dk, qt, 32 * u, dp, seen);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -372,8 +372,8 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
             for (int d = 0; d < NDT; ++d)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    mine[(32 * d + row16(i, h)) * 32 + (lane & 31)] = dk[d][i];
-                    mine[(DP + 32 * d + row16(i, h)) * 32 + (lane & 31)] = dv[d][i];
+                    mine[(32 * d + row16(i, h)) * 32 + (lane & 31)] = dk[0][d][i];
+                    mine[(DP + 32 * d + row16(i, h)) * 32 + (lane & 31)] = dv[0][d][i];
                 }
         }
         __syncthreads();
@@ -384,8 +384,8 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
             for (int d = 0; d < NDT; ++d)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    dk[d][i] += o[(32 * d + row16(i, h)) * 32 + (lane & 31)];
-                    dv[d][i] += o[(DP + 32 * d + row16(i, h)) * 32 + (lane & 31)];
+                    dk[0][d][i] += o[(32 * d + row16(i, h)) * 32 + (lane & 31)];
+                    dv[0][d][i] += o[(DP + 32 * d + row16(i, h)) * 32 + (lane & 31)];
                 }
         }
     }
@@ -396,15 +396,15 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
         const int64_t all = p.splits * p.M * p.HK * p.D;
 #pragma unroll
         for (int d = 0; d < NDT; ++d) {
-            store_col<float>((uint8_t*)o, dk[d], scale, d, p.D);
-            store_col<float>((uint8_t*)(o + all), dv[d], 1.f, d, p.D);
+            store_col<float>((uint8_t*)o, dk[0][d], scale, d, p.D);
+            store_col<float>((uint8_t*)(o + all), dv[0][d], 1.f, d, p.D);
         }
         return;
     }
 #pragma unroll
     for (int d = 0; d < NDT; ++d) {
-        store_col<T>(p.dk + krow * p.dks[0] + hk * p.dks[1], dk[d], scale, d, p.D);
-        store_col<T>(p.dv + krow * p.dvs[0] + hk * p.dvs[1], dv[d], 1.f, d, p.D);
+        store_col<T>(p.dk + krow * p.dks[0] + hk * p.dks[1], dk[0][d], scale, d, p.D);
+        store_col<T>(p.dv + krow * p.dvs[0] + hk * p.dvs[1], dv[0][d], 1.f, d, p.D);
     }
 }
 

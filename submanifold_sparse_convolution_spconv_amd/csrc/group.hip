@@ -26,7 +26,6 @@ namespace spc {
 namespace {
 
 constexpr int kGrpThreads = 256;
-constexpr int kGrpJoin = 256;
 
 struct GroupParams {
     const void* x;
@@ -44,6 +43,7 @@ struct GroupParams {
     int64_t N, items;
     int C, G, B, rows;         // rows: per chunk
     int tx;                    // threads along the channels (a power of two)
+    int jx;                    // the same for the channels of a group, in the join
     float eps;
     int act;
     bool stream;
@@ -82,7 +82,7 @@ struct Moments {
 template <typename T, int ACT, int MODE>
 __global__ void __launch_bounds__(kGrpThreads) k_group_part(GroupParams p) {
     constexpr int V = Piece<T>::V;
-    constexpr int U = 4;                           // rows in flight
+    constexpr int U = MODE == 0 ? 8 : 4;           // rows in flight
     __shared__ float s0[kGrpThreads * V], s1[kGrpThreads * V];
     const int t = threadIdx.x, tx = t & (p.tx - 1), ty = t / p.tx, TY = kGrpThreads / p.tx;
     const int cb = blockIdx.y * p.tx * V;          // the workgroup's first channel
@@ -205,7 +205,16 @@ __global__ void __launch_bounds__(kGrpThreads) k_group_part(GroupParams p) {
     }
 }
 
-// Sum over a workgroup, the same bits in every thread.
+// dweight and dbias (kJoinCols of both) from the parts of all places.
+__device__ __forceinline__ void group_sums(const float* part, int64_t items, int C, float* dweight, float* dbias,
+                                           int block) {
+    const float t = join_columns<64, 1>(part, items, 2 * C, block).f[0];
+    const int e = block * kJoinCols + threadIdx.x;
+    if (threadIdx.x < kJoinCols && e < 2 * C) (e < C ? dbias : dweight - C)[e] = t;
+}
+
+// Sum over a workgroup of THR threads, the same bits in every thread.
+template <int THR>
 __device__ __forceinline__ float block_sum(float v, float* red) {
     v = group_sum<64>(v);
     __syncthreads();
@@ -213,51 +222,88 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
     __syncthreads();
     float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < kGrpJoin / 64; ++k) s += red[k];
+    for (int k = 0; k < THR / 64; ++k) s += red[k];
     return s;
 }
 
 // The chunks' parts of one scene and group: its statistics, or its two means
-// of the gradient.
-template <int MODE>
-__global__ void __launch_bounds__(kGrpJoin) k_group_join(GroupParams p) {
-    __shared__ float red[kGrpJoin / 64];
+// of the gradient.  Threads stand along the group's channels (a power of two of
+// them), the others on chunks side by side; the first few chunks of a thread
+// stay in registers.  The gradient's channel sums over all places are further
+// workgroups of the same launch (or, where a wave is enough for a scene and
+// group, a launch of their own).
+constexpr int kGrpKeep = 8;
+template <int MODE, int THR>
+__global__ void __launch_bounds__(THR) k_group_join(GroupParams p) {
+    __shared__ float red[THR / 64];
+    const int stats = p.B * p.G;
+    if constexpr (MODE == 1 && THR == kJoinCols * 64) {
+        if ((int)blockIdx.x >= stats) {
+            group_sums(p.part, p.items, p.C, p.dweight, p.dbias, blockIdx.x - stats);
+            return;
+        }
+    }
     const int b = blockIdx.x / p.G, g = blockIdx.x % p.G, cg = p.C / p.G;
     const int64_t o0 = clamp_to(p.offsets[b], 0, p.N), len = clamp_to(p.offsets[b + 1], o0, p.N) - o0;
     const int64_t item = o0 / p.rows + b;
     const int chunks = (int)((len + p.rows - 1) / p.rows);
-    const int64_t all = (int64_t)chunks * cg;
     const float* part = p.part + item * 2 * p.C + g * cg;
-    const auto rows_of = [&](int64_t k) { return (float)min((int64_t)p.rows, len - k * p.rows); };
+    const auto rows_of = [&](int k) { return (float)min((int64_t)p.rows, len - (int64_t)k * p.rows); };
     const float inv = len ? 1.f / ((float)len * cg) : 0.f;
-    float v0 = 0.f, v1 = 0.f;
-    for (int64_t e = threadIdx.x; e < all; e += kGrpJoin) {
-        const int64_t k = e / cg, c = e - k * cg;
-        const float* q = part + k * 2 * p.C + c;
-        if constexpr (MODE == 0) {
-            v0 = fmaf(q[0], rows_of(k), v0);
+    const int jx = min(p.jx, THR), tc = threadIdx.x & (jx - 1), tk = threadIdx.x / jx, step = THR / jx;
+    float q0[kGrpKeep], q1[kGrpKeep], v0 = 0.f, v1 = 0.f;
+    // element i of the thread: its channel and chunk
+    const int mine = tk < chunks ? (chunks - tk + step - 1) / step : 0, all = mine * ((cg - tc + jx - 1) / jx);
+    const auto at = [&](int i, int& c, int& k) {
+        if (i < mine) {
+            c = tc;
+            k = tk + i * step;
         } else {
-            const float w = p.weight ? p.weight[g * cg + c] : 1.f;
-            v0 = fmaf(q[0], w, v0);
-            v1 = fmaf(q[p.C], w, v1);
+            const int w = i / mine;
+            c = tc + w * jx;
+            k = tk + (i - w * mine) * step;
         }
-    }
-    v0 = block_sum(v0, red) * inv;
-    if constexpr (MODE == 0) {
-        for (int64_t e = threadIdx.x; e < all; e += kGrpJoin) {
-            const int64_t k = e / cg, c = e - k * cg;
-            const float* q = part + k * 2 * p.C + c;
-            const float d = q[0] - v0;
-            v1 += fmaf(d * d, rows_of(k), q[p.C]);
+        return part + (int64_t)k * 2 * p.C + c;
+    };
+    const auto each = [&](auto use) {
+#pragma unroll
+        for (int i = 0; i < kGrpKeep; ++i)
+            if (i < all && tc < cg) {
+                int c, k;
+                at(i, c, k);
+                use(q0[i], q1[i], c, k);
+            }
+        for (int i = kGrpKeep; i < all && tc < cg; ++i) {
+            int c, k;
+            const float* q = at(i, c, k);
+            use(q[0], q[p.C], c, k);
         }
-        v1 = block_sum(v1, red) * inv;
-        if (threadIdx.x == 0) {
+    };
+#pragma unroll
+    for (int i = 0; i < kGrpKeep; ++i)
+        if (i < all && tc < cg) {
+            int c, k;
+            const float* q = at(i, c, k);
+            q0[i] = q[0];
+            q1[i] = q[p.C];
+        }
+    each([&](float a0, float a1, int c, int k) {
+        const float w = MODE == 0 ? rows_of(k) : p.weight ? p.weight[g * cg + c] : 1.f;
+        v0 = fmaf(a0, w, v0);
+        if constexpr (MODE == 1) v1 = fmaf(a1, w, v1);
+    });
+    v0 = block_sum<THR>(v0, red) * inv;
+    if constexpr (MODE == 0)
+        each([&](float a0, float a1, int, int k) {
+            const float d = a0 - v0;
+            v1 += fmaf(d * d, rows_of(k), a1);
+        });
+    v1 = block_sum<THR>(v1, red) * inv;
+    if (threadIdx.x == 0) {
+        if constexpr (MODE == 0) {
             p.mean[blockIdx.x] = v0;
             p.rstd[blockIdx.x] = 1.f / sqrtf(v1 + p.eps);
-        }
-    } else {
-        v1 = block_sum(v1, red) * inv;
-        if (threadIdx.x == 0) {
+        } else {
             p.m12[2 * blockIdx.x] = v0;
             p.m12[2 * blockIdx.x + 1] = v1;
         }
@@ -266,9 +312,7 @@ __global__ void __launch_bounds__(kGrpJoin) k_group_join(GroupParams p) {
 
 __global__ void __launch_bounds__(kJoinCols * 64) k_group_sums(const float* part, int64_t items, int C, float* dweight,
                                                                float* dbias) {
-    const float t = join_columns<64, 1>(part, items, 2 * C, blockIdx.x).f[0];
-    const int e = blockIdx.x * kJoinCols + threadIdx.x;
-    if (threadIdx.x < kJoinCols && e < 2 * C) (e < C ? dbias : dweight - C)[e] = t;
+    group_sums(part, items, C, dweight, dbias, blockIdx.x);
 }
 
 template <typename T, int ACT, bool GRAD>
@@ -277,7 +321,7 @@ __global__ void __launch_bounds__(kGrpThreads) k_group_apply(GroupParams p) {
     constexpr int U = 4;
     const int t = threadIdx.x, tx = t & (p.tx - 1), ty = t / p.tx, TY = kGrpThreads / p.tx;
     const int c = (blockIdx.y * p.tx + tx) * V, nv = p.C - c;
-    const Chunk ch = find_chunk(p, blockIdx.x);
+    const Chunk ch = find_chunk(p, p.items - 1 - blockIdx.x);
     if (ch.n == 0 || nv <= 0) return;
     const T* x = (const T*)p.x + ch.row * p.C + c;
     const T* dout = (const T*)p.dout + ch.row * p.C + c;
@@ -326,11 +370,135 @@ __global__ void __launch_bounds__(kGrpThreads) k_group_apply(GroupParams p) {
     }
 }
 
+// Few rows: a workgroup per scene and group keeps the group's elements in
+// registers between the statistics and the outputs (kOneElems per thread), a
+// launch in place of three.  A thread holds W channels (all of a 16-byte piece,
+// where groups and rows are whole numbers of those, else one) of rows one
+// stride apart.  part: the gradient's sums by scene, [scenes][2][C].
+constexpr int kOneThreads = 1024, kOneElems = 32;
+template <typename T, int W, int ACT, bool GRAD>
+__global__ void __launch_bounds__(kOneThreads) k_group_one(GroupParams p) {
+    constexpr int NE = kOneElems / W;
+    typedef T vec __attribute__((ext_vector_type(W)));
+    __shared__ float red[kOneThreads / 64];
+    const int b = blockIdx.x / p.G, g = blockIdx.x % p.G, cg = p.C / p.G, per = cg / W, side = kOneThreads / per;
+    const int64_t o0 = clamp_to(p.offsets[b], 0, p.N);
+    const int len = (int)(clamp_to(p.offsets[b + 1], o0, p.N) - o0);
+    const int t = threadIdx.x, tr = t / per, c = g * cg + (t - tr * per) * W;
+    const bool mine = tr < side;
+    const int64_t first = (o0 + tr) * p.C + c, step = (int64_t)side * p.C;
+    const T* x = (const T*)p.x + first;
+    const T* dout = (const T*)p.dout + first;
+    T* y = (T*)p.y + first;
+    const float inv = len ? 1.f / ((float)len * cg) : 0.f;
+    float wt[W], bs[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        wt[i] = p.weight && mine ? p.weight[c + i] : 1.f;
+        bs[i] = p.bias && mine ? p.bias[c + i] : 0.f;
+    }
+    vec vx[NE], vd[NE];
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int e = 0; e < NE; ++e) {
+        const bool in = mine && tr + e * side < len;
+        vx[e] = in ? *(const vec*)(x + e * step) : vec{};
+        if constexpr (GRAD) vd[e] = in ? *(const vec*)(dout + e * step) : vec{};
+    }
+    float mean, rstd;
+    if constexpr (!GRAD) {
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+#pragma unroll
+            for (int i = 0; i < W; ++i) s0 += (float)vx[e][i];
+        mean = block_sum<kOneThreads>(s0, red) * inv;
+#pragma unroll
+        for (int e = 0; e < NE; ++e) {
+            const bool in = mine && tr + e * side < len;
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const float d = (float)vx[e][i] - mean;
+                s1 += in ? d * d : 0.f;
+            }
+        }
+        rstd = 1.f / sqrtf(block_sum<kOneThreads>(s1, red) * inv + p.eps);
+        if (t == 0) {
+            p.mean[blockIdx.x] = mean;
+            p.rstd[blockIdx.x] = rstd;
+        }
+    } else {
+        mean = p.mean[blockIdx.x];
+        rstd = p.rstd[blockIdx.x];
+    }
+    if constexpr (!GRAD) {
+#pragma unroll
+        for (int e = 0; e < NE; ++e) {
+            if (!mine || tr + e * side >= len) continue;
+            vec o;
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                o[i] = (T)group_act<ACT>(fmaf(((float)vx[e][i] - mean) * rstd, wt[i], bs[i])).v;
+            *(vec*)(y + e * step) = o;
+        }
+    } else {
+        // products are rounded before they are added and before the mean is taken
+        // off them: a group of one element gives 0
+#pragma clang fp contract(off)
+        __shared__ float col[kOneThreads * W];
+        float a0[W], a1[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) a0[i] = a1[i] = 0.f;
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                // (past the rows dout is 0)
+                const float xh = ((float)vx[e][i] - mean) * rstd;
+                const float dz = (float)vd[e][i] * group_act<ACT>(fmaf(xh, wt[i], bs[i])).d;
+                const float gw = dz * wt[i];
+                a0[i] += dz;
+                a1[i] += dz * xh;
+                s0 += gw;
+                s1 += gw * xh;
+            }
+        s0 = block_sum<kOneThreads>(s0, red) * inv;
+        s1 = block_sum<kOneThreads>(s1, red) * inv;
+#pragma unroll
+        for (int e = 0; e < NE; ++e) {
+            if (!mine || tr + e * side >= len) continue;
+            vec o;
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const float xh = ((float)vx[e][i] - mean) * rstd;
+                const float gw = (float)vd[e][i] * group_act<ACT>(fmaf(xh, wt[i], bs[i])).d * wt[i];
+                o[i] = (T)((gw - s0 - xh * s1) * rstd);
+            }
+            *(vec*)(y + e * step) = o;
+        }
+        if (!p.dweight) return;
+        // the channels' sums over the rows side by side, in their order
+        for (int k = 0; k < 2; ++k) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < W; ++i) col[t * W + i] = k ? a1[i] : a0[i];
+            __syncthreads();
+            for (int e = t; e < cg; e += kOneThreads) {
+                float s = 0.f;
+                for (int r = 0; r < min(side, len); ++r) s += col[r * cg + e];
+                if (p.B > 1)
+                    p.part[((int64_t)b * 2 + k) * p.C + g * cg + e] = s;
+                else
+                    (k ? p.dweight : p.dbias)[g * cg + e] = s;
+            }
+        }
+    }
+}
+
 struct GroupShape {
     int tx, cols, rows;
     int64_t items;
 };
-// Chunks of about a thousandth of the rows, but four rows per thread at least.
+// Chunks of about 1 / 2,048 of the rows, but four rows per thread at least.
 GroupShape group_shape(int64_t N, int C, int scenes, int dtype) {
     const int V = dtype == SPCONV_BF16 ? 8 : 4, pieces = (C + V - 1) / V;
     GroupShape s;
@@ -338,26 +506,55 @@ GroupShape group_shape(int64_t N, int C, int scenes, int dtype) {
     while (s.tx < 64 && s.tx < pieces) s.tx *= 2;
     s.cols = (pieces + s.tx - 1) / s.tx;
     const int64_t batch = kGrpThreads / s.tx * 4;
-    s.rows = (int)(std::max<int64_t>(1, (N / 1024 + batch - 1) / batch) * batch);
+    s.rows = (int)(std::max<int64_t>(1, (N / 2048 + batch - 1) / batch) * batch);
     s.items = N / s.rows + scenes;
     return s;
+}
+
+// Whether a scene's share of a group fits the registers of a workgroup, and the
+// whole is small enough for workgroups that read parts of rows (4,096 x 32 fp32
+// in 8 groups: 16.2 us of kernels in three launches, 8.5 in one).
+bool group_one(int64_t N, int C, int G, int W) {
+    const int per = C / G / W;
+    return per <= kOneThreads && N <= (int64_t)(kOneThreads / per) * (kOneElems / W) && N * C <= (1 << 18);
 }
 
 template <typename T, int ACT>
 hipError_t group_go(const GroupParams& p, bool grad, const GroupShape& s, hipStream_t st) {
     const dim3 grid((unsigned)s.items, s.cols);
     const unsigned stats = (unsigned)(p.B * p.G);
+    constexpr int V = Piece<T>::V;
+    const bool whole = p.C / p.G % V == 0 && ((uintptr_t)p.x | (uintptr_t)p.y | (uintptr_t)p.dout) % 16 == 0;
+    if (group_one(p.N, p.C, p.G, whole ? V : 1)) {
+        if (grad)
+            (whole ? k_group_one<T, V, ACT, true> : k_group_one<T, 1, ACT, true>)<<<stats, kOneThreads, 0, st>>>(p);
+        else
+            (whole ? k_group_one<T, V, ACT, false> : k_group_one<T, 1, ACT, false>)<<<stats, kOneThreads, 0, st>>>(p);
+        if (grad && p.dweight && p.B > 1)
+            k_group_sums<<<(2 * p.C + kJoinCols - 1) / kJoinCols, kJoinCols * 64, 0, st>>>(p.part, p.B, p.C, p.dweight,
+                                                                                        p.dbias);
+        return hipGetLastError();
+    }
+    // threads that join a scene's parts: a wave where it has a few on average
+    constexpr int kMany = kJoinCols * 64;
+    const bool many = (p.N / p.B / p.rows + 1) * (p.C / p.G) > 256;
+    const unsigned sums = (2 * p.C + kJoinCols - 1) / kJoinCols;
     if (!grad) {
         k_group_part<T, ACT, 0><<<grid, kGrpThreads, 0, st>>>(p);
-        k_group_join<0><<<stats, kGrpJoin, 0, st>>>(p);
+        if (many)
+            k_group_join<0, kMany><<<stats, kMany, 0, st>>>(p);
+        else
+            k_group_join<0, 64><<<stats, 64, 0, st>>>(p);
         k_group_apply<T, ACT, false><<<grid, kGrpThreads, 0, st>>>(p);
         return hipGetLastError();
     }
     k_group_part<T, ACT, 1><<<grid, kGrpThreads, 0, st>>>(p);
-    k_group_join<1><<<stats, kGrpJoin, 0, st>>>(p);
-    if (p.dweight)
-        k_group_sums<<<(2 * p.C + kJoinCols - 1) / kJoinCols, kJoinCols * 64, 0, st>>>(p.part, p.items, p.C, p.dweight,
-                                                                                    p.dbias);
+    if (many) {
+        k_group_join<1, kMany><<<stats + (p.dweight ? sums : 0), kMany, 0, st>>>(p);
+    } else {
+        k_group_join<1, 64><<<stats, 64, 0, st>>>(p);
+        if (p.dweight) k_group_sums<<<sums, kMany, 0, st>>>(p.part, p.items, p.C, p.dweight, p.dbias);
+    }
     k_group_apply<T, ACT, true><<<grid, kGrpThreads, 0, st>>>(p);
     return hipGetLastError();
 }
@@ -376,7 +573,7 @@ size_t stats_bytes(int scenes, int groups) { return align_up((size_t)scenes * gr
 
 bool group_fits(int64_t N, int C, int scenes, int groups, int dtype) {
     const GroupShape s = group_shape(N, C, scenes, dtype);
-    return s.items * s.cols * kGrpThreads < (1ll << 32) && (int64_t)scenes * groups * kGrpJoin < (1ll << 32);
+    return s.items * s.cols * kGrpThreads < (1ll << 32) && (int64_t)scenes * groups * kOneThreads < (1ll << 32);
 }
 size_t group_workspace_bytes(int64_t N, int C, int scenes, int groups, int dtype) {
     return stats_bytes(scenes, groups) + align_up((size_t)group_shape(N, C, scenes, dtype).items * 2 * C * 4, 256);
@@ -406,6 +603,8 @@ hipError_t launch_group(const GroupArgs& a, bool grad, hipStream_t stream) {
     p.B = a.scenes;
     p.rows = s.rows;
     p.tx = s.tx;
+    p.jx = 1;
+    while (p.jx < 1024 && p.jx < a.C / a.groups) p.jx *= 2;
     p.eps = a.eps;
     p.act = a.act;
     p.stream = a.N * a.C * (a.dtype == SPCONV_BF16 ? 2 : 4) > kStreamBytes;

@@ -43,7 +43,7 @@ __device__ __forceinline__ Place find_place(const int32_t* offs, int B, int64_t 
 
 // The row of a position; whatever `order` holds, one of the n rows.
 __device__ __forceinline__ int64_t row_of(const int32_t* order, int64_t pos, int64_t n) {
-    return order ? clamp_to(order[pos], 0, n - 1) : pos;
+    return order ? (int64_t)min((uint32_t)order[pos], (uint32_t)n - 1) : pos;
 }
 
 }  // namespace spc

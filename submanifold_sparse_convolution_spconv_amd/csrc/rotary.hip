@@ -7,7 +7,10 @@
 // gradient is the turn the other way, with the same gain.
 //
 // Bound by memory.  A workgroup takes some rows, works out their cosines and
-// sines once for all heads (LDS), then walks the rows' 16-byte pieces.  Angles
+// sines once for all heads (LDS), then walks the heads in 16-byte pieces, a
+// head's on neighbouring lanes of one wave.  A last piece that does not come
+// out even starts earlier instead and repeats some of its neighbour's elements
+// (in place too: the wave has read both before either is written).  Angles
 // are 64-bit turns less whole turns: in 32 bits the angle of position 1e6 would
 // be off by 0.06.
 #include "places.h"
@@ -30,9 +33,12 @@ struct RotParams {
     int64_t N;
     int H, D, P, per;                // per: pairs of an axis
     int rows;                        // per workgroup
-    int turn, rest;                  // 16-byte pieces of a head that turn, and of those that are copied
+    int tx;                          // lanes along a head (a power of two)
+    int end;                         // elements in pieces that turn (interleaved: copies among them)
+    int turn, rest;                  // such pieces, and those that are only copied
+    bool repeat;                     // whether a last piece may start earlier
     float gain, sign;
-    uint32_t heads_magic, pieces_magic;
+    uint32_t heads_magic;
     bool stream;
 };
 
@@ -66,43 +72,47 @@ __global__ void __launch_bounds__(kRotThreads) k_rotary(RotParams p) {
             table[e] = {c * p.gain, s * p.gain * p.sign};
         }
         __syncthreads();
-        const uint32_t pieces = p.turn + p.rest, all = (uint32_t)rows * p.H * pieces;
-        for (uint32_t e = threadIdx.x; e < all; e += kRotThreads) {
-            const Div a = divide(e, pieces, p.pieces_magic), b = divide(a.q, p.H, p.heads_magic);
+        const int tx = threadIdx.x & (p.tx - 1), step = kRotThreads / p.tx;
+        for (uint32_t e = threadIdx.x / p.tx; e < (uint32_t)rows * p.H; e += step) {
+            const Div b = divide(e, p.H, p.heads_magic);
             const T* x = (const T*)(p.x + (n0 + b.q) * p.xs[0] + b.r * p.xs[1]);
             T* y = (T*)(p.y + (n0 + b.q) * p.ys[0] + b.r * p.ys[1]);
             const float2* cs = table + b.q * p.P;
-            const int c = (int)a.r;
-            if (c >= p.turn) {
-                const int d = 2 * p.P + (c - p.turn) * V;
+            for (int c = tx; c < p.rest; c += p.tx) {
+                const int d = 2 * p.P + c * V;
                 const auto v = load_piece(x + d, p.D - d);
                 float o[V];
 #pragma unroll
                 for (int j = 0; j < V; ++j) o[j] = (float)v[j];
                 store_piece(y + d, o, p.D - d, p.stream);
-            } else if constexpr (HALF) {
-                const int i = c * V, n = p.P - i;
-                const auto va = load_piece(x + i, n), vb = load_piece(x + p.P + i, n);
-                float oa[V], ob[V];
+            }
+            for (int c = tx; c < p.turn; c += p.tx) {
+                const int i = p.repeat ? min(c * V, p.end - V) : c * V, n = p.end - i;
+                if constexpr (HALF) {
+                    const auto va = load_piece(x + i, n), vb = load_piece(x + p.P + i, n);
+                    float oa[V], ob[V];
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float2 w = cs[min(i + j, p.P - 1)];
-                    oa[j] = (float)va[j] * w.x - (float)vb[j] * w.y;
-                    ob[j] = (float)vb[j] * w.x + (float)va[j] * w.y;
-                }
-                store_piece(y + i, oa, n, p.stream);
-                store_piece(y + p.P + i, ob, n, p.stream);
-            } else {
-                const int i = c * V, n = 2 * p.P - i;
-                const auto v = load_piece(x + i, n);
-                float o[V];
+                    for (int j = 0; j < V; ++j) {
+                        const float2 w = cs[min(i + j, p.P - 1)];
+                        oa[j] = (float)va[j] * w.x - (float)vb[j] * w.y;
+                        ob[j] = (float)vb[j] * w.x + (float)va[j] * w.y;
+                    }
+                    store_piece(y + i, oa, n, p.stream);
+                    store_piece(y + p.P + i, ob, n, p.stream);
+                } else {
+                    const auto v = load_piece(x + i, n);
+                    float o[V];
 #pragma unroll
-                for (int j = 0; j < V; j += 2) {
-                    const float2 w = cs[min((i + j) / 2, p.P - 1)];
-                    o[j] = (float)v[j] * w.x - (float)v[j + 1] * w.y;
-                    o[j + 1] = (float)v[j + 1] * w.x + (float)v[j] * w.y;
+                    for (int j = 0; j < V; j += 2) {
+                        const int pair = (i + j) / 2;
+                        const float2 w = cs[min(pair, p.P - 1)];
+                        const float ra = (float)v[j] * w.x - (float)v[j + 1] * w.y;
+                        const float rb = (float)v[j + 1] * w.x + (float)v[j] * w.y;
+                        o[j] = pair < p.P ? ra : (float)v[j];
+                        o[j + 1] = pair < p.P ? rb : (float)v[j + 1];
+                    }
+                    store_piece(y + i, o, n, p.stream);
                 }
-                store_piece(y + i, o, n, p.stream);
             }
         }
     }
@@ -131,15 +141,20 @@ hipError_t launch_rotary(const RotaryArgs& a, bool back, hipStream_t stream) {
     p.P = a.pairs;
     p.per = a.pairs / a.axes;
     const bool half = a.layout == SPCONV_HALF;
-    p.turn = ((half ? a.pairs : 2 * a.pairs) + V - 1) / V;
-    p.rest = a.x == a.y ? 0 : (a.D - 2 * a.pairs + V - 1) / V;      // in place there is nothing to copy
+    // in place there is nothing to copy; interleaved pairs run on into it, where they can
+    const bool in_place = a.x == a.y, through = !half && !in_place && a.D % 2 == 0;
+    p.end = half ? a.pairs : through ? a.D : 2 * a.pairs;
+    p.turn = (p.end + V - 1) / V;
+    p.rest = in_place || through ? 0 : (a.D - 2 * a.pairs + V - 1) / V;
+    p.tx = 1;
+    while (p.tx < 64 && p.tx < p.turn) p.tx *= 2;
+    p.repeat = p.end >= V && p.turn <= p.tx;
     p.rows = std::max(1, std::min(kRotTable / a.pairs, 32));
     // few rows: over as many workgroups as there are rows
     p.rows = (int)std::max<int64_t>(1, std::min<int64_t>(p.rows, a.N / 512));
     p.gain = a.gain;
     p.sign = back ? -1.f : 1.f;
     p.heads_magic = a.H > 1 ? magic(a.H) : 0;
-    p.pieces_magic = p.turn + p.rest > 1 ? magic(p.turn + p.rest) : 0;
     p.stream = a.N * a.H * a.D * es > kStreamBytes;
     // (a launch's threads are counted in 32 bits: more rows take turns)
     const unsigned blocks = (unsigned)std::min<int64_t>((a.N + p.rows - 1) / p.rows, 1 << 20);
