@@ -602,12 +602,21 @@ def _call(name, dev, *args):
         _check(rc, name)
 
 
+_sizes = {}
+
+
 def _size(name, *args):
-    n = ctypes.c_size_t(0)
-    rc = getattr(_lib or load_library(), name)(*args, ctypes.byref(n))
-    if rc:
-        _check(rc, name)
-    return n.value
+    # (a function of its numbers alone: a loop's calls ask for the same ones)
+    size = _sizes.get((name, args))
+    if size is None:
+        n = ctypes.c_size_t(0)
+        rc = getattr(_lib or load_library(), name)(*args, ctypes.byref(n))
+        if rc:
+            _check(rc, name)
+        if len(_sizes) >= 1024:
+            _sizes.clear()
+        size = _sizes[name, args] = n.value
+    return size
 
 
 def _like(t, shape, dtype, device, name):
@@ -898,6 +907,8 @@ def _heads(t, name, like=None, shape=None):
 
 
 def _strides(*tensors):
+    if all([t.is_contiguous() for t in tensors]):
+        return None
     # (a contiguous tensor's strides along a dimension of one are anything)
     s = [n for t in tensors for n in ((t.shape[1] * t.shape[2], t.shape[2]) if t.is_contiguous()
                                       else (t.stride(0), t.stride(1)))]
@@ -944,7 +955,7 @@ def _rotary(name, x, positions, freqs, layout, gain, out):
         if out.stride(2) != 1:
             raise ValueError("out must have its last dimension contiguous")
     _call(name, dev, _at(x), _at(positions), positions.stride(0), _at(freqs.contiguous()), _at(out),
-          None if x.is_contiguous() and out.is_contiguous() else _strides(x, out), N, H, D, freqs.numel(), axes,
+          _strides(x, out), N, H, D, freqs.numel(), axes,
           _LAYOUTS[layout], gain, dt)
     return out
 
@@ -986,7 +997,7 @@ def _head_input(t):
 
 def _head_output(out, shape, like, name):
     if out is None:
-        return _torch.empty(shape, dtype=like.dtype, device=like.device)
+        return like.new_empty(shape)
     _heads(out, name, like, shape)
     if not _lies_well(out):
         raise ValueError(f"{name} must have contiguous heads that start at multiples of 16 bytes")

@@ -12,7 +12,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libspconv_mi355x.so")
 SOURCES = ["capi.hip", "nmap.hip", "forward.hip", "wgrad.hip", "norm.hip", "scan.hip", "glu.hip", "glu_rows.hip",
-           "rotary.hip", "group.hip", "attn.hip", "attn_grad.hip"]
+           "rotary.hip", "group.hip", "attn.hip", "attn_few.hip",
+           "attn_grad.hip"]
 ARCH = "gfx950"
 
 

@@ -44,14 +44,12 @@ struct AttnParams {
     float scale, scale2;        // of the scores; the same times log2 e
 };
 
-// What a call's sizes choose: the waves' share (KS, see attn.hip) and the parts
-// that the keys (or, in the keys' gradient, the queries) are split into.
-struct AttnPlan {
-    bool ks;
-    int splits;
-};
-AttnPlan attn_plan(const AttnArgs& a);
 AttnParams attn_params(const AttnArgs& a);
+// Few queries (attn_few.hip): rows of a workgroup.
+constexpr int kFewRows = 16;
+hipError_t launch_attn_few(const AttnParams& p, int dtype, hipStream_t st);
+// A query's sum from which its reference is taken again (see attn.hip).
+constexpr float kAttnMost = 0x1p64f;
 
 __device__ __forceinline__ f32x16_t mfma32(bf16x8r_t a, bf16x8r_t b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
@@ -104,16 +102,15 @@ __device__ __forceinline__ void find_keys(const AttnParams& p, Place& pl) {
     }
 }
 
-// A wave's 32 NB query rows, NB per lane (both halves), and the keys they see:
-// each lane's own first `limit`, at most `most` in the wave, and `least` to
-// `longest` over the workgroup.  Lanes past the sequence repeat its last row.
-template <int NB>
+// A wave's COLS query rows, one per column, and the keys they see: each its own
+// first `limit`, at most `most` in the wave, and `least` to `longest` over the
+// workgroup.  Columns past the sequence repeat its last row.
+template <int COLS = 32>
 struct QueryRows {
     Place pl;
-    int pos[NB], head[NB], limit[NB];
-    uint32_t row[NB];
-    int least, most, longest;
-    bool valid[NB];
+    int pos, head, limit, least, most, longest;
+    uint32_t row;
+    bool valid;
     // wave_row: the wave's first row in the tile of tq
     __device__ __forceinline__ bool find(const AttnParams& p, int tq, int wave_row, int hk, int64_t item) {
         pl = find_place(p.offsets, p.B, p.N, p.G, tq, item);
@@ -122,30 +119,26 @@ struct QueryRows {
         const int R = pl.Lq * p.G;
         // a causal sequence's long tiles first
         const int tile = p.causal ? (R - 1) / tq - pl.tile : pl.tile;
-        const int first = tile * tq + wave_row;
+        const int first = tile * tq + wave_row, mine = first + (threadIdx.x & (COLS - 1));
         const int past = pl.Lk - pl.Lq + 1;
         const auto sees = [&](int pos) { return p.causal ? min(max(pos + past, 0), pl.Lk) : pl.Lk; };
         const auto pos_of = [&](int r) { return split_row(min(r, R - 1), p.G, p.magic).pos; };
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            const int mine = first + 32 * n + (threadIdx.x & 31);
-            const RowHead rh = split_row(min(mine, R - 1), p.G, p.magic);
-            valid[n] = mine < R;
-            pos[n] = rh.pos;
-            head[n] = hk * p.G + rh.head;
-            row[n] = row_of(p.order, pl.q0 + rh.pos, p.N);
-            limit[n] = sees(rh.pos);
-        }
+        const RowHead rh = split_row(min(mine, R - 1), p.G, p.magic);
+        valid = mine < R;
+        pos = rh.pos;
+        head = hk * p.G + rh.head;
+        row = row_of(p.order, pl.q0 + rh.pos, p.N);
+        limit = sees(rh.pos);
         least = sees(pos_of(tile * tq));
-        most = first < R ? sees(pos_of(first + 32 * NB - 1)) : 0;
+        most = first < R ? sees(pos_of(first + COLS - 1)) : 0;
         longest = sees(pos_of(tile * tq + tq - 1));
         return true;
     }
-    __device__ __forceinline__ const uint8_t* at(const uint8_t* t, const int64_t (&s)[2], int n) const {
-        return t + row[n] * s[0] + head[n] * s[1];
+    __device__ __forceinline__ const uint8_t* at(const uint8_t* t, const int64_t (&s)[2]) const {
+        return t + row * s[0] + head * s[1];
     }
-    __device__ __forceinline__ uint8_t* at(uint8_t* t, const int64_t (&s)[2], int n) const {
-        return t + row[n] * s[0] + head[n] * s[1];
+    __device__ __forceinline__ uint8_t* at(uint8_t* t, const int64_t (&s)[2]) const {
+        return t + row * s[0] + head * s[1];
     }
 };
 
@@ -258,8 +251,11 @@ struct KeyStager {
                     rk[i] = fetch16(bk, r * (uint32_t)p.ks[0] + ok[i]);
                     rv[i] = fetch16(bv, r * (uint32_t)p.vs[0] + ov[i]);
                 } else {
-                    rk[i] = fetch16(k + r * p.ks[0] + ok[i], ok[i] != kNoUnit);
-                    rv[i] = fetch16(v + r * p.vs[0] + ov[i], ov[i] != kNoUnit);
+                    // (kept from being worked out ahead for all units: registers)
+                    uint32_t by = ok[i];
+                    asm volatile("" : "+v"(by));
+                    rk[i] = fetch16(k + r * p.ks[0] + by, by != kNoUnit);
+                    rv[i] = fetch16(v + r * p.vs[0] + by, by != kNoUnit);
                 }
             }
             return;
@@ -323,6 +319,8 @@ struct Operand<__bf16, DP> {
         if (d < D) f = *(const frag*)(src + 2 * d);
         return f;
     }
+    // whether step s has elements of D (fp32: its four instructions are 256 cycles)
+    static __device__ __forceinline__ bool wanted(int, int) { return true; }
     // values 8 c .. 8 c + 7 of a result as an operand, rounded
     static __device__ __forceinline__ frag pack(const f32x16_t& p, int c) {
         frag f;
@@ -384,6 +382,7 @@ struct Operand<float, DP> {
         if (d < D) f = *(const frag4*)(src + 4 * d);
         return f;
     }
+    static __device__ __forceinline__ bool wanted(int s, int D) { return 8 * s < D; }
     static __device__ __forceinline__ frag pack(const f32x16_t& p, int c) { return p[c]; }
     static __device__ __forceinline__ f32x16_t mma(frag4 a, frag4 b, f32x16_t c) {
 #pragma unroll
@@ -402,25 +401,31 @@ struct Operand<float, DP> {
     }
     static __device__ __forceinline__ frag only(frag f, int, bool mine) { return mine ? f : 0.f; }
 };
+template <typename T>
+__device__ __forceinline__ void store_four(uint8_t* p, f32x4r_t v, float f) {
+    typedef T vec __attribute__((ext_vector_type(4)));
+    vec o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = (T)(v[j] * f);
+    *(vec*)p = o;
+}
 // a row's operand has the type of along()
 template <typename T, int DP>
 using RowFrag = decltype(Operand<T, DP>::row((const uint8_t*)nullptr, 0, 0));
 
-// acc[n][dt] += (rows' transpose) x w[n] for 32 rows of a tile, w 32 x 32 results
+// acc[dt] += (rows' transpose) x w for 32 rows of a tile, w a 32 x 32 result
 // whose hidden entries (bit i of `seen` clear) are zero.  A zero times an infinite
 // or NaN element of the tile would still be NaN, so masked tiles multiply the
 // others only, and where there are some, these are added row by row, to the
 // columns that see the row.
-template <typename T, int DP, bool MASKED, int NB>
-__device__ __forceinline__ void add_rows(f32x16_t (&acc)[NB][DP / 32], const lds_u8* tile, int row0,
-                                         const f32x16_t (&w)[NB], const uint32_t (&seen)[NB]) {
+template <typename T, int DP, bool MASKED>
+__device__ __forceinline__ void add_rows(f32x16_t (&acc)[DP / 32], const lds_u8* tile, int row0, const f32x16_t& w,
+                                         uint32_t seen) {
     using O = Operand<T, DP>;
     bool some = false;
 #pragma unroll
     for (int c = 0; c < O::CROSS; ++c) {
-        typename O::frag b[NB];
-#pragma unroll
-        for (int n = 0; n < NB; ++n) b[n] = O::pack(w[n], c);
+        const auto b = O::pack(w, c);
 #pragma unroll
         for (int dt = 0; dt < DP / 32; ++dt) {
             auto a = O::across(tile, row0, c, dt);
@@ -429,31 +434,27 @@ __device__ __forceinline__ void add_rows(f32x16_t (&acc)[NB][DP / 32], const lds
                 some |= O::any(x);
                 a = O::without(a, x);
             }
-#pragma unroll
-            for (int n = 0; n < NB; ++n) acc[n][dt] = O::mma(a, b[n], acc[n][dt]);
+            acc[dt] = O::mma(a, b, acc[dt]);
         }
     }
     if (MASKED && __builtin_expect(__ballot(some) != 0, 0)) {
         const int h = (threadIdx.x >> 5) & 1;
+        // a column's two lane halves see different rows: ask the half that holds it
+        const uint32_t other = (uint32_t)__shfl_xor((int)seen, 32);
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            // a column's two lane halves see different rows: ask the half that holds it
-            const uint32_t other = (uint32_t)__shfl_xor((int)seen[n], 32);
-#pragma unroll
-            for (int c = 0; c < O::CROSS; ++c) {
-                const auto b = O::pack(w[n], c);
+        for (int c = 0; c < O::CROSS; ++c) {
+            const auto b = O::pack(w, c);
 #pragma unroll 1
-                for (int j = 0; j < 2 * O::ROWS; ++j) {
-                    const int half = j & 1, e = j >> 1;
-                    const bool see = ((h == half ? seen[n] : other) >> O::index(c, e)) & 1;
+            for (int j = 0; j < 2 * O::ROWS; ++j) {
+                const int half = j & 1, e = j >> 1;
+                const bool see = ((h == half ? seen : other) >> O::index(c, e)) & 1;
 #pragma unroll
-                    for (int dt = 0; dt < DP / 32; ++dt) {
-                        const auto x = O::only(O::bad(O::across(tile, row0, c, dt)), e, h == half);
-                        const f32x16_t t = O::mma(x, O::only(b, e, h == half), zero16());
+                for (int dt = 0; dt < DP / 32; ++dt) {
+                    const auto x = O::only(O::bad(O::across(tile, row0, c, dt)), e, h == half);
+                    const f32x16_t t = O::mma(x, O::only(b, e, h == half), zero16());
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[n][dt][i] += see ? t[i] : 0.f;
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
+                    for (int i = 0; i < 16; ++i) acc[dt][i] += see ? t[i] : 0.f;
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
@@ -468,11 +469,7 @@ __device__ __forceinline__ void store_col(uint8_t* row, const f32x16_t& v, float
     for (int i = 0; i < 4; ++i) {
         const int d = 32 * dt + 8 * i + 4 * h;
         if (d < D) {
-            typedef T vec __attribute__((ext_vector_type(4)));
-            vec o;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] = (T)(v[4 * i + j] * f);
-            *(vec*)(row + d * (int)sizeof(T)) = o;
+            store_four<T>(row + d * (int)sizeof(T), f32x4r_t{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]}, f);
         }
     }
 }

@@ -35,7 +35,7 @@ struct GradShape {
     static constexpr int WAVE = 4 * TILE + 2 * STATS;               // two buffers
     static constexpr int LDS = WAVE * (KS ? NW : 1);
     static constexpr int DQ_OCC = ES == 2 && DP == 32 ? 4 : DP <= 32 || (ES == 2 && DP == 64) ? 2 : 1;   // waves of a SIMD that registers are for
-    static constexpr int DKV_OCC = DP <= 64 ? 2 : 1;
+    static constexpr int DKV_OCC = DP <= 32 || (ES == 2 && DP == 64) ? 2 : 1;
 };
 
 // lse in powers of two; rows without keys: p = 2^-inf = 0
@@ -53,15 +53,15 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
     const int split = (int)(id % p.splits);
     const int hk = (int)(id / p.splits / p.items);
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6), h = lane >> 5;
-    QueryRows<1> qr;
+    QueryRows<> qr;
     if (!qr.find(p, S::TR, KS ? 0 : 32 * wave, hk, id / p.splits % p.items)) return;
     RowFrag<T, DP> qf[O::STEPS], df[O::STEPS];
     f32x16_t dd = zero16();
 #pragma unroll
     for (int s = 0; s < O::STEPS; ++s) {
-        qf[s] = O::row(qr.at(p.q, p.qs, 0), s, p.D);
-        df[s] = O::row(qr.at(p.dout, p.dos, 0), s, p.D);
-        dd = O::mma(O::row(qr.at((const uint8_t*)p.out, p.os, 0), s, p.D), df[s], dd);
+        qf[s] = O::row(qr.at(p.q, p.qs), s, p.D);
+        df[s] = O::row(qr.at(p.dout, p.dos), s, p.D);
+        dd = O::mma(O::row(qr.at((const uint8_t*)p.out, p.os), s, p.D), df[s], dd);
     }
     // the diagonal: row16(i, h) = lane & 31
     float delta = 0.f;
@@ -69,8 +69,8 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
     for (int i = 0; i < 16; ++i) delta = row16(i, h) == (lane & 31) ? dd[i] : delta;
     const float other = __shfl_xor(delta, 32);
     delta = ((lane >> 2) & 1) == h ? delta : other;
-    const float lse2 = stat2(p.lse[(int64_t)qr.row[0] * p.H + qr.head[0]]);
-    if (qr.valid[0] && h == 0 && split == 0 && (!KS || wave == 0)) p.delta[(int64_t)qr.row[0] * p.H + qr.head[0]] = delta;
+    const float lse2 = stat2(p.lse[(int64_t)qr.row * p.H + qr.head]);
+    if (qr.valid && h == 0 && split == 0 && (!KS || wave == 0)) p.delta[(int64_t)qr.row * p.H + qr.head] = delta;
 
     // where the sums of dout v start: -delta
     f32x16_t less;
@@ -84,9 +84,9 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
     lds_u8* buf = (lds_u8*)smem + (KS ? wave * S::WAVE : 0);
     KeyStager<T, DP, KT, KS ? 64 : 64 * NW> keys(p, qr.pl, hk, KS ? lane : t);
 
-    f32x16_t acc[1][NDT];
+    f32x16_t acc[NDT];
 #pragma unroll
-    for (int d = 0; d < NDT; ++d) acc[0][d] = zero16();
+    for (int d = 0; d < NDT; ++d) acc[d] = zero16();
 
     auto compute = [&](int tl, int b, auto masked) {
         constexpr bool MASKED = decltype(masked)::value;
@@ -94,24 +94,25 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
         const lds_u8* vt = kt + S::TILE;
 #pragma unroll
         for (int u = 0; u < KT / 32; ++u) {
-            f32x16_t s[1] = {zero16()}, dp = less;
+            f32x16_t s = zero16(), dp = less;
 #pragma unroll
             for (int c = 0; c < O::STEPS; ++c) {
-                s[0] = O::mma(O::along(kt, 32 * u, c), qf[c], s[0]);
+                if (!O::wanted(c, p.D)) continue;
+                s = O::mma(O::along(kt, 32 * u, c), qf[c], s);
                 dp = O::mma(O::along(vt, 32 * u, c), df[c], dp);
             }
-            uint32_t seen[1] = {0xFFFFu};
+            uint32_t seen = 0xFFFFu;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float e = __builtin_amdgcn_exp2f(fmaf(s[0][i], p.scale2, -lse2));
-                s[0][i] = e * dp[i];
+                const float e = __builtin_amdgcn_exp2f(fmaf(s[i], p.scale2, -lse2));
+                s[i] = e * dp[i];
                 if constexpr (MASKED) {
-                    const bool see = tl * KT + 32 * u + row16(i, h) < qr.limit[0];
-                    seen[0] = see ? seen[0] : seen[0] & ~(1u << i);
-                    s[0][i] = see ? s[0][i] : 0.f;
+                    const bool see = tl * KT + 32 * u + row16(i, h) < qr.limit;
+                    seen = see ? seen : seen & ~(1u << i);
+                    s[i] = see ? s[i] : 0.f;
                 }
             }
-            add_rows<T, DP, MASKED, 1>(acc, kt, 32 * u, s, seen);
+            add_rows<T, DP, MASKED>(acc, kt, 32 * u, s, seen);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
 #pragma unroll
             for (int d = 0; d < NDT; ++d)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) mine[(32 * d + row16(i, h)) * 32 + (lane & 31)] = acc[0][d][i];
+                for (int i = 0; i < 16; ++i) mine[(32 * d + row16(i, h)) * 32 + (lane & 31)] = acc[d][i];
         }
         __syncthreads();
         if (wave > 0) return;
@@ -156,21 +157,21 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
 #pragma unroll
             for (int d = 0; d < NDT; ++d)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) acc[0][d][i] += o[(32 * d + row16(i, h)) * 32 + (lane & 31)];
+                for (int i = 0; i < 16; ++i) acc[d][i] += o[(32 * d + row16(i, h)) * 32 + (lane & 31)];
         }
     }
-    if (!qr.valid[0]) return;
+    if (!qr.valid) return;
     // (the weight of a single key is 1, whatever its score)
-    const float scale = qr.limit[0] > 1 ? p.scale : 0.f;
+    const float scale = qr.limit > 1 ? p.scale : 0.f;
     if (p.splits > 1) {
-        float* o = p.part + ((split * p.N + qr.pl.q0 + qr.pos[0]) * p.H + qr.head[0]) * p.D;
+        float* o = p.part + ((split * p.N + qr.pl.q0 + qr.pos) * p.H + qr.head) * p.D;
 #pragma unroll
-        for (int d = 0; d < NDT; ++d) store_col<float>((uint8_t*)o, acc[0][d], scale, d, p.D);
+        for (int d = 0; d < NDT; ++d) store_col<float>((uint8_t*)o, acc[d], scale, d, p.D);
         return;
     }
-    uint8_t* o = qr.at(p.dq, p.dqs, 0);
+    uint8_t* o = qr.at(p.dq, p.dqs);
 #pragma unroll
-    for (int d = 0; d < NDT; ++d) store_col<T>(o, acc[0][d], scale, d, p.D);
+    for (int d = 0; d < NDT; ++d) store_col<T>(o, acc[d], scale, d, p.D);
 }
 
 template <typename T, int DP, bool KS>
@@ -301,9 +302,9 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
         }
     };
 
-    f32x16_t dk[1][NDT], dv[1][NDT];
+    f32x16_t dk[NDT], dv[NDT];
 #pragma unroll
-    for (int d = 0; d < NDT; ++d) dk[0][d] = dv[0][d] = zero16();
+    for (int d = 0; d < NDT; ++d) dk[d] = dv[d] = zero16();
 
     auto compute = [&](int tl, int b, auto masked) {
         constexpr bool MASKED = decltype(masked)::value;
@@ -312,29 +313,30 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
 #pragma unroll
         for (int u = 0; u < KT / 32; ++u) {
             const float* l2 = stats + b * 2 * KT + 32 * u;
-            f32x16_t s[1] = {zero16()}, dp[1];
+            f32x16_t s = zero16(), dp;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) dp[0][i] = l2[KT + row16(i, h)];
+            for (int i = 0; i < 16; ++i) dp[i] = l2[KT + row16(i, h)];
 #pragma unroll
             for (int c = 0; c < O::STEPS; ++c) {
-                s[0] = O::mma(O::along(qt, 32 * u, c), kf[c], s[0]);
-                dp[0] = O::mma(O::along(dt, 32 * u, c), vf[c], dp[0]);
+                if (!O::wanted(c, p.D)) continue;
+                s = O::mma(O::along(qt, 32 * u, c), kf[c], s);
+                dp = O::mma(O::along(dt, 32 * u, c), vf[c], dp);
             }
-            uint32_t seen[1] = {0xFFFFu};
+            uint32_t seen = 0xFFFFu;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float e = __builtin_amdgcn_exp2f(fmaf(s[0][i], p.scale2, -l2[row16(i, h)]));
-                dp[0][i] *= e;
-                s[0][i] = e;
+                const float e = __builtin_amdgcn_exp2f(fmaf(s[i], p.scale2, -l2[row16(i, h)]));
+                dp[i] *= e;
+                s[i] = e;
                 if constexpr (MASKED) {
                     const bool see = tl * KT + 32 * u + row16(i, h) >= from;
-                    seen[0] = see ? seen[0] : seen[0] & ~(1u << i);
-                    s[0][i] = see ? s[0][i] : 0.f;
-                    dp[0][i] = see ? dp[0][i] : 0.f;
+                    seen = see ? seen : seen & ~(1u << i);
+                    s[i] = see ? s[i] : 0.f;
+                    dp[i] = see ? dp[i] : 0.f;
                 }
             }
-            add_rows<T, DP, MASKED, 1>(dv, dt, 32 * u, s, seen);
-            add_rows<T, DP, MASKED, 1>(dk, qt, 32 * u, dp, seen);
+            add_rows<T, DP, MASKED>(dv, dt, 32 * u, s, seen);
+            add_rows<T, DP, MASKED>(dk, qt, 32 * u, dp, seen);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -372,8 +374,8 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
             for (int d = 0; d < NDT; ++d)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    mine[(32 * d + row16(i, h)) * 32 + (lane & 31)] = dk[0][d][i];
-                    mine[(DP + 32 * d + row16(i, h)) * 32 + (lane & 31)] = dv[0][d][i];
+                    mine[(32 * d + row16(i, h)) * 32 + (lane & 31)] = dk[d][i];
+                    mine[(DP + 32 * d + row16(i, h)) * 32 + (lane & 31)] = dv[d][i];
                 }
         }
         __syncthreads();
@@ -384,8 +386,8 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
             for (int d = 0; d < NDT; ++d)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    dk[0][d][i] += o[(32 * d + row16(i, h)) * 32 + (lane & 31)];
-                    dv[0][d][i] += o[(DP + 32 * d + row16(i, h)) * 32 + (lane & 31)];
+                    dk[d][i] += o[(32 * d + row16(i, h)) * 32 + (lane & 31)];
+                    dv[d][i] += o[(DP + 32 * d + row16(i, h)) * 32 + (lane & 31)];
                 }
         }
     }
@@ -396,15 +398,15 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
         const int64_t all = p.splits * p.M * p.HK * p.D;
 #pragma unroll
         for (int d = 0; d < NDT; ++d) {
-            store_col<float>((uint8_t*)o, dk[0][d], scale, d, p.D);
-            store_col<float>((uint8_t*)(o + all), dv[0][d], 1.f, d, p.D);
+            store_col<float>((uint8_t*)o, dk[d], scale, d, p.D);
+            store_col<float>((uint8_t*)(o + all), dv[d], 1.f, d, p.D);
         }
         return;
     }
 #pragma unroll
     for (int d = 0; d < NDT; ++d) {
-        store_col<T>(p.dk + krow * p.dks[0] + hk * p.dks[1], dk[0][d], scale, d, p.D);
-        store_col<T>(p.dv + krow * p.dvs[0] + hk * p.dvs[1], dv[0][d], 1.f, d, p.D);
+        store_col<T>(p.dk + krow * p.dks[0] + hk * p.dks[1], dk[d], scale, d, p.D);
+        store_col<T>(p.dv + krow * p.dvs[0] + hk * p.dvs[1], dv[d], 1.f, d, p.D);
     }
 }
 
@@ -429,11 +431,15 @@ __global__ void __launch_bounds__(256) k_attn_sum(const float* part, int splits,
     *(vec*)(out + row_of(order, pos, n) * rs + e / quads % heads * hs + e % quads * 4 * (int)sizeof(T)) = r;
 }
 
+struct Plan {
+    bool ks;
+    int splits;
+};
 // A gradient kernel owns rows (queries or keys) of one axis and sums over the
 // other: the waves' share and the splits from both axes' sizes.
-AttnPlan side_plan(int64_t n, int64_t per, int64_t B, int64_t HK, int64_t along) {
+Plan side_plan(int64_t n, int64_t per, int64_t B, int64_t HK, int64_t along) {
     const int64_t seqs = std::max<int64_t>(1, std::min(B, n));
-    AttnPlan r;
+    Plan r;
     const int64_t shared = attn_places(n, per, 128, seqs) * HK;
     r.ks = n * per / seqs <= 32 || shared < 256;
     const int64_t blocks = std::max<int64_t>(1, r.ks ? attn_places(n, per, 32, seqs) * HK : shared);
@@ -442,10 +448,10 @@ AttnPlan side_plan(int64_t n, int64_t per, int64_t B, int64_t HK, int64_t along)
     if (attn_places(n, per, 32, B) * HK * r.splits > (1 << 20)) r.splits = 1;     // (many empty sequences)
     return r;
 }
-AttnPlan dq_plan(const AttnArgs& a) {
+Plan dq_plan(const AttnArgs& a) {
     return side_plan(a.N, a.H / a.HK, a.B, a.HK, a.M / std::max<int64_t>(1, std::min<int64_t>(a.B, a.M)));
 }
-AttnPlan dkv_plan(const AttnArgs& a) {
+Plan dkv_plan(const AttnArgs& a) {
     return side_plan(a.M, 1, a.B, a.HK, a.N * (a.H / a.HK) / std::max<int64_t>(1, std::min<int64_t>(a.B, a.N)));
 }
 size_t delta_bytes(const AttnArgs& a) { return align_up((size_t)a.N * a.H * 4, 256); }
@@ -482,14 +488,14 @@ hipError_t grad_width(const AttnArgs& a, AttnParams p, hipStream_t st) {
     };
     hipError_t e = hipSuccess;
     if (p.N > 0) {
-        const AttnPlan r = dq_plan(a);
+        const Plan r = dq_plan(a);
         p.splits = r.splits;
         e = r.ks ? dq_go<T, DP, true>(p, st) : dq_go<T, DP, false>(p, st);
         if (e == hipSuccess && r.splits > 1) e = sum(p.part, p.offsets, p.order, p.N, p.H, p.dq, p.dqs);
         if (e != hipSuccess) return e;
     }
     if (p.M > 0) {
-        const AttnPlan r = dkv_plan(a);
+        const Plan r = dkv_plan(a);
         p.splits = r.splits;
         e = r.ks ? dkv_go<T, DP, true>(p, st) : dkv_go<T, DP, false>(p, st);
         if (e == hipSuccess && r.splits > 1) {
@@ -514,7 +520,7 @@ hipError_t grad_type(const AttnArgs& a, const AttnParams& p, hipStream_t st) {
 }  // namespace
 
 size_t attn_grad_workspace_bytes(const AttnArgs& a) {
-    const AttnPlan q = dq_plan(a), k = dkv_plan(a);
+    const Plan q = dq_plan(a), k = dkv_plan(a);
     size_t part = 0;
     if (q.splits > 1) part = (size_t)q.splits * a.N * a.H * a.D * 4;
     if (k.splits > 1) part = std::max(part, (size_t)k.splits * a.M * a.HK * a.D * 8);
