@@ -151,22 +151,23 @@ __device__ __forceinline__ int64_t xcd_order(int64_t id) {
 }
 inline int64_t xcd_blocks(int64_t n) { return (n + kXcds * kRun - 1) / (kXcds * kRun) * (kXcds * kRun); }
 
-// A tile of ROWS rows of DP elements in LDS, in 16-byte units.  Units of a row
-// are permuted so that both ways of reading are free of bank conflicts: eight
-// consecutive rows' unit u (the operand along the row) lie on eight different
-// bank groups, and so do the unit pairs of four consecutive rows (the
-// transposing read).
+// A tile of rows of DP elements in LDS, in 16-byte units.  Units of a row are
+// permuted so that both ways of reading are free of bank conflicts (banks repeat
+// after 256 bytes, which 16 lanes' units or 32 lanes' half units fill): 16
+// consecutive rows' unit u (the operand along the row) lie on 16 different
+// units of the banks, and so do the four units side by side of four
+// consecutive rows (the transposing read).
 template <typename T, int DP>
 struct Tile {
     static constexpr int E = 16 / sizeof(T);        // elements per unit
     static constexpr int U = DP / E;                // units per row
     static constexpr int ROWB = DP * (int)sizeof(T);
-    static constexpr bool WIDE = U % 8 == 0;        // a row is whole turns of the banks
+    static constexpr bool WIDE = U % 8 == 0;        // a row is whole halves of the banks
     static __device__ __forceinline__ int key(int row) {
         if constexpr (WIDE)
-            return ((row & 3) << 1) | ((row >> 2) & 1);
+            return (((row >> 1) & 1) << 2) | (((row >> 2) & 1) << 1) | ((row >> 3) & 1);
         else
-            return (((row >> 1) & 1) << 1) | ((row >> 2) & 1);
+            return (row >> 2) & 3;
     }
     static __device__ __forceinline__ int at(int row, int unit) { return row * ROWB + ((unit ^ key(row)) << 4); }
 };
@@ -305,11 +306,11 @@ struct Operand<__bf16, DP> {
     }
     static __device__ __forceinline__ frag across(const lds_u8* tile, int row0, int c, int dt) {
         const int l = threadIdx.x & 63, a = l & 15, h = l >> 5;
-        const int row = 4 * h + (a >> 2);                     // and 8 rows on, whose key is the same
+        const int row = 4 * h + (a >> 2);
         const int unit = 4 * dt + 2 * ((l >> 4) & 1) + ((a & 3) >> 1);
-        const lds_u8* p = tile + (row0 + 16 * c) * L::ROWB + L::at(row, unit) + 8 * (a & 1);
-        const bf16x4a_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4a_t*)p);
-        const bf16x4a_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4a_t*)(p + 8 * L::ROWB));
+        const lds_u8* p = tile + (row0 + 16 * c) * L::ROWB + 8 * (a & 1);
+        const bf16x4a_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4a_t*)(p + L::at(row, unit)));
+        const bf16x4a_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4a_t*)(p + L::at(row + 8, unit)));
         return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
     // the lane's operand for column row `src` (elements 16 s + 8 h ..)

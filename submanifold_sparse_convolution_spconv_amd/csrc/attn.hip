@@ -92,21 +92,24 @@ __global__ void __launch_bounds__((64 * FwdShape<T, DP>::NW), (FwdShape<T, DP>::
         base = ref == -INFINITY ? 0.f : S::ES == 4 ? ref : ref * p.scale2;
     };
     const auto compute = [&](int tl, int b, auto masked) {
+        // the next 32 keys' scores under the exponentials of these
+        uint32_t seen[NSUB];
+        f32x16_t s[NSUB];
+        s[0] = scores(tl, b, 0, masked, seen[0]);
 #pragma unroll
         for (int u = 0; u < NSUB; ++u) {
-            uint32_t seen;
-            f32x16_t s = scores(tl, b, u, masked, seen);
+            if (u + 1 < NSUB) s[u + 1] = scores(tl, b, u + 1, masked, seen[u + 1]);
             float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 // fp32: the reference's own weight is 1 to the bit, so that one key's
                 // value comes out as it is; in bf16 the rounding sees to that
-                s[i] = __builtin_amdgcn_exp2f(S::ES == 4 ? (s[i] - base) * p.scale2 : fmaf(s[i], p.scale2, -base));
-                part[i & 3] += s[i];
+                s[u][i] = __builtin_amdgcn_exp2f(S::ES == 4 ? (s[u][i] - base) * p.scale2
+                                                            : fmaf(s[u][i], p.scale2, -base));
+                part[i & 3] += s[u][i];
             }
             sum += (part[0] + part[1]) + (part[2] + part[3]);
-            add_rows<T, DP, decltype(masked)::value>(acc, buf + b * 2 * S::TILE + S::TILE, 32 * u, s, seen);
-            __builtin_amdgcn_sched_barrier(0);
+            add_rows<T, DP, decltype(masked)::value>(acc, buf + b * 2 * S::TILE + S::TILE, 32 * u, s[u], seen[u]);
         }
     };
 
