@@ -245,19 +245,24 @@ struct KeyStager {
     __device__ __forceinline__ void fetch(int tile) {
         if (p.korder) {
             const auto bk = rows_at(k), bv = rows_at(v);
+            const uint32_t last = (uint32_t)p.M - 1;
+            if (p.near) {
 #pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                const uint32_t r = min((uint32_t)row[i], (uint32_t)p.M - 1);
-                if (p.near) {
+                for (int i = 0; i < NP; ++i) {
+                    const uint32_t r = min((uint32_t)row[i], last);
                     rk[i] = fetch16(bk, r * (uint32_t)p.ks[0] + ok[i]);
                     rv[i] = fetch16(bv, r * (uint32_t)p.vs[0] + ov[i]);
-                } else {
-                    // (kept from being worked out ahead for all units: registers)
-                    uint32_t by = ok[i];
-                    asm volatile("" : "+v"(by));
-                    rk[i] = fetch16(k + r * p.ks[0] + by, by != kNoUnit);
-                    rv[i] = fetch16(v + r * p.vs[0] + by, by != kNoUnit);
                 }
+                return;
+            }
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const uint32_t r = min((uint32_t)row[i], last);
+                // (kept from being worked out ahead for all units: registers)
+                uint32_t by = ok[i];
+                asm volatile("" : "+v"(by));
+                rk[i] = fetch16(k + r * p.ks[0] + by, by != kNoUnit);
+                rv[i] = fetch16(v + r * p.vs[0] + by, by != kNoUnit);
             }
             return;
         }
