@@ -91,7 +91,7 @@ def main():
     a.add_argument("--heads", type=int, default=4)
     a.add_argument("--run", type=int, default=1024, help="voxels that attend to each other")
     a.add_argument("--steps", type=int, default=10)
-    a.add_argument("--lr", type=float, default=0.05)
+    a.add_argument("--lr", type=float, default=0.0005)
     a = a.parse_args()
     wl = W.by_name(a.workload)
     coords = torch.from_numpy(W.geometry(wl)).cuda()

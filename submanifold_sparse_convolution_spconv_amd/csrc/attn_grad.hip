@@ -34,8 +34,8 @@ struct GradShape {
     static constexpr int STATS = 2 * KT * 4;                        // lse and delta of a tile of queries
     static constexpr int WAVE = 4 * TILE + 2 * STATS;               // two buffers
     static constexpr int LDS = WAVE * (KS ? NW : 1);
-    static constexpr int DQ_OCC = ES == 2 && DP == 32 ? 4 : DP <= 32 || (ES == 2 && DP == 64) ? 2 : 1;   // waves of a SIMD that registers are for
-    static constexpr int DKV_OCC = DP <= 32 || (ES == 2 && DP == 64) ? 2 : 1;
+    static constexpr int DQ_OCC = ES == 2 && DP == 32 ? 4 : DP <= 32 || (DP == 64 && (ES == 2 || !KS)) ? 2 : 1;   // waves of a SIMD that registers are for
+    static constexpr int DKV_OCC = DP <= 32 || (DP == 64 && (ES == 2 || !KS)) ? 2 : 1;
 };
 
 // lse in powers of two; rows without keys: p = 2^-inf = 0
@@ -411,24 +411,28 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
 }
 
 // Sums of the splits' parts in their order: four elements of a (position, head)
-// per thread.
+// per thread.  A second tensor's parts (dv next to dk) follow the first's.
+struct SumOut {
+    uint8_t* t;
+    int64_t rs, hs;        // bytes from row to row and from head to head
+};
 template <typename T>
 __global__ void __launch_bounds__(256) k_attn_sum(const float* part, int splits, const int32_t* offsets, int B,
-                                                  const int32_t* order, int64_t n, int heads, int D, uint8_t* out,
-                                                  int64_t rs, int64_t hs) {
+                                                  const int32_t* order, int64_t n, int heads, int D, SumOut out0,
+                                                  SumOut out1) {
     const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x, quads = D / 4, all = n * heads * quads;
     if (e >= all) return;
     const int64_t pos = e / quads / heads;
     const int64_t begin = clamp_to(offsets[0], 0, n);
     if (pos < begin || pos >= clamp_to(offsets[B], begin, n)) return;
+    const SumOut out = blockIdx.y ? out1 : out0;
+    part += blockIdx.y * splits * all * 4;
     f32x4r_t s = {};
 #pragma unroll 8
     for (int k = 0; k < splits; ++k) s += *(const f32x4r_t*)(part + 4 * (k * all + e));
-    typedef T vec __attribute__((ext_vector_type(4)));
-    vec r;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r[j] = (T)s[j];
-    *(vec*)(out + row_of(order, pos, n) * rs + e / quads % heads * hs + e % quads * 4 * (int)sizeof(T)) = r;
+    store_four<T>(out.t + row_of(order, pos, n) * out.rs + e / quads % heads * out.hs +
+                      e % quads * 4 * (int)sizeof(T),
+                  s, 1.f);
 }
 
 struct Plan {
@@ -436,14 +440,16 @@ struct Plan {
     int splits;
 };
 // A gradient kernel owns rows (queries or keys) of one axis and sums over the
-// other: the waves' share and the splits from both axes' sizes.
+// other: the waves' share and the splits from both axes' sizes.  Waves that take
+// turns serve few rows only (4,097 rows of 2 heads in fp32, keys' gradient: 219
+// us, 156 with rows of their own and the queries in parts).
 Plan side_plan(int64_t n, int64_t per, int64_t B, int64_t HK, int64_t along) {
     const int64_t seqs = std::max<int64_t>(1, std::min(B, n));
     Plan r;
     const int64_t shared = attn_places(n, per, 128, seqs) * HK;
-    r.ks = n * per / seqs <= 32 || shared < 256;
+    r.ks = n * per / seqs <= 32 || shared < 64;
     const int64_t blocks = std::max<int64_t>(1, r.ks ? attn_places(n, per, 32, seqs) * HK : shared);
-    const int64_t splits = blocks >= 512 ? 1 : std::min((1024 + blocks - 1) / blocks, along / 512);
+    const int64_t splits = blocks >= 512 ? 1 : std::min((2048 + blocks - 1) / blocks, along / 128);
     r.splits = (int)std::max<int64_t>(1, std::min<int64_t>(splits, 256));
     if (attn_places(n, per, 32, B) * HK * r.splits > (1 << 20)) r.splits = 1;     // (many empty sequences)
     return r;
@@ -479,11 +485,10 @@ hipError_t dkv_go(AttnParams p, hipStream_t st) {
 
 template <typename T, int DP>
 hipError_t grad_width(const AttnArgs& a, AttnParams p, hipStream_t st) {
-    const auto sum = [&](const float* part, const int32_t* offs, const int32_t* order, int64_t n, int heads,
-                         uint8_t* out, const int64_t(&s)[2]) {
+    const auto sum = [&](const int32_t* offs, const int32_t* order, int64_t n, int heads, SumOut a, SumOut b) {
         const int64_t quads = n * heads * (p.D / 4);
-        k_attn_sum<T><<<(unsigned)((quads + 255) / 256), 256, 0, st>>>(part, p.splits, offs, p.B, order, n, heads, p.D,
-                                                                     out, s[0], s[1]);
+        k_attn_sum<T><<<dim3((unsigned)((quads + 255) / 256), b.t ? 2 : 1), 256, 0, st>>>(
+            p.part, p.splits, offs, p.B, order, n, heads, p.D, a, b);
         return hipGetLastError();
     };
     hipError_t e = hipSuccess;
@@ -491,19 +496,17 @@ hipError_t grad_width(const AttnArgs& a, AttnParams p, hipStream_t st) {
         const Plan r = dq_plan(a);
         p.splits = r.splits;
         e = r.ks ? dq_go<T, DP, true>(p, st) : dq_go<T, DP, false>(p, st);
-        if (e == hipSuccess && r.splits > 1) e = sum(p.part, p.offsets, p.order, p.N, p.H, p.dq, p.dqs);
+        if (e == hipSuccess && r.splits > 1)
+            e = sum(p.offsets, p.order, p.N, p.H, {p.dq, p.dqs[0], p.dqs[1]}, {});
         if (e != hipSuccess) return e;
     }
     if (p.M > 0) {
         const Plan r = dkv_plan(a);
         p.splits = r.splits;
         e = r.ks ? dkv_go<T, DP, true>(p, st) : dkv_go<T, DP, false>(p, st);
-        if (e == hipSuccess && r.splits > 1) {
-            const int32_t* offs = p.koffsets ? p.koffsets : p.offsets;
-            e = sum(p.part, offs, p.korder, p.M, p.HK, p.dk, p.dks);
-            if (e == hipSuccess)
-                e = sum(p.part + r.splits * p.M * p.HK * p.D, offs, p.korder, p.M, p.HK, p.dv, p.dvs);
-        }
+        if (e == hipSuccess && r.splits > 1)
+            e = sum(p.koffsets ? p.koffsets : p.offsets, p.korder, p.M, p.HK, {p.dk, p.dks[0], p.dks[1]},
+                    {p.dv, p.dvs[0], p.dvs[1]});
     }
     return e;
 }
