@@ -334,6 +334,13 @@ struct Operand<__bf16, DP> {
         for (int j = 0; j < 8; ++j) f[j] = (__bf16)p[8 * c + j];
         return f;
     }
+    // what that rounding left out, as an operand
+    static __device__ __forceinline__ frag pack_rest(const f32x16_t& p, frag b, int c) {
+        frag f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = (__bf16)(p[8 * c + j] - (float)b[j]);
+        return f;
+    }
     static __device__ __forceinline__ f32x16_t mma(frag a, frag b, f32x16_t c) { return mfma32(a, b, c); }
     // the rows that the lane's element j of instruction c stands for
     static constexpr int ROWS = 8;
@@ -423,8 +430,8 @@ using RowFrag = decltype(Operand<T, DP>::row((const uint8_t*)nullptr, 0, 0));
 // whose hidden entries (bit i of `seen` clear) are zero.  A zero times an infinite
 // or NaN element of the tile would still be NaN, so masked tiles multiply the
 // others only, and where there are some, these are added row by row, to the
-// columns that see the row.
-template <typename T, int DP, bool MASKED>
+// columns that see the row.  FINE (bf16): w in two parts, rounded and rest.
+template <typename T, int DP, bool MASKED, bool FINE = false>
 __device__ __forceinline__ void add_rows(f32x16_t (&acc)[DP / 32], const lds_u8* tile, int row0, const f32x16_t& w,
                                          uint32_t seen) {
     using O = Operand<T, DP>;
@@ -441,6 +448,7 @@ __device__ __forceinline__ void add_rows(f32x16_t (&acc)[DP / 32], const lds_u8*
                 a = O::without(a, x);
             }
             acc[dt] = O::mma(a, b, acc[dt]);
+            if constexpr (FINE) acc[dt] = O::mma(a, O::pack_rest(w, b, c), acc[dt]);
         }
     }
     if (MASKED && __builtin_expect(__ballot(some) != 0, 0)) {

@@ -10,8 +10,17 @@
 // over the heads that share them).  Each computes p and ds again: 7 products
 // where 5 are needed, against atomics in dq.  As in the forward the results of
 // the first products are the operands of the next as they lie in the
-// registers: (key, query) tiles for dq, (query, key) tiles for dk and dv; p
-// and ds are rounded to bf16 there, all sums are fp32.
+// registers: (key, query) tiles for dq, (query, key) tiles for dk and dv; all
+// sums are fp32.
+//
+// In bf16, p and ds are rounded once as operands, which is as much again as the
+// results' own rounding (2.4e-3 of a gradient's norm in all, 1.7e-3 without).
+// delta suffers from the rounding of out, little where a query sees many keys, but
+// where it sees a few dout v - delta cancels (two keys, causal: 1.0e-2).  So a
+// tile of queries that see kFineKeys at most works out delta = sum_j p dout v from
+// the keys first, and ds and p, also of the keys of such sequences, are taken in two
+// parts: their gradients are then off by the results' rounding only, for a third more
+// time (120 causal runs of 250, 4 heads on 2 of 64: 92 -> 123 us).
 #include "attn.h"
 
 #include <algorithm>
@@ -20,6 +29,7 @@ namespace spc {
 
 namespace {
 
+constexpr int kFineKeys = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // KS: the waves of a workgroup take turns at the long axis for 32 rows instead
@@ -70,14 +80,9 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
     const float other = __shfl_xor(delta, 32);
     delta = ((lane >> 2) & 1) == h ? delta : other;
     const float lse2 = stat2(p.lse[(int64_t)qr.row * p.H + qr.head]);
-    if (qr.valid && h == 0 && split == 0 && (!KS || wave == 0)) p.delta[(int64_t)qr.row * p.H + qr.head] = delta;
-
-    // where the sums of dout v start: -delta
-    f32x16_t less;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) less[i] = -delta;
 
     const int nt = (qr.longest + KT - 1) / KT;
+    const bool fine = S::ES == 2 && qr.longest <= kFineKeys;
     const int t0 = (int)((int64_t)nt * split / p.splits), t1 = (int)((int64_t)nt * (split + 1) / p.splits);
     constexpr int STEP = KS ? NW : 1;
     const int begin = t0 + (KS ? wave : 0);
@@ -88,58 +93,106 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
 #pragma unroll
     for (int d = 0; d < NDT; ++d) acc[d] = zero16();
 
-    auto compute = [&](int tl, int b, auto masked) {
-        constexpr bool MASKED = decltype(masked)::value;
+    // where the sums of dout v start: -delta
+    f32x16_t less;
+    const auto probabilities = [&](int tl, int b, int u, auto masked, f32x16_t& e, f32x16_t& dp, uint32_t& seen) {
         const lds_u8* kt = buf + b * 2 * S::TILE;
         const lds_u8* vt = kt + S::TILE;
+        e = zero16();
+        dp = less;
+#pragma unroll
+        for (int c = 0; c < O::STEPS; ++c) {
+            if (!O::wanted(c, p.D)) continue;
+            e = O::mma(O::along(kt, 32 * u, c), qf[c], e);
+            dp = O::mma(O::along(vt, 32 * u, c), df[c], dp);
+        }
+        seen = 0xFFFFu;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            e[i] = __builtin_amdgcn_exp2f(fmaf(e[i], p.scale2, -lse2));
+            if constexpr (decltype(masked)::value) {
+                const bool see = tl * KT + 32 * u + row16(i, h) < qr.limit;
+                seen = see ? seen : seen & ~(1u << i);
+                e[i] = see ? e[i] : 0.f;
+                dp[i] = see ? dp[i] : 0.f;
+            }
+        }
+    };
+    const auto compute = [&](int tl, int b, auto masked, auto two) {
 #pragma unroll
         for (int u = 0; u < KT / 32; ++u) {
-            f32x16_t s = zero16(), dp = less;
+            uint32_t seen;
+            f32x16_t e, dp;
+            probabilities(tl, b, u, masked, e, dp, seen);
 #pragma unroll
-            for (int c = 0; c < O::STEPS; ++c) {
-                if (!O::wanted(c, p.D)) continue;
-                s = O::mma(O::along(kt, 32 * u, c), qf[c], s);
-                dp = O::mma(O::along(vt, 32 * u, c), df[c], dp);
-            }
-            uint32_t seen = 0xFFFFu;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float e = __builtin_amdgcn_exp2f(fmaf(s[i], p.scale2, -lse2));
-                s[i] = e * dp[i];
-                if constexpr (MASKED) {
-                    const bool see = tl * KT + 32 * u + row16(i, h) < qr.limit;
-                    seen = see ? seen : seen & ~(1u << i);
-                    s[i] = see ? s[i] : 0.f;
-                }
-            }
-            add_rows<T, DP, MASKED>(acc, kt, 32 * u, s, seen);
+            for (int i = 0; i < 16; ++i) e[i] *= dp[i];
+            add_rows<T, DP, decltype(masked)::value, decltype(two)::value>(acc, buf + b * 2 * S::TILE, 32 * u, e, seen);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
 
-    if (begin < t1) {
-        keys.look_up(begin);
-        keys.fetch(begin);
-        keys.store(buf);
-        keys.look_up(begin + STEP);
-    }
-    wait_loads();
-    next_tile<KS>();
-    // tiles that every query sees whole, then those that some do not
-    int b = 0, tl = begin;
-    const auto sweep = [&](int end, auto masked) {
-        for (; tl < end; tl += STEP, b ^= 1) {
-            if (tl + STEP < t1) {
-                keys.fetch(tl + STEP);
-                keys.look_up(tl + 2 * STEP);
-            }
-            if (tl * KT < qr.most) compute(tl, b, masked);
-            if (tl + STEP < t1) keys.store(buf + (b ^ 1) * 2 * S::TILE);
-            next_tile<KS>();
+    // the tiles from `from` on
+    const auto sweep = [&](int from, int to, int whole, auto each, auto rest) {
+        if (from < to) {
+            keys.look_up(from);
+            keys.fetch(from);
+            keys.store(buf);
+            keys.look_up(from + STEP);
         }
+        wait_loads();
+        next_tile<KS>();
+        int b = 0, tl = from;
+        const auto run = [&](int end, auto f) {
+            for (; tl < end; tl += STEP, b ^= 1) {
+                if (tl + STEP < to) {
+                    keys.fetch(tl + STEP);
+                    keys.look_up(tl + 2 * STEP);
+                }
+                if (tl * KT < qr.most) f(tl, b);
+                if (tl + STEP < to) keys.store(buf + (b ^ 1) * 2 * S::TILE);
+                next_tile<KS>();
+            }
+        };
+        run(min(to, whole), each);
+        run(to, rest);
     };
-    sweep(min(t1, qr.least / KT), std::false_type{});
-    sweep(t1, std::true_type{});
+    const auto none = [](int, int) {};
+    if constexpr (S::ES == 2)
+        if (fine) {
+            less = zero16();
+            float d = 0.f;
+            sweep(KS ? wave : 0, nt, 0, none, [&](int tl, int b) {
+#pragma unroll 1
+                for (int u = 0; u < KT / 32; ++u) {
+                    uint32_t seen;
+                    f32x16_t e, dp;
+                    probabilities(tl, b, u, std::true_type{}, e, dp, seen);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) d = fmaf(e[i], dp[i], d);
+                }
+            });
+            delta = half_sum(d);
+            if constexpr (KS) {
+                __shared__ float parts[NW][32];
+                if (h == 0) parts[wave][lane] = delta;
+                __syncthreads();
+                delta = 0.f;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) delta += parts[w][lane & 31];
+            }
+        }
+    if (qr.valid && h == 0 && split == 0 && (!KS || wave == 0)) p.delta[(int64_t)qr.row * p.H + qr.head] = delta;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) less[i] = -delta;
+    const auto masked = [&](int tl, int b) { compute(tl, b, std::true_type{}, std::false_type{}); };
+    if (fine) {
+        if constexpr (S::ES == 2)
+            sweep(begin, t1, 0, none, [&](int tl, int b) { compute(tl, b, std::true_type{}, std::true_type{}); });
+    } else {
+        // tiles that every query sees whole, then those that some do not
+        sweep(begin, t1, qr.least / KT, [&](int tl, int b) { compute(tl, b, std::false_type{}, std::false_type{}); },
+              masked);
+    }
 
     if constexpr (KS) {
         __syncthreads();
@@ -306,8 +359,9 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
 #pragma unroll
     for (int d = 0; d < NDT; ++d) dk[d] = dv[d] = zero16();
 
-    auto compute = [&](int tl, int b, auto masked) {
-        constexpr bool MASKED = decltype(masked)::value;
+    const bool fine = S::ES == 2 && pl.Lk <= kFineKeys;
+    auto compute = [&](int tl, int b, auto masked, auto two) {
+        constexpr bool MASKED = decltype(masked)::value, TWO = decltype(two)::value;
         const lds_u8* qt = buf + b * 2 * S::TILE;
         const lds_u8* dt = qt + S::TILE;
 #pragma unroll
@@ -335,8 +389,8 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
                     dp[i] = see ? dp[i] : 0.f;
                 }
             }
-            add_rows<T, DP, MASKED>(dv, dt, 32 * u, s, seen);
-            add_rows<T, DP, MASKED>(dk, qt, 32 * u, dp, seen);
+            add_rows<T, DP, MASKED, TWO>(dv, dt, 32 * u, s, seen);
+            add_rows<T, DP, MASKED, TWO>(dk, qt, 32 * u, dp, seen);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -349,21 +403,25 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
     }
     wait_loads();
     next_tile<KS>();
-    // tiles that some keys are hidden from, then those that see every key
     int b = 0, tl = begin;
-    const auto sweep = [&](int end, auto masked) {
+    const auto sweep = [&](int end, auto masked, auto two) {
         for (; tl < end; tl += STEP, b ^= 1) {
             if (tl + STEP < t1) {
                 fetch(tl + STEP);
                 look_up(tl + 2 * STEP);
             }
-            if ((tl + 1) * KT > wave_first) compute(tl, b, masked);
+            if ((tl + 1) * KT > wave_first) compute(tl, b, masked, two);
             if (tl + STEP < t1) store(b ^ 1);
             next_tile<KS>();
         }
     };
-    sweep(min(t1, (block_last + KT - 1) / KT), std::true_type{});
-    sweep(t1, std::false_type{});
+    if (fine) {
+        if constexpr (S::ES == 2) sweep(t1, std::true_type{}, std::true_type{});
+    } else {
+        // tiles that some keys are hidden from, then those that see every key
+        sweep(min(t1, (block_last + KT - 1) / KT), std::true_type{}, std::false_type{});
+        sweep(t1, std::false_type{}, std::false_type{});
+    }
 
     if constexpr (KS) {
         static_assert(DP * 32 * 4 * 2 <= 4 * S::TILE);
