@@ -14,7 +14,10 @@
 // writes one partial result per chunk and channel, one joins them per scene
 // and group in a fixed order, and one walks the chunks again.  The forward's
 // partials are (mean, sum of squared deviations), taken batch by batch in
-// registers and joined by counts: no difference of large squares.
+// registers and joined by counts: no difference of large squares.  The second
+// walk goes backwards, over what the first left in the memory-side cache.  At
+// 1,006,716 x 128 bf16 in four scenes: 63 + 9 + 89 us forward (4.1 TB/s reading, 5.8
+// reading and writing), 112 + 9 + 142 us gradient.
 #include "glu.h"
 #include "join.h"
 #include "places.h"
@@ -374,9 +377,10 @@ __global__ void __launch_bounds__(kGrpThreads) k_group_apply(GroupParams p) {
 // registers between the statistics and the outputs (kOneElems per thread), a
 // launch in place of three.  A thread holds W channels (all of a 16-byte piece,
 // where groups and rows are whole numbers of those, else one) of rows one
-// stride apart.  part: the gradient's sums by scene, [scenes][2][C].
+// stride apart.  The gradient has no such form: with two inputs to hold it took 35.7
+// us where three launches took 13.4 (4,096 x 32 in one scene of 8 groups).
 constexpr int kOneThreads = 1024, kOneElems = 32;
-template <typename T, int W, int ACT, bool GRAD>
+template <typename T, int W, int ACT>
 __global__ void __launch_bounds__(kOneThreads) k_group_one(GroupParams p) {
     constexpr int NE = kOneElems / W;
     typedef T vec __attribute__((ext_vector_type(W)));
@@ -388,7 +392,6 @@ __global__ void __launch_bounds__(kOneThreads) k_group_one(GroupParams p) {
     const bool mine = tr < side;
     const int64_t first = (o0 + tr) * p.C + c, step = (int64_t)side * p.C;
     const T* x = (const T*)p.x + first;
-    const T* dout = (const T*)p.dout + first;
     T* y = (T*)p.y + first;
     const float inv = len ? 1.f / ((float)len * cg) : 0.f;
     float wt[W], bs[W];
@@ -397,100 +400,40 @@ __global__ void __launch_bounds__(kOneThreads) k_group_one(GroupParams p) {
         wt[i] = p.weight && mine ? p.weight[c + i] : 1.f;
         bs[i] = p.bias && mine ? p.bias[c + i] : 0.f;
     }
-    vec vx[NE], vd[NE];
+    vec vx[NE];
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
     for (int e = 0; e < NE; ++e) {
         const bool in = mine && tr + e * side < len;
         vx[e] = in ? *(const vec*)(x + e * step) : vec{};
-        if constexpr (GRAD) vd[e] = in ? *(const vec*)(dout + e * step) : vec{};
     }
-    float mean, rstd;
-    if constexpr (!GRAD) {
 #pragma unroll
-        for (int e = 0; e < NE; ++e)
+    for (int e = 0; e < NE; ++e)
 #pragma unroll
-            for (int i = 0; i < W; ++i) s0 += (float)vx[e][i];
-        mean = block_sum<kOneThreads>(s0, red) * inv;
+        for (int i = 0; i < W; ++i) s0 += (float)vx[e][i];
+    const float mean = block_sum<kOneThreads>(s0, red) * inv;
 #pragma unroll
-        for (int e = 0; e < NE; ++e) {
-            const bool in = mine && tr + e * side < len;
+    for (int e = 0; e < NE; ++e) {
+        const bool in = mine && tr + e * side < len;
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-                const float d = (float)vx[e][i] - mean;
-                s1 += in ? d * d : 0.f;
-            }
+        for (int i = 0; i < W; ++i) {
+            const float d = (float)vx[e][i] - mean;
+            s1 += in ? d * d : 0.f;
         }
-        rstd = 1.f / sqrtf(block_sum<kOneThreads>(s1, red) * inv + p.eps);
-        if (t == 0) {
-            p.mean[blockIdx.x] = mean;
-            p.rstd[blockIdx.x] = rstd;
-        }
-    } else {
-        mean = p.mean[blockIdx.x];
-        rstd = p.rstd[blockIdx.x];
     }
-    if constexpr (!GRAD) {
+    const float rstd = 1.f / sqrtf(block_sum<kOneThreads>(s1, red) * inv + p.eps);
+    if (t == 0) {
+        p.mean[blockIdx.x] = mean;
+        p.rstd[blockIdx.x] = rstd;
+    }
 #pragma unroll
-        for (int e = 0; e < NE; ++e) {
-            if (!mine || tr + e * side >= len) continue;
-            vec o;
+    for (int e = 0; e < NE; ++e) {
+        if (!mine || tr + e * side >= len) continue;
+        vec o;
 #pragma unroll
-            for (int i = 0; i < W; ++i)
-                o[i] = (T)group_act<ACT>(fmaf(((float)vx[e][i] - mean) * rstd, wt[i], bs[i])).v;
-            *(vec*)(y + e * step) = o;
-        }
-    } else {
-        // products are rounded before they are added and before the mean is taken
-        // off them: a group of one element gives 0
-#pragma clang fp contract(off)
-        __shared__ float col[kOneThreads * W];
-        float a0[W], a1[W];
-#pragma unroll
-        for (int i = 0; i < W; ++i) a0[i] = a1[i] = 0.f;
-#pragma unroll
-        for (int e = 0; e < NE; ++e)
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                // (past the rows dout is 0)
-                const float xh = ((float)vx[e][i] - mean) * rstd;
-                const float dz = (float)vd[e][i] * group_act<ACT>(fmaf(xh, wt[i], bs[i])).d;
-                const float gw = dz * wt[i];
-                a0[i] += dz;
-                a1[i] += dz * xh;
-                s0 += gw;
-                s1 += gw * xh;
-            }
-        s0 = block_sum<kOneThreads>(s0, red) * inv;
-        s1 = block_sum<kOneThreads>(s1, red) * inv;
-#pragma unroll
-        for (int e = 0; e < NE; ++e) {
-            if (!mine || tr + e * side >= len) continue;
-            vec o;
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                const float xh = ((float)vx[e][i] - mean) * rstd;
-                const float gw = (float)vd[e][i] * group_act<ACT>(fmaf(xh, wt[i], bs[i])).d * wt[i];
-                o[i] = (T)((gw - s0 - xh * s1) * rstd);
-            }
-            *(vec*)(y + e * step) = o;
-        }
-        if (!p.dweight) return;
-        // the channels' sums over the rows side by side, in their order
-        for (int k = 0; k < 2; ++k) {
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < W; ++i) col[t * W + i] = k ? a1[i] : a0[i];
-            __syncthreads();
-            for (int e = t; e < cg; e += kOneThreads) {
-                float s = 0.f;
-                for (int r = 0; r < min(side, len); ++r) s += col[r * cg + e];
-                if (p.B > 1)
-                    p.part[((int64_t)b * 2 + k) * p.C + g * cg + e] = s;
-                else
-                    (k ? p.dweight : p.dbias)[g * cg + e] = s;
-            }
-        }
+        for (int i = 0; i < W; ++i)
+            o[i] = (T)group_act<ACT>(fmaf(((float)vx[e][i] - mean) * rstd, wt[i], bs[i])).v;
+        *(vec*)(y + e * step) = o;
     }
 }
 
@@ -511,12 +454,15 @@ GroupShape group_shape(int64_t N, int C, int scenes, int dtype) {
     return s;
 }
 
-// Whether a scene's share of a group fits the registers of a workgroup, and the
-// whole is small enough for workgroups that read parts of rows (4,096 x 32 fp32
-// in 8 groups: 16.2 us of kernels in three launches, 8.5 in one).
-bool group_one(int64_t N, int C, int G, int W) {
+// Whether a scene's share of a group fits the registers of a workgroup, the
+// whole is small enough for workgroups that read parts of rows, and they are as
+// many as the card takes at a time (4,096 x 32 fp32, 8 groups, forward, one launch
+// against three: 1 scene 7.8 and 12.6 us, 64 scenes 8.3 and 12.9, 128 scenes 14.5
+// and 13.6; 2,048 x 128, 32 groups, 1,024 scenes: 389 and 29).
+bool group_one(int64_t N, int C, int B, int G, int W) {
     const int per = C / G / W;
-    return per <= kOneThreads && N <= (int64_t)(kOneThreads / per) * (kOneElems / W) && N * C <= (1 << 18);
+    return per <= kOneThreads && N <= (int64_t)(kOneThreads / per) * (kOneElems / W) && N * C <= (1 << 18) &&
+           (int64_t)B * G <= 512;
 }
 
 template <typename T, int ACT>
@@ -524,15 +470,9 @@ hipError_t group_go(const GroupParams& p, bool grad, const GroupShape& s, hipStr
     const dim3 grid((unsigned)s.items, s.cols);
     const unsigned stats = (unsigned)(p.B * p.G);
     constexpr int V = Piece<T>::V;
-    const bool whole = p.C / p.G % V == 0 && ((uintptr_t)p.x | (uintptr_t)p.y | (uintptr_t)p.dout) % 16 == 0;
-    if (group_one(p.N, p.C, p.G, whole ? V : 1)) {
-        if (grad)
-            (whole ? k_group_one<T, V, ACT, true> : k_group_one<T, 1, ACT, true>)<<<stats, kOneThreads, 0, st>>>(p);
-        else
-            (whole ? k_group_one<T, V, ACT, false> : k_group_one<T, 1, ACT, false>)<<<stats, kOneThreads, 0, st>>>(p);
-        if (grad && p.dweight && p.B > 1)
-            k_group_sums<<<(2 * p.C + kJoinCols - 1) / kJoinCols, kJoinCols * 64, 0, st>>>(p.part, p.B, p.C, p.dweight,
-                                                                                        p.dbias);
+    const bool whole = p.C / p.G % V == 0 && ((uintptr_t)p.x | (uintptr_t)p.y) % 16 == 0;
+    if (!grad && group_one(p.N, p.C, p.B, p.G, whole ? V : 1)) {
+        (whole ? k_group_one<T, V, ACT> : k_group_one<T, 1, ACT>)<<<stats, kOneThreads, 0, st>>>(p);
         return hipGetLastError();
     }
     // threads that join a scene's parts: a wave where it has a few on average

@@ -217,3 +217,13 @@ def test_gradient_against_differences():
             want = (f(*up) - f(*down)) / (2 * step)
             size = float(do.double().norm()) * float(v.double().norm()) * (90 if i else 1) ** 0.5
             assert abs(float((got.double() * v.double()).sum()) - want) <= size * (step ** 2 + 2 ** -24 * 8 / step)
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("scenes,C,G", [(64, 32, 8), (65, 32, 8), (300, 128, 32)])
+def test_many_small_scenes(scenes, C, G, dt):
+    """Scenes of 0 to 3 rows, as many groups as run at a time, one scene more, and
+    many: the sums over the scenes stay below the 80 additions that the bounds count
+    (a 64th of the chunks and 6 levels)."""
+    lens = [i % 4 for i in range(scenes)]
+    run(sum(lens), C, G, lens, dt, "silu")
