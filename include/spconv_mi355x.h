@@ -485,7 +485,8 @@ int spconv_groupnorm_grad(const void* dout, const void* x, const int32_t* offset
  * key gives out 0 and lse -inf.  A key that a query does not see has no effect
  * on it, whatever it holds.
  *   q        (dev) (N, H, D);  k, v (dev) (M, HK, D);  out (dev) (N, H, D)
- *            written; of dtype, 16-byte aligned, strides multiples of 16 bytes
+ *            written; of dtype, 16-byte aligned, strides multiples of 16 bytes,
+ *            rows at most 16 MiB apart
  *   offsets  (dev) int32 (B + 1,): the sequences' queries
  *   koffsets (dev) int32 (B + 1,): their keys; or NULL: the queries' own rows (then
  *            M = N, and order holds for the keys too)
@@ -512,8 +513,11 @@ int spconv_attention(const void* q, const void* k, const void* v, const int32_t*
  *   dout, out, dq as q;  dk, dv as k;  all of dtype
  *   strides  q, k, v, out, dout, dq, dk, dv
  *   workspace (dev) spconv_attention_grad_workspace_size bytes, 256-byte aligned
- * With SPCONV_BF16, p and ds are rounded to bfloat16 once, as operands.  Other
- * arguments, and what is said about them, are spconv_attention's. */
+ * With SPCONV_BF16, p and ds are rounded to bfloat16 once, as operands; where a
+ * tile's queries see 256 keys at most (and for the keys of such sequences) they are
+ * taken in two parts, and dout out is worked out from the keys instead of the
+ * rounded output.  Other arguments, and what is said about them, are
+ * spconv_attention's. */
 int spconv_attention_grad_workspace_size(int64_t N, int64_t M, int B, int H, int HK, int D, int dtype,
                                          size_t* bytes);
 int spconv_attention_grad(const void* dout, const void* q, const void* k, const void* v, const void* out,

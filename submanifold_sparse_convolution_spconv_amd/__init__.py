@@ -986,9 +986,11 @@ def spconv_attention_grad_workspace_size(N: int, M: int, B: int, H: int, HK: int
 
 
 def _lies_well(t):
-    """Whether rows and heads start at multiples of 16 bytes and heads lie in one piece."""
+    """Whether rows (at most 16 MiB apart) and heads start at multiples of 16 bytes
+    and heads lie in one piece."""
     unit = 16 // t.element_size()
-    return t.is_contiguous() or t.stride(2) == 1 and t.stride(0) % unit == 0 and t.stride(1) % unit == 0
+    return t.is_contiguous() or (t.stride(2) == 1 and t.stride(0) % unit == 0 and t.stride(1) % unit == 0
+                                 and t.stride(0) <= unit << 20)
 
 
 def _head_input(t):
@@ -1000,7 +1002,8 @@ def _head_output(out, shape, like, name):
         return like.new_empty(shape)
     _heads(out, name, like, shape)
     if not _lies_well(out):
-        raise ValueError(f"{name} must have contiguous heads that start at multiples of 16 bytes")
+        raise ValueError(f"{name} must have contiguous heads that start at multiples of 16 bytes, "
+                         "rows at most 16 MiB apart")
     return out
 
 

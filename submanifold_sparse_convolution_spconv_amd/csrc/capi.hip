@@ -906,6 +906,9 @@ static int attention_impl(spc::AttnArgs& a, bool grad, const int64_t* strides, s
         tensors[i].s[1] = strides ? strides[2 * i + 1] : a.D;
         if (!aligned(tensors[i].t, 16) || tensors[i].s[0] % unit || tensors[i].s[1] % unit)
             return fail(SPCONV_E_INVALID, "rows and heads must start at 16-byte addresses");
+        if (tensors[i].s[0] < 0 || tensors[i].s[1] < 0) return fail(SPCONV_E_INVALID, "strides must be >= 0");
+        if (tensors[i].s[0] * (16 / unit) > spc::kMaxRowStride)
+            return fail(SPCONV_E_UNSUPPORTED, "rows must be at most %lld bytes apart", (long long)spc::kMaxRowStride);
     }
     const size_t need = grad ? spc::attn_grad_workspace_bytes(a) : spc::attn_workspace_bytes(a);
     if (need) {

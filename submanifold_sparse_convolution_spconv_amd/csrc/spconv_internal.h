@@ -307,8 +307,10 @@ bool group_fits(int64_t N, int C, int scenes, int groups, int dtype);
 size_t group_workspace_bytes(int64_t N, int C, int scenes, int groups, int dtype);
 hipError_t launch_group(const GroupArgs& a, bool grad, hipStream_t stream);
 
-// Attention: elements of a head up to this.
+// Attention: elements of a head up to this; bytes from row to row (a tile's 64
+// rows are addressed in 31 bits).
 constexpr int kMaxHeadDim = 128;
+constexpr int64_t kMaxRowStride = 1 << 24;
 
 struct AttnArgs {
     const void* q;

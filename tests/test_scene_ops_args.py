@@ -104,6 +104,9 @@ def test_attention_refusals(lib):
         bad = list(good)
         bad[i] += 4
         assert f(st=strides(*bad)) == INVALID, i
+        bad[i] = -8
+        assert f(st=strides(*bad)) == INVALID, i
+    assert f(st=strides(256, 64, (1 << 23) + 8, 64, 128, 64, 256, 64)) == UNSUPPORTED      # rows too far apart
     long = dict(N=1, M=100000, B=1, H=8, D=128, ko=FAKE)
     assert f(**long) == INVALID and f(**long, ws=FAKE, wb=split - 1) == WORKSPACE
     assert f(**long, ws=FAKE + 128, wb=split) == INVALID
