@@ -13,6 +13,10 @@
 // registers: (key, query) tiles for dq, (query, key) tiles for dk and dv; all
 // sums are fp32.
 //
+// Two causal scenes of 29,578 rows, 8 heads on 2 of 64 bf16: 790 us for dq, 1,090
+// for dk and dv in five parts (900 and 870 TFLOP/s of executed products), vector
+// issue 43% and matrix unit 44% of the time.
+//
 // In bf16, p and ds are rounded once as operands, which is as much again as the
 // results' own rounding (2.4e-3 of a gradient's norm in all, 1.7e-3 without).
 // delta suffers from the rounding of out, little where a query sees many keys, but
@@ -280,10 +284,11 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
     float* stats = (float*)(smem + (KS ? wave * S::WAVE : 0) + 4 * S::TILE);
 
     // The queries' rows.  Where a tile is a whole number of positions, and those one
-    // after the other, as the keys are fetched; else each row's place is looked
+    // after the other (and its heads in reach), as the keys are fetched; else each row's place is looked
     // up one tile before.
     constexpr int NP = St::NP;
-    const bool plain = !p.order && KT % p.G == 0;
+    const auto close = [&](const int64_t(&s)[2]) { return KT / p.G * s[0] + p.G * s[1] < (1ll << 31); };
+    const bool plain = !p.order && KT % p.G == 0 && close(p.qs) && close(p.dos);
     uint32_t oq[NP], od[NP];
     int qrow[NP], qhead[NP];
     u32x4a_t rq[NP], rd[NP];

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import submanifold_sparse_convolution_spconv_amd as sp
+from attn_ref import attention64, check
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -66,3 +67,30 @@ def test_rows_far_apart_are_copied():
     assert torch.equal(sp.spconv_attention(far, far, far, o), sp.spconv_attention(*[far.contiguous()] * 3, o))
     with pytest.raises(ValueError):
         sp.spconv_attention(far, far, far, o, out=far)
+
+
+def test_heads_far_apart():
+    """Heads of whole tensors one after the other: past 2 GiB from first to last.
+
+    The same rows in a small tensor need not give the same bits: which kernel a call
+    takes goes by its rows in all per sequence (2,200,000 here, 300 there), since the
+    offsets are on the device, and the kernels add in different orders.  Both are
+    within attn_ref's bound of the definition."""
+    N, H, D = 2_200_000, 8, 64
+    t = torch.zeros(H, N, D, dtype=BF, device="cuda")
+    assert t.numel() * 2 > 1 << 31
+    n = 300
+    g = torch.Generator(device="cuda").manual_seed(2)
+    for i in range(H):
+        t[i, :n] = torch.randn(n, D, generator=g, device="cuda")
+    q = t.transpose(0, 1)
+    o = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    k = torch.zeros(N, 1, D, dtype=BF, device="cuda")
+    k[:n] = torch.randn(n, 1, D, generator=g, device="cuda")
+    small = [x[:n].contiguous() for x in (q, k)]
+    for qq, kk in ((q, k), small):
+        out, lse = sp.spconv_attention(qq, kk, kk, o, causal=True, stats=True)
+        grads = sp.spconv_attention_grad(qq, qq, kk, kk, out, lse, o, causal=True)
+        want = attention64(*[small[i] for i in (0, 1, 1)], o, causal=True, dout=small[0])
+        for name, got in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *grads)):
+            check(got[:n], want[name], f"{name} of {len(qq)} rows")
