@@ -941,6 +941,7 @@ def _rotary(name, x, positions, freqs, layout, gain, out):
         raise ValueError("positions must be an int32 (N,) or (N, axes) tensor on the features' device")
     if freqs is None or freqs.dtype != _torch.float64 or freqs.dim() != 1 or freqs.device != dev:
         raise ValueError("freqs must be a float64 (pairs,) tensor on the features' device")
+    freqs = freqs.contiguous()
     if x.stride(2) != 1:
         x = x.contiguous()
     axes = 1
@@ -954,7 +955,7 @@ def _rotary(name, x, positions, freqs, layout, gain, out):
         _heads(out, "out", x, x.shape)
         if out.stride(2) != 1:
             raise ValueError("out must have its last dimension contiguous")
-    _call(name, dev, _at(x), _at(positions), positions.stride(0), _at(freqs.contiguous()), _at(out),
+    _call(name, dev, _at(x), _at(positions), positions.stride(0), _at(freqs), _at(out),
           _strides(x, out), N, H, D, freqs.numel(), axes,
           _LAYOUTS[layout], gain, dt)
     return out

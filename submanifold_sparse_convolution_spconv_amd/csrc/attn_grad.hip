@@ -283,9 +283,9 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
     lds_u8* buf = (lds_u8*)smem + (KS ? wave * S::WAVE : 0);
     float* stats = (float*)(smem + (KS ? wave * S::WAVE : 0) + 4 * S::TILE);
 
-    // The queries' rows.  Where a tile is a whole number of positions, and those one
-    // after the other (and its heads in reach), as the keys are fetched; else each row's place is looked
-    // up one tile before.
+    // The queries' rows.  Where a tile is a whole number of positions, those one after
+    // the other and its heads within 31 bits, as the keys are fetched; else each row's
+    // place is looked up one tile before.
     constexpr int NP = St::NP;
     const auto close = [&](const int64_t(&s)[2]) { return KT / p.G * s[0] + p.G * s[1] < (1ll << 31); };
     const bool plain = !p.order && KT % p.G == 0 && close(p.qs) && close(p.dos);
