@@ -237,8 +237,7 @@ hipError_t attn_type(const AttnParams& p, hipStream_t st) {
 bool attn_fits(const AttnArgs& a, bool grad) {
     // most workgroups of 256 threads that any plan launches per sequence and split
     const auto fits = [&](int64_t n, int64_t per) {
-        return n * per < (1ll << 31) &&
-               (attn_places(n, per, kFewRows, a.B) * a.HK + kXcds * kRun) * 256 < (1ll << 32);
+        return (attn_places(n, per, kFewRows, a.B) * a.HK + kXcds * kRun) * 256 < (1ll << 32);
     };
     return fits(a.N, a.H / a.HK) && (!grad || fits(a.M, 1));
 }

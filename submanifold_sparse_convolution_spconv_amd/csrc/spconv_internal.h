@@ -311,6 +311,10 @@ hipError_t launch_group(const GroupArgs& a, bool grad, hipStream_t stream);
 // rows are addressed in 31 bits).
 constexpr int kMaxHeadDim = 128;
 constexpr int64_t kMaxRowStride = 1 << 24;
+// Rows of a sequence: keys, or queries times the heads that share keys.  Kernels
+// number them in 31 bits, and the rows of tiles past the last one too, which their
+// loops look ahead to (by 8 tiles of 64 at most).
+constexpr int64_t kMaxAttnRows = (1ll << 31) - 1024;
 
 struct AttnArgs {
     const void* q;

@@ -1,0 +1,29 @@
+"""The ends of the operators' ranges within scenes (no GPU needed): sizes that a
+kernel's 32-bit counts of rows cannot hold are refused, and the largest ones that
+they can are not."""
+import ctypes
+
+import pytest
+
+import submanifold_sparse_convolution_spconv_amd as sp
+
+OK, UNSUPPORTED = 0, -2
+LAST = (1 << 31) - 1024         # rows of a sequence: the loops look up to 8 tiles of 64 rows past the end
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return sp.load_library()
+
+
+def test_attention_rows_past_31_bits(lib):
+    """Tiles past the last row are numbered too (tile * rows + row): their numbers
+    have to stay within 31 bits, for keys, and for queries times the heads that
+    share keys."""
+    n = ctypes.c_size_t(0)
+    for S in (lib.spconv_attention_workspace_size, lib.spconv_attention_grad_workspace_size):
+        Z = lambda N, M, G=1: S(N, M, 1, G, 1, 8, sp.SPCONV_BF16, ctypes.byref(n))
+        for past in (LAST + 1, (1 << 31) - 256, (1 << 31) - 128, (1 << 31) - 64, (1 << 31) - 2, (1 << 31) - 1):
+            assert Z(1, past) == UNSUPPORTED and Z(past, 1) == UNSUPPORTED, past
+        assert Z(LAST // 8 + 1, 1, G=8) == UNSUPPORTED and Z((1 << 28) - 1, 1, G=8) == UNSUPPORTED
+    assert lib.spconv_attention_workspace_size(1, LAST, 1, 1, 1, 8, sp.SPCONV_BF16, ctypes.byref(n)) == OK
