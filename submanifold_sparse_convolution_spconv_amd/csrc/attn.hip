@@ -166,11 +166,15 @@ __global__ void __launch_bounds__((64 * FwdShape<T, DP>::NW), (FwdShape<T, DP>::
         for (int i = 0; i < 16; ++i) again |= !(fabsf(acc[d][i]) < INFINITY);
     // (a pass of its own each: as modes of one loop they cost the first 7%)
     if (__builtin_expect(__syncthreads_or(again), 0)) {
+        // the tile's other queries keep their reference, and so their bits: what made
+        // this one's too small may be hidden from them
+        const float kept = half_max(again ? 1.f : 0.f) > 0.f ? INFINITY : ref;
         sweep([]() {},
               [&](int tl, int b, auto) {
 #pragma unroll 1
                   for (int u = 0; u < NSUB; ++u) raise(tl, b, u);
               });
+        ref = kept == INFINITY ? ref : kept;
         set_base();
         clear();
         sweep([]() {}, compute);

@@ -244,8 +244,9 @@ __global__ void __launch_bounds__((64 * FewShape<T, DP>::NW), (FewShape<T, DP>::
         add_rows16<T, DP, decltype(masked)::value>(acc, vt, s, seen);
     };
     // One pass over the tiles, or, where its reference does not do, one for the maximum
-    // and another with that.
+    // and another with that (columns whose reference did keep it, as in attn.hip).
     enum { kFirst, kMaximum, kAgain } pass = kFirst;
+    float kept = -INFINITY;
     for (;;) {
         sum = 0.f;
 #pragma unroll
@@ -279,6 +280,7 @@ __global__ void __launch_bounds__((64 * FewShape<T, DP>::NW), (FewShape<T, DP>::
         }
         if (pass == kAgain) break;
         if (pass == kMaximum) {
+            ref = kept == INFINITY ? ref : kept;
             set_base();
             pass = kAgain;
             continue;
@@ -289,6 +291,7 @@ __global__ void __launch_bounds__((64 * FewShape<T, DP>::NW), (FewShape<T, DP>::
 #pragma unroll
             for (int i = 0; i < 4; ++i) again |= !(fabsf(acc[d][i]) < INFINITY);
         if (__builtin_expect(__ballot(again) == 0, 1)) break;
+        kept = column_max(again ? 1.f : 0.f) > 0.f ? INFINITY : ref;
         pass = kMaximum;
     }
     sum = column_sum(sum);
