@@ -482,7 +482,7 @@ int spconv_groupnorm_grad(const void* dout, const void* x, const int32_t* offset
  * heads of queries share a head of keys and values.  With Lq queries and Lk
  * keys, `causal` lets query i see the keys j <= i + Lk - Lq: the last query sees
  * all of them (a new voxel the keys of those before it).  A query that sees no
- * key gives out 0 and lse -inf.  A key that a query does not see has no effect
+ * key, or whose scores are all -inf, gives out 0 and lse -inf.  A key that a query does not see has no effect
  * on it, whatever it holds.
  *   q        (dev) (N, H, D);  k, v (dev) (M, HK, D);  out (dev) (N, H, D)
  *            written; of dtype, 16-byte aligned, strides multiples of 16 bytes,
@@ -517,7 +517,8 @@ int spconv_attention(const void* q, const void* k, const void* v, const int32_t*
  * With SPCONV_BF16, p and ds are rounded to bfloat16 once, as operands; where a
  * tile's queries see 256 keys at most (and for the keys of such sequences) they are
  * taken in two parts, and dout out is worked out from the keys instead of the
- * rounded output.  Other arguments, and what is said about them, are
+ * rounded output.  The weights are p = exp(score - lse), off by 2^-23 |lse| of
+ * themselves: with scores of millions, gradients say little.  Other arguments, and what is said about them, are
  * spconv_attention's. */
 int spconv_attention_grad_workspace_size(int64_t N, int64_t M, int B, int H, int HK, int D, int dtype,
                                          size_t* bytes);

@@ -21,8 +21,9 @@
 // the first 32 keys, so that the largest weight is 1 at least; larger ones do
 // floating point no harm until they leave its range.  No maximum is needed on
 // the way, and nothing rescaled (which cost a fifth of the time, most of it in
-// copies of the sums around the branch).  Where the sum reaches 2^64, or a
-// result is not finite, the tile is done again with the maximum of all keys.
+// copies of the sums around the branch).  Where a query's sum leaves 2^-64 .. 2^64,
+// a result is not finite, or all scores of its first keys are -inf, the tile is
+// done again with that query's maximum of all keys.
 #include "attn.h"
 
 #include <algorithm>
@@ -65,9 +66,9 @@ __global__ void __launch_bounds__((64 * FwdShape<T, DP>::NW), (FwdShape<T, DP>::
     KeyStager<T, DP, KT, 64 * S::NW> keys(p, qr.pl, hk, t);
 
     f32x16_t acc[NDT];
-    // the reference of the lane's query (a score, -inf if it sees no key here), and
-    // what it takes off exponents (in bf16 powers of two)
-    float ref = -INFINITY, base = 0.f, sum;
+    // the reference of the lane's query (a score, -inf if it sees no key here), what of
+    // it is taken off the scores, and what off their exponents
+    float ref = -INFINITY, less = 0.f, base = 0.f, sum;
 
     // scores of 32 keys of a tile
     const auto scores = [&](int tl, int b, int u, auto masked, uint32_t& seen) {
@@ -96,9 +97,10 @@ __global__ void __launch_bounds__((64 * FwdShape<T, DP>::NW), (FwdShape<T, DP>::
     };
     const auto set_base = [&]() {
         ref = half_max(ref);
-        base = ref == -INFINITY ? 0.f : S::ES == 4 ? ref : ref * p.scale2;
+        less = ref == -INFINITY ? 0.f : ref;
+        base = less * p.scale2;
     };
-    const auto compute = [&](int tl, int b, auto masked) {
+    const auto compute = [&](int tl, int b, auto masked, auto exact) {
         // the next 32 keys' scores under the exponentials of these
         uint32_t seen[NSUB];
         f32x16_t s[NSUB];
@@ -110,9 +112,12 @@ __global__ void __launch_bounds__((64 * FwdShape<T, DP>::NW), (FwdShape<T, DP>::
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 // fp32: the reference's own weight is 1 to the bit, so that one key's
-                // value comes out as it is; in bf16 the rounding sees to that
-                s[u][i] = __builtin_amdgcn_exp2f(S::ES == 4 ? (s[u][i] - base) * p.scale2
-                                                            : fmaf(s[u][i], p.scale2, -base));
+                // value comes out as it is; in bf16 the rounding sees to that, and
+                // base may be off by half a step, the same for all of a query's keys
+                s[u][i] = __builtin_amdgcn_exp2f(S::ES == 4 ? (s[u][i] - less) * p.scale2
+                                                 : decltype(exact)::value
+                                                     ? fmaf(s[u][i] - less, p.scale2, -base)
+                                                     : fmaf(s[u][i], p.scale2, -base));
                 part[i & 3] += s[u][i];
             }
             sum += (part[0] + part[1]) + (part[2] + part[3]);
@@ -158,37 +163,46 @@ __global__ void __launch_bounds__((64 * FwdShape<T, DP>::NW), (FwdShape<T, DP>::
             raise(0, 0, 0);
             set_base();
         },
-        compute);
-    bool again = !(sum < kAttnMost);
+        [&](int tl, int b, auto masked) { compute(tl, b, masked, std::false_type{}); });
+    sum = half_sum(sum);
+    bool again = qr.limit > 0 && (!(sum < kAttnMost && sum > 1.f / kAttnMost) || ref == -INFINITY);
 #pragma unroll
     for (int d = 0; d < NDT; ++d)
 #pragma unroll
         for (int i = 0; i < 16; ++i) again |= !(fabsf(acc[d][i]) < INFINITY);
+    again &= qr.valid;       // (columns past the sequence do not count; a wave of them saw no key)
     // (a pass of its own each: as modes of one loop they cost the first 7%)
     if (__builtin_expect(__syncthreads_or(again), 0)) {
-        // the tile's other queries keep their reference, and so their bits: what made
-        // this one's too small may be hidden from them
-        const float kept = half_max(again ? 1.f : 0.f) > 0.f ? INFINITY : ref;
+        again = half_max(again ? 1.f : 0.f) > 0.f;
+        const float kept = ref, kept_base = base;
         sweep([]() {},
               [&](int tl, int b, auto) {
 #pragma unroll 1
                   for (int u = 0; u < NSUB; ++u) raise(tl, b, u);
               });
-        ref = kept == INFINITY ? ref : kept;
         set_base();
+        // (the reference off the score first: base, of scores like 1e30, is too far from it)
+        base = 0.f;
+        // the tile's other queries keep what they had, and so their bits: what made this
+        // one's reference too small may be hidden from them
+        if (!again) {
+            ref = kept;
+            less = S::ES == 4 && ref > -INFINITY ? ref : 0.f;
+            base = kept_base;
+        }
         clear();
-        sweep([]() {}, compute);
+        sweep([]() {}, [&](int tl, int b, auto masked) { compute(tl, b, masked, std::true_type{}); });
+        sum = half_sum(sum);
     }
-    sum = half_sum(sum);
 
     if (!qr.valid) return;
-    const bool sees = qr.limit > 0;
-    const float f = sees ? 1.f / sum : 0.f;
+    // (no key, or no score above -inf: no weight either)
+    const float f = sum == 0.f ? 0.f : 1.f / sum;
     uint8_t* o = qr.at(p.out, p.os);
 #pragma unroll
     for (int d = 0; d < NDT; ++d) store_col<T>(o, acc[d], f, d, p.D);
     if (p.lse && h == 0)
-        p.lse[(int64_t)qr.row * p.H + qr.head] = sees ? fmaf(ref, p.scale, logf(sum)) : -INFINITY;
+        p.lse[(int64_t)qr.row * p.H + qr.head] = sum == 0.f ? -INFINITY : fmaf(ref, p.scale, logf(sum));
 }
 
 template <typename T, int DP>

@@ -194,7 +194,8 @@ __global__ void __launch_bounds__((64 * FewShape<T, DP>::NW), (FewShape<T, DP>::
     KeyStager<T, DP, KT, 64> keys(p, qr.pl, hk, lane);
 
     f32x4a_t acc[NDT];
-    float ref = -INFINITY, base = 0.f, sum;
+    // (as in attn.hip; bf16 has less only after a first pass that did not do)
+    float ref = -INFINITY, less = 0.f, base = 0.f, sum;
     const auto scores = [&](int tl, auto masked, float(&s)[8], uint32_t& seen) {
         f32x4a_t c0 = {}, c1 = {};
 #pragma unroll
@@ -218,6 +219,9 @@ __global__ void __launch_bounds__((64 * FewShape<T, DP>::NW), (FewShape<T, DP>::
             }
         }
     };
+    // One pass over the tiles, or, where its reference does not do, one for the maximum
+    // and another with that (columns whose reference did keep it, as in attn.hip).
+    enum { kFirst, kMaximum, kAgain } pass = kFirst;
     const auto raise = [&](int tl) {
         uint32_t seen;
         float s[8];
@@ -227,7 +231,9 @@ __global__ void __launch_bounds__((64 * FewShape<T, DP>::NW), (FewShape<T, DP>::
     };
     const auto set_base = [&]() {
         ref = column_max(ref);
-        base = ref == -INFINITY ? 0.f : S::ES == 4 ? ref : ref * p.scale2;
+        less = ref == -INFINITY ? 0.f : ref;
+        base = less * p.scale2;
+        (S::ES == 4 || pass != kFirst ? base : less) = 0.f;
     };
     const auto compute = [&](int tl, auto masked) {
         uint32_t seen;
@@ -236,17 +242,14 @@ __global__ void __launch_bounds__((64 * FewShape<T, DP>::NW), (FewShape<T, DP>::
         float part[2] = {0.f, 0.f};
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
-            // (fp32: as in attn.hip)
-            s[v] = __builtin_amdgcn_exp2f(S::ES == 4 ? (s[v] - base) * p.scale2 : fmaf(s[v], p.scale2, -base));
+            s[v] = __builtin_amdgcn_exp2f(S::ES == 4 ? (s[v] - less) * p.scale2 : fmaf(s[v] - less, p.scale2, -base));
             part[v & 1] += s[v];
         }
         sum += part[0] + part[1];
         add_rows16<T, DP, decltype(masked)::value>(acc, vt, s, seen);
     };
-    // One pass over the tiles, or, where its reference does not do, one for the maximum
-    // and another with that (columns whose reference did keep it, as in attn.hip).
-    enum { kFirst, kMaximum, kAgain } pass = kFirst;
-    float kept = -INFINITY;
+    bool again = false;
+    float kept = 0.f, kept_base = 0.f;
     for (;;) {
         sum = 0.f;
 #pragma unroll
@@ -278,23 +281,31 @@ __global__ void __launch_bounds__((64 * FewShape<T, DP>::NW), (FewShape<T, DP>::
             if (tl + NW < t1) keys.store(kt);
             next_tile<true>();
         }
-        if (pass == kAgain) break;
         if (pass == kMaximum) {
-            ref = kept == INFINITY ? ref : kept;
             set_base();
+            if (!again) {
+                ref = kept;
+                less = S::ES == 4 && ref > -INFINITY ? ref : 0.f;
+                base = kept_base;
+            }
             pass = kAgain;
             continue;
         }
-        bool again = !(sum < kAttnMost);
+        sum = column_sum(sum);
+        if (pass == kAgain) break;
+        // (a column that sees none of the wave's first keys sees none of the others)
+        const bool sees = begin < t1 && begin * KT < qr.limit;
+        again = sees && (!(sum < kAttnMost && sum > 1.f / kAttnMost) || ref == -INFINITY);
 #pragma unroll
         for (int d = 0; d < NDT; ++d)
 #pragma unroll
             for (int i = 0; i < 4; ++i) again |= !(fabsf(acc[d][i]) < INFINITY);
         if (__builtin_expect(__ballot(again) == 0, 1)) break;
-        kept = column_max(again ? 1.f : 0.f) > 0.f ? INFINITY : ref;
+        again = column_max(again ? 1.f : 0.f) > 0.f;
+        kept = ref;
+        kept_base = base;
         pass = kMaximum;
     }
-    sum = column_sum(sum);
 
     // the waves' parts, in their order: the columns, references and sums
     __syncthreads();
@@ -315,8 +326,8 @@ __global__ void __launch_bounds__((64 * FewShape<T, DP>::NW), (FewShape<T, DP>::
     if (wave > 0) return;
     float top = ref;
     for (int w = 1; w < NW; ++w) top = fmaxf(top, ((const float*)(smem + w * S::WAVE))[DP * 16 + (lane & 15)]);
-    base = top == -INFINITY ? 0.f : top;
-    const float f0 = __builtin_amdgcn_exp2f((ref - base) * p.scale2);
+    const float from = top == -INFINITY ? 0.f : top;
+    const float f0 = __builtin_amdgcn_exp2f((ref - from) * p.scale2);
     sum *= f0;
 #pragma unroll
     for (int d = 0; d < NDT; ++d)
@@ -325,7 +336,7 @@ __global__ void __launch_bounds__((64 * FewShape<T, DP>::NW), (FewShape<T, DP>::
 #pragma unroll 1
     for (int w = 1; w < NW; ++w) {
         const float* o = (const float*)(smem + w * S::WAVE);
-        const float f = __builtin_amdgcn_exp2f((o[DP * 16 + (lane & 15)] - base) * p.scale2);
+        const float f = __builtin_amdgcn_exp2f((o[DP * 16 + (lane & 15)] - from) * p.scale2);
         sum = fmaf(o[DP * 16 + 16 + (lane & 15)], f, sum);
 #pragma unroll
         for (int d = 0; d < NDT; ++d)
@@ -333,7 +344,8 @@ __global__ void __launch_bounds__((64 * FewShape<T, DP>::NW), (FewShape<T, DP>::
             for (int i = 0; i < 4; ++i) acc[d][i] = fmaf(o[(16 * d + 4 * g + i) * 16 + (lane & 15)], f, acc[d][i]);
     }
     if (!qr.valid) return;
-    const bool sees = qr.limit > 0;
+    // (no key, or no score above -inf: no weight either)
+    const bool none = sum == 0.f;
     float f = 1.f;
     uint8_t* out;
     if (p.splits > 1) {
@@ -341,14 +353,14 @@ __global__ void __launch_bounds__((64 * FewShape<T, DP>::NW), (FewShape<T, DP>::
         out = (uint8_t*)(p.part + at * p.D);
         if (g == 0) {
             float* m = p.part + p.splits * NH * p.D + at * 2;
-            m[0] = top * p.scale2;
-            m[1] = sees ? sum : -1.f;
+            m[0] = top;
+            m[1] = sum;
         }
     } else {
-        f = sees ? 1.f / sum : 0.f;
+        f = none ? 0.f : 1.f / sum;
         out = qr.at(p.out, p.os);
         if (p.lse && g == 0)
-            p.lse[(int64_t)qr.row * p.H + qr.head] = sees ? fmaf(top, p.scale, logf(sum)) : -INFINITY;
+            p.lse[(int64_t)qr.row * p.H + qr.head] = none ? -INFINITY : fmaf(top, p.scale, logf(sum));
     }
 #pragma unroll
     for (int dt = 0; dt < NDT; ++dt) {
@@ -380,14 +392,13 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(AttnParams p) {
     for (int s = t & 63; s < p.splits; s += 64) top = fmaxf(top, ml[s * NH * 2]);
 #pragma unroll
     for (int m = 32; m; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
-    const bool none = ml[1] < 0.f;
     const float base = top == -INFINITY ? 0.f : top;
     f32x4r_t o = {};
     float l = 0.f;
     const int per = (p.splits + kJoinParts - 1) / kJoinParts;
 #pragma unroll 4
     for (int s = g * per; s < min(p.splits, (g + 1) * per); ++s) {
-        const float f = __builtin_amdgcn_exp2f(ml[s * NH * 2] - base);
+        const float f = __builtin_amdgcn_exp2f((ml[s * NH * 2] - base) * p.scale2);
         l = fmaf(ml[s * NH * 2 + 1], f, l);
         if (4 * q < p.D) o += *(const f32x4r_t*)(p.part + (s * NH + at) * p.D + 4 * q) * f;
     }
@@ -399,12 +410,13 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(AttnParams p) {
         o += so[k][q];
         l += sl[k];
     }
+    const bool none = l == 0.f;
     const int64_t row = row_of(p.order, pos, p.N);
     if (4 * q < p.D) {
         uint8_t* out = p.out + row * p.os[0] + head * p.os[1] + 4 * q * (int)sizeof(T);
         store_four<T>(out, o, none ? 0.f : 1.f / l);
     }
-    if (p.lse && q == 0) p.lse[row * p.H + head] = none ? -INFINITY : fmaf(top, 0.69314718055994531f, logf(l));
+    if (p.lse && q == 0) p.lse[row * p.H + head] = none ? -INFINITY : fmaf(top, p.scale, logf(l));
 }
 
 template <typename T, int DP>
