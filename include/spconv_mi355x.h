@@ -518,8 +518,8 @@ int spconv_attention(const void* q, const void* k, const void* v, const int32_t*
  * tile's queries see 256 keys at most (and for the keys of such sequences) they are
  * taken in two parts, and dout out is worked out from the keys instead of the
  * rounded output.  The weights are p = exp(score - lse), off by 2^-23 |lse| of
- * themselves: with scores of millions, gradients say little.  Other arguments, and what is said about them, are
- * spconv_attention's. */
+ * themselves: with scores of millions, gradients say little.  Other arguments, and
+ * what is said about them, are spconv_attention's. */
 int spconv_attention_grad_workspace_size(int64_t N, int64_t M, int B, int H, int HK, int D, int dtype,
                                          size_t* bytes);
 int spconv_attention_grad(const void* dout, const void* q, const void* k, const void* v, const void* out,
