@@ -150,6 +150,9 @@ __device__ __forceinline__ int64_t xcd_order(int64_t id) {
     return (slot / kRun * kXcds + xcd) * kRun + slot % kRun;
 }
 inline int64_t xcd_blocks(int64_t n) { return (n + kXcds * kRun - 1) / (kXcds * kRun) * (kXcds * kRun); }
+// Whether a launch of n places, of 256 threads at most each, stays within the 2^32
+// that a launch's threads are counted in.
+inline bool attn_threads_fit(int64_t n) { return xcd_blocks(n) * 256 < (1ll << 32); }
 
 // A tile of rows of DP elements in LDS, in 16-byte units.  Units of a row are
 // permuted so that both ways of reading are free of bank conflicts (banks repeat

@@ -252,12 +252,9 @@ hipError_t attn_type(const AttnParams& p, hipStream_t st) {
 
 }  // namespace
 
-bool attn_fits(const AttnArgs& a, bool grad) {
-    // most workgroups of 256 threads that any plan launches per sequence and split
-    const auto fits = [&](int64_t n, int64_t per) {
-        return (attn_places(n, per, kFewRows, a.B) * a.HK + kXcds * kRun) * 256 < (1ll << 32);
-    };
-    return fits(a.N, a.H / a.HK) && (!grad || fits(a.M, 1));
+bool attn_fits(const AttnArgs& a) {
+    const Plan r = plan(a);
+    return attn_threads_fit(attn_places(a.N, a.H / a.HK, r.few ? kFewRows : 128, a.B) * a.HK * r.splits);
 }
 
 size_t attn_workspace_bytes(const AttnArgs& a) {

@@ -585,6 +585,12 @@ hipError_t grad_type(const AttnArgs& a, const AttnParams& p, hipStream_t st) {
 
 }  // namespace
 
+bool attn_grad_fits(const AttnArgs& a) {
+    const auto fits = [&](const Plan& r, int64_t n, int64_t per) {
+        return attn_threads_fit(attn_places(n, per, r.ks ? 32 : 128, a.B) * a.HK * r.splits);
+    };
+    return fits(dq_plan(a), a.N, a.H / a.HK) && fits(dkv_plan(a), a.M, 1);
+}
 size_t attn_grad_workspace_bytes(const AttnArgs& a) {
     const Plan q = dq_plan(a), k = dkv_plan(a);
     size_t part = 0;

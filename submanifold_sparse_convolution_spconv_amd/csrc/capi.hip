@@ -844,7 +844,7 @@ static int check_attention(const spc::AttnArgs& a, bool grad) {
     if (a.N * (a.H / a.HK) > spc::kMaxAttnRows || a.M > spc::kMaxAttnRows)
         return fail(SPCONV_E_UNSUPPORTED, "no more than %lld rows N H / HK and keys M (got N=%lld M=%lld H=%d HK=%d)",
                     (long long)spc::kMaxAttnRows, (long long)a.N, (long long)a.M, a.H, a.HK);
-    if (!spc::attn_fits(a, grad))
+    if (!(grad ? spc::attn_grad_fits(a) : spc::attn_fits(a)))
         return fail(SPCONV_E_UNSUPPORTED, "N=%lld M=%lld B=%d H=%d HK=%d need more than 2^32 threads",
                     (long long)a.N, (long long)a.M, a.B, a.H, a.HK);
     return SPCONV_OK;

@@ -342,7 +342,8 @@ struct AttnArgs {
 // least as many as any partition into B sequences needs.
 constexpr int64_t attn_places(int64_t N, int64_t G, int64_t rows, int64_t B) { return N * G / rows + B; }
 // A launch's threads are counted in 32 bits: false where a kernel would need more.
-bool attn_fits(const AttnArgs& a, bool grad);
+bool attn_fits(const AttnArgs& a);
+bool attn_grad_fits(const AttnArgs& a);
 size_t attn_workspace_bytes(const AttnArgs& a);
 size_t attn_grad_workspace_bytes(const AttnArgs& a);
 hipError_t launch_attn(const AttnArgs& a, hipStream_t stream);

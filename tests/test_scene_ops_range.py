@@ -27,3 +27,18 @@ def test_attention_rows_past_31_bits(lib):
             assert Z(1, past) == UNSUPPORTED and Z(past, 1) == UNSUPPORTED, past
         assert Z(LAST // 8 + 1, 1, G=8) == UNSUPPORTED and Z((1 << 28) - 1, 1, G=8) == UNSUPPORTED
     assert lib.spconv_attention_workspace_size(1, LAST, 1, 1, 1, 8, sp.SPCONV_BF16, ctypes.byref(n)) == OK
+
+
+def test_attention_threads_are_counted_by_the_kernel_taken(lib):
+    """A launch's threads are counted in 32 bits.  Calls of many rows have 128 of them
+    a workgroup: 11 million rows (the largest cloud here) of 32 heads are an eighth of
+    the limit, not past it."""
+    n = ctypes.c_size_t(0)
+    for S in (lib.spconv_attention_workspace_size, lib.spconv_attention_grad_workspace_size):
+        Z = lambda N, B, H=32: S(N, N, B, H, H, 8, sp.SPCONV_BF16, ctypes.byref(n))
+        assert Z(11_000_000, 11_000) == OK
+        # (N / 128 + B) 32 workgroups of 256 threads, in runs of 64
+        assert Z((1 << 26) - (1 << 14), 1) == OK and Z((1 << 26) - 128, 1) == UNSUPPORTED
+        # sequences of few rows: 16 or 32 rows a workgroup, and one for each sequence at least
+        assert Z(1 << 19, 1 << 19, H=16) == OK and Z(1 << 20, 1 << 20, H=16) == UNSUPPORTED
+        assert Z(1, (1 << 24) - 128, H=1) == OK and Z(1, 1 << 24, H=1) == UNSUPPORTED
