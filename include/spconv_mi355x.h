@@ -456,7 +456,8 @@ int spconv_rotary_grad(const void* dout, const int32_t* positions, int64_t pos_s
  *   act      SPCONV_SILU, SPCONV_GELU or SPCONV_LINEAR
  *   workspace (dev) spconv_groupnorm_workspace_size bytes, 256-byte aligned
  * C up to 4096, a multiple of groups; eps >= 0.  Calls of more than 2^32
- * threads (from 4.2e6 scenes times groups on) give SPCONV_E_UNSUPPORTED. */
+ * threads (from 4.2e6 scenes times groups on, in the gradient C / 8 fewer) give
+ * SPCONV_E_UNSUPPORTED. */
 int spconv_groupnorm_workspace_size(int64_t N, int C, int scenes, int groups, int dtype, size_t* bytes);
 int spconv_groupnorm(const void* x, const int32_t* offsets, const float* weight, const float* bias, void* workspace,
                      size_t workspace_bytes, void* y, float* mean, float* rstd, int64_t N, int C, int scenes,

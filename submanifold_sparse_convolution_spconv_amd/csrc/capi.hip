@@ -773,23 +773,28 @@ int spconv_rotary_grad(const void* dout, const int32_t* positions, int64_t pos_s
                        stream, true, "spconv_rotary_grad");
 }
 
-int spconv_groupnorm_workspace_size(int64_t N, int C, int scenes, int groups, int dtype, size_t* bytes) {
-    if (!bytes) return fail(SPCONV_E_INVALID, "bytes pointer is NULL");
+// Sizes of a group norm, and the workspace they need.
+static int check_group(int64_t N, int C, int scenes, int groups, int dtype, bool grad, size_t* bytes) {
     int rc = check_rows(N, C, dtype, "C");
     if (rc) return rc;
     if (scenes < 1) return fail(SPCONV_E_INVALID, "scenes must be >= 1 (got %d)", scenes);
     if (groups < 1 || C % groups)
         return fail(SPCONV_E_INVALID, "C must be a multiple of groups (got C=%d groups=%d)", C, groups);
-    if (!spc::group_fits(N, C, scenes, groups, dtype))
+    if (!spc::group_fits(N, C, scenes, groups, dtype, grad))
         return fail(SPCONV_E_UNSUPPORTED, "%d scenes of %d groups need more than 2^32 threads", scenes, groups);
     *bytes = spc::group_workspace_bytes(N, C, scenes, groups, dtype);
     return SPCONV_OK;
 }
 
+int spconv_groupnorm_workspace_size(int64_t N, int C, int scenes, int groups, int dtype, size_t* bytes) {
+    if (!bytes) return fail(SPCONV_E_INVALID, "bytes pointer is NULL");
+    return check_group(N, C, scenes, groups, dtype, false, bytes);
+}
+
 // Checks of both directions.
 static int group_impl(const spc::GroupArgs& a, bool grad, size_t workspace_bytes, void* stream, const char* name) {
     size_t need = 0;
-    int rc = spconv_groupnorm_workspace_size(a.N, a.C, a.scenes, a.groups, a.dtype, &need);
+    int rc = check_group(a.N, a.C, a.scenes, a.groups, a.dtype, grad, &need);
     if (rc) return rc;
     if (!(a.eps >= 0.f)) return fail(SPCONV_E_INVALID, "eps must be >= 0 (got %g)", (double)a.eps);
     if (a.act != SPCONV_SILU && a.act != SPCONV_GELU && a.act != SPCONV_LINEAR)

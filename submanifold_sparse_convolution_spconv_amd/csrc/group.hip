@@ -465,6 +465,9 @@ bool group_one(int64_t N, int C, int B, int G, int W) {
            (int64_t)B * G <= 512;
 }
 
+// Workgroups of group_sums.
+unsigned channel_sums(int C) { return (2 * C + kJoinCols - 1) / kJoinCols; }
+
 template <typename T, int ACT>
 hipError_t group_go(const GroupParams& p, bool grad, const GroupShape& s, hipStream_t st) {
     const dim3 grid((unsigned)s.items, s.cols);
@@ -478,7 +481,7 @@ hipError_t group_go(const GroupParams& p, bool grad, const GroupShape& s, hipStr
     // threads that join a scene's parts: a wave where it has a few on average
     constexpr int kMany = kJoinCols * 64;
     const bool many = (p.N / p.B / p.rows + 1) * (p.C / p.G) > 256;
-    const unsigned sums = (2 * p.C + kJoinCols - 1) / kJoinCols;
+    const unsigned sums = channel_sums(p.C);
     if (!grad) {
         k_group_part<T, ACT, 0><<<grid, kGrpThreads, 0, st>>>(p);
         if (many)
@@ -511,9 +514,10 @@ size_t stats_bytes(int scenes, int groups) { return align_up((size_t)scenes * gr
 
 }  // namespace
 
-bool group_fits(int64_t N, int C, int scenes, int groups, int dtype) {
+bool group_fits(int64_t N, int C, int scenes, int groups, int dtype, bool grad) {
     const GroupShape s = group_shape(N, C, scenes, dtype);
-    return s.items * s.cols * kGrpThreads < (1ll << 32) && (int64_t)scenes * groups * kOneThreads < (1ll << 32);
+    const int64_t joins = (int64_t)scenes * groups + (grad ? channel_sums(C) : 0);
+    return s.items * s.cols * kGrpThreads < (1ll << 32) && joins * kOneThreads < (1ll << 32);
 }
 size_t group_workspace_bytes(int64_t N, int C, int scenes, int groups, int dtype) {
     return stats_bytes(scenes, groups) + align_up((size_t)group_shape(N, C, scenes, dtype).items * 2 * C * 4, 256);

@@ -303,7 +303,7 @@ struct GroupArgs {
     int act, dtype;
 };
 // A launch's threads are counted in 32 bits: false where a kernel would need more.
-bool group_fits(int64_t N, int C, int scenes, int groups, int dtype);
+bool group_fits(int64_t N, int C, int scenes, int groups, int dtype, bool grad);
 size_t group_workspace_bytes(int64_t N, int C, int scenes, int groups, int dtype);
 hipError_t launch_group(const GroupArgs& a, bool grad, hipStream_t stream);
 

@@ -7,7 +7,7 @@ import pytest
 
 import submanifold_sparse_convolution_spconv_amd as sp
 
-OK, UNSUPPORTED = 0, -2
+OK, UNSUPPORTED, WORKSPACE = 0, -2, -5
 LAST = (1 << 31) - 1024         # rows of a sequence: the loops look up to 8 tiles of 64 rows past the end
 
 
@@ -42,3 +42,17 @@ def test_attention_threads_are_counted_by_the_kernel_taken(lib):
         # sequences of few rows: 16 or 32 rows a workgroup, and one for each sequence at least
         assert Z(1 << 19, 1 << 19, H=16) == OK and Z(1 << 20, 1 << 20, H=16) == UNSUPPORTED
         assert Z(1, (1 << 24) - 128, H=1) == OK and Z(1, 1 << 24, H=1) == UNSUPPORTED
+
+
+def test_groupnorm_gradient_counts_its_channel_sums(lib):
+    """The gradient's launch that joins scenes and groups has workgroups for dweight
+    and dbias too: with them 2^32 threads are reached where the forward's are not."""
+    p = ctypes.c_void_p(0x7f0000000000)         # never read: every call fails a check
+    n = ctypes.c_size_t(0)
+    C, G = 4096, 4
+    for B, want in (((1 << 20) - 1, UNSUPPORTED), ((1 << 20) - 100, UNSUPPORTED), ((1 << 20) - 128 - 1, WORKSPACE)):
+        assert lib.spconv_groupnorm_workspace_size(1, C, B, G, sp.SPCONV_BF16, ctypes.byref(n)) == OK
+        assert lib.spconv_groupnorm(p, p, None, None, p, 0, p, None, None, 1, C, B, G, 1e-5, 0, sp.SPCONV_BF16,
+                                    None) == WORKSPACE
+        assert lib.spconv_groupnorm_grad(p, p, p, p, p, None, None, p, 0, p, p, p, 1, C, B, G, 0, sp.SPCONV_BF16,
+                                         None) == want, B
