@@ -406,7 +406,8 @@ int spconv_scan_grad(const void* dout, const void* x, const void* z, const int32
  * the parts of one projection (N, 3, H, D) are used where they lie.  `strides`
  * (host) holds, for each tensor in the order that the call states, two
  * numbers: elements from row to row and from head to head; NULL: all
- * contiguous.  A head's elements are consecutive. */
+ * contiguous.  A head's elements are consecutive, and an output's rows and heads
+ * do not lie in one another (SPCONV_E_INVALID). */
 
 /* Frequencies of rotary positions (host; freqs is host memory of `pairs`
  * doubles, to be copied to the device by the caller), in radians per step of a

@@ -729,6 +729,15 @@ int spconv_rotary_freqs(int pairs, int axes, double base, double factor, double 
     return SPCONV_OK;
 }
 
+// Whether an output's rows or heads, D elements each, lie in one another: a stride
+// is shorter than D, or the longer one than all that the shorter one spans.
+static bool heads_overlap(const int64_t* strides, int64_t rows, int heads, int D) {
+    const int64_t r = std::abs(strides[0]), h = std::abs(strides[1]);
+    if ((rows > 1 && r < D) || (heads > 1 && h < D)) return true;
+    if (rows <= 1 || heads <= 1) return false;
+    return (r < h ? rows : heads) - 1 > (std::max(r, h) - D) / std::min(r, h);
+}
+
 static int rotary_impl(const void* x, const int32_t* positions, int64_t pos_stride, const double* freqs, void* y,
                        const int64_t* strides, int64_t N, int H, int D, int pairs, int axes, int layout, float gain,
                        int dtype, void* stream, bool back, const char* name) {
@@ -754,6 +763,7 @@ static int rotary_impl(const void* x, const int32_t* positions, int64_t pos_stri
         }
         if (x == y && (a.xs[0] != a.ys[0] || a.xs[1] != a.ys[1]))
             return fail(SPCONV_E_INVALID, "in place, both strides must be the same");
+        if (heads_overlap(a.ys, N, H, D)) return fail(SPCONV_E_INVALID, "rows or heads of the output overlap");
     }
     hipError_t e = spc::launch_rotary(a, back, (hipStream_t)stream);
     return e == hipSuccess ? SPCONV_OK : hip_fail(e, name);
@@ -917,6 +927,9 @@ static int attention_impl(spc::AttnArgs& a, bool grad, const int64_t* strides, s
         if (tensors[i].s[0] < 0 || tensors[i].s[1] < 0) return fail(SPCONV_E_INVALID, "strides must be >= 0");
         if (tensors[i].s[0] * (16 / unit) > spc::kMaxRowStride)
             return fail(SPCONV_E_UNSUPPORTED, "rows must be at most %lld bytes apart", (long long)spc::kMaxRowStride);
+        const int64_t rows = tensors[i].s == a.dks || tensors[i].s == a.dvs ? a.M : a.N;
+        if ((grad ? i > 4 : i == 3) && heads_overlap(tensors[i].s, rows, tensors[i].heads, a.D))
+            return fail(SPCONV_E_INVALID, "rows or heads of an output overlap");
     }
     const size_t need = grad ? spc::attn_grad_workspace_bytes(a) : spc::attn_workspace_bytes(a);
     if (need) {
