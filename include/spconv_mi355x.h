@@ -500,8 +500,8 @@ int spconv_groupnorm_grad(const void* dout, const void* x, const int32_t* offset
  *            be NULL when that is 0)
  * D a multiple of 8 up to 128, H and HK up to 4096, H a multiple of HK, scale >
  * 0.  Scores and sums are fp32; with SPCONV_BF16 the weights p (before their
- * division by the sum) are rounded to bfloat16 once, as the operand of the
- * second product.  More than 2^31 - 1024 keys M or rows N H / HK, and calls of more
+ * division by the sum) are the second product's operand, rounded to bfloat16 once
+ * in calls of many rows and in two parts, rounded and rest, in those of few.  More than 2^31 - 1024 keys M or rows N H / HK, and calls of more
  * than 2^32 threads, give SPCONV_E_UNSUPPORTED. */
 int spconv_attention_workspace_size(int64_t N, int64_t M, int B, int H, int HK, int D, int dtype, size_t* bytes);
 int spconv_attention(const void* q, const void* k, const void* v, const int32_t* offsets, const int32_t* koffsets,

@@ -9,8 +9,13 @@
 // second kernel.  Bound by memory where it is about single tokens: a wave has
 // the next 32 keys and values in flight (16 KB at D = 128 bf16) while it works
 // on the last.  64 single tokens against 262,144 keys, 8 heads on 2 of 128 bf16:
-// 69 us and 4.4 for the join (3.9 TB/s; with the 32 columns of the other kernel
-// and half as many waves 215).
+// 95 us a call (2.8 TB/s; with the 32 columns of the other kernel and half as many
+// waves 215).
+//
+// bf16 weights are the second product's operand in two parts, rounded and rest: its
+// instructions are not what bounds these calls, and the outputs then have their own
+// rounding only (1.7e-3 of their norm; 2.2e-3 with weights rounded once, at 92 us
+// for that call, and 10.7 instead of 11.2 for 4,096 rows in 16 scenes).
 #include "attn.h"
 
 #include <algorithm>
@@ -66,6 +71,13 @@ struct Operand16<__bf16, DP> {
         frag f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = (__bf16)w[j];
+        return f;
+    }
+    // what that rounding left out, as an operand
+    static __device__ __forceinline__ frag pack_rest(const float (&w)[8], frag b, int) {
+        frag f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = (__bf16)(w[j] - (float)b[j]);
         return f;
     }
     static __device__ __forceinline__ f32x4a_t mma(frag a, frag b, f32x4a_t c) { return mfma16(a, b, c); }
@@ -135,6 +147,7 @@ __device__ __forceinline__ void add_rows16(f32x4a_t (&acc)[DP / 16], const lds_u
                 a = W::without(a, x);
             }
             acc[dt] = O::mma(a, b, acc[dt]);
+            if constexpr (sizeof(T) == 2) acc[dt] = O::mma(a, O::pack_rest(w, b, c), acc[dt]);
         }
     }
     if (MASKED && __builtin_expect(__ballot(some) != 0, 0)) {
