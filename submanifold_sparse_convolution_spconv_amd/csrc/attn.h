@@ -41,7 +41,8 @@ struct AttnParams {
     int causal;
     int near;                   // 1: rows are below 2 GiB from their tensor's start
     int splits;                 // of the long axis over workgroups
-    float scale, scale2;        // of the scores; the same times log2 e
+    float scale, scale2;        // of the scores; the same times log2 e, rounded
+    float per_lse, per_lse_rest; // scale2 / scale: lse in powers of two
 };
 
 AttnParams attn_params(const AttnArgs& a);

@@ -304,7 +304,12 @@ AttnParams attn_params(const AttnArgs& a) {
     const auto below = [&](const int64_t(&s)[2]) { return a.M * s[0] * es < (1ll << 31); };
     p.near = below(a.ks) && below(a.vs);
     p.scale = a.scale;
+    // (both directions multiply every score by scale2 as it is rounded; a gradient whose
+    // lse went by log2 e instead would have all weights off the same way)
     p.scale2 = a.scale * 1.4426950408889634f;
+    const double per_lse = (double)p.scale2 / a.scale;
+    p.per_lse = (float)per_lse;
+    p.per_lse_rest = (float)(per_lse - p.per_lse);
     return p;
 }
 

@@ -34,7 +34,6 @@ namespace spc {
 namespace {
 
 constexpr int kFineKeys = 256;
-constexpr float kLog2e = 1.4426950408889634f;
 
 // KS: the waves of a workgroup take turns at the long axis for 32 rows instead
 // of sharing its tiles for 32 rows each.
@@ -52,8 +51,11 @@ struct GradShape {
     static constexpr int DKV_OCC = DP <= 32 || (DP == 64 && (ES == 2 || !KS)) ? 2 : 1;
 };
 
-// lse in powers of two; rows without keys: p = 2^-inf = 0
-__device__ __forceinline__ float stat2(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
+// lse in powers of two; rows without keys (-inf), and places without a row (inf): p =
+// 2^-inf = 0
+__device__ __forceinline__ float stat2(const AttnParams& p, float lse) {
+    return fabsf(lse) == INFINITY ? INFINITY : fmaf(lse, p.per_lse, lse * p.per_lse_rest);
+}
 
 template <typename T, int DP, bool KS>
 __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T, DP, KS>::DQ_OCC)) k_attn_dq(AttnParams p) {
@@ -83,7 +85,7 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
     for (int i = 0; i < 16; ++i) delta = row16(i, h) == (lane & 31) ? dd[i] : delta;
     const float other = __shfl_xor(delta, 32);
     delta = ((lane >> 2) & 1) == h ? delta : other;
-    const float lse2 = stat2(p.lse[(int64_t)qr.row * p.H + qr.head]);
+    const float lse2 = stat2(p, p.lse[(int64_t)qr.row * p.H + qr.head]);
 
     const int nt = (qr.longest + KT - 1) / KT;
     const bool fine = S::ES == 2 && qr.longest <= kFineKeys;
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__((64 * GradShape<T, DP, KS>::NW), (GradShape<T,
         St::store(rq, qt, st);
         St::store(rd, qt + S::TILE, st);
         if (st < KT) {
-            stats[b * 2 * KT + st] = stat2(lse);
+            stats[b * 2 * KT + st] = stat2(p, lse);
             stats[b * 2 * KT + KT + st] = -delta;
         }
     };
