@@ -14,9 +14,9 @@
 // (32 in fp32), fetched into registers while the tile before is worked on.
 //
 // Bound by issue: exponentials at heads of 32 (1,006,716 rows in runs of 1,024
-// by order, 4 heads bf16: 1,010 us, 522 TFLOP/s), exponentials and matrix
-// instructions at 64 (29,578 rows in two causal scenes, 8 heads on 2: 530 us,
-// 888 TFLOP/s).
+// by order, 4 heads bf16: 1,036 us a call, 509 TFLOP/s), exponentials and matrix
+// instructions at 64 (29,578 rows in two causal scenes, 8 heads on 2: 541 us,
+// 870 TFLOP/s).
 //
 // The reference that a query's exponentials are taken against is the maximum of
 // the first 32 keys, so that the largest weight is 1 at least; larger ones do
@@ -219,6 +219,20 @@ hipError_t attn_go(AttnParams p, hipStream_t st) {
 
 // What a call's sizes choose: 16 rows a workgroup (attn_few.hip), and the parts
 // that the keys are split into; else 128.
+//
+// Few workgroups of 128 leave the card idle, workgroups of 16 read the keys eight
+// times as often.  One scene, 8 heads on 2 of 64, us with 16 and with 128 rows:
+//   rows (workgroups of 128)   2,000 (126)   3,000 (188)   4,000 (252)   8,000 (502)
+//   bf16, causal                  26, 30        42, 42        61, 55       193, 139
+//   bf16, full                    37, 31        64, 43       105, 56       372, 155
+//   fp32, causal                  88, 168      168, 248      277, 329      979, 1051
+//   fp32, full                   138, 172      290, 251      490, 333     1855, 1088
+// One bound for all: 256 workgroups, where causal bf16 changes sides.  Sequences of
+// 32 rows at most take 16 whatever their number, for the sake of single tokens and
+// long caches (64 tokens against 262,144 keys: 95, 215); many short sequences on their
+// own keys lose by it (1,000 of 16 rows, 4 heads of 32 bf16: 37, 23; of 32: 44, 25).
+// Averages decide, since offsets are on the device: a long sequence among many
+// short ones is treated as they are.
 struct Plan {
     bool few;
     int splits;

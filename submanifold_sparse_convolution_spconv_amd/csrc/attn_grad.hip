@@ -13,9 +13,10 @@
 // registers: (key, query) tiles for dq, (query, key) tiles for dk and dv; all
 // sums are fp32.
 //
-// Two causal scenes of 29,578 rows, 8 heads on 2 of 64 bf16: 790 us for dq, 1,090
-// for dk and dv in five parts (900 and 870 TFLOP/s of executed products), vector
-// issue 43% and matrix unit 44% of the time.
+// Two causal scenes of 29,578 rows, 8 heads on 2 of 64 bf16: 1,803 us a call; under
+// the profiler 828 for dq, 1,120 for dk and dv in five parts and 27 for their sums
+// (850 and 840 TFLOP/s of executed products), vector issue 43% and matrix unit 44%
+// of the time.
 //
 // In bf16, p and ds are rounded once as operands, which is as much again as the
 // results' own rounding (2.4e-3 of a gradient's norm in all, 1.7e-3 without).

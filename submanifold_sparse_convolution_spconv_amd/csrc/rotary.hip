@@ -12,7 +12,7 @@
 // out even starts earlier instead and repeats some of its neighbour's elements
 // (in place too: the wave has read both before either is written).  Angles
 // are 64-bit turns less whole turns: in 32 bits the angle of position 1e6 would
-// be off by 0.06.  1,006,716 rows of 8 heads of 32 bf16: 190 us (5.4 TB/s).
+// be off by 0.06.  1,006,716 rows of 8 heads of 32 bf16: 187 us (5.6 TB/s).
 #include "places.h"
 
 #include <algorithm>
