@@ -1046,7 +1046,8 @@ def spconv_attention(q, k, v, offsets, koffsets=None, order=None, korder=None, c
     koffsets.  ``causal``: the last query of a sequence sees all its keys, the one
     before it all but one, and so on.  scale: of the scores, > 0 (None: D^-0.5).
     Returns out (N, H, D), with ``stats`` (out, lse), lse float32 (N, H), for the
-    gradient; a query without keys gives 0 and -inf.  Rows behind the last
+    gradient; a query without keys, or whose scores are all -inf, gives 0 and
+    -inf.  ``out`` may be strided, its rows and heads apart.  Rows behind the last
     sequence are not read, and not written in ``out`` (in a new output they hold
     anything).  workspace: a uint8 tensor of at least
     spconv_attention_workspace_size bytes (allocated when None)."""
@@ -1066,8 +1067,8 @@ def spconv_attention_grad(dout, q, k, v, out, lse, offsets, koffsets=None, order
     """Gradient of spconv_attention: dout (N, H, D), the forward's arguments, its
     output and lse.  Returns (dq, dk, dv) in their dtype, dk and dv summed over
     the heads that share them.  ``grads``: the three tensors to write into, such as
-    views of one projection's gradient (rows behind the last sequence stay as
-    they were).  workspace: a uint8 tensor of at least
+    views of one projection's gradient, rows and heads apart (rows behind the last
+    sequence stay as they were).  workspace: a uint8 tensor of at least
     spconv_attention_grad_workspace_size bytes (allocated when None)."""
     dt, N, M, B, H, HK, D, dev, q, k, v, offsets, koffsets, order, korder, scale = _attention_args(
         q, k, v, offsets, koffsets, order, korder, scale)

@@ -9,9 +9,10 @@
 // 32 on), the sum needs no exchange until the end, and the scores' layout is
 // already that of the second product's operand (rounded to bf16 there, which
 // adds as much error as the output's own rounding; sums and references stay
-// fp32.  In two parts, rounded and rest, outputs would have their own rounding only,
-// for 805 instead of 537 and 1,401 instead of 1,037 us of the calls below).  Values are read transposed from LDS.  Four waves share tiles of 64 keys
-// (32 in fp32), fetched into registers while the tile before is worked on.
+// fp32.  In two parts, rounded and rest, outputs would have their own rounding
+// only, but the calls below would take 1,401 instead of 1,037 us and 805 instead
+// of 537).  Values are read transposed from LDS.  Four waves share tiles of 64
+// keys (32 in fp32), fetched into registers while the tile before is worked on.
 //
 // Bound by issue: exponentials at heads of 32 (1,006,716 rows in runs of 1,024
 // by order, 4 heads bf16: 1,036 us a call, 509 TFLOP/s), exponentials and matrix
